@@ -1,6 +1,6 @@
 """Build libgather_lora.so (sm_103a) in-tree with nvcc.
 
-Two translation units compiled in parallel (device code, host ABI), then linked
+The translation units (device code, host ABI) compiled in parallel, then linked
 into one shared library with the static CUDA runtime. Used by
 ``__graft_entry__.build()``; run directly with ``python -m gather_lora_gb300.build``.
 """
@@ -18,7 +18,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgather_lora.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-Xcompiler", "-Wall"]
-SOURCES = ["kernels.cu", "dense.cu", "abi.cpp"]
+SOURCES = ["kernels.cu", "dense.cu", "kv_cache.cu", "attn_decode.cu", "attn_prefill.cu", "abi.cpp", "attn_abi.cpp"]
 
 
 def nvcc() -> str:

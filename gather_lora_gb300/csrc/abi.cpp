@@ -13,12 +13,16 @@
 #include <cstdio>
 #include <cstring>
 
+#include "abi_common.h"
+#include "attn_types.h"
 #include "dense_types.h"
 #include "fold_types.h"
 
 namespace {
-
 thread_local char g_err[512] = "";
+}
+
+namespace glora {
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -33,15 +37,9 @@ int ok() {
   return LORA_OK;
 }
 
-inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
-inline int round_up(int a, int m) { return (a + m - 1) / m * m; }
-inline int round_down(int a, int m) { return a / m * m; }
-inline int pow2_floor(int v) {
-  int p = 1;
-  while (p * 2 <= v) p *= 2;
-  return p;
+int cuda_fail(int err, const char* what) {
+  return fail(LORA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(static_cast<cudaError_t>(err)));
 }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // SMs of the current device, or `fallback` without one (host-only geometry queries).
 int device_sm_count_or(int fallback) {
@@ -53,6 +51,25 @@ int device_sm_count_or(int fallback) {
   }
   return v;
 }
+
+}  // namespace glora
+
+namespace {
+
+using glora::cuda_fail;
+using glora::device_sm_count_or;
+using glora::fail;
+using glora::ok;
+
+inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+inline int round_up(int a, int m) { return (a + m - 1) / m * m; }
+inline int round_down(int a, int m) { return a / m * m; }
+inline int pow2_floor(int v) {
+  int p = 1;
+  while (p * 2 <= v) p *= 2;
+  return p;
+}
+using glora::aligned16;
 
 // Shared-memory budgets: two CTAs per SM, or one when the fixed part is large.
 // The tuning constants can be overridden at build time for measurement sweeps.
@@ -348,10 +365,6 @@ int check_shape(int32_t max_rank, int32_t k_in, int32_t n_out, int64_t xs, int64
   if (xs % 8 || os % 8)
     return fail(LORA_ERR_ALIGN, "row strides must be multiples of 8 elements (%lld, %lld)", (long long)xs, (long long)os);
   return LORA_OK;
-}
-
-int cuda_fail(int err, const char* what) {
-  return fail(LORA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(static_cast<cudaError_t>(err)));
 }
 
 // ---- dense single-adapter delta ----------------------------------------------

@@ -25,6 +25,46 @@ TMAP_MIN_RANK = 32         # LORA_TMAP_MIN_RANK: a_tmaps are used from this max_
 DELTA_DENSE_MIN_ROWS = 256  # LORA_DELTA_DENSE_MIN_ROWS: lora_delta's tensor-core path from this m up
 
 
+# enum lora_kv_format, and the scratch lora_attn_decode wants (zero-filled once)
+KV_BF16, KV_E4M3, KV_INT8 = 0, 1, 2
+ATTN_WORKSPACE = 16 << 20   # LORA_ATTN_WORKSPACE
+
+
+class _KvCacheStruct(ctypes.Structure):
+    """lora_kv_cache of include/gather_lora.h."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("num_pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class KvCache:
+    """A paged key-value cache (lora_kv_cache): k_pages and v_pages are torch tensors (or views of
+    any strides, the same for both, innermost 1) of shape [num_pages, kv_heads, page_size, head_dim]
+    in bfloat16, float8_e4m3fn or int8; k_scale and v_scale, for the 8-bit types, contiguous float32
+    [num_pages, kv_heads, page_size]. The object keeps the tensors alive."""
+
+    def __init__(self, k_pages, v_pages, k_scale=None, v_scale=None):
+        import torch
+        formats = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3, torch.int8: KV_INT8}
+        if k_pages.dtype not in formats or v_pages.dtype != k_pages.dtype:
+            raise ValueError(f"cache pages are bfloat16, float8_e4m3fn or int8, K and V alike: got {k_pages.dtype}, {v_pages.dtype}")
+        if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride() or k_pages.stride(3) != 1:
+            raise ValueError("cache pages are [num_pages, kv_heads, page_size, head_dim], K and V with the same strides, innermost 1")
+        fmt = formats[k_pages.dtype]
+        for s in (k_scale, v_scale) if fmt != KV_BF16 else ():
+            if s is None or s.dtype != torch.float32 or s.shape != k_pages.shape[:3] or not s.is_contiguous():
+                raise ValueError("8-bit pages want contiguous float32 scales [num_pages, kv_heads, page_size] for K and V")
+        self.tensors = (k_pages, v_pages, k_scale, v_scale)
+        self.struct = _KvCacheStruct(_addr(k_pages), _addr(v_pages), _addr(k_scale), _addr(v_scale),
+                                     *k_pages.stride()[:3], *k_pages.shape, fmt)
+
+
+def _cache(c):
+    return c if c is None else ctypes.byref(c.struct if isinstance(c, KvCache) else c)
+
+
 class LoraError(RuntimeError):
     def __init__(self, code: int, text: str):
         super().__init__(f"{STATUS_NAMES.get(code, code)}: {text}")
@@ -60,6 +100,16 @@ def load():
     lib.lora_encode_a_tmaps.argtypes = [P, I32, I32, I32, P]
     lib.lora_selftest_wait_timeout.restype = ctypes.c_int
     lib.lora_selftest_wait_timeout.argtypes = [I64, P]
+    KV = ctypes.POINTER(_KvCacheStruct)
+    lib.lora_kv_write.restype = ctypes.c_int
+    lib.lora_kv_write.argtypes = [P, I64, P, I64, P, I32, KV, P]
+    lib.lora_kv_read.restype = ctypes.c_int
+    lib.lora_kv_read.argtypes = [P, I64, P, I64, P, I32, KV, P]
+    lib.lora_attn_decode.restype = ctypes.c_int
+    lib.lora_attn_decode.argtypes = [P, I64, P, I64, I32, I32, ctypes.c_float, KV, P, I64, I32, P, P, P, I64, P]
+    lib.lora_attn_prefill.restype = ctypes.c_int
+    lib.lora_attn_prefill.argtypes = [P, I64, P, I64, P, I64, P, I64, P, P, I32, I32, I32, I32, I32, I32,
+                                      ctypes.c_float, P, P]
     lib.lora_last_error.restype = ctypes.c_char_p
     lib.lora_last_error.argtypes = []
     lib.lora_read_device_status.restype = ctypes.c_int
@@ -167,6 +217,38 @@ def lora_moe_gather_bgmv(x, x_row_stride, base_out, out_row_stride, indices, n_r
         _addr(row_adapter), num_tokens, num_experts, _addr(a_table), _addr(b_table),
         _addr(scale_table), max_loras, max_rank, k_in, n_out, _addr(xa), _addr(a_tmaps),
         int(flags), _stream(stream)))
+
+
+def lora_kv_write(k, k_row_stride, v, v_row_stride, slots, n, cache, stream=None):
+    """K and V rows into their cache slots (see lora_kv_write in include/gather_lora.h). slots:
+    int64 [n]; cache: a KvCache."""
+    return _check(load().lora_kv_write(_addr(k), k_row_stride, _addr(v), v_row_stride, _addr(slots), n,
+                                       _cache(cache), _stream(stream)))
+
+
+def lora_kv_read(k_out, k_row_stride, v_out, v_row_stride, slots, n, cache, stream=None):
+    """Cache slots back into BF16 rows (see lora_kv_read in include/gather_lora.h)."""
+    return _check(load().lora_kv_read(_addr(k_out), k_row_stride, _addr(v_out), v_row_stride, _addr(slots), n,
+                                      _cache(cache), _stream(stream)))
+
+
+def lora_attn_decode(q, q_row_stride, out, out_row_stride, batch, q_heads, scale, cache, block_table,
+                     table_stride, max_pages, seq_lens, workspace, workspace_bytes, lse=None, stream=None):
+    """Attention of one new token per sequence over the cache (see lora_attn_decode in
+    include/gather_lora.h). workspace: at least ATTN_WORKSPACE bytes, zero-filled once."""
+    return _check(load().lora_attn_decode(_addr(q), q_row_stride, _addr(out), out_row_stride, batch, q_heads, scale,
+                                          _cache(cache), _addr(block_table), table_stride, max_pages,
+                                          _addr(seq_lens), _addr(lse), _addr(workspace), workspace_bytes,
+                                          _stream(stream)))
+
+
+def lora_attn_prefill(q, q_row_stride, k, k_row_stride, v, v_row_stride, out, out_row_stride, cu_q, cu_k, batch,
+                      total_q, total_k, q_heads, kv_heads, head_dim, scale, lse=None, stream=None):
+    """Causal attention over packed sequences (see lora_attn_prefill in include/gather_lora.h)."""
+    return _check(load().lora_attn_prefill(_addr(q), q_row_stride, _addr(k), k_row_stride, _addr(v), v_row_stride,
+                                           _addr(out), out_row_stride, _addr(cu_q), _addr(cu_k), batch, total_q,
+                                           total_k, q_heads, kv_heads, head_dim, scale, _addr(lse),
+                                           _stream(stream)))
 
 
 def lora_encode_a_tmaps(a_ptrs, max_rank: int, k_in: int):

@@ -9,6 +9,12 @@
  *   lora_moe_gather_bgmv  the decode-path MoE fold over flat (token, slot) rows
  *   lora_delta            one adapter pair folded into every row (prefill)
  *
+ * the attention beside them in a serving step (the section further down):
+ *
+ *   lora_kv_write, lora_kv_read   a paged key-value cache in BF16 or 8 bits
+ *   lora_attn_decode              one new token per sequence over that cache
+ *   lora_attn_prefill             causal attention over packed prompts
+ *
  * plus lora_encode_a_tmaps (TMA tensor maps of the A matrices, encoded once on
  * the host), diagnostics (status word, geometry queries, a bounded-wait self
  * test) and five pure host helpers (no GPU needed) for the MoE windows, grids
@@ -344,6 +350,131 @@ int lora_read_device_status(void* stream, uint32_t* status_out, int clear);
  */
 int lora_launch_geometry(int moe, int32_t rows, int32_t max_loras, int32_t max_rank,
                          int32_t k_in, int32_t n_out, int64_t out[12]);
+
+/* ---- attention beside the folds -------------------------------------------
+ *
+ * The [Q|K|V] rows that lora_bgmv folds in place go into a paged key-value cache
+ * (lora_kv_write), and attention reads them: one new token per sequence over the
+ * cache (lora_attn_decode), or whole prompts and prompt chunks over packed K and
+ * V rows (lora_attn_prefill), a cached prefix being read back into such rows
+ * first (lora_kv_read). The conventions above hold: device pointers owned by
+ * the caller, strides in elements, checks on the host before any launch, no
+ * allocation, no synchronization, launch shapes from host integers alone
+ * (capture-safe), bad device data is never a fault. q_heads query heads share
+ * kv_heads key-value heads, q_heads a multiple of kv_heads: query head h reads
+ * key-value head h / (q_heads / kv_heads). Scores, softmax statistics and sums
+ * are fp32. None of these has a counterpart in the pages.
+ */
+
+/* What a cache element is. The 8-bit formats keep one f32 scale per token and
+ * key-value head, for K and for V: value = code * scale. */
+enum lora_kv_format {
+    LORA_KV_BF16 = 0,   /* BF16, no scales */
+    LORA_KV_E4M3 = 1,   /* 8-bit float, 4 exponent and 3 mantissa bits, largest 448 */
+    LORA_KV_INT8 = 2    /* signed 8-bit integer, -127 .. 127 */
+};
+
+/*
+ * A paged cache. Token slot t of page p, key-value head h, starts at element
+ *   p * page_stride + h * head_stride + t * token_stride
+ * of k_pages and of v_pages and is head_dim elements wide, so pages may be
+ * [kv_heads, page_size, head_dim], [page_size, kv_heads, head_dim], or K and V
+ * halves of one buffer. k_scale and v_scale (8-bit formats; ignored for BF16)
+ * are contiguous [num_pages, kv_heads, page_size] f32.
+ * k_pages and v_pages are 16-byte aligned, the strides multiples of 16 bytes.
+ */
+typedef struct lora_kv_cache {
+    void *k_pages, *v_pages;
+    float *k_scale, *v_scale;
+    int64_t page_stride, head_stride, token_stride;
+    int32_t num_pages, kv_heads, page_size, head_dim;
+    int32_t format;                /* enum lora_kv_format */
+} lora_kv_cache;
+
+#define LORA_MAX_HEADS 1024        /* q_heads and kv_heads in [1, 1024] */
+#define LORA_MAX_KV_ROWS (1 << 24) /* n of lora_kv_write / lora_kv_read, total rows of lora_attn_prefill */
+#define LORA_MAX_SEQS 8192         /* batch of lora_attn_decode / lora_attn_prefill in [0, 8192] */
+                                   /* head_dim is 64 or 128 */
+
+/*
+ * lora_kv_write — K and V rows into their cache slots, quantised as they are written.
+ *
+ * Row i of k and of v holds kv_heads * head_dim BF16 values (row strides in
+ * elements, multiples of 8); slots[i] = page * page_size + slot in the page, any
+ * value outside [0, num_pages * page_size) skips the row. Two rows of one call
+ * with the same slot leave one of the two, which one is not defined.
+ * E4M3 and INT8, per row and head, Q = 448 or 127, a = the largest magnitude:
+ *   scale = a / Q,  code = round(x * (Q / a))    (f32 operations, ties to even);
+ *   a < 2^-100: scale 0 and codes 0; a value that is not finite: scale NaN and
+ *   codes 0, so that the whole row reads back as NaN.
+ */
+int lora_kv_write(const lora_bf16_t* k, int64_t k_row_stride, const lora_bf16_t* v, int64_t v_row_stride,
+                  const int64_t* slots, int32_t n, const lora_kv_cache* cache, void* stream);
+
+/*
+ * lora_kv_read — cache slots back into BF16 rows: row i of k_out and v_out is
+ * the token at slots[i] (as lora_kv_write numbers them), bf16(code * scale) in the
+ * 8-bit formats; a slot outside the cache gives a row of zeros.
+ */
+int lora_kv_read(lora_bf16_t* k_out, int64_t k_row_stride, lora_bf16_t* v_out, int64_t v_row_stride,
+                 const int64_t* slots, int32_t n, const lora_kv_cache* cache, void* stream);
+
+/*
+ * lora_attn_decode — attention of one new token per sequence over the cache.
+ *
+ * For sequence b, query head h and the L = seq_lens[b] cached tokens (clamped to
+ * [0, max_pages * page_size]; token t lies in page block_table[b, t / page_size]
+ * at slot t % page_size):
+ *   z_t = scale * (q[b, h] . k_t),   out[b, h] = sum_t softmax(z)_t v_t.
+ * A token whose page is outside [0, num_pages) is left out; a sequence with no
+ * token gives zeros and lse = -infinity. Nothing outside a sequence's tokens is
+ * read (a page's unused slots may hold anything).
+ *   q, out       [batch, row stride] BF16, q_heads * head_dim values used, 16-byte
+ *                aligned, strides multiples of 8
+ *   block_table  [batch, table_stride] int32, max_pages entries used per sequence
+ *   seq_lens     [batch] int32, the new token (already written) included
+ *   lse          optional [batch, q_heads] f32: ln sum_t exp(z_t)
+ *   workspace    device scratch of at least LORA_ATTN_WORKSPACE bytes, 16-byte
+ *                aligned, zero-filled by the caller once; every call leaves it
+ *                ready for the next on the same stream. Calls that may run at the
+ *                same time need one each.
+ *   scale        positive and finite (1 / sqrt(head_dim) as a rule)
+ * How a sequence is split over the GPU follows the lengths of the whole batch:
+ * results are the same bits for the same batch, and may differ in the last bits
+ * between batches.
+ */
+#define LORA_ATTN_WORKSPACE (16 << 20)
+int lora_attn_decode(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* out, int64_t out_row_stride,
+                     int32_t batch, int32_t q_heads, float scale, const lora_kv_cache* cache,
+                     const int32_t* block_table, int64_t table_stride, int32_t max_pages,
+                     const int32_t* seq_lens, float* lse, void* workspace, int64_t workspace_bytes,
+                     void* stream);
+
+/*
+ * lora_attn_prefill — causal attention over packed sequences of different lengths.
+ *
+ * Sequence b has query rows [cu_q[b], cu_q[b+1]) of q and key rows
+ * [cu_k[b], cu_k[b+1]) of k and v (Lq and Lk of them). Its query row i sees the
+ * keys j <= i + Lk - Lq: with Lk > Lq the first Lk - Lq keys are a prefix that
+ * all rows see. Per row and head
+ *   z_j = scale * (q_i . k_j),   out_i = sum_j softmax(z)_j v_j;
+ * a row that sees no key (Lk < Lq) gives zeros and lse = -infinity. Keys that a
+ * row does not see have no influence on it, whatever they hold.
+ *   q, out    [total_q, row stride] BF16, q_heads * head_dim values used
+ *   k, v      [total_k, row stride] BF16, kv_heads * head_dim values used
+ *   cu_q, cu_k  [batch + 1] int32, non-decreasing, in [0, total_q] / [0, total_k]
+ *             (a sequence whose offsets are not is left out); query rows of no
+ *             sequence stay unchanged
+ *   lse       optional [total_q, q_heads] f32: ln sum_j exp(z_j)
+ *   scale     positive and finite
+ * All four matrices are 16-byte aligned with row strides that are multiples of 8,
+ * so q, k and v may be the parts of [Q|K|V] rows.
+ */
+int lora_attn_prefill(const lora_bf16_t* q, int64_t q_row_stride, const lora_bf16_t* k, int64_t k_row_stride,
+                      const lora_bf16_t* v, int64_t v_row_stride, lora_bf16_t* out, int64_t out_row_stride,
+                      const int32_t* cu_q, const int32_t* cu_k, int32_t batch, int32_t total_q,
+                      int32_t total_k, int32_t q_heads, int32_t kv_heads, int32_t head_dim, float scale,
+                      float* lse, void* stream);
 
 /* ---- pure host helpers (no GPU) ------------------------------------------ */
 
