@@ -1,95 +1,718 @@
 // Attention of one new token per sequence over the paged cache (sm_103a).
-#include "attn_row.cuh"
+//
+// For sequence b and the G query heads that share key-value head h:
+//   z[g, t] = scale (q_g . k_t),  out_g = sum_t softmax(z_g)_t v_t.
+// Every cached byte is used once per call (2 G multiply-adds per element), so HBM bandwidth
+// bounds the kernel; what it needs is enough bytes in flight on every SM and an even share of the
+// batch's tokens for each, whatever the lengths are.
+//
+// Split. The work unit is a tile of kTile tokens of one segment: a segment is (sequence, key-value
+// head, block of 16 query heads). All tiles of the batch, segment after segment, are cut into equal
+// contiguous ranges, one per CTA (two CTAs per SM; fewer CTAs when there would be less than one tile
+// for each warp). A range is walked piece by piece (a piece: its part of one segment). A piece that is
+// a whole segment is finished by its CTA; otherwise the CTA stores (maximum, sum, unnormalised output)
+// in the workspace and the last CTA of the segment to arrive joins them in CTA order, so the bits never
+// depend on who was last. Segments over many CTAs join in two levels (kJoinGroup).
+//
+// Tile. A warp streams its own tiles (every kDecWarps-th of a piece) through a ring of kStages 8 KB stages of
+// cp.async copies that runs on across pieces; the CTA's warps join once per piece. On the tensor cores
+// (mma.sync m16n8k16) the 16 rows of A are the query heads, so the scores' accumulator layout is the
+// layout of A in the product with V. Running maximum m and sum l per row as usual.
+//
+// 8-bit formats. K's codes become f16 pairs in registers (exact: E4M3 and integers to 127 fit f16's 11
+// bits; Q is scaled by a power of two into f16's range), V's become BF16 pairs (exact too), because K's scale
+// multiplies the score but V's the weight, p_t s_t, and scales may differ by any factor from token to
+// token: BF16 has fp32's range. A lane's 4 consecutive code bytes of K are 4 consecutive dimensions, so the
+// dimensions of Q are dealt to the MMA's k index in that order; V is read transposed as byte pairs and
+// split into even and odd dimensions.
+//
+// Rounding to fewer bits: softmax weights to BF16 before they multiply V, as the tensor cores take 16-bit
+// operands; sums and statistics are fp32; the output rounds once to BF16.
+#include "attn_common.cuh"
 
 namespace glora {
 
 namespace {
 
-constexpr int kDecodeWarps = 4;
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = kDecWarps * 32;
+constexpr int kStages = 3;
+constexpr int kHalfStage = 4096;                 // bytes of K (and of V) in a stage
+constexpr int kCtasPerSm = 2;
+constexpr int kJoinGroup = 16;                   // partial results joined by one CTA
+constexpr int kMaxCtas = 512;                    // counters in the workspace
+constexpr int kRows = 16;                        // query heads of a segment
 
-template <int FMT, int E>
-__device__ __forceinline__ void load_cached(const unsigned char* row, float s, int lane, float (&f)[E]) {
-  if constexpr (FMT == kKvBf16) {
-    load_bf16<E>(reinterpret_cast<const uint16_t*>(row) + lane * E, f);
-  } else {
-    uint32_t c = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) c |= static_cast<uint32_t>(row[lane * E + e]) << (8 * e);
-    float g[4];
-    codes_to_f32<FMT>(c, g);
-#pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = g[e] * s;
+// Workspace: counters [3][kMaxCtas] (a segment's first join group, by its first CTA; its other groups, by
+// theirs: that CTA may also start the next segment; its groups together), then 2 slots per CTA of m[16],
+// l[16], O[16][D].
+constexpr int kCounterBytes = 3 * kMaxCtas * 4;
+template <int D>
+constexpr int kSlotFloats = 2 * kRows + kRows * D;
+static_assert(kCounterBytes + 2LL * kMaxCtas * kSlotFloats<128> * 4 <= (16 << 20), "workspace");
+
+template <int FMT, int D>
+struct Tile {
+  static constexpr int row_bytes = D * (FMT == kKvBf16 ? 2 : 1);
+  static constexpr int chunks = row_bytes / 16;               // 16-byte chunks of a token's row
+  static constexpr int tokens = kHalfStage / row_bytes;       // 16, 32 or 64
+  static constexpr int per_lane = (tokens + 31) / 32;         // tokens whose page a lane looks up
+  static constexpr int scale_bytes = FMT == kKvBf16 ? 0 : 2 * tokens * 4;
+  static constexpr int stage_bytes = 2 * kHalfStage + scale_bytes;
+  // Shared address of chunk c of token row t: chunks permuted by the row so that the 8 rows of a
+  // matrix load fall into different banks.
+  static __device__ __forceinline__ uint32_t at(int t, int c) {
+    return t * row_bytes + ((c ^ (chunks >= 8 ? (t & 7) : ((t >> 1) & 3))) << 4);
   }
+};
+
+__device__ __forceinline__ void cp_async16_n(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4_n(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait_n() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Codes (b0, b1, b2, b3) -> f16 pairs (b0, b1) and (b2, b3).
+template <int FMT>
+__device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
+  if constexpr (FMT == kKvE4m3) {
+    e4m3x4_to_f16(c, lo, hi);
+  } else {   // 0x6400 | (code + 128) is the f16 number 1152 + code
+    c ^= 0x80808080u;
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    uint32_t l = __byte_perm(c, 0x64646464u, 0x4140), h = __byte_perm(c, 0x64646464u, 0x4342);
+    const __half2 a = __hsub2(*reinterpret_cast<__half2*>(&l), off), b = __hsub2(*reinterpret_cast<__half2*>(&h), off);
+    lo = *reinterpret_cast<const uint32_t*>(&a);
+    hi = *reinterpret_cast<const uint32_t*>(&b);
+  }
+}
+
+// V's codes of tokens t0, t1 and dimensions d0, d1, as bytes (t0 d0, t0 d1, t1 d0, t1 d1) -> BF16 pairs
+// (t0, t1) of d0 and of d1, exact.
+template <int FMT>
+__device__ __forceinline__ void codes_to_bf16(uint32_t c, uint32_t& even, uint32_t& odd) {
+  if constexpr (FMT == kKvE4m3) {
+    // Sign, then the 4 + 3 bits in BF16's lowest exponent and highest mantissa bits: the value times
+    // 2^-120 (E4M3's subnormals are BF16's there), multiplied back up.
+    const __nv_bfloat162 up = __halves2bfloat162(__ushort_as_bfloat16(0x7b80), __ushort_as_bfloat16(0x7b80));
+    uint32_t e = ((c << 4) & 0x07f007f0u) | ((c << 8) & 0x80008000u), o = ((c >> 4) & 0x07f007f0u) | (c & 0x80008000u);
+    const __nv_bfloat162 a = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&e), up), b = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o), up);
+    even = *reinterpret_cast<const uint32_t*>(&a);
+    odd = *reinterpret_cast<const uint32_t*>(&b);
+  } else {
+    // 0x4300 | low 7 bits is 128 + them; minus 128 or, for a set sign bit, 256
+    const uint32_t x = __byte_perm(c, 0x43434343u, 0x4240), y = __byte_perm(c, 0x43434343u, 0x4341);
+    const uint32_t xl = x & 0xff7fff7fu, xs = x & 0xff80ff80u, yl = y & 0xff7fff7fu, ys = y & 0xff80ff80u;
+    const __nv_bfloat162 a = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&xl), *reinterpret_cast<const __nv_bfloat162*>(&xs));
+    const __nv_bfloat162 b = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&yl), *reinterpret_cast<const __nv_bfloat162*>(&ys));
+    even = *reinterpret_cast<const uint32_t*>(&a);
+    odd = *reinterpret_cast<const uint32_t*>(&b);
+  }
+}
+
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// The batch's segments in order: where a walk stands, and how it goes on.
+struct Walk {
+  int b, sub;          // sequence; key-value head * blocks + block of 16 query heads
+  int tiles;           // tiles of sequence b
+  int len;
+};
+
+template <int TOK>
+__device__ __forceinline__ int tiles_of(const DecodeArgs& p, int b, int& len) {
+  const long long most = static_cast<long long>(p.max_pages) * p.c.page_size;
+  len = static_cast<int>(min(static_cast<long long>(max(p.lens[b], 0)), most));
+  return (len - 1) / TOK + (len > 0 ? 1 : 0);
+}
+
+// Next segment that has tiles (the caller knows there is one).
+template <int TOK>
+__device__ __forceinline__ void next_segment(const DecodeArgs& p, int subs, Walk& w) {
+  if (++w.sub < subs) return;
+  w.sub = 0;
+  do ++w.b, w.tiles = tiles_of<TOK>(p, w.b, w.len);
+  while (w.tiles == 0);
 }
 
 }  // namespace
 
-// One CTA per (sequence, query head): its warps take the tokens in turn, each with
-// its own running softmax, and join through shared memory.
-template <int FMT, int D>
-__global__ void __launch_bounds__(kDecodeWarps * 32) decode_row_kernel(const DecodeArgs p) {
-  constexpr int E = D / 32;
+// HALF: at most 8 query heads share a key-value head (the lower 8 rows of a tile are unused).
+template <int FMT, int D, bool HALF>
+__global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const DecodeArgs p) {
+  using T = Tile<FMT, D>;
+  constexpr int TOK = T::tokens, NT = TOK / 8, KS = D / 16, R = HALF ? 1 : 2;
+  constexpr int PL = T::per_lane;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ long long s_sum[kDecWarps];
+  __shared__ int s_b, s_sub, s_tiles, s_len, s_tile0, s_last;
+  __shared__ float s_m[kDecWarps][kRows], s_l[kDecWarps][kRows];
+  __shared__ uint64_t s_live[kDecWarps][kStages];     // valid tokens of each stage
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3;
+  float* const s_o = reinterpret_cast<float*>(smem + kDecWarps * kStages * T::stage_bytes);   // two buffers of D / 8 / R accumulator tiles
+
   pdl_wait_then_release();
-  const int b = blockIdx.x / p.q_heads, h = blockIdx.x - b * p.q_heads;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = h / (p.q_heads / p.c.kv_heads);
-  const long long most = static_cast<long long>(p.max_pages) * p.c.page_size;
-  const int len = static_cast<int>(min(static_cast<long long>(max(p.lens[b], 0)), most));
-  RowState<D> st;
-  st.begin(p.q + b * p.q_stride + h * D, p.scale * kLog2e, lane);
-  for (int t = warp; t < len; t += kDecodeWarps) {
-    const int page = p.table[b * p.table_stride + t / p.c.page_size], slot = t % p.c.page_size;
-    if (page < 0 || page >= p.c.num_pages) continue;
-    const long long at = page * p.c.page_bytes + kvh * p.c.head_bytes + slot * p.c.token_bytes;
-    float ks = 1.f, vs = 1.f;
-    if constexpr (FMT != kKvBf16) {
-      const long long si = scale_index(p.c, page, kvh, slot);
-      ks = p.c.ks[si];
-      vs = p.c.vs[si];
+
+  const int G = p.q_heads / p.c.kv_heads, blocks = (G + kRows - 1) / kRows, subs = p.c.kv_heads * blocks;
+  // Sequences without tokens: zeros.
+  auto zero_empty = [&]() {
+    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+      int len;
+      if (tiles_of<TOK>(p, b, len) > 0) continue;
+      for (int i = tid; i < p.q_heads * D / 8; i += kDecThreads)
+        *reinterpret_cast<uint4*>(p.out + b * p.out_stride + i * 8) = make_uint4(0, 0, 0, 0);
+      if (p.lse)
+        for (int i = tid; i < p.q_heads; i += kDecThreads) p.lse[static_cast<long long>(b) * p.q_heads + i] = -INFINITY;
     }
-    float k[E], v[E];
-    load_cached<FMT, E>(p.c.k + at, ks, lane, k);
-    load_cached<FMT, E>(p.c.v + at, vs, lane, v);
-    st.add(k, v);
+  };
+
+  // The batch's tiles, and this CTA's range [u0, u1) of them.
+  const int per = (p.batch + kDecThreads - 1) / kDecThreads, b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+  long long mine = 0, before, total = 0;
+  for (int b = b0; b < b1; ++b) {
+    int len;
+    mine += tiles_of<TOK>(p, b, len);
   }
-  __shared__ float sm[kDecodeWarps], sl[kDecodeWarps], so[kDecodeWarps][D];
-  if (lane == 0) {
-    sm[warp] = st.m;
-    sl[warp] = st.l;
-  }
+  before = mine;
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = st.acc[e];
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += t;
+  }
+  if (lane == 31) s_sum[warp] = before;
+  before -= mine;
   __syncthreads();
-  float m = -INFINITY, l = 0.f;
-  for (int w = 0; w < kDecodeWarps; ++w) m = fmaxf(m, sm[w]);
-  float f[kDecodeWarps];
-  for (int w = 0; w < kDecodeWarps; ++w) {
-    f[w] = (sm[w] == -INFINITY && sl[w] == 0.f) ? 0.f : exp2_fast(sm[w] - m);
-    l += f[w] * sl[w];
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
   }
-  for (int d = threadIdx.x; d < D; d += kDecodeWarps * 32) {
-    float o = 0.f;
-    for (int w = 0; w < kDecodeWarps; ++w) o += f[w] * so[w][d];
-    p.out[b * p.out_stride + h * D + d] = f32_to_bf16_bits(l == 0.f ? 0.f : o / l);
+  before *= subs;
+  mine *= subs;
+  total *= subs;
+  const long long n = min(static_cast<long long>(gridDim.x), (total + kDecWarps - 1) / kDecWarps);   // CTAs with work
+  const int c = blockIdx.x;
+  if (c >= n) {
+    zero_empty();
+    return;
   }
-  if (p.lse && threadIdx.x == 0) p.lse[static_cast<long long>(b) * p.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  const long long u0 = c * total / n, u1 = (c + 1) * total / n;
+  if (u0 >= before && u0 < before + mine) {   // this thread's sequences hold u0
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      int len;
+      const int t = tiles_of<TOK>(p, b, len);
+      const long long span = static_cast<long long>(t) * subs;
+      if (u0 < at + span) {
+        s_b = b;
+        s_tiles = t;
+        s_len = len;
+        s_sub = static_cast<int>((u0 - at) / t);
+        s_tile0 = static_cast<int>((u0 - at) % t);
+        break;
+      }
+      at += span;
+    }
+  }
+  __syncthreads();
+
+  const uint32_t ring = smem_u32(smem) + warp * kStages * T::stage_bytes;
+  const unsigned char* const ring_ptr = smem + warp * kStages * T::stage_bytes;
+
+  // ---- loads: a cursor over this warp's tiles, one tile ahead of the copies in its page look-up
+  Walk lw{s_b, s_sub, s_tiles, s_len};
+  long long lu = u0;                       // first unit of the cursor's piece
+  int lt0 = s_tile0, lt1 = static_cast<int>(min(static_cast<long long>(lw.tiles), s_tile0 + (u1 - u0)));
+  int lt = lt0 + warp;
+  bool more = true;
+  int page[PL], slot[PL];
+  auto settle = [&]() {                    // to the next tile of this warp, or the end
+    while (lt >= lt1) {
+      lu += lt1 - lt0;
+      if (lu >= u1) {
+        more = false;
+        return;
+      }
+      next_segment<TOK>(p, subs, lw);
+      lt0 = 0;
+      lt1 = static_cast<int>(min(static_cast<long long>(lw.tiles), u1 - lu));
+      lt = warp;
+    }
+  };
+  auto look_up = [&]() {
+    if (!more) return;
+#pragma unroll
+    for (int j = 0; j < PL; ++j) {
+      const int i = lane + 32 * j, t = lt * TOK + i;
+      page[j] = -1;
+      slot[j] = 0;
+      if (i < TOK && t < lw.len) {
+        const int e = t / p.c.page_size;
+        slot[j] = t - e * p.c.page_size;
+        page[j] = __ldg(p.table + lw.b * p.table_stride + e);
+      }
+    }
+  };
+  auto load = [&](int s) {                 // the cursor's tile into stage s, then the cursor moves on
+    if (more) {
+      const uint32_t st = ring + s * T::stage_bytes;
+      const int head = lw.sub / blocks;
+      long long off[PL];
+      uint64_t live = 0;
+#pragma unroll
+      for (int j = 0; j < PL; ++j) {
+        const bool ok = page[j] >= 0 && page[j] < p.c.num_pages;
+        off[j] = ok ? page[j] * p.c.page_bytes + head * p.c.head_bytes + slot[j] * p.c.token_bytes : -1;
+        live |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << (32 * j);
+        if constexpr (FMT != kKvBf16) {
+          const long long si = ok ? scale_index(p.c, page[j], head, slot[j]) : 0;
+          const uint32_t to = st + 2 * kHalfStage + (lane + 32 * j) * 4;
+          cp_async4_n(to, p.c.ks + si, ok ? 4 : 0);
+          cp_async4_n(to + TOK * 4, p.c.vs + si, ok ? 4 : 0);
+        }
+      }
+      if (lane == 0) s_live[warp][s] = live;
+      constexpr int RPI = 32 / T::chunks;  // token rows per copy instruction
+#pragma unroll
+      for (int i = 0; i < TOK / RPI; ++i) {
+        const int t = i * RPI + lane / T::chunks, ch = lane % T::chunks;
+        const long long o = __shfl_sync(0xffffffffu, off[(i * RPI) / 32], t & 31);
+        const uint32_t to = st + T::at(t, ch);
+        const long long from = (o < 0 ? 0 : o) + ch * 16;
+        cp_async16_n(to, p.c.k + from, o < 0 ? 0 : 16);
+        cp_async16_n(to + kHalfStage, p.c.v + from, o < 0 ? 0 : 16);
+      }
+      lt += kDecWarps;
+      settle();
+      look_up();
+    }
+    cp_async_commit();
+  };
+  settle();
+  look_up();
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) load(s);
+
+  // ---- pieces
+  Walk w{s_b, s_sub, s_tiles, s_len};
+  int ta = s_tile0, it = 0;
+  for (long long u = u0; u < u1;) {
+    const int tb = static_cast<int>(min(static_cast<long long>(w.tiles), ta + (u1 - u)));
+    const int head = w.sub / blocks, h0 = head * G + (w.sub - head * blocks) * kRows;
+    const int rows = min(kRows, head * G + G - h0);
+
+    // Q as A fragments; scores come out in units of zscale (base-2 exponents).
+    uint32_t qa[KS][2 * R];
+    float zscale[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int row = g + 8 * r;
+      const uint16_t* q = p.q + w.b * p.q_stride + (h0 + row) * D;
+      zscale[r] = p.scale * kLog2e;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int d = FMT == kKvBf16 ? k * 16 + j * 8 + qd * 2 : k * 16 + qd * 4 + j * 2;
+          qa[k][j * R + r] = row < rows ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
+        }
+      if constexpr (FMT != kKvBf16) {      // BF16 -> f16, the row's largest magnitude at 2^14 .. 2^15
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t v = qa[k][j * R + r];
+            top = max(top, max(v & 0x7fffu, (v >> 16) & 0x7fffu));
+          }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // factor 2^(14 - e) of the exponent e; rows of zeros (or not finite) are taken as they are
+        const int e = static_cast<int>(top >> 7) - 127;
+        const int up = top == 0 || e == 128 ? 0 : max(-126, min(126, 14 - e));
+        const float f = __int_as_float((127 + up) << 23);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t v = qa[k][j * R + r];
+            qa[k][j * R + r] = pack_f16x2(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
+          }
+        zscale[r] *= __int_as_float((127 - up) << 23);
+      }
+    }
+
+    uint32_t nan_codes = 0;
+    float o[D / 8][4], m[R], l[R];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+
+    for (int t = ta + warp; t < tb; t += kDecWarps, ++it) {
+      const int s = it % kStages;
+      cp_async_wait_n<kStages - 2>();
+      __syncwarp();
+      load((it + kStages - 1) % kStages);
+      const uint32_t sk = ring + s * T::stage_bytes, sv = sk + kHalfStage;
+      const float* const sc = reinterpret_cast<const float*>(ring_ptr + s * T::stage_bytes + 2 * kHalfStage);
+      const uint64_t live = s_live[warp][s];
+
+      // scores [16 heads][TOK tokens]
+      float z[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        z[i][0] = z[i][1] = z[i][2] = z[i][3] = 0.f;
+        if constexpr (FMT == kKvBf16) {
+#pragma unroll
+          for (int k = 0; k < KS; k += 2) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4(sk + T::at(i * 8 + (lane & 7), k * 2 + (lane >> 3)), b0, b1, b2, b3);
+            mma_k16(z[i], qa[k][0], HALF ? 0u : qa[k][R - 1], qa[k][R], HALF ? 0u : qa[k][2 * R - 1], b0, b1);
+            mma_k16(z[i], qa[k + 1][0], HALF ? 0u : qa[k + 1][R - 1], qa[k + 1][R], HALF ? 0u : qa[k + 1][2 * R - 1], b2, b3);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < KS; k += 4) {
+            uint32_t c[4];
+            ldsm_x4(sk + T::at(i * 8 + (lane & 7), k + (lane >> 3)), c[0], c[1], c[2], c[3]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t b0, b1;
+              codes_to_f16<FMT>(c[j], b0, b1);
+              mma_f16(z[i], qa[k + j][0], HALF ? 0u : qa[k + j][R - 1], qa[k + j][R], HALF ? 0u : qa[k + j][2 * R - 1], b0, b1);
+            }
+          }
+        }
+      }
+      // to base-2 exponents, masked; running maximum
+      float mt[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) mt[r] = -INFINITY;
+      const bool whole = live == (TOK == 64 ? ~0ull : (1ull << (TOK & 63)) - 1);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        float2 ks = make_float2(1.f, 1.f);
+        if constexpr (FMT != kKvBf16) ks = *reinterpret_cast<const float2*>(sc + i * 8 + qd * 2);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          z[i][2 * r] *= zscale[r] * ks.x;
+          z[i][2 * r + 1] *= zscale[r] * ks.y;
+          if (!whole) {
+            const uint32_t bits = static_cast<uint32_t>(live >> (i * 8 + qd * 2));
+            if (!(bits & 1)) z[i][2 * r] = -INFINITY;
+            if (!(bits & 2)) z[i][2 * r + 1] = -INFINITY;
+          }
+          mt[r] = fmaxf(mt[r], fmaxf(z[i][2 * r], z[i][2 * r + 1]));
+        }
+      }
+      float keep[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float mn = fmaxf(m[r], quad_max(mt[r]));
+        const float ref = mn == -INFINITY ? 0.f : mn;    // nothing seen so far: every weight is 0
+        keep[r] = exp2_fast(m[r] - ref);
+        m[r] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float w0 = exp2_fast(z[i][2 * r + j] - ref);
+            sum += w0;
+            z[i][2 * r + j] = FMT == kKvBf16 ? w0 : w0 * sc[TOK + i * 8 + qd * 2 + j];
+          }
+        l[r] = l[r] * keep[r] + sum;
+      }
+      if (__any_sync(0xffffffffu, keep[0] != 1.f || (!HALF && keep[R - 1] != 1.f))) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 2 * R; ++j) o[i][j] *= keep[j >> 1];
+      }
+      // O += P V
+#pragma unroll
+      for (int k = 0; k < TOK / 16; ++k) {
+        const uint32_t a0 = pack_bf16x2(z[2 * k][0], z[2 * k][1]), a2 = pack_bf16x2(z[2 * k + 1][0], z[2 * k + 1][1]);
+        const uint32_t a1 = HALF ? 0u : pack_bf16x2(z[2 * k][2], z[2 * k][3]);
+        const uint32_t a3 = HALF ? 0u : pack_bf16x2(z[2 * k + 1][2], z[2 * k + 1][3]);
+        if constexpr (FMT == kKvBf16) {
+#pragma unroll
+          for (int i = 0; i < D / 8; i += 2) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4_t(sv + T::at(k * 16 + (lane & 15), i + (lane >> 4)), b0, b1, b2, b3);
+            mma_k16(o[i], a0, a1, a2, a3, b0, b1);
+            mma_k16(o[i + 1], a0, a1, a2, a3, b2, b3);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 16; i += 2) {
+            uint32_t c[4];               // (tokens 0-7, 8-15) of 16-dimension blocks i and i + 1
+            ldsm_x4_t(sv + T::at(k * 16 + (lane & 15), i + (lane >> 4)), c[0], c[1], c[2], c[3]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              // bytes of a register: token 2 qd: dimensions 2g, 2g + 1; token 2 qd + 1: the same
+              uint32_t e0, e1, f0, f1;
+              codes_to_bf16<FMT>(c[2 * j], e0, f0);
+              codes_to_bf16<FMT>(c[2 * j + 1], e1, f1);
+              mma_k16(o[2 * (i + j)], a0, a1, a2, a3, e0, e1);
+              mma_k16(o[2 * (i + j) + 1], a0, a1, a2, a3, f0, f1);
+              if constexpr (FMT == kKvE4m3)   // a NaN code (0x7f, 0xff) carries into its byte's top bit
+                nan_codes |= ((c[2 * j] & 0x7f7f7f7fu) + 0x01010101u) | ((c[2 * j + 1] & 0x7f7f7f7fu) + 0x01010101u);
+            }
+          }
+        }
+      }
+    }
+    // (lora_kv_write makes no NaN codes; a cache that holds them gives NaN, as a scale of NaN does)
+    if (FMT == kKvE4m3 && __any_sync(0xffffffffu, (nan_codes & 0x80808080u) != 0))
+#pragma unroll
+      for (int r = 0; r < R; ++r) l[r] = __int_as_float(0x7fffffff);
+
+    // ---- join the warps: (m, l) of each row, then O in two steps through two buffers
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      l[r] = quad_sum(l[r]);
+      if (qd == 0) {
+        s_m[warp][g + 8 * r] = m[r];
+        s_l[warp][g + 8 * r] = l[r];
+      }
+    }
+    __syncthreads();
+    float mj[R], lj[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mj[r] = -INFINITY;
+      lj[r] = 0.f;
+#pragma unroll
+      for (int x = 0; x < kDecWarps; ++x) mj[r] = fmaxf(mj[r], s_m[x][g + 8 * r]);
+      const float ref = mj[r] == -INFINITY ? 0.f : mj[r];
+#pragma unroll
+      for (int x = 0; x < kDecWarps; ++x) lj[r] += s_l[x][g + 8 * r] * exp2_fast(s_m[x][g + 8 * r] - ref);
+      const float f = exp2_fast(m[r] - ref);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        o[i][2 * r] *= f;
+        o[i][2 * r + 1] *= f;
+      }
+    }
+    // (16 rows go through the buffers in two halves of the dimensions)
+    constexpr int NB = D / 8 / R;
+    auto buffer = [&](int x, int i, int j) -> float& { return s_o[(x * NB * 2 * R + i * 2 * R + j) * 32 + lane]; };
+#pragma unroll
+    for (int h = 0; h < R; ++h) {
+#pragma unroll
+      for (int step = kDecWarps / 2; step > 0; step >>= 1) {
+        if (warp >= step && warp < 2 * step)
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int j = 0; j < 2 * R; ++j) buffer(warp - step, i, j) = o[h * NB + i][j];
+        __syncthreads();
+        if (warp < step)
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int j = 0; j < 2 * R; ++j) o[h * NB + i][j] += buffer(warp, i, j);
+        if (step > 1 || h + 1 < R) __syncthreads();
+      }
+    }
+
+    // ---- the piece's result (warp 0 holds it)
+    // The dimensions of accumulator pair i: BF16 8 i + 2 qd, + 1; 8-bit, blocks of 16 as (even, odd) pairs.
+    auto dim = [&](int i, int j) { return FMT == kKvBf16 ? 8 * i + 2 * qd + j : 16 * (i >> 1) + 4 * qd + 2 * j + (i & 1); };
+    const bool complete = ta == 0 && tb == w.tiles;
+    if (complete) {
+      if (warp == 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int row = g + 8 * r;
+          if (row >= rows) continue;
+          const float f = lj[r] == 0.f ? 0.f : 1.f / lj[r];
+          uint16_t* const to = p.out + w.b * p.out_stride + (h0 + row) * D;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            if constexpr (FMT == kKvBf16) {
+              *reinterpret_cast<uint32_t*>(to + 8 * i + 2 * qd) = pack_bf16x2(o[i][2 * r] * f, o[i][2 * r + 1] * f);
+            } else if ((i & 1) == 0) {
+              *reinterpret_cast<uint2*>(to + 8 * i + 4 * qd) =
+                  make_uint2(pack_bf16x2(o[i][2 * r] * f, o[i + 1][2 * r] * f), pack_bf16x2(o[i][2 * r + 1] * f, o[i + 1][2 * r + 1] * f));
+            }
+          }
+          if (p.lse && qd == 0)
+            p.lse[static_cast<long long>(w.b) * p.q_heads + h0 + row] = lj[r] == 0.f ? -INFINITY : (mj[r] + log2f(lj[r])) * kLn2;
+        }
+      }
+    } else {
+      int* const counters = static_cast<int*>(p.workspace);
+      float* const slots = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kCounterBytes);
+      constexpr int SF = kSlotFloats<D>;
+      if (warp == 0) {
+        float* const to = slots + static_cast<long long>(2 * c + (ta == 0)) * SF;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int row = g + 8 * r;
+          if (row >= rows) continue;
+          if (qd == 0) {
+            to[row] = mj[r];
+            to[kRows + row] = lj[r];
+          }
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            if constexpr (FMT == kKvBf16) {
+              *reinterpret_cast<float2*>(to + 2 * kRows + row * D + dim(i, 0)) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
+            } else if ((i & 1) == 0) {
+              *reinterpret_cast<float4*>(to + 2 * kRows + row * D + dim(i, 0)) =
+                  make_float4(o[i][2 * r], o[i + 1][2 * r], o[i][2 * r + 1], o[i + 1][2 * r + 1]);
+            }
+          }
+        }
+      }
+      // The segment's CTAs c0 .. c1, in groups of kJoinGroup; slot of CTA x: its part either starts
+      // the segment (x == c0: slot 2 x + 1) or goes on with it (slot 2 x).
+      const long long s0 = u - ta, s1 = s0 + w.tiles - 1;
+      const int c0 = static_cast<int>(((s0 + 1) * n - 1) / total), c1 = static_cast<int>(((s1 + 1) * n - 1) / total);
+      const int groups = (c1 - c0) / kJoinGroup + 1, gi = (c - c0) / kJoinGroup;
+      // Joins slots first, first + step, ..; the result goes to the output, or in place into slot `first`.
+      auto join = [&](int first_cta, int count, int step, bool last) {
+        auto slot_of = [&](int x) { return slots + static_cast<long long>(2 * x + (x == c0)) * SF; };
+        // thread: 4 consecutive dimensions of one row at a time
+        for (int i = tid; i < rows * D / 4; i += kDecThreads) {
+          const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
+          float mm = -INFINITY;
+          for (int x = 0; x < count; ++x) mm = fmaxf(mm, __ldcg(slot_of(first_cta + x * step) + row));
+          const float ref = mm == -INFINITY ? 0.f : mm;
+          float ll = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int x = 0; x < count; ++x) {
+            const float* const from = slot_of(first_cta + x * step);
+            const float f = exp2_fast(__ldcg(from + row) - ref);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(from + 2 * kRows + row * D + d));
+            ll += __ldcg(from + kRows + row) * f;
+            acc.x += v.x * f;
+            acc.y += v.y * f;
+            acc.z += v.z * f;
+            acc.w += v.w * f;
+          }
+          if (last) {
+            const float f = ll == 0.f ? 0.f : 1.f / ll;
+            *reinterpret_cast<uint2*>(p.out + w.b * p.out_stride + (h0 + row) * D + d) =
+                make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+            if (p.lse && d == 0)
+              p.lse[static_cast<long long>(w.b) * p.q_heads + h0 + row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+          } else {
+            float* const to = slot_of(first_cta);
+            *reinterpret_cast<float4*>(to + 2 * kRows + row * D + d) = acc;
+            // (m and l of the row are read by its other threads: written after the barrier below)
+            if (d == 0) {
+              s_m[0][row] = mm;
+              s_l[0][row] = ll;
+            }
+          }
+        }
+        if (!last) {
+          __syncthreads();
+          if (tid < rows) {
+            slot_of(first_cta)[tid] = s_m[0][tid];
+            slot_of(first_cta)[kRows + tid] = s_l[0][tid];
+          }
+        }
+      };
+      // Arrive at a counter; true in the CTA that is the last of `count`, which sets it back to 0.
+      auto last_of = [&](int* counter, int count) {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+          s_last = atomicAdd(counter, 1) == count - 1;
+          if (s_last) *counter = 0;
+        }
+        __syncthreads();
+        const bool yes = s_last != 0;
+        if (yes) __threadfence();
+        return yes;
+      };
+      const int first = c0 + gi * kJoinGroup, count = min(kJoinGroup, c1 - first + 1);
+      if (last_of(counters + (gi ? kMaxCtas : 0) + first, count)) {
+        join(first, count, 1, groups == 1);
+        if (groups > 1 && last_of(counters + 2 * kMaxCtas + c0, groups)) join(c0, groups, kJoinGroup, true);
+      }
+    }
+    u += tb - ta;
+    if (u < u1) next_segment<TOK>(p, subs, w);
+    ta = 0;
+    __syncthreads();
+  }
+  cp_async_wait_n<0>();
+  zero_empty();
 }
 
 namespace {
 
-template <int FMT>
-int launch_format(const DecodeArgs& a, void* stream) {
+template <int FMT, int D, bool HALF>
+int launch_one(const DecodeArgs& a, void* stream) {
+  using T = Tile<FMT, D>;
+  constexpr int smem = kDecWarps * kStages * T::stage_bytes + (kDecWarps / 2) * (D / 8) * 2 * 32 * 4;
+  const auto kernel = decode_kernel<FMT, D, HALF>;
+  // (set on every call: the attribute belongs to the current device, like the launch)
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  int dev = 0, sms = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return static_cast<int>(e);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * a.q_heads, 1, 1);
-  cfg.blockDim = dim3(kDecodeWarps * 32, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(sms * kCtasPerSm < kMaxCtas ? sms * kCtasPerSm : kMaxCtas), 1, 1);
+  cfg.blockDim = dim3(kDecThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return static_cast<int>(a.head_dim == 128 ? cudaLaunchKernelEx(&cfg, decode_row_kernel<FMT, 128>, a)
-                                            : cudaLaunchKernelEx(&cfg, decode_row_kernel<FMT, 64>, a));
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, a));
+}
+
+template <int FMT>
+int launch_format(const DecodeArgs& a, void* stream) {
+  const bool half = a.q_heads / a.c.kv_heads <= 8;
+  if (a.head_dim == 128) return half ? launch_one<FMT, 128, true>(a, stream) : launch_one<FMT, 128, false>(a, stream);
+  return half ? launch_one<FMT, 64, true>(a, stream) : launch_one<FMT, 64, false>(a, stream);
 }
 
 }  // namespace
