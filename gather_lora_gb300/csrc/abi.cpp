@@ -52,6 +52,35 @@ int device_sm_count_or(int fallback) {
   return v;
 }
 
+namespace {
+
+// cuTensorMapEncodeTiled from the driver, looked up once (NULL without a driver).
+PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+}  // namespace
+
+int encode_bf16_map(TensorMapBytes* out, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box, CUtensorMapSwizzle swz, const char* what) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_tiled();
+  if (!enc) return fail(LORA_ERR_CUDA, "cuTensorMapEncodeTiled is not available (no CUDA driver)");
+  static_assert(sizeof(TensorMapBytes) == sizeof(CUtensorMap), "tensor map size");
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(reinterpret_cast<CUtensorMap*>(out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr),
+                         dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? LORA_OK : fail(LORA_ERR_CUDA, "cuTensorMapEncodeTiled failed for %s (%d)", what, static_cast<int>(r));
+}
+
 }  // namespace glora
 
 namespace {
@@ -328,19 +357,6 @@ bool moe_geometry(int window, int adapters, int num_experts, int max_rank, int k
   return moe_geometry_cfg(0, window, adapters, num_experts, max_rank, k_in, n_out, sms, g);
 }
 
-// cuTensorMapEncodeTiled from the driver, looked up once (NULL without a driver).
-PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
-}
-
 // Launch geometry for a fold call, with A as tensor-map boxes when maps are given
 // and max_rank >= LORA_TMAP_MIN_RANK (falls back to padded A rows otherwise, or
 // when the tiled layout does not fit). Measured on GB300: at rank 16 the boxes
@@ -409,17 +425,9 @@ int device_sm_count() { return device_sm_count_or(0); }
 // One 2-D BF16 tensor map: `inner` x `outer` elements, rows `row_bytes` apart.
 int encode_map(glora::TensorMapBytes* out, const void* ptr, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz, const char* what) {
-  const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_tiled();
-  if (!enc) return fail(LORA_ERR_CUDA, "cuTensorMapEncodeTiled is not available (no CUDA driver)");
-  static_assert(sizeof(glora::TensorMapBytes) == sizeof(CUtensorMap), "tensor map size");
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = enc(reinterpret_cast<CUtensorMap*>(out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr),
-                         dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? LORA_OK : fail(LORA_ERR_CUDA, "cuTensorMapEncodeTiled failed for %s (%d)", what, static_cast<int>(r));
+  const uint64_t dims[2] = {inner, outer};
+  const uint32_t box[2] = {box_inner, box_outer};
+  return glora::encode_bf16_map(out, ptr, 2, dims, &row_bytes, box, swz, what);
 }
 
 }  // namespace
@@ -678,10 +686,11 @@ int lora_selftest_wait_timeout(int64_t limit_cycles, void* stream) {
 
 int lora_read_device_status(void* stream, uint32_t* status_out, int clear) {
   if (!status_out) return fail(LORA_ERR_NULL, "status_out is NULL");
-  uint32_t a = 0, b = 0;
+  uint32_t a = 0, b = 0, c = 0;
   int rc = glora::read_device_status(stream, &a, clear);
   if (!rc) rc = glora::read_dense_status(stream, &b, clear);
-  *status_out = a | b;
+  if (!rc) rc = glora::read_prefill_status(stream, &c, clear);
+  *status_out = a | b | c;
   return rc ? cuda_fail(rc, "lora_read_device_status") : ok();
 }
 
@@ -738,7 +747,7 @@ int lora_encode_a_tmaps(const uint64_t* a_ptrs, int32_t count, int32_t max_rank,
   if (count == 0) return ok();
   if (!a_ptrs || !maps_out) return fail(LORA_ERR_NULL, "a_ptrs and maps_out are required");
   if (reinterpret_cast<uintptr_t>(maps_out) & 63u) return fail(LORA_ERR_ALIGN, "maps_out must be 64-byte aligned");
-  const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_tiled();
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = glora::encode_tiled();
   if (!enc) return fail(LORA_ERR_CUDA, "cuTensorMapEncodeTiled is not available (no CUDA driver)");
   const int mr16 = (max_rank + 15) / 16 * 16;
   auto* maps = static_cast<CUtensorMap*>(maps_out);

@@ -205,7 +205,23 @@ int lora_attn_prefill(const lora_bf16_t* q, int64_t q_row_stride, const lora_bf1
   a.head_dim = head_dim;
   a.scale = scale;
   a.lse = lse;
-  const int rc = glora::launch_prefill(a, stream);
+  // Heads of a group in equal blocks of at most 128 (one block up to 128), as many whole tokens as fit 128 rows.
+  const int group = q_heads / kv_heads, blocks = (group + 127) / 128;
+  a.head_block = (group + blocks - 1) / blocks;
+  a.tile_tokens = 128 / a.head_block;
+  const uint64_t qd[3] = {static_cast<uint64_t>(head_dim), static_cast<uint64_t>(q_heads), static_cast<uint64_t>(total_q)};
+  const uint64_t qs[2] = {static_cast<uint64_t>(head_dim) * 2, static_cast<uint64_t>(q_row_stride) * 2};
+  const uint32_t qb[3] = {64, static_cast<uint32_t>(a.head_block), static_cast<uint32_t>(a.tile_tokens)};
+  // (without any key nothing is loaded through the K and V maps: they describe one row of q then)
+  const uint64_t kd[2] = {static_cast<uint64_t>(total_k ? k_width : head_dim), static_cast<uint64_t>(total_k ? total_k : 1)};
+  const uint64_t ks = static_cast<uint64_t>(k_row_stride) * 2, vs = static_cast<uint64_t>(v_row_stride) * 2;
+  const uint32_t kb[2] = {64, 128};
+  int rc;
+  if ((rc = glora::encode_bf16_map(&a.map_q, q, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B, "q")) ||
+      (rc = glora::encode_bf16_map(&a.map_k, total_k ? k : q, 2, kd, &ks, kb, CU_TENSOR_MAP_SWIZZLE_128B, "k")) ||
+      (rc = glora::encode_bf16_map(&a.map_v, total_k ? v : q, 2, kd, &vs, kb, CU_TENSOR_MAP_SWIZZLE_128B, "v")))
+    return rc;
+  rc = glora::launch_prefill(a, stream);
   return rc ? cuda_fail(rc, "lora_attn_prefill launch") : ok();
 }
 

@@ -1,65 +1,520 @@
 // Causal attention over packed sequences of different lengths (sm_103a).
+//
+//   z_ij = scale (q_i . k_j) for j <= i + Lk - Lq,   out_i = sum_j softmax(z_i)_j v_j
+//
+// Both products run on the fifth-generation tensor cores (tcgen05, M = 128, fp32 accumulators in tensor
+// memory), with a running softmax between them: per 128 x 128 block of pairs 4 * 128^2 * D flops of MMA
+// (512 clocks of the SM's tensor pipe at D = 128), 128^2 exponentials and as many multiply-adds, sums and
+// maxima, so past a few hundred keys the kernel is bound by the tensor pipe and the exponentials together.
+//
+// Rows of a tile. The G query heads that share a key-value head read the same keys, so a 128-row tile
+// holds TT = 128 / G tokens x G heads (row = token * G + head; one 3-D TMA box): short prompts and
+// single-token chunks fill tiles G times as well, and one stream of K and V serves all heads of the group.
+// A work item is two such row tiles of one sequence, key-value head and (G > 128) block of heads.
+//
+// CTA: one per SM, persistent over the items. Two warpgroups each own one row tile: thread = row, with its
+// running reference and sum in registers. They alternate on the tensor pipe: while one does its softmax,
+// the other's P V and the next Q K^T run. Warp 8 issues the MMAs, warp 9 picks the items and issues TMA: K and
+// V tiles of 128 keys through one ring of stages, the next item's Q as soon as the last Q K^T has read the old
+// (warps 10 and 11 only complete the warpgroup that gives its registers to the softmax).
+// Tensor memory: S0, S1 (128 columns each; P as BF16 pairs over the first half of its S), O0, O1.
+//
+// Softmax: exponents are base 2. The reference that exponents are relative to follows the running maximum
+// only when that has grown by more than 2^8 (one vote per warp): then l and O are multiplied by
+// 2^(old - new); otherwise weights up to 2^8 are kept as they are, which BF16 and fp32 hold alike.
+//
+// Rounding to fewer bits: the weights to BF16 before P V (the tensor cores' operand type), the output once.
+// Keys that a row does not see get weight zero, but zero times NaN or infinity in their V rows is NaN in
+// an MMA: a row whose result is not finite is computed again key by key over its own keys (attn_row.cuh).
 #include "attn_row.cuh"
+#include "tc05.cuh"
 
 namespace glora {
 
+__device__ unsigned int g_prefill_status = 0;
+
 namespace {
 
-constexpr int kRowWarps = 4;
+constexpr unsigned kPrefillTimeoutBit = 0x2u;   // LORA_DEV_TIMEOUT
+constexpr int kTile = 128;                      // rows of a tile, keys of a tile
+constexpr int kSoftmaxWarps = 8;
+constexpr int kPreMmaWarp = 8, kPreTmaWarp = 9;
+constexpr int kPreThreads = 384;
+// Registers a thread: 168 at launch (65536 over 12 warps); the helper warpgroup gives 80 away, the softmax
+// warpgroups hold a whole row of scores: 2 * 208 + 88 = 3 * 168.
+constexpr int kHelperRegs = 88, kSoftmaxRegs = 208;
+constexpr int kItems = 4;                       // depth of the item ring
+constexpr uint32_t kColO = 256;                 // tensor memory: S at 0 and 128, O at 256 and 384
+constexpr float kRescale = 8.f;                 // reference moves when the maximum grew by 2^8
 
-// The sequence that holds query row r (cu_q non-decreasing), or -1.
-__device__ __forceinline__ int sequence_of(const PrefillArgs& p, int r) {
-  int lo = 0, hi = p.batch;   // the last b with cu_q[b] <= r
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (p.cu_q[mid + 1] <= r) lo = mid + 1; else hi = mid;
+template <int D>
+struct PrefillShape {
+  static constexpr int atoms = D / 64;                          // 64-column boxes of a tile
+  static constexpr int tile_bytes = kTile * D * 2;              // Q row tile, K tile or V tile
+  static constexpr int stages = D == 128 ? 5 : 8;
+  static constexpr int smem = (2 + stages) * tile_bytes + 2048; // + control, alignment
+};
+
+struct PrefillItem {
+  int valid;
+  int q0, k0;          // first query row of the item, first key row of its sequence
+  int tok0, lq, lk;    // first token of the item in the sequence; the sequence's rows and keys
+  int n[2];            // key tiles of each row tile
+  int h0, heads, kvh;  // first query head, how many, key-value head
+};
+
+struct PrefillCtl {
+  unsigned long long full[8], empty[8];
+  unsigned long long q_full, q_empty;
+  unsigned long long s_full[2], p_ready[2], o_full[2];
+  unsigned long long item_full[kItems], item_empty[kItems];
+  unsigned long long drain;
+  PrefillItem item[kItems];
+  uint32_t tmem;
+  int failed;
+};
+static_assert(sizeof(PrefillCtl) <= 1024, "control block");
+
+// Bounded wait; once one wait of the CTA has run out, all others end at once.
+__device__ __forceinline__ bool pre_wait(PrefillCtl& c, unsigned long long& bar, uint32_t parity) {
+  const uint32_t b = smem_u32(&bar);
+  if (mbar_try_wait(b, parity, 100000)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(b, parity, 100000)) {
+    if (*reinterpret_cast<volatile int*>(&c.failed)) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      *reinterpret_cast<volatile int*>(&c.failed) = 1;
+      atomicOr(&g_prefill_status, kPrefillTimeoutBit);
+      return false;
+    }
   }
-  return lo < p.batch && p.cu_q[lo] <= r && r < p.cu_q[lo + 1] ? lo : -1;
+  return true;
+}
+
+// The same for a whole warp, which goes on or gives up together.
+__device__ __forceinline__ bool warp_wait(PrefillCtl& c, unsigned long long& bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, pre_wait(c, bar, parity));
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n"
+               ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+               : "memory");
 }
 
 }  // namespace
 
-// One warp per (query row, query head).
 template <int D>
-__global__ void __launch_bounds__(kRowWarps * 32) prefill_row_kernel(const PrefillArgs p) {
-  constexpr int E = D / 32;
-  pdl_wait_then_release();
-  const long long unit = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int r = static_cast<int>(unit / p.q_heads), h = static_cast<int>(unit - static_cast<long long>(r) * p.q_heads);
-  if (r >= p.total_q) return;
-  const int b = sequence_of(p, r);
-  if (b < 0) return;
-  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
-  if (q0 < 0 || q1 > p.total_q || k0 < 0 || k1 < k0 || k1 > p.total_k) return;
-  const int seen = min(k1 - k0, (r - q0) + (k1 - k0) - (q1 - q0) + 1);
-  const int kvh = h / (p.q_heads / p.kv_heads);
-  RowState<D> st;
-  st.begin(p.q + r * p.q_stride + h * D, p.scale * kLog2e, lane);
-  for (int j = 0; j < seen; ++j) {
-    float k[E], v[E];
-    load_bf16<E>(p.k + (k0 + j) * p.k_stride + kvh * D + lane * E, k);
-    load_bf16<E>(p.v + (k0 + j) * p.v_stride + kvh * D + lane * E, v);
-    st.add(k, v);
+__global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs p) {
+  using Sh = PrefillShape<D>;
+  constexpr int NS = Sh::stages;
+  extern __shared__ unsigned char prefill_smem_raw[];
+  const uint32_t raw = smem_u32(prefill_smem_raw), pad = ((raw + 1023u) & ~1023u) - raw;
+  const uint32_t q_s = raw + pad, ring = q_s + 2 * Sh::tile_bytes;
+  PrefillCtl& c = *reinterpret_cast<PrefillCtl*>(prefill_smem_raw + pad + (2 + NS) * Sh::tile_bytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(smem_u32(&c.full[s]), 1);
+      mbar_init(smem_u32(&c.empty[s]), 1);
+    }
+    mbar_init(smem_u32(&c.q_full), 1);
+    mbar_init(smem_u32(&c.q_empty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&c.s_full[i]), 1);
+      mbar_init(smem_u32(&c.p_ready[i]), 4);
+      mbar_init(smem_u32(&c.o_full[i]), 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(smem_u32(&c.item_full[i]), 1);
+      mbar_init(smem_u32(&c.item_empty[i]), kSoftmaxWarps + 1);
+    }
+    mbar_init(smem_u32(&c.drain), 1);
+    c.failed = 0;
+    mbar_fence_init();
   }
-  const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
+  if (warp == kPreMmaWarp) {
+    tmem_alloc(smem_u32(&c.tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c.tmem;
+
+  pdl_wait_then_release();
+
+  const int TT = p.tile_tokens, step = 2 * TT, GB = p.head_block;
+  const int G = p.q_heads / p.kv_heads, blocks = (G + GB - 1) / GB, subs = p.kv_heads * blocks;
+
+  if (warp >= kSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kHelperRegs));
+  if (warp == kPreTmaWarp) {
+    // ======================= items and TMA loads ==========================
+    int b0 = 0, it = 0, items = 0;      // chunk of 32 sequences under search; items, those with keys
+    uint32_t kv = 0;                    // ring tiles issued
+    long long base = 0;                 // row-tile pairs before sequence b0
+    bool go = true;
+    for (long long idx = blockIdx.x; go; idx += gridDim.x, ++it) {
+      // Item idx: sequences in order, within one its last rows (the most keys) first, heads fastest.
+      const long long x = idx / subs;
+      const int sub = static_cast<int>(idx - x * subs);
+      int q0 = 0, lq = 0, k0 = 0, lk = 0, tile = -1;
+      while (b0 < p.batch) {
+        const int b = b0 + lane;
+        int a0 = 0, a1 = 0, e0 = 0, e1 = 0;
+        if (b < p.batch) {
+          a0 = __ldg(p.cu_q + b);
+          a1 = __ldg(p.cu_q + b + 1);
+          e0 = __ldg(p.cu_k + b);
+          e1 = __ldg(p.cu_k + b + 1);
+        }
+        const bool good = a0 >= 0 && a1 > a0 && a1 <= p.total_q && e0 >= 0 && e1 >= e0 && e1 <= p.total_k;
+        const int mine = good ? (a1 - a0 - 1) / step + 1 : 0;
+        int incl = mine;
 #pragma unroll
-  for (int e = 0; e < E; ++e) p.out[r * p.out_stride + h * D + lane * E + e] = f32_to_bf16_bits(st.l == 0.f ? 0.f : st.acc[e] * inv);
-  if (p.lse && lane == 0) p.lse[static_cast<long long>(r) * p.q_heads + h] = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += t;
+        }
+        const long long lo = base + incl - mine;
+        const uint32_t hit = __ballot_sync(0xffffffffu, x >= lo && x < lo + mine);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          q0 = __shfl_sync(0xffffffffu, a0, src);
+          lq = __shfl_sync(0xffffffffu, a1 - a0, src);
+          k0 = __shfl_sync(0xffffffffu, e0, src);
+          lk = __shfl_sync(0xffffffffu, e1 - e0, src);
+          tile = __shfl_sync(0xffffffffu, mine - 1 - static_cast<int>(x - lo), src);
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+        b0 += 32;
+      }
+      go = tile >= 0;
+      if (lane == 0) {
+        const int sl = it % kItems;
+        if (it >= kItems) go = pre_wait(c, c.item_empty[sl], ((it / kItems) - 1) & 1) && go;
+        PrefillItem w;
+        w.valid = go;
+        w.tok0 = tile * step;
+        w.q0 = q0 + w.tok0;
+        w.k0 = k0;
+        w.lq = lq;
+        w.lk = lk;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int first = w.tok0 + i * TT, last = min(first + TT, lq);       // the row tile's tokens
+          const int keys = min(lk, last + lk - lq);
+          w.n[i] = first < lq && keys > 0 ? (keys - 1) / kTile + 1 : 0;
+        }
+        w.kvh = sub / blocks;
+        w.h0 = w.kvh * G + (sub - w.kvh * blocks) * GB;
+        w.heads = min(GB, w.kvh * G + G - w.h0);
+        c.item[sl] = w;
+        mbar_arrive(smem_u32(&c.item_full[sl]));
+        const int n = max(w.n[0], w.n[1]);
+        if (go && n > 0) {
+          if (items > 0) go = pre_wait(c, c.q_empty, (items - 1) & 1);
+          ++items;
+          if (go) {
+            const uint32_t fb = smem_u32(&c.q_full);
+            mbar_arrive_expect_tx(fb, 2 * Sh::atoms * GB * TT * 128);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int a = 0; a < Sh::atoms; ++a)
+                tma_load_3d(q_s + i * Sh::tile_bytes + a * (kTile * 128), &p.map_q, a * 64, w.h0, w.q0 + i * TT, fb);
+          }
+          for (int j = 0; go && j < 2 * n; ++j) {      // K0 V0 K1 V1 ..
+            const uint32_t s = kv % NS;
+            if (kv >= NS && !pre_wait(c, c.empty[s], ((kv / NS) - 1) & 1)) {
+              go = false;
+              break;
+            }
+            ++kv;
+            const uint32_t fb = smem_u32(&c.full[s]), to = ring + s * Sh::tile_bytes;
+            mbar_arrive_expect_tx(fb, Sh::tile_bytes);
+#pragma unroll
+            for (int a = 0; a < Sh::atoms; ++a)
+              tma_load_2d(to + a * (kTile * 128), (j & 1) ? &p.map_v : &p.map_k, w.kvh * D + a * 64, k0 + (j >> 1) * kTile, fb);
+          }
+        }
+      }
+      go = __shfl_sync(0xffffffffu, go, 0);
+    }
+    if (lane == 0 && *reinterpret_cast<volatile int*>(&c.failed)) {   // let the loads in flight land
+      for (uint32_t k = kv > NS ? kv - NS : 0; k < kv; ++k)
+        mbar_wait_limit(smem_u32(&c.full[k % NS]), (k / NS) & 1, kDrainLimitCycles);
+      if (items > 0) mbar_wait_limit(smem_u32(&c.q_full), (items - 1) & 1, kDrainLimitCycles);
+    }
+    __syncwarp();
+  } else if (warp == kPreMmaWarp) {
+    // ============================ MMA issue ===============================
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile);
+      constexpr uint32_t id_o = idesc_bf16_f32(kTile, D) | (1u << 16);   // V: MN-major
+      uint32_t kv = 0, pc = 0;           // pc: bit i, the phase of p_ready[i] to wait for
+      int items = 0;
+      auto scores = [&](int i, uint32_t s) {           // S_i = Q_i K^T, K in stage s
+        const uint64_t qa = smem_desc(q_s + i * Sh::tile_bytes, 1024, Swz::k128);
+        const uint64_t ka = smem_desc(ring + s * Sh::tile_bytes, 1024, Swz::k128);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {          // (descriptors hold addresses in 16-byte units)
+          const uint64_t o = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+          umma_bf16(tmem + i * kTile, qa + o, ka + o, id_s, kk != 0);
+        }
+        umma_commit(smem_u32(&c.s_full[i]));
+      };
+      auto values = [&](int i, uint32_t s, bool add) {   // O_i (+)= P_i V, V in stage s
+        const uint64_t va = smem_desc_mn128(ring + s * Sh::tile_bytes, kTile * 128, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma_bf16_ts(tmem + kColO + i * kTile, tmem + i * kTile + kk * 8, va + kk * (2048 >> 4), id_o, kk != 0 || add);
+      };
+      bool go = true;
+      for (int it = 0; go; ++it) {
+        const int sl = it % kItems;
+        if (!pre_wait(c, c.item_full[sl], (it / kItems) & 1)) break;
+        const bool valid = c.item[sl].valid;
+        const int n0 = c.item[sl].n[0], n1 = c.item[sl].n[1], n = max(n0, n1);
+        mbar_arrive(smem_u32(&c.item_empty[sl]));
+        if (!valid) break;
+        if (n == 0) continue;
+        go = pre_wait(c, c.q_full, items & 1) && pre_wait(c, c.full[kv % NS], (kv / NS) & 1);
+        ++items;
+        if (!go) break;
+        tc_fence_after();
+        if (n0 > 0) scores(0, kv % NS);
+        if (n1 > 0) scores(1, kv % NS);
+        umma_commit(smem_u32(&c.empty[kv % NS]));
+        ++kv;
+        if (n == 1) umma_commit(smem_u32(&c.q_empty));
+        for (int j = 0; go && j < n; ++j) {
+          const uint32_t vs = kv % NS, ks = (kv + 1) % NS;
+          go = pre_wait(c, c.full[vs], (kv / NS) & 1) && (j + 1 == n || pre_wait(c, c.full[ks], ((kv + 1) / NS) & 1));
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) {
+            const int ni = i ? n1 : n0;
+            if (go && j < ni) {
+              go = pre_wait(c, c.p_ready[i], (pc >> i) & 1);
+              pc ^= 1u << i;
+              if (!go) break;
+              tc_fence_after();
+              values(i, vs, j != 0);
+              if (j + 1 == ni) umma_commit(smem_u32(&c.o_full[i]));
+            }
+            if (go && j + 1 < ni) scores(i, ks);
+          }
+          if (!go) break;
+          umma_commit(smem_u32(&c.empty[vs]));
+          if (j + 1 < n) umma_commit(smem_u32(&c.empty[ks]));
+          if (j + 2 == n) umma_commit(smem_u32(&c.q_empty));   // the item's last scores are issued
+          kv += j + 1 < n ? 2 : 1;
+        }
+      }
+      if (*reinterpret_cast<volatile int*>(&c.failed)) {   // let the MMAs in flight end
+        umma_commit(smem_u32(&c.drain));
+        mbar_wait_limit(smem_u32(&c.drain), 0, kDrainLimitCycles);
+      }
+    }
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+    // ============================= softmax ================================
+    const int i = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t col_s = lane_base + i * kTile, col_o = lane_base + kColO + i * kTile;
+    const float sl2 = p.scale * kLog2e, grow = kRescale / sl2;
+    const int t_in = row / GB, g = row - t_in * GB;
+    uint32_t sc = 0, oc = 0;
+    for (int it = 0;; ++it) {
+      const int sl = it % kItems;
+      if (!warp_wait(c, c.item_full[sl], (it / kItems) & 1)) break;
+      const PrefillItem w = c.item[sl];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c.item_empty[sl]));
+      if (!w.valid) break;
+      const int tok = w.tok0 + i * TT + t_in, n = w.n[i];
+      const bool live = t_in < TT && g < w.heads && tok < w.lq;
+      const int lim = live ? max(0, min(w.lk, tok + 1 + w.lk - w.lq)) : 0x7fffffff;   // keys the row sees
+      float ref = -INFINITY, l = 0.f;      // exponents are relative to ref (in units of raw scores)
+      bool go = true;
+      for (int j = 0; j < n; ++j) {
+        go = warp_wait(c, c.s_full[i], sc & 1);
+        ++sc;
+        if (!go) break;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(col_s + q * 32, s[q]);
+        tmem_ld_wait();
+        const int seen = lim - j * kTile;
+        if (__any_sync(0xffffffffu, seen < kTile)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (q * 32 + e >= seen) s[q][e] = 0xff800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mx[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][e]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (j == 0) {
+          ref = top;
+        } else if (__any_sync(0xffffffffu, top > ref + grow)) {
+          const float nr = fmaxf(ref, top);
+          const float f = nr == -INFINITY ? 1.f : exp2_fast((ref - nr) * sl2);
+          ref = nr;
+          l *= f;
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32(col_o + q * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(col_o + q * 32, o);
+          }
+        }
+        const float off = ref == -INFINITY ? 0.f : -ref * sl2;   // (nothing seen: every weight is 0)
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int q = 2 * h + (e >> 4), f = (e & 15) * 2;
+            const float w0 = exp2_fast(__fmaf_rn(__uint_as_float(s[q][f]), sl2, off));
+            const float w1 = exp2_fast(__fmaf_rn(__uint_as_float(s[q][f + 1]), sl2, off));
+            sum[2 * h] += w0;
+            sum[2 * h + 1] += w1;
+            pk[e] = pack_bf16x2(w0, w1);
+          }
+          tmem_st32(col_s + h * 32, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.p_ready[i]));
+      }
+      if (!go) break;
+      // The row's result.
+      uint16_t* const to = p.out + static_cast<long long>(w.q0 + i * TT + t_in) * p.out_stride + (w.h0 + g) * D;
+      bool bad = false;
+      if (n > 0) {
+        if (!warp_wait(c, c.o_full[i], oc & 1)) break;
+        ++oc;
+        tc_fence_after();
+        const float inv = 1.f / l;
+        float check = 0.f;
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          tmem_ld32(col_o + q * 32, o);
+          tmem_ld_wait();
+          if (!live) continue;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            float f[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              f[x] = l == 0.f ? 0.f : __uint_as_float(o[e + x]) * inv;
+              check = __fmaf_rn(f[x], 0.f, check);       // stays 0 while all are finite
+            }
+            *reinterpret_cast<uint4*>(to + q * 32 + e) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                                    pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+          }
+        }
+        tc_fence_before();
+        bad = live && !(check == 0.f);
+      } else if (live) {
+#pragma unroll
+        for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(to + e) = make_uint4(0, 0, 0, 0);
+      }
+      const long long out_row = w.q0 + i * TT + t_in;
+      if (p.lse && live) p.lse[out_row * p.q_heads + w.h0 + g] = l == 0.f ? -INFINITY : (ref * sl2 + log2f(l)) * kLn2;
+      // Rows that are not finite: once more, over their own keys alone.
+      for (uint32_t left = __ballot_sync(0xffffffffu, bad); left; left &= left - 1) {
+        const int src = __ffs(left) - 1;
+        const int r = w.q0 + i * TT + __shfl_sync(0xffffffffu, t_in, src), h = w.h0 + __shfl_sync(0xffffffffu, g, src);
+        const int keys = __shfl_sync(0xffffffffu, lim, src);
+        RowState<D> st;
+        st.begin(p.q + r * p.q_stride + h * D, sl2, lane);
+        for (int j = 0; j < keys; ++j) {
+          constexpr int E = D / 32;
+          float k[E], v[E];
+          load_bf16<E>(p.k + (w.k0 + j) * p.k_stride + w.kvh * D + lane * E, k);
+          load_bf16<E>(p.v + (w.k0 + j) * p.v_stride + w.kvh * D + lane * E, v);
+          st.add(k, v);
+        }
+        for (int e = 0; e < D / 32; ++e)
+          p.out[r * p.out_stride + h * D + lane * (D / 32) + e] = f32_to_bf16_bits(st.l == 0.f ? 0.f : st.acc[e] / st.l);
+        if (p.lse && lane == 0)
+          p.lse[static_cast<long long>(r) * p.q_heads + h] = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kPreMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
-int launch_prefill(const PrefillArgs& a, void* stream) {
+namespace {
+
+template <int D>
+int launch_one(const PrefillArgs& a, void* stream) {
+  // (set on every call: the attribute belongs to the current device, like the launch)
+  cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefillShape<D>::smem);
+  int dev = 0, sms = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  // At most this many items: a sequence adds one more than its whole pairs of row tiles.
+  const long long subs = a.kv_heads * ((a.q_heads / a.kv_heads + a.head_block - 1) / a.head_block);
+  const long long most = (a.total_q / (2 * a.tile_tokens) + static_cast<long long>(a.batch)) * subs;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(a.total_q) * a.q_heads + kRowWarps - 1) / kRowWarps), 1, 1);
-  cfg.blockDim = dim3(kRowWarps * 32, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(most < sms ? most : sms), 1, 1);
+  cfg.blockDim = dim3(kPreThreads, 1, 1);
+  cfg.dynamicSmemBytes = PrefillShape<D>::smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return static_cast<int>(a.head_dim == 128 ? cudaLaunchKernelEx(&cfg, prefill_row_kernel<128>, a)
-                                            : cudaLaunchKernelEx(&cfg, prefill_row_kernel<64>, a));
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, prefill_kernel<D>, a));
+}
+
+}  // namespace
+
+int launch_prefill(const PrefillArgs& a, void* stream) {
+  return a.head_dim == 128 ? launch_one<128>(a, stream) : launch_one<64>(a, stream);
+}
+
+int read_prefill_status(void* stream, uint32_t* out, int clear) {
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint32_t v = 0;
+  cudaError_t err = cudaMemcpyFromSymbolAsync(&v, g_prefill_status, sizeof v, 0, cudaMemcpyDeviceToHost, s);
+  if (err == cudaSuccess && clear) {
+    static const uint32_t z = 0;
+    err = cudaMemcpyToSymbolAsync(g_prefill_status, &z, sizeof z, 0, cudaMemcpyHostToDevice, s);
+  }
+  if (err == cudaSuccess) err = cudaStreamSynchronize(s);
+  *out = v;
+  return static_cast<int>(err);
 }
 
 }  // namespace glora

@@ -48,6 +48,9 @@ struct DecodeArgs {
 };
 
 struct PrefillArgs {
+  TensorMapBytes map_q;      // q as [total_q, q_heads, head_dim], box {64, head_block, tile_tokens}, 128-byte swizzle
+  TensorMapBytes map_k;      // k [total_k, kv_heads * head_dim], box {64, 128}, 128-byte swizzle
+  TensorMapBytes map_v;
   const uint16_t* q;
   const uint16_t* k;
   const uint16_t* v;
@@ -56,6 +59,8 @@ struct PrefillArgs {
   const int32_t* cu_q;
   const int32_t* cu_k;
   int batch, total_q, total_k, q_heads, kv_heads, head_dim;
+  int head_block;            // query heads of a row tile: the group's, in blocks of at most 128
+  int tile_tokens;           // tokens of a row tile: 128 / head_block
   float scale;
   float* lse;
 };
@@ -65,5 +70,7 @@ int launch_kv_write(const KvRowsArgs& a, void* stream);
 int launch_kv_read(const KvRowsArgs& a, void* stream);
 int launch_decode(const DecodeArgs& a, void* stream);
 int launch_prefill(const PrefillArgs& a, void* stream);
+// OR of the prefill kernel's device status bits since the last clear (synchronizes `stream`).
+int read_prefill_status(void* stream, uint32_t* out, int clear);
 
 }  // namespace glora
