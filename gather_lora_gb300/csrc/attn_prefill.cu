@@ -66,9 +66,10 @@ struct PrefillItem {
 struct PrefillCtl {
   unsigned long long full[8], empty[8];
   unsigned long long q_full, q_empty;
-  unsigned long long s_full[2], p_ready[2], o_full[2];
+  unsigned long long s_full[2], p_ready[2][2], o_full[2];   // (p_ready: halves of the keys)
   unsigned long long item_full[kItems], item_empty[kItems];
-  unsigned long long drain;
+  unsigned long long drain, next_full;
+  uint4 next;                          // the answer to ask_next_block
   PrefillItem item[kItems];
   uint32_t tmem;
   int failed;
@@ -102,6 +103,54 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int c
                : "memory");
 }
 
+// Pairs of fp32 operations in one instruction, and the maximum of three.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The grid's next block that has not started, taken over by this CTA: the answer (16 bytes at shared
+// address `to`) arrives on mbarrier `bar`.
+__device__ __forceinline__ void ask_next_block(uint32_t to, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n" ::"r"(to), "r"(bar)
+               : "memory");
+}
+// Its blockIdx.x, or -1: no block was left.
+__device__ __forceinline__ long long next_block(uint32_t from) {
+  uint32_t x, got;
+  asm volatile(
+      "{\n .reg .b128 h;\n .reg .pred p;\n .reg .b32 y, z, w;\n"
+      " ld.shared.b128 h, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
+      " selp.u32 %1, 1, 0, p;\n mov.u32 %0, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, h;\n}\n"
+      : "=&r"(x), "=&r"(got)
+      : "r"(from)
+      : "memory");
+  return got ? static_cast<long long>(x) : -1;
+}
+
 }  // namespace
 
 template <int D>
@@ -123,7 +172,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     mbar_init(smem_u32(&c.q_empty), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&c.s_full[i]), 1);
-      mbar_init(smem_u32(&c.p_ready[i]), 4);
+      mbar_init(smem_u32(&c.p_ready[i][0]), 4);
+      mbar_init(smem_u32(&c.p_ready[i][1]), 4);
       mbar_init(smem_u32(&c.o_full[i]), 1);
     }
     for (int i = 0; i < kItems; ++i) {
@@ -131,6 +181,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       mbar_init(smem_u32(&c.item_empty[i]), kSoftmaxWarps + 1);
     }
     mbar_init(smem_u32(&c.drain), 1);
+    mbar_init(smem_u32(&c.next_full), 1);
     c.failed = 0;
     mbar_fence_init();
   }
@@ -156,12 +207,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     uint32_t kv = 0;                    // ring tiles issued
     long long base = 0;                 // row-tile pairs before sequence b0
     bool go = true;
-    for (long long idx = blockIdx.x; go; idx += gridDim.x, ++it) {
-      // Item idx: sequences in order, within one its last rows (the most keys) first, heads fastest.
-      const long long x = idx / subs;
-      const int sub = static_cast<int>(idx - x * subs);
+    auto ask = [&]() {                  // (lane 0) the next item, once the current one's loads are nearly out
+      fence_proxy_async_smem();
+      mbar_arrive_expect_tx(smem_u32(&c.next_full), 16);
+      ask_next_block(smem_u32(&c.next), smem_u32(&c.next_full));
+    };
+    for (long long idx = blockIdx.x; go; ++it) {
+      // Item idx (-1: none): sequences in order, within one its last rows (the most keys) first, heads fastest.
+      const long long x = idx < 0 ? -1 : idx / subs;
+      const int sub = idx < 0 ? 0 : static_cast<int>(idx - x * subs);
       int q0 = 0, lq = 0, k0 = 0, lk = 0, tile = -1;
-      while (b0 < p.batch) {
+      if (x < base) base = 0, b0 = 0;   // (blocks are handed out in rising order as a rule)
+      while (idx >= 0 && b0 < p.batch) {
         const int b = b0 + lane;
         int a0 = 0, a1 = 0, e0 = 0, e1 = 0;
         if (b < p.batch) {
@@ -215,6 +272,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         c.item[sl] = w;
         mbar_arrive(smem_u32(&c.item_full[sl]));
         const int n = max(w.n[0], w.n[1]);
+        bool asked = go && n == 0;
+        if (asked) ask();
         if (go && n > 0) {
           if (items > 0) go = pre_wait(c, c.q_empty, (items - 1) & 1);
           ++items;
@@ -228,6 +287,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
                 tma_load_3d(q_s + i * Sh::tile_bytes + a * (kTile * 128), &p.map_q, a * 64, w.h0, w.q0 + i * TT, fb);
           }
           for (int j = 0; go && j < 2 * n; ++j) {      // K0 V0 K1 V1 ..
+            if (j == 2 * n - 2) {
+              ask();
+              asked = true;
+            }
             const uint32_t s = kv % NS;
             if (kv >= NS && !pre_wait(c, c.empty[s], ((kv / NS) - 1) & 1)) {
               go = false;
@@ -241,7 +304,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
               tma_load_2d(to + a * (kTile * 128), (j & 1) ? &p.map_v : &p.map_k, w.kvh * D + a * 64, k0 + (j >> 1) * kTile, fb);
           }
         }
+        if (asked) {
+          const bool told = pre_wait(c, c.next_full, it & 1) || mbar_wait_limit(smem_u32(&c.next_full), it & 1, kDrainLimitCycles);
+          idx = told ? next_block(smem_u32(&c.next)) : -1;
+        } else {
+          idx = -1;
+        }
       }
+      idx = __shfl_sync(0xffffffffu, idx, 0);
       go = __shfl_sync(0xffffffffu, go, 0);
     }
     if (lane == 0 && *reinterpret_cast<volatile int*>(&c.failed)) {   // let the loads in flight land
@@ -267,11 +337,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         }
         umma_commit(smem_u32(&c.s_full[i]));
       };
-      auto values = [&](int i, uint32_t s, bool add) {   // O_i (+)= P_i V, V in stage s
-        const uint64_t va = smem_desc_mn128(ring + s * Sh::tile_bytes, kTile * 128, 1024);
+      auto values = [&](int i, uint32_t s, int half, bool add) {   // O_i (+)= P_i V over half of the keys, V in stage s
+        const uint64_t va = smem_desc_mn128(ring + s * Sh::tile_bytes + half * (kTile / 2 * 128), kTile * 128, 1024);
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_bf16_ts(tmem + kColO + i * kTile, tmem + i * kTile + kk * 8, va + kk * (2048 >> 4), id_o, kk != 0 || add);
+        for (int kk = 0; kk < kTile / 32; ++kk)
+          umma_bf16_ts(tmem + kColO + i * kTile, tmem + i * kTile + half * (kTile / 4) + kk * 8, va + kk * (2048 >> 4), id_o, kk != 0 || add);
       };
       bool go = true;
       for (int it = 0; go; ++it) {
@@ -298,11 +368,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
           for (int i = 0; i < 2; ++i) {
             const int ni = i ? n1 : n0;
             if (go && j < ni) {
-              go = pre_wait(c, c.p_ready[i], (pc >> i) & 1);
-              pc ^= 1u << i;
+              go = pre_wait(c, c.p_ready[i][0], (pc >> i) & 1);
               if (!go) break;
               tc_fence_after();
-              values(i, vs, j != 0);
+              values(i, vs, 0, j != 0);
+              go = pre_wait(c, c.p_ready[i][1], (pc >> i) & 1);
+              if (!go) break;
+              tc_fence_after();
+              values(i, vs, 1, true);
+              pc ^= 1u << i;
               if (j + 1 == ni) umma_commit(smem_u32(&c.o_full[i]));
             }
             if (go && j + 1 < ni) scores(i, ks);
@@ -364,9 +438,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         for (int q = 0; q < 4; ++q) {
           mx[q] = __uint_as_float(s[q][0]);
 #pragma unroll
-          for (int e = 1; e < 32; ++e) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][e]));
+          for (int e = 1; e < 31; e += 2) mx[q] = max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+          mx[q] = fmaxf(mx[q], __uint_as_float(s[q][31]));
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         if (j == 0) {
           ref = top;
         } else if (__any_sync(0xffffffffu, top > ref + grow)) {
@@ -385,26 +460,27 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
           }
         }
         const float off = ref == -INFINITY ? 0.f : -ref * sl2;   // (nothing seen: every weight is 0)
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t sl2p = pair(sl2, sl2), offp = pair(off, off);
+        uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const int q = 2 * h + (e >> 4), f = (e & 15) * 2;
-            const float w0 = exp2_fast(__fmaf_rn(__uint_as_float(s[q][f]), sl2, off));
-            const float w1 = exp2_fast(__fmaf_rn(__uint_as_float(s[q][f + 1]), sl2, off));
-            sum[2 * h] += w0;
-            sum[2 * h + 1] += w1;
+            const float2 x = unpair(fma2(pair(__uint_as_float(s[q][f]), __uint_as_float(s[q][f + 1])), sl2p, offp));
+            const float w0 = exp2_fast(x.x), w1 = exp2_fast(x.y);
+            sum[e & 3] = add2(sum[e & 3], pair(w0, w1));
             pk[e] = pack_bf16x2(w0, w1);
           }
           tmem_st32(col_s + h * 32, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&c.p_ready[i][h]));
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&c.p_ready[i]));
+        const float2 all = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+        l += all.x + all.y;
       }
       if (!go) break;
       // The row's result.
@@ -478,15 +554,12 @@ template <int D>
 int launch_one(const PrefillArgs& a, void* stream) {
   // (set on every call: the attribute belongs to the current device, like the launch)
   cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefillShape<D>::smem);
-  int dev = 0, sms = 0;
-  if (e == cudaSuccess) e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return static_cast<int>(e);
   // At most this many items: a sequence adds one more than its whole pairs of row tiles.
   const long long subs = a.kv_heads * ((a.q_heads / a.kv_heads + a.head_block - 1) / a.head_block);
   const long long most = (a.total_q / (2 * a.tile_tokens) + static_cast<long long>(a.batch)) * subs;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(most < sms ? most : sms), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(most), 1, 1);
   cfg.blockDim = dim3(kPreThreads, 1, 1);
   cfg.dynamicSmemBytes = PrefillShape<D>::smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
