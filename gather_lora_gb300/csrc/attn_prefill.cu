@@ -322,76 +322,79 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     __syncwarp();
   } else if (warp == kPreMmaWarp) {
     // ============================ MMA issue ===============================
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile);
-      constexpr uint32_t id_o = idesc_bf16_f32(kTile, D) | (1u << 16);   // V: MN-major
-      uint32_t kv = 0, pc = 0;           // pc: bit i, the phase of p_ready[i] to wait for
-      int items = 0;
-      auto scores = [&](int i, uint32_t s) {           // S_i = Q_i K^T, K in stage s
-        const uint64_t qa = smem_desc(q_s + i * Sh::tile_bytes, 1024, Swz::k128);
-        const uint64_t ka = smem_desc(ring + s * Sh::tile_bytes, 1024, Swz::k128);
+    // (the whole warp takes every step, one elected lane issues)
+    constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile);
+    constexpr uint32_t id_o = idesc_bf16_f32(kTile, D) | (1u << 16);   // V: MN-major
+    uint32_t kv = 0, pc = 0;             // pc: bit i, the phase of p_ready[i] to wait for
+    int items = 0;
+    auto scores = [&](int i, uint32_t s) {             // S_i = Q_i K^T, K in stage s
+      const uint64_t qa = smem_desc(q_s + i * Sh::tile_bytes, 1024, Swz::k128);
+      const uint64_t ka = smem_desc(ring + s * Sh::tile_bytes, 1024, Swz::k128);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {          // (descriptors hold addresses in 16-byte units)
-          const uint64_t o = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
-          umma_bf16(tmem + i * kTile, qa + o, ka + o, id_s, kk != 0);
-        }
-        umma_commit(smem_u32(&c.s_full[i]));
-      };
-      auto values = [&](int i, uint32_t s, int half, bool add) {   // O_i (+)= P_i V over half of the keys, V in stage s
-        const uint64_t va = smem_desc_mn128(ring + s * Sh::tile_bytes + half * (kTile / 2 * 128), kTile * 128, 1024);
+      for (int kk = 0; kk < D / 16; ++kk) {            // (descriptors hold addresses in 16-byte units)
+        const uint64_t o = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+        umma_bf16_warp(tmem + i * kTile, qa + o, ka + o, id_s, kk != 0);
+      }
+      umma_commit_warp(smem_u32(&c.s_full[i]));
+    };
+    auto values = [&](int i, uint32_t s, int half, bool add) {   // O_i (+)= P_i V over half of the keys, V in stage s
+      const uint64_t va = smem_desc_mn128(ring + s * Sh::tile_bytes + half * (kTile / 2 * 128), kTile * 128, 1024);
 #pragma unroll
-        for (int kk = 0; kk < kTile / 32; ++kk)
-          umma_bf16_ts(tmem + kColO + i * kTile, tmem + i * kTile + half * (kTile / 4) + kk * 8, va + kk * (2048 >> 4), id_o, kk != 0 || add);
-      };
-      bool go = true;
-      for (int it = 0; go; ++it) {
-        const int sl = it % kItems;
-        if (!pre_wait(c, c.item_full[sl], (it / kItems) & 1)) break;
-        const bool valid = c.item[sl].valid;
-        const int n0 = c.item[sl].n[0], n1 = c.item[sl].n[1], n = max(n0, n1);
-        mbar_arrive(smem_u32(&c.item_empty[sl]));
-        if (!valid) break;
-        if (n == 0) continue;
-        go = pre_wait(c, c.q_full, items & 1) && pre_wait(c, c.full[kv % NS], (kv / NS) & 1);
-        ++items;
-        if (!go) break;
-        tc_fence_after();
-        if (n0 > 0) scores(0, kv % NS);
-        if (n1 > 0) scores(1, kv % NS);
-        umma_commit(smem_u32(&c.empty[kv % NS]));
-        ++kv;
-        if (n == 1) umma_commit(smem_u32(&c.q_empty));
-        for (int j = 0; go && j < n; ++j) {
-          const uint32_t vs = kv % NS, ks = (kv + 1) % NS;
-          go = pre_wait(c, c.full[vs], (kv / NS) & 1) && (j + 1 == n || pre_wait(c, c.full[ks], ((kv + 1) / NS) & 1));
-#pragma unroll 1
-          for (int i = 0; i < 2; ++i) {
-            const int ni = i ? n1 : n0;
-            if (go && j < ni) {
-              go = pre_wait(c, c.p_ready[i][0], (pc >> i) & 1);
-              if (!go) break;
-              tc_fence_after();
-              values(i, vs, 0, j != 0);
-              go = pre_wait(c, c.p_ready[i][1], (pc >> i) & 1);
-              if (!go) break;
-              tc_fence_after();
-              values(i, vs, 1, true);
-              pc ^= 1u << i;
-              if (j + 1 == ni) umma_commit(smem_u32(&c.o_full[i]));
-            }
-            if (go && j + 1 < ni) scores(i, ks);
+      for (int kk = 0; kk < kTile / 32; ++kk)
+        umma_bf16_ts_warp(tmem + kColO + i * kTile, tmem + i * kTile + half * (kTile / 4) + kk * 8, va + kk * (2048 >> 4), id_o,
+                          kk != 0 || add);
+    };
+    bool go = true;
+    for (int it = 0; go; ++it) {
+      const int sl = it % kItems;
+      go = warp_wait(c, c.item_full[sl], (it / kItems) & 1);
+      if (!go) break;
+      const bool valid = __shfl_sync(0xffffffffu, c.item[sl].valid, 0);
+      const int n0 = __shfl_sync(0xffffffffu, c.item[sl].n[0], 0), n1 = __shfl_sync(0xffffffffu, c.item[sl].n[1], 0), n = max(n0, n1);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c.item_empty[sl]));
+      __syncwarp();
+      if (!valid) break;
+      if (n == 0) continue;
+      go = warp_wait(c, c.q_full, items & 1) && warp_wait(c, c.full[kv % NS], (kv / NS) & 1);
+      ++items;
+      if (!go) break;
+      tc_fence_after();
+      if (n0 > 0) scores(0, kv % NS);
+      if (n1 > 0) scores(1, kv % NS);
+      umma_commit_warp(smem_u32(&c.empty[kv % NS]));
+      ++kv;
+      if (n == 1) umma_commit_warp(smem_u32(&c.q_empty));
+      for (int j = 0; go && j < n; ++j) {
+        const uint32_t vs = kv % NS, ks = (kv + 1) % NS;
+        go = warp_wait(c, c.full[vs], (kv / NS) & 1) && (j + 1 == n || warp_wait(c, c.full[ks], ((kv + 1) / NS) & 1));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int ni = i ? n1 : n0;
+          if (go && j < ni) {
+            go = warp_wait(c, c.p_ready[i][0], (pc >> i) & 1);
+            if (!go) break;
+            tc_fence_after();
+            values(i, vs, 0, j != 0);
+            go = warp_wait(c, c.p_ready[i][1], (pc >> i) & 1);
+            if (!go) break;
+            tc_fence_after();
+            values(i, vs, 1, true);
+            pc ^= 1u << i;
+            if (j + 1 == ni) umma_commit_warp(smem_u32(&c.o_full[i]));
           }
-          if (!go) break;
-          umma_commit(smem_u32(&c.empty[vs]));
-          if (j + 1 < n) umma_commit(smem_u32(&c.empty[ks]));
-          if (j + 2 == n) umma_commit(smem_u32(&c.q_empty));   // the item's last scores are issued
-          kv += j + 1 < n ? 2 : 1;
+          if (go && j + 1 < ni) scores(i, ks);
         }
+        if (!go) break;
+        umma_commit_warp(smem_u32(&c.empty[vs]));
+        if (j + 1 < n) umma_commit_warp(smem_u32(&c.empty[ks]));
+        if (j + 2 == n) umma_commit_warp(smem_u32(&c.q_empty));   // the item's last scores are issued
+        kv += j + 1 < n ? 2 : 1;
       }
-      if (*reinterpret_cast<volatile int*>(&c.failed)) {   // let the MMAs in flight end
-        umma_commit(smem_u32(&c.drain));
-        mbar_wait_limit(smem_u32(&c.drain), 0, kDrainLimitCycles);
-      }
+    }
+    if (!go) {                           // let the MMAs in flight end
+      umma_commit_warp(smem_u32(&c.drain));
+      mbar_wait_limit(smem_u32(&c.drain), 0, kDrainLimitCycles);
     }
     __syncwarp();
   }
