@@ -43,6 +43,7 @@ constexpr int kPreThreads = 384;
 // Registers a thread: 168 at launch (65536 over 12 warps); the helper warpgroup gives 80 away, the softmax
 // warpgroups hold a whole row of scores: 2 * 208 + 88 = 3 * 168.
 constexpr int kHelperRegs = 88, kSoftmaxRegs = 208;
+constexpr int kOutBytes = 4096;                 // staging of a warp's results: 32 rows x 64 columns
 constexpr int kItems = 4;                       // depth of the item ring
 constexpr uint32_t kColO = 256;                 // tensor memory: S at 0 and 128, O at 256 and 384
 constexpr float kRescale = 8.f;                 // reference moves when the maximum grew by 2^8
@@ -51,8 +52,8 @@ template <int D>
 struct PrefillShape {
   static constexpr int atoms = D / 64;                          // 64-column boxes of a tile
   static constexpr int tile_bytes = kTile * D * 2;              // Q row tile, K tile or V tile
-  static constexpr int stages = D == 128 ? 5 : 8;
-  static constexpr int smem = (2 + stages) * tile_bytes + 2048; // + control, alignment
+  static constexpr int stages = D == 128 ? 4 : 8;
+  static constexpr int smem = (2 + stages) * tile_bytes + kSoftmaxWarps * kOutBytes + 2048;   // + control, alignment
 };
 
 struct PrefillItem {
@@ -160,7 +161,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
   extern __shared__ unsigned char prefill_smem_raw[];
   const uint32_t raw = smem_u32(prefill_smem_raw), pad = ((raw + 1023u) & ~1023u) - raw;
   const uint32_t q_s = raw + pad, ring = q_s + 2 * Sh::tile_bytes;
-  PrefillCtl& c = *reinterpret_cast<PrefillCtl*>(prefill_smem_raw + pad + (2 + NS) * Sh::tile_bytes);
+  const uint32_t out_s = ring + NS * Sh::tile_bytes;
+  PrefillCtl& c = *reinterpret_cast<PrefillCtl*>(prefill_smem_raw + pad + (2 + NS) * Sh::tile_bytes + kSoftmaxWarps * kOutBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -417,6 +419,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       const int tok = w.tok0 + i * TT + t_in, n = w.n[i];
       const bool live = t_in < TT && g < w.heads && tok < w.lq;
       const int lim = live ? max(0, min(w.lk, tok + 1 + w.lk - w.lq)) : 0x7fffffff;   // keys the row sees
+      const int least = __reduce_min_sync(0xffffffffu, lim);
       float ref = -INFINITY, l = 0.f;      // exponents are relative to ref (in units of raw scores)
       bool go = true;
       for (int j = 0; j < n; ++j) {
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         for (int q = 0; q < 4; ++q) tmem_ld32(col_s + q * 32, s[q]);
         tmem_ld_wait();
         const int seen = lim - j * kTile;
-        if (__any_sync(0xffffffffu, seen < kTile)) {
+        if (least - j * kTile < kTile) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -486,35 +489,49 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         l += all.x + all.y;
       }
       if (!go) break;
-      // The row's result.
+      // The row's result, through shared memory so that a store instruction writes 4 whole 128-byte lines
+      // (one row per lane, 16 bytes each, wrote 32 and held up the SM's loads: 5000 clocks an item, now 1000).
       uint16_t* const to = p.out + static_cast<long long>(w.q0 + i * TT + t_in) * p.out_stride + (w.h0 + g) * D;
+      const uint32_t lives = __ballot_sync(0xffffffffu, live);
       bool bad = false;
       if (n > 0) {
         if (!warp_wait(c, c.o_full[i], oc & 1)) break;
         ++oc;
         tc_fence_after();
         const float inv = 1.f / l;
-        float check = 0.f;
+        const uint32_t stage = out_s + warp * kOutBytes;
+        float check[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
-          tmem_ld32(col_o + q * 32, o);
-          tmem_ld_wait();
-          if (!live) continue;
+        for (int half = 0; half < D / 64; ++half) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            float f[8];
+          for (int q = 0; q < 2; ++q) {
+            uint32_t o[32];
+            tmem_ld32(col_o + half * 64 + q * 32, o);
+            tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              f[x] = l == 0.f ? 0.f : __uint_as_float(o[e + x]) * inv;
-              check = __fmaf_rn(f[x], 0.f, check);       // stays 0 while all are finite
+            for (int e = 0; e < 32; e += 8) {
+              float f[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                f[x] = l == 0.f ? 0.f : __uint_as_float(o[e + x]) * inv;
+                check[x & 3] = __fmaf_rn(f[x], 0.f, check[x & 3]);       // stays 0 while all are finite
+              }
+              sts128(stage + lane * 128 + (((q * 4 + e / 8) ^ (lane & 7)) << 4),
+                     make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
             }
-            *reinterpret_cast<uint4*>(to + q * 32 + e) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                                                    pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
           }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int r = k * 4 + lane / 8, ch = lane % 8;
+            const uint4 v = lds128(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+            uint16_t* const at = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), r));
+            if ((lives >> r) & 1) *reinterpret_cast<uint4*>(at + half * 64 + ch * 8) = v;
+          }
+          __syncwarp();
         }
         tc_fence_before();
-        bad = live && !(check == 0.f);
+        bad = live && !(check[0] + check[1] + check[2] + check[3] == 0.f);
       } else if (live) {
 #pragma unroll
         for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(to + e) = make_uint4(0, 0, 0, 0);

@@ -64,18 +64,6 @@ __device__ __forceinline__ void epi_sync() {
   asm volatile("bar.sync 1, %0;\n" ::"n"(kEpiThreads) : "memory");
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-
 // Byte offset, inside the xa tile [128 rows, max_rank] (the expand's A
 // operand), of the 16-byte chunk holding columns [8c, 8c + 8) of row i.
 // max_rank >= 64: 128-byte swizzle, atoms of 64 columns 16 KB apart;
