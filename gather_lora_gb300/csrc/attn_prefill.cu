@@ -120,6 +120,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
@@ -498,28 +503,30 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         if (!warp_wait(c, c.o_full[i], oc & 1)) break;
         ++oc;
         tc_fence_after();
-        const float inv = 1.f / l;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const uint64_t invp = pair(inv, inv);
         const uint32_t stage = out_s + warp * kOutBytes;
-        float check[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t check[2] = {0, 0};          // stays 0 while all results are finite
 #pragma unroll
         for (int half = 0; half < D / 64; ++half) {
+          uint32_t o[2][32];
+          tmem_ld32(col_o + half * 64, o[0]);
+          tmem_ld32(col_o + half * 64 + 32, o[1]);
+          tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t o[32];
-            tmem_ld32(col_o + half * 64 + q * 32, o);
-            tmem_ld_wait();
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
-              float f[8];
+              uint32_t r[4];
 #pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                f[x] = l == 0.f ? 0.f : __uint_as_float(o[e + x]) * inv;
-                check[x & 3] = __fmaf_rn(f[x], 0.f, check[x & 3]);       // stays 0 while all are finite
+              for (int x = 0; x < 4; ++x) {
+                const uint64_t f = mul2(pair(__uint_as_float(o[q][e + 2 * x]), __uint_as_float(o[q][e + 2 * x + 1])), invp);
+                check[x & 1] = fma2(f, 0, check[x & 1]);
+                const float2 v = unpair(f);
+                r[x] = pack_bf16x2(v.x, v.y);
               }
-              sts128(stage + lane * 128 + (((q * 4 + e / 8) ^ (lane & 7)) << 4),
-                     make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
+              sts128(stage + lane * 128 + (((q * 4 + e / 8) ^ (lane & 7)) << 4), make_uint4(r[0], r[1], r[2], r[3]));
             }
-          }
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -531,7 +538,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
           __syncwarp();
         }
         tc_fence_before();
-        bad = live && !(check[0] + check[1] + check[2] + check[3] == 0.f);
+        const float2 sum0 = unpair(add2(check[0], check[1]));
+        bad = live && !(sum0.x + sum0.y == 0.f);
       } else if (live) {
 #pragma unroll
         for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(to + e) = make_uint4(0, 0, 0, 0);
