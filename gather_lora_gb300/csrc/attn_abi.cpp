@@ -93,6 +93,10 @@ int kv_rows(const void* k, int64_t k_row_stride, const void* v, int64_t v_row_st
   a.n = n;
   a.head_dim = cache->head_dim;
   a.format = cache->format;
+  a.page_shift = -1;
+  if ((cache->page_size & (cache->page_size - 1)) == 0)
+    for (a.page_shift = 0; (1 << a.page_shift) < cache->page_size;) ++a.page_shift;
+  a.heads_magic = static_cast<uint32_t>(((1ull << 32) + cache->kv_heads - 1) / cache->kv_heads);
   return LORA_OK;
 }
 

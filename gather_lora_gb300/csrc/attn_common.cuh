@@ -51,8 +51,9 @@ __device__ __forceinline__ void codes_to_f32(uint32_t c, float (&f)[4]) {
     const float2 a = f16x2_to_f32(lo), b = f16x2_to_f32(hi);
     f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
   } else {
+    c ^= 0x80808080u;   // 0x4b000000 | (code + 128) is the number 2^23 + 128 + code
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = static_cast<float>(static_cast<int8_t>((c >> (8 * i)) & 0xffu));
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(__byte_perm(c, 0x4b000000u, 0x7440 | i)) - 8388736.f;
   }
 }
 

@@ -29,6 +29,8 @@ struct KvRowsArgs {
   long long k_stride, v_stride;
   const long long* slots;
   int n, head_dim, format;
+  int page_shift;            // log2 of page_size, or -1: not a power of two
+  uint32_t heads_magic;      // ceil(2^32 / kv_heads): x / kv_heads = hi(x * magic) for x * kv_heads < 2^32, kv_heads > 1
 };
 
 struct DecodeArgs {

@@ -5,11 +5,11 @@
 //   a = max |x|,  scale = a / Q,  code = round(x * (Q / a)),  Q = 448 or 127.
 // read: x = bf16(code * scale).
 //
-// Both move every byte once and compute almost nothing: HBM bandwidth bounds
-// them, latency at a few rows. One thread holds 8 values (16 bytes of BF16) of a
-// K row and the same 8 of the V row, so the slot is divided into page and slot
-// once for both and two independent loads are in flight; the 8 or 16 threads of
-// a head row find its largest magnitude by shuffles.
+// Both move every byte once and compute almost nothing: HBM bandwidth bounds them, latency at a few
+// rows. A thread holds 8 values (16 bytes of BF16) of a K row and the same 8 of the V row, so the slot is
+// divided into page and slot once for both; the 8 or 16 threads of a head row find its largest magnitude by
+// shuffles. Large calls give a thread kMany such pieces, whose loads are all in flight before the first is
+// used (with one, the wait for the slot number left half of the memory system idle).
 #include "attn_common.cuh"
 
 namespace glora {
@@ -17,15 +17,20 @@ namespace glora {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kMany = 4;          // pieces of a thread in large calls
 constexpr float kZeroRow = 7.888609052210118e-31f;   // 2^-100: below it a row is stored as zeros
 
 // Page and slot of slots[i]; false outside the cache.
-__device__ __forceinline__ bool locate(const KvView& c, long long at, int& page, int& slot) {
+__device__ __forceinline__ bool locate(const KvRowsArgs& p, long long at, int& page, int& slot) {
+  const KvView& c = p.c;
   if (at < 0 || at >= static_cast<long long>(c.num_pages) * c.page_size) return false;
-  if ((at >> 32) == 0) {   // 32-bit division where it is enough
-    const uint32_t p = static_cast<uint32_t>(at) / static_cast<uint32_t>(c.page_size);
-    page = static_cast<int>(p);
-    slot = static_cast<int>(static_cast<uint32_t>(at) - p * static_cast<uint32_t>(c.page_size));
+  if (p.page_shift >= 0) {
+    page = static_cast<int>(at >> p.page_shift);
+    slot = static_cast<int>(at) & (c.page_size - 1);
+  } else if ((at >> 32) == 0) {   // 32-bit division where it is enough
+    const uint32_t q = static_cast<uint32_t>(at) / static_cast<uint32_t>(c.page_size);
+    page = static_cast<int>(q);
+    slot = static_cast<int>(static_cast<uint32_t>(at) - q * static_cast<uint32_t>(c.page_size));
   } else {
     page = static_cast<int>(at / c.page_size);
     slot = static_cast<int>(at - static_cast<long long>(page) * c.page_size);
@@ -33,14 +38,19 @@ __device__ __forceinline__ bool locate(const KvView& c, long long at, int& page,
   return true;
 }
 
-// The 8 BF16 values in `x` as codes; `a` is the bit pattern of the row's largest
-// magnitude. The scale goes to *scale_out.
+// Larger of two BF16 pairs, NaN if either is.
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+__device__ __forceinline__ uint32_t abs_max8(const uint4& x) {
+  constexpr uint32_t abs = 0x7fff7fffu;
+  return max2_nan(max2_nan(x.x & abs, x.y & abs), max2_nan(x.z & abs, x.w & abs));
+}
+
+// The 8 BF16 values in `x` times `inv`, rounded to codes.
 template <int FMT>
-__device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t a, float* scale_out) {
-  const float amax = bf16_bits_to_f32(static_cast<uint16_t>(a));
-  const bool finite = a < 0x7f80u, keep = finite && amax >= kZeroRow;
-  const float inv = keep ? __fdiv_rn(kv_qmax<FMT>(), amax) : 0.f;
-  *scale_out = !finite ? __int_as_float(0x7fffffff) : keep ? __fdiv_rn(amax, kv_qmax<FMT>()) : 0.f;
+__device__ __forceinline__ uint2 quantise8(const uint4& x, float inv) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t code[2];
 #pragma unroll
@@ -48,114 +58,153 @@ __device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t a, float* sc
     float f[4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      f[2 * j] = __uint_as_float(w[2 * h + j] << 16) * inv;
-      f[2 * j + 1] = __uint_as_float(w[2 * h + j] & 0xffff0000u) * inv;
+      f[2 * j] = __fmul_rn(__uint_as_float(w[2 * h + j] << 16), inv);
+      f[2 * j + 1] = __fmul_rn(__uint_as_float(w[2 * h + j] & 0xffff0000u), inv);
     }
     if constexpr (FMT == kKvE4m3) {
-      uint32_t c;
       asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n"
           " mov.b32 %0, {l, h};\n}\n"
-          : "=r"(c)
+          : "=r"(code[h])
           : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]));
-      code[h] = c;
-    } else {
-      uint32_t c = 0;
+    } else {   // at most 127 (1 + 2^-23) in magnitude: 1.5 * 2^23 + f holds the rounded integer in its low byte
+      uint32_t t[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int q = max(-127, min(127, __float2int_rn(f[j])));
-        c |= static_cast<uint32_t>(q & 0xff) << (8 * j);
-      }
-      code[h] = c;
+      for (int j = 0; j < 4; ++j) t[j] = __float_as_uint(__fadd_rn(f[j], 12582912.f));
+      code[h] = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
     }
   }
-  // (a row that is not finite holds NaN or infinity times zero here: its codes are zeros)
-  return finite ? make_uint2(code[0], code[1]) : make_uint2(0u, 0u);
-}
-
-__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t pair) {
-  return max(m, max(pair & 0x7fffu, (pair >> 16) & 0x7fffu));
+  return make_uint2(code[0], code[1]);
 }
 
 }  // namespace
 
-template <int FMT, int D>
+// Row and head of this thread's piece j: head rows in order, heads fastest, kRowThreads * U / TPR of them a block.
+template <int TPR, int U>
+__device__ __forceinline__ int piece(const KvRowsArgs& p, int j, int& head) {
+  constexpr uint32_t UNITS = kRowThreads * U / TPR;
+  const uint32_t kvh = static_cast<uint32_t>(p.c.kv_heads), q = blockIdx.x / kvh, r = blockIdx.x - q * kvh;
+  const uint32_t at = r * UNITS + j * (kRowThreads / TPR) + threadIdx.x / TPR;   // < 2^17
+  const uint32_t row = kvh == 1 ? at : __umulhi(at, p.heads_magic);
+  head = static_cast<int>(at - row * kvh);
+  return static_cast<int>(q * UNITS + row);
+}
+
+template <int FMT, int D, int U>
 __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const KvRowsArgs p) {
   constexpr int TPR = D / 8;   // threads of a head row
-  pdl_wait_then_release();
-  const long long unit = (static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x) / TPR;
   const int part = threadIdx.x % TPR;
-  const long long row = unit / p.c.kv_heads;
-  const int head = static_cast<int>(unit - row * p.c.kv_heads);
-  int page = 0, slot = 0;
-  const bool live = row < p.n && locate(p.c, p.slots[row], page, slot);
-  uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-  if (live) {
-    const int col = head * D + part * 8;
-    x[0] = *reinterpret_cast<const uint4*>(p.k + row * p.k_stride + col);
-    x[1] = *reinterpret_cast<const uint4*>(p.v + row * p.v_stride + col);
+  pdl_wait_then_release();
+  uint4 x[U][2];
+  long long at[U];
+  int row[U], head[U];
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    row[j] = piece<TPR, U>(p, j, head[j]);
+    x[j][0] = x[j][1] = make_uint4(0, 0, 0, 0);
+    at[j] = -1;
+    if (row[j] < p.n) {
+      const int col = head[j] * D + part * 8;
+      at[j] = __ldg(p.slots + row[j]);
+      x[j][0] = __ldg(reinterpret_cast<const uint4*>(p.k + row[j] * p.k_stride + col));
+      x[j][1] = __ldg(reinterpret_cast<const uint4*>(p.v + row[j] * p.v_stride + col));
+    }
   }
-  const long long at = page * p.c.page_bytes + head * p.c.head_bytes + slot * p.c.token_bytes;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    unsigned char* to = (j ? p.c.v : p.c.k) + at;
+  for (int j = 0; j < U; ++j) {
+    int page = 0, slot = 0;
+    const bool live = locate(p, at[j], page, slot);
+    const long long to = page * p.c.page_bytes + head[j] * p.c.head_bytes + slot * p.c.token_bytes;
     if constexpr (FMT == kKvBf16) {
-      if (live) *reinterpret_cast<uint4*>(to + part * 16) = x[j];
-    } else {
-      uint32_t a = abs_max2(abs_max2(abs_max2(abs_max2(0u, x[j].x), x[j].y), x[j].z), x[j].w);
-#pragma unroll
-      for (int o = TPR / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-      float scale;
-      const uint2 code = quantise8<FMT>(x[j], a, &scale);
       if (live) {
-        *reinterpret_cast<uint2*>(to + part * 8) = code;
-        if (part == 0) (j ? p.c.vs : p.c.ks)[scale_index(p.c, page, head, slot)] = scale;
+        *reinterpret_cast<uint4*>(p.c.k + to + part * 16) = x[j][0];
+        *reinterpret_cast<uint4*>(p.c.v + to + part * 16) = x[j][1];
+      }
+    } else {
+      // Largest magnitudes of the K row (low half) and the V row (high half).
+      const uint32_t mk = abs_max8(x[j][0]), mv = abs_max8(x[j][1]);
+      uint32_t m = max2_nan(__byte_perm(mk, mv, 0x5410), __byte_perm(mk, mv, 0x7632));
+#pragma unroll
+      for (int o = TPR / 2; o > 0; o >>= 1) m = max2_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+      // The four divisions of a row by four threads: Q / a of K and of V, a / Q of K and of V.
+      const uint32_t mine = (part & 1) ? m >> 16 : m & 0xffffu;
+      const float amax = __uint_as_float(mine << 16);
+      const bool finite = mine < 0x7f80u;
+      const float quot = finite && amax >= kZeroRow ? ((part & 2) ? __fdiv_rn(amax, kv_qmax<FMT>()) : __fdiv_rn(kv_qmax<FMT>(), amax)) : 0.f;
+      const float ik = __shfl_sync(0xffffffffu, quot, 0, TPR), iv = __shfl_sync(0xffffffffu, quot, 1, TPR);
+      if (live) {
+        // (a row that is not finite, or all but zero, has codes of zero)
+        const uint2 zero = make_uint2(0u, 0u);
+        *reinterpret_cast<uint2*>(p.c.k + to + part * 8) = ik != 0.f ? quantise8<FMT>(x[j][0], ik) : zero;
+        *reinterpret_cast<uint2*>(p.c.v + to + part * 8) = iv != 0.f ? quantise8<FMT>(x[j][1], iv) : zero;
+        if ((part & ~1) == 2)
+          (part == 2 ? p.c.ks : p.c.vs)[scale_index(p.c, page, head[j], slot)] = finite ? quot : __int_as_float(0x7fffffff);
       }
     }
   }
 }
 
-template <int FMT, int D>
+template <int FMT, int D, int U>
 __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const KvRowsArgs p) {
   constexpr int TPR = D / 8;
-  pdl_wait_then_release();
-  const long long unit = (static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x) / TPR;
   const int part = threadIdx.x % TPR;
-  const long long row = unit / p.c.kv_heads;
-  const int head = static_cast<int>(unit - row * p.c.kv_heads);
-  if (row >= p.n) return;
-  int page = 0, slot = 0;
-  const bool live = locate(p.c, p.slots[row], page, slot);
-  const long long at = page * p.c.page_bytes + head * p.c.head_bytes + slot * p.c.token_bytes;
-  uint4 x[2];
+  pdl_wait_then_release();
+  long long at[U];
+  int row[U], head[U];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    x[j] = make_uint4(0, 0, 0, 0);
-    if (!live) continue;
-    const unsigned char* from = (j ? p.c.v : p.c.k) + at;
-    if constexpr (FMT == kKvBf16) {
-      x[j] = *reinterpret_cast<const uint4*>(from + part * 16);
-    } else {
-      const uint2 code = *reinterpret_cast<const uint2*>(from + part * 8);
-      const float s = (j ? p.c.vs : p.c.ks)[scale_index(p.c, page, head, slot)];
-      float f[4], g[4];
-      codes_to_f32<FMT>(code.x, f);
-      codes_to_f32<FMT>(code.y, g);
-      x[j] = make_uint4(pack_bf16x2(f[0] * s, f[1] * s), pack_bf16x2(f[2] * s, f[3] * s),
-                        pack_bf16x2(g[0] * s, g[1] * s), pack_bf16x2(g[2] * s, g[3] * s));
+  for (int j = 0; j < U; ++j) {
+    row[j] = piece<TPR, U>(p, j, head[j]);
+    at[j] = row[j] < p.n ? __ldg(p.slots + row[j]) : -1;
+  }
+  uint4 x[U][2];       // BF16 values, or 8 codes in the first two words
+  float s[U][2];
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    int page = 0, slot = 0;
+    const bool live = locate(p, at[j], page, slot);
+    const long long from0 = page * p.c.page_bytes + head[j] * p.c.head_bytes + slot * p.c.token_bytes;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      x[j][h] = make_uint4(0, 0, 0, 0);
+      s[j][h] = 0.f;
+      if (!live) continue;
+      const unsigned char* from = (h ? p.c.v : p.c.k) + from0;
+      if constexpr (FMT == kKvBf16) {
+        x[j][h] = __ldg(reinterpret_cast<const uint4*>(from + part * 16));
+      } else {
+        const uint2 code = __ldg(reinterpret_cast<const uint2*>(from + part * 8));
+        x[j][h].x = code.x;
+        x[j][h].y = code.y;
+        s[j][h] = __ldg((h ? p.c.vs : p.c.ks) + scale_index(p.c, page, head[j], slot));
+      }
     }
   }
-  const int col = head * D + part * 8;
-  *reinterpret_cast<uint4*>(p.k_out + row * p.k_stride + col) = x[0];
-  *reinterpret_cast<uint4*>(p.v_out + row * p.v_stride + col) = x[1];
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    if (row[j] >= p.n) continue;
+    const int col = head[j] * D + part * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 v = x[j][h];
+      if constexpr (FMT != kKvBf16) {
+        float f[4], g[4];
+        codes_to_f32<FMT>(v.x, f);
+        codes_to_f32<FMT>(v.y, g);
+        const float sc = s[j][h];
+        v = make_uint4(pack_bf16x2(f[0] * sc, f[1] * sc), pack_bf16x2(f[2] * sc, f[3] * sc),
+                       pack_bf16x2(g[0] * sc, g[1] * sc), pack_bf16x2(g[2] * sc, g[3] * sc));
+      }
+      *reinterpret_cast<uint4*>((h ? p.v_out + row[j] * p.v_stride : p.k_out + row[j] * p.k_stride) + col) = v;
+    }
+  }
 }
 
 namespace {
 
 template <class K>
-int launch_rows(K kernel, const KvRowsArgs& a, void* stream) {
-  const long long threads = static_cast<long long>(a.n) * a.c.kv_heads * (a.head_dim / 8);
+int launch_rows(K kernel, int pieces, const KvRowsArgs& a, void* stream) {
+  const long long units = static_cast<long long>(a.n) * a.c.kv_heads, per = kRowThreads * pieces / (a.head_dim / 8);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((threads + kRowThreads - 1) / kRowThreads), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((units + per - 1) / per), 1, 1);
   cfg.blockDim = dim3(kRowThreads, 1, 1);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
@@ -166,23 +215,35 @@ int launch_rows(K kernel, const KvRowsArgs& a, void* stream) {
   return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, a));
 }
 
+// One piece a thread while the call is too small to fill the GPU's 152 x 2048 threads twice, else kMany.
+bool many(const KvRowsArgs& a) { return static_cast<long long>(a.n) * a.c.kv_heads * (a.head_dim / 8) >= 2LL * 152 * 2048; }
+
+template <int FMT, int D>
+int launch_write(const KvRowsArgs& a, void* stream) {
+  return many(a) ? launch_rows(kv_write_kernel<FMT, D, kMany>, kMany, a, stream) : launch_rows(kv_write_kernel<FMT, D, 1>, 1, a, stream);
+}
+template <int FMT, int D>
+int launch_read(const KvRowsArgs& a, void* stream) {
+  return many(a) ? launch_rows(kv_read_kernel<FMT, D, kMany>, kMany, a, stream) : launch_rows(kv_read_kernel<FMT, D, 1>, 1, a, stream);
+}
+
 }  // namespace
 
 int launch_kv_write(const KvRowsArgs& a, void* stream) {
   const bool wide = a.head_dim == 128;
   switch (a.format) {
-    case kKvBf16: return wide ? launch_rows(kv_write_kernel<kKvBf16, 128>, a, stream) : launch_rows(kv_write_kernel<kKvBf16, 64>, a, stream);
-    case kKvE4m3: return wide ? launch_rows(kv_write_kernel<kKvE4m3, 128>, a, stream) : launch_rows(kv_write_kernel<kKvE4m3, 64>, a, stream);
-    default: return wide ? launch_rows(kv_write_kernel<kKvInt8, 128>, a, stream) : launch_rows(kv_write_kernel<kKvInt8, 64>, a, stream);
+    case kKvBf16: return wide ? launch_write<kKvBf16, 128>(a, stream) : launch_write<kKvBf16, 64>(a, stream);
+    case kKvE4m3: return wide ? launch_write<kKvE4m3, 128>(a, stream) : launch_write<kKvE4m3, 64>(a, stream);
+    default: return wide ? launch_write<kKvInt8, 128>(a, stream) : launch_write<kKvInt8, 64>(a, stream);
   }
 }
 
 int launch_kv_read(const KvRowsArgs& a, void* stream) {
   const bool wide = a.head_dim == 128;
   switch (a.format) {
-    case kKvBf16: return wide ? launch_rows(kv_read_kernel<kKvBf16, 128>, a, stream) : launch_rows(kv_read_kernel<kKvBf16, 64>, a, stream);
-    case kKvE4m3: return wide ? launch_rows(kv_read_kernel<kKvE4m3, 128>, a, stream) : launch_rows(kv_read_kernel<kKvE4m3, 64>, a, stream);
-    default: return wide ? launch_rows(kv_read_kernel<kKvInt8, 128>, a, stream) : launch_rows(kv_read_kernel<kKvInt8, 64>, a, stream);
+    case kKvBf16: return wide ? launch_read<kKvBf16, 128>(a, stream) : launch_read<kKvBf16, 64>(a, stream);
+    case kKvE4m3: return wide ? launch_read<kKvE4m3, 128>(a, stream) : launch_read<kKvE4m3, 64>(a, stream);
+    default: return wide ? launch_read<kKvInt8, 128>(a, stream) : launch_read<kKvInt8, 64>(a, stream);
   }
 }
 

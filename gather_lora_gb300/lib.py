@@ -142,10 +142,24 @@ def _addr(v):
     return v.data_ptr() or None       # torch tensor
 
 
+_current = None
+
+
+def _current_stream():
+    """torch's current stream as an integer. torch.cuda.current_stream() builds an object and looks the
+    device up by name, 3 us a call; the raw lookup behind it takes 0.2."""
+    global _current
+    if _current is None:
+        import torch
+        torch.cuda.current_stream()   # initialises CUDA
+        raw, device = (getattr(torch._C, f, None) for f in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        _current = (lambda: raw(device())) if raw and device else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _current()
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream or None
+        return _current_stream() or None
     if isinstance(s, int):
         return s or None
     return s.cuda_stream or None      # torch.cuda.Stream
