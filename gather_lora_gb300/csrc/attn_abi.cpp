@@ -38,6 +38,14 @@ int check_scale(float scale) {
   return std::isfinite(scale) && scale > 0.f ? LORA_OK : fail(LORA_ERR_SIZE, "scale %g is not positive and finite", (double)scale);
 }
 
+// log2 of v (>= 1), or -1 if v is no power of two.
+int log2_or(int32_t v) {
+  if (v & (v - 1)) return -1;
+  int s = 0;
+  while ((int64_t{1} << s) < v) ++s;
+  return s;
+}
+
 // The cache's description, checked; `c` gets the kernels' view of it.
 int check_cache(const lora_kv_cache* cache, glora::KvView& c) {
   if (!cache) return fail(LORA_ERR_NULL, "cache is NULL");
@@ -93,9 +101,7 @@ int kv_rows(const void* k, int64_t k_row_stride, const void* v, int64_t v_row_st
   a.n = n;
   a.head_dim = cache->head_dim;
   a.format = cache->format;
-  a.page_shift = -1;
-  if ((cache->page_size & (cache->page_size - 1)) == 0)
-    for (a.page_shift = 0; (1 << a.page_shift) < cache->page_size;) ++a.page_shift;
+  a.page_shift = log2_or(cache->page_size);
   a.heads_magic = static_cast<uint32_t>(((1ull << 32) + cache->kv_heads - 1) / cache->kv_heads);
   return LORA_OK;
 }
@@ -164,6 +170,7 @@ int lora_attn_decode(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* ou
   a.q_heads = q_heads;
   a.head_dim = cache->head_dim;
   a.format = cache->format;
+  a.page_shift = log2_or(cache->page_size);
   a.scale = scale;
   const int rc = glora::launch_decode(a, stream);
   return rc ? cuda_fail(rc, "lora_attn_decode launch") : ok();

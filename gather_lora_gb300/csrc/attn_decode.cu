@@ -156,6 +156,13 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs& p, int b, int& len) {
   return (len - 1) / TOK + (len > 0 ? 1 : 0);
 }
 
+// a * b / d, in 32 bits where the product fits (a 64-bit division is a call of a hundred instructions).
+__device__ __forceinline__ long long mul_div(long long a, long long b, long long d) {
+  const unsigned long long ab = static_cast<unsigned long long>(a) * static_cast<unsigned long long>(b);
+  if (((ab | static_cast<unsigned long long>(d)) >> 32) == 0) return static_cast<uint32_t>(ab) / static_cast<uint32_t>(d);
+  return static_cast<long long>(ab / static_cast<unsigned long long>(d));
+}
+
 // Next segment that has tiles (the caller knows there is one).
 template <int TOK>
 __device__ __forceinline__ void next_segment(const DecodeArgs& p, int subs, Walk& w) {
@@ -177,6 +184,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
   __shared__ long long s_sum[kDecWarps];
   __shared__ int s_b, s_sub, s_tiles, s_len, s_tile0, s_last;
   __shared__ float s_m[kDecWarps][kRows], s_l[kDecWarps][kRows];
+  __shared__ float s_jm[kJoinGroup * kRows], s_jl[kJoinGroup * kRows];
   __shared__ uint64_t s_live[kDecWarps][kStages];     // valid tokens of each stage
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3;
   float* const s_o = reinterpret_cast<float*>(smem + kDecWarps * kStages * T::stage_bytes);   // two buffers of D / 8 / R accumulator tiles
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
     zero_empty();
     return;
   }
-  const long long u0 = c * total / n, u1 = (c + 1) * total / n;
+  const long long u0 = mul_div(c, total, n), u1 = mul_div(c + 1, total, n);
   if (u0 >= before && u0 < before + mine) {   // this thread's sequences hold u0
     long long at = before;
     for (int b = b0; b < b1; ++b) {
@@ -237,8 +245,8 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
         s_b = b;
         s_tiles = t;
         s_len = len;
-        s_sub = static_cast<int>((u0 - at) / t);
-        s_tile0 = static_cast<int>((u0 - at) % t);
+        s_sub = static_cast<int>(mul_div(u0 - at, 1, t));
+        s_tile0 = static_cast<int>(u0 - at - static_cast<long long>(s_sub) * t);
         break;
       }
       at += span;
@@ -277,7 +285,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
       page[j] = -1;
       slot[j] = 0;
       if (i < TOK && t < lw.len) {
-        const int e = t / p.c.page_size;
+        const int e = p.page_shift >= 0 ? t >> p.page_shift : t / p.c.page_size;
         slot[j] = t - e * p.c.page_size;
         page[j] = __ldg(p.table + lw.b * p.table_stride + e);
       }
@@ -606,29 +614,46 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
       // The segment's CTAs c0 .. c1, in groups of kJoinGroup; slot of CTA x: its part either starts
       // the segment (x == c0: slot 2 x + 1) or goes on with it (slot 2 x).
       const long long s0 = u - ta, s1 = s0 + w.tiles - 1;
-      const int c0 = static_cast<int>(((s0 + 1) * n - 1) / total), c1 = static_cast<int>(((s1 + 1) * n - 1) / total);
+      auto cta_of = [&](long long unit) {   // the last x with x * total / n <= unit: ((unit + 1) n - 1) / total
+        const long long v = (unit + 1) * n - 1;
+        return static_cast<int>(mul_div(v, 1, total));
+      };
+      const int c0 = cta_of(s0), c1 = cta_of(s1);
       const int groups = (c1 - c0) / kJoinGroup + 1, gi = (c - c0) / kJoinGroup;
       // Joins slots first, first + step, ..; the result goes to the output, or in place into slot `first`.
+      // All loads of a thread are in flight together: one trip to L2 for up to kJoinGroup parts.
       auto join = [&](int first_cta, int count, int step, bool last) {
         auto slot_of = [&](int x) { return slots + static_cast<long long>(2 * x + (x == c0)) * SF; };
+        for (int i = tid; i < count * kRows; i += kDecThreads) {
+          const float* const from = slot_of(first_cta + (i / kRows) * step) + i % kRows;
+          s_jm[i] = i % kRows < rows ? __ldcg(from) : -INFINITY;
+          s_jl[i] = i % kRows < rows ? __ldcg(from + kRows) : 0.f;
+        }
+        __syncthreads();
         // thread: 4 consecutive dimensions of one row at a time
         for (int i = tid; i < rows * D / 4; i += kDecThreads) {
           const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
+          float4 v[kJoinGroup];
+#pragma unroll
+          for (int x = 0; x < kJoinGroup; ++x) {
+            v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x < count) v[x] = __ldcg(reinterpret_cast<const float4*>(slot_of(first_cta + x * step) + 2 * kRows + row * D + d));
+          }
           float mm = -INFINITY;
-          for (int x = 0; x < count; ++x) mm = fmaxf(mm, __ldcg(slot_of(first_cta + x * step) + row));
+          for (int x = 0; x < count; ++x) mm = fmaxf(mm, s_jm[x * kRows + row]);
           const float ref = mm == -INFINITY ? 0.f : mm;
           float ll = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int x = 0; x < count; ++x) {
-            const float* const from = slot_of(first_cta + x * step);
-            const float f = exp2_fast(__ldcg(from + row) - ref);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(from + 2 * kRows + row * D + d));
-            ll += __ldcg(from + kRows + row) * f;
-            acc.x += v.x * f;
-            acc.y += v.y * f;
-            acc.z += v.z * f;
-            acc.w += v.w * f;
+#pragma unroll
+          for (int x = 0; x < kJoinGroup; ++x) {
+            if (x < count) {
+              const float f = exp2_fast(s_jm[x * kRows + row] - ref);
+              ll += s_jl[x * kRows + row] * f;
+              acc.x += v[x].x * f;
+              acc.y += v[x].y * f;
+              acc.z += v[x].z * f;
+              acc.w += v[x].w * f;
+            }
           }
           if (last) {
             const float f = ll == 0.f ? 0.f : 1.f / ll;
@@ -639,33 +664,24 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
           } else {
             float* const to = slot_of(first_cta);
             *reinterpret_cast<float4*>(to + 2 * kRows + row * D + d) = acc;
-            // (m and l of the row are read by its other threads: written after the barrier below)
-            if (d == 0) {
-              s_m[0][row] = mm;
-              s_l[0][row] = ll;
+            if (d == 0) {   // (m and l were read before the barrier above)
+              to[row] = mm;
+              to[kRows + row] = ll;
             }
-          }
-        }
-        if (!last) {
-          __syncthreads();
-          if (tid < rows) {
-            slot_of(first_cta)[tid] = s_m[0][tid];
-            slot_of(first_cta)[kRows + tid] = s_l[0][tid];
           }
         }
       };
       // Arrive at a counter; true in the CTA that is the last of `count`, which sets it back to 0.
       auto last_of = [&](int* counter, int count) {
-        __threadfence();
         __syncthreads();
-        if (tid == 0) {
-          s_last = atomicAdd(counter, 1) == count - 1;
+        if (tid == 0) {   // releases the CTA's writes before the barrier, acquires those of the CTAs before it
+          int seen;
+          asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;\n" : "=r"(seen) : "l"(counter) : "memory");
+          s_last = seen == count - 1;
           if (s_last) *counter = 0;
         }
         __syncthreads();
-        const bool yes = s_last != 0;
-        if (yes) __threadfence();
-        return yes;
+        return s_last != 0;
       };
       const int first = c0 + gi * kJoinGroup, count = min(kJoinGroup, c1 - first + 1);
       if (last_of(counters + (gi ? kMaxCtas : 0) + first, count)) {

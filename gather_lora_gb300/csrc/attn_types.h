@@ -46,6 +46,7 @@ struct DecodeArgs {
   float* lse;
   void* workspace;
   int batch, q_heads, head_dim, format;
+  int page_shift;            // log2 of page_size, or -1: not a power of two
   float scale;
 };
 
