@@ -17,7 +17,8 @@
 // the other's P V and the next Q K^T run. Warp 8 issues the MMAs, warp 9 picks the items and issues TMA: K and
 // V tiles of 128 keys through one ring of stages, the next item's Q as soon as the last Q K^T has read the old
 // (warps 10 and 11 only complete the warpgroup that gives its registers to the softmax).
-// Tensor memory: S0, S1 (128 columns each; P as BF16 pairs over the first half of its S), O0, O1.
+// Tensor memory: two (D = 128) or three (D = 64) score buffers of 128 columns, P as BF16 pairs over the first
+// half of its scores, and O0, O1.
 //
 // Softmax: exponents are base 2. The reference that exponents are relative to follows the running maximum
 // only when that has grown by more than 2^8 (one vote per warp): then l and O are multiplied by
@@ -26,8 +27,14 @@
 // Rounding to fewer bits: the weights to BF16 before P V (the tensor cores' operand type), the output once.
 // Keys that a row does not see get weight zero, but zero times NaN or infinity in their V rows is NaN in
 // an MMA: a row whose result is not finite is computed again key by key over its own keys (attn_row.cuh).
+#include <cooperative_groups.h>
+
+#include <type_traits>
+
 #include "attn_row.cuh"
 #include "tc05.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace glora {
 
@@ -40,12 +47,11 @@ constexpr int kTile = 128;                      // rows of a tile, keys of a til
 constexpr int kSoftmaxWarps = 8;
 constexpr int kPreMmaWarp = 8, kPreTmaWarp = 9;
 constexpr int kPreThreads = 384;
-// Registers a thread: 168 at launch (65536 over 12 warps); the helper warpgroup gives 80 away, the softmax
-// warpgroups hold a whole row of scores: 2 * 208 + 88 = 3 * 168.
-constexpr int kHelperRegs = 88, kSoftmaxRegs = 208;
+// Registers a thread: 168 at launch (65536 over 12 warps); the helper warpgroup gives 96 away, the softmax
+// warpgroups hold a whole row of scores: 2 * 216 + 72 = 3 * 168.
+constexpr int kHelperRegs = 72, kSoftmaxRegs = 216;
 constexpr int kOutBytes = 4096;                 // staging of a warp's results: 32 rows x 64 columns
 constexpr int kItems = 4;                       // depth of the item ring
-constexpr uint32_t kColO = 256;                 // tensor memory: S at 0 and 128, O at 256 and 384
 constexpr float kRescale = 8.f;                 // reference moves when the maximum grew by 2^8
 
 template <int D>
@@ -53,6 +59,10 @@ struct PrefillShape {
   static constexpr int atoms = D / 64;                          // 64-column boxes of a tile
   static constexpr int tile_bytes = kTile * D * 2;              // Q row tile, K tile or V tile
   static constexpr int stages = D == 128 ? 4 : 8;
+  static constexpr int bufs = D == 128 ? 2 : 3;                 // score buffers in tensor memory: what O0 and O1 leave
+  static constexpr uint32_t col_o = 512 - 2 * D;                // columns: scores at 0, 128 (, 256), O0, O1 at the end
+  // Score buffer of row tile i and key tile j.
+  static __device__ __forceinline__ uint32_t buf(int i, int j) { return bufs == 2 ? i : (2u * j + i) % 3u; }
   static constexpr int smem = (2 + stages) * tile_bytes + kSoftmaxWarps * kOutBytes + 2048;   // + control, alignment
 };
 
@@ -60,14 +70,15 @@ struct PrefillItem {
   int valid;
   int q0, k0;          // first query row of the item, first key row of its sequence
   int tok0, lq, lk;    // first token of the item in the sequence; the sequence's rows and keys
-  int n[2];            // key tiles of each row tile
+  int n[2];            // key tiles of each row tile (split: of this CTA's part of the keys)
+  int shift;           // keys of the sequence before the first of them (0 unless split)
   int h0, heads, kvh;  // first query head, how many, key-value head
 };
 
 struct PrefillCtl {
   unsigned long long full[8], empty[8];
   unsigned long long q_full, q_empty;
-  unsigned long long s_full[2], p_ready[2][2], o_full[2];   // (p_ready: halves of the keys)
+  unsigned long long s_full[2][2], p_ready[2][2][2], o_done[2][2];   // [row tile][parity of its key tile] ([half])
   unsigned long long item_full[kItems], item_empty[kItems];
   unsigned long long drain, next_full;
   uint4 next;                          // the answer to ask_next_block
@@ -77,25 +88,24 @@ struct PrefillCtl {
 };
 static_assert(sizeof(PrefillCtl) <= 1024, "control block");
 
-// Bounded wait; once one wait of the CTA has run out, all others end at once.
+__device__ __forceinline__ bool failed(const PrefillCtl& c) { return *reinterpret_cast<const volatile int*>(&c.failed) != 0; }
+
+// Bounded wait; true if it ran out. Once one has, all others of the CTA end at once, the roles leave their
+// loops at the next point where their warp is together, nothing more is stored and no further item is taken
+// (what runs on until then stays in bounds).
 __device__ __forceinline__ bool pre_wait(PrefillCtl& c, unsigned long long& bar, uint32_t parity) {
   const uint32_t b = smem_u32(&bar);
-  if (mbar_try_wait(b, parity, 100000)) return true;
+  if (mbar_try_wait(b, parity, 100000)) return false;
   const long long t0 = clock64();
   while (!mbar_try_wait(b, parity, 100000)) {
-    if (*reinterpret_cast<volatile int*>(&c.failed)) return false;
+    if (failed(c)) return true;
     if (clock64() - t0 > kWaitLimitCycles) {
       *reinterpret_cast<volatile int*>(&c.failed) = 1;
       atomicOr(&g_prefill_status, kPrefillTimeoutBit);
-      return false;
+      return true;
     }
   }
-  return true;
-}
-
-// The same for a whole warp, which goes on or gives up together.
-__device__ __forceinline__ bool warp_wait(PrefillCtl& c, unsigned long long& bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, pre_wait(c, bar, parity));
+  return false;
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int c0, int c1, int c2, uint32_t bar) {
@@ -159,7 +169,26 @@ __device__ __forceinline__ long long next_block(uint32_t from) {
 
 }  // namespace
 
+// Query row r, head h, over its first `keys` keys from row k0 on, by one warp: result and lse.
 template <int D>
+__device__ __noinline__ void row_again(const PrefillArgs& p, int r, int h, int kvh, int k0, int keys, float sl2, int lane) {
+  constexpr int E = D / 32;
+  RowState<D> st;
+  st.begin(p.q + r * p.q_stride + h * D, sl2, lane);
+  for (int j = 0; j < keys; ++j) {
+    float k[E], v[E];
+    load_bf16<E>(p.k + (k0 + j) * p.k_stride + kvh * D + lane * E, k);
+    load_bf16<E>(p.v + (k0 + j) * p.v_stride + kvh * D + lane * E, v);
+    st.add(k, v);
+  }
+  for (int e = 0; e < E; ++e)
+    p.out[r * p.out_stride + h * D + lane * E + e] = f32_to_bf16_bits(st.l == 0.f ? 0.f : st.acc[e] / st.l);
+  if (p.lse && lane == 0) p.lse[static_cast<long long>(r) * p.q_heads + h] = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
+}
+
+// SPLIT: a cluster of CTAs takes one item, each an equal part of its key tiles, and joins through the others'
+// shared memory; otherwise a CTA takes items one after the other.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs p) {
   using Sh = PrefillShape<D>;
   constexpr int NS = Sh::stages;
@@ -169,6 +198,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
   const uint32_t out_s = ring + NS * Sh::tile_bytes;
   PrefillCtl& c = *reinterpret_cast<PrefillCtl*>(prefill_smem_raw + pad + (2 + NS) * Sh::tile_bytes + kSoftmaxWarps * kOutBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int parts = SPLIT ? static_cast<int>(cluster.num_blocks()) : 1, part = SPLIT ? static_cast<int>(cluster.block_rank()) : 0;
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -177,11 +208,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     }
     mbar_init(smem_u32(&c.q_full), 1);
     mbar_init(smem_u32(&c.q_empty), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&c.s_full[i]), 1);
-      mbar_init(smem_u32(&c.p_ready[i][0]), 4);
-      mbar_init(smem_u32(&c.p_ready[i][1]), 4);
-      mbar_init(smem_u32(&c.o_full[i]), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&c.s_full[i >> 1][i & 1]), 1);
+      mbar_init(smem_u32(&c.p_ready[i >> 1][i & 1][0]), 4);
+      mbar_init(smem_u32(&c.p_ready[i >> 1][i & 1][1]), 4);
+      mbar_init(smem_u32(&c.o_done[i >> 1][i & 1]), 1);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(smem_u32(&c.item_full[i]), 1);
@@ -203,6 +234,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
 
   pdl_wait_then_release();
 
+  int met = 0;           // cluster barriers this thread has passed
   const int TT = p.tile_tokens, step = 2 * TT, GB = p.head_block;
   const int G = p.q_heads / p.kv_heads, blocks = (G + GB - 1) / GB, subs = p.kv_heads * blocks;
 
@@ -219,7 +251,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       mbar_arrive_expect_tx(smem_u32(&c.next_full), 16);
       ask_next_block(smem_u32(&c.next), smem_u32(&c.next_full));
     };
-    for (long long idx = blockIdx.x; go; ++it) {
+    for (long long idx = blockIdx.x / parts; go; ++it) {
       // Item idx (-1: none): sequences in order, within one its last rows (the most keys) first, heads fastest.
       const long long x = idx < 0 ? -1 : idx / subs;
       const int sub = idx < 0 ? 0 : static_cast<int>(idx - x * subs);
@@ -259,12 +291,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       go = tile >= 0;
       if (lane == 0) {
         const int sl = it % kItems;
-        if (it >= kItems) go = pre_wait(c, c.item_empty[sl], ((it / kItems) - 1) & 1) && go;
+        if (it >= kItems) pre_wait(c, c.item_empty[sl], ((it / kItems) - 1) & 1);
+        go = go && !failed(c);
         PrefillItem w;
         w.valid = go;
         w.tok0 = tile * step;
         w.q0 = q0 + w.tok0;
-        w.k0 = k0;
         w.lq = lq;
         w.lk = lk;
 #pragma unroll
@@ -273,47 +305,53 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
           const int keys = min(lk, last + lk - lq);
           w.n[i] = first < lq && keys > 0 ? (keys - 1) / kTile + 1 : 0;
         }
+        if constexpr (SPLIT) {
+          const long long all = max(w.n[0], w.n[1]);
+          const int from = static_cast<int>(part * all / parts), to = static_cast<int>((part + 1) * all / parts);
+          w.n[0] = max(0, min(w.n[0], to) - from);
+          w.n[1] = max(0, min(w.n[1], to) - from);
+          w.shift = from * kTile;
+        } else {
+          w.shift = 0;
+        }
+        w.k0 = k0 + w.shift;
         w.kvh = sub / blocks;
         w.h0 = w.kvh * G + (sub - w.kvh * blocks) * GB;
         w.heads = min(GB, w.kvh * G + G - w.h0);
         c.item[sl] = w;
         mbar_arrive(smem_u32(&c.item_full[sl]));
         const int n = max(w.n[0], w.n[1]);
-        bool asked = go && n == 0;
+        bool asked = !SPLIT && go && n == 0;
         if (asked) ask();
         if (go && n > 0) {
-          if (items > 0) go = pre_wait(c, c.q_empty, (items - 1) & 1);
+          if (items > 0) pre_wait(c, c.q_empty, (items - 1) & 1);
           ++items;
-          if (go) {
-            const uint32_t fb = smem_u32(&c.q_full);
-            mbar_arrive_expect_tx(fb, 2 * Sh::atoms * GB * TT * 128);
+          const uint32_t qb = smem_u32(&c.q_full);
+          mbar_arrive_expect_tx(qb, 2 * Sh::atoms * GB * TT * 128);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int a = 0; a < Sh::atoms; ++a)
-                tma_load_3d(q_s + i * Sh::tile_bytes + a * (kTile * 128), &p.map_q, a * 64, w.h0, w.q0 + i * TT, fb);
-          }
-          for (int j = 0; go && j < 2 * n; ++j) {      // K0 V0 K1 V1 ..
-            if (j == 2 * n - 2) {
+            for (int a = 0; a < Sh::atoms; ++a)
+              tma_load_3d(q_s + i * Sh::tile_bytes + a * (kTile * 128), &p.map_q, a * 64, w.h0, w.q0 + i * TT, qb);
+          for (int j = 0; j < 2 * n; ++j) {      // K0 V0 K1 V1 ..
+            if (!SPLIT && j == 2 * n - 2) {
               ask();
               asked = true;
             }
             const uint32_t s = kv % NS;
-            if (kv >= NS && !pre_wait(c, c.empty[s], ((kv / NS) - 1) & 1)) {
-              go = false;
-              break;
-            }
+            if (kv >= NS && pre_wait(c, c.empty[s], ((kv / NS) - 1) & 1)) break;
             ++kv;
             const uint32_t fb = smem_u32(&c.full[s]), to = ring + s * Sh::tile_bytes;
             mbar_arrive_expect_tx(fb, Sh::tile_bytes);
 #pragma unroll
             for (int a = 0; a < Sh::atoms; ++a)
-              tma_load_2d(to + a * (kTile * 128), (j & 1) ? &p.map_v : &p.map_k, w.kvh * D + a * 64, k0 + (j >> 1) * kTile, fb);
+              tma_load_2d(to + a * (kTile * 128), (j & 1) ? &p.map_v : &p.map_k, w.kvh * D + a * 64, w.k0 + (j >> 1) * kTile, fb);
           }
         }
         if (asked) {
-          const bool told = pre_wait(c, c.next_full, it & 1) || mbar_wait_limit(smem_u32(&c.next_full), it & 1, kDrainLimitCycles);
-          idx = told ? next_block(smem_u32(&c.next)) : -1;
+          pre_wait(c, c.next_full, it & 1);
+          if (failed(c)) mbar_wait_limit(smem_u32(&c.next_full), it & 1, kDrainLimitCycles);
+          idx = failed(c) ? -1 : next_block(smem_u32(&c.next));
         } else {
           idx = -1;
         }
@@ -321,7 +359,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       idx = __shfl_sync(0xffffffffu, idx, 0);
       go = __shfl_sync(0xffffffffu, go, 0);
     }
-    if (lane == 0 && *reinterpret_cast<volatile int*>(&c.failed)) {   // let the loads in flight land
+    if (lane == 0 && failed(c)) {        // let the loads in flight land
       for (uint32_t k = kv > NS ? kv - NS : 0; k < kv; ++k)
         mbar_wait_limit(smem_u32(&c.full[k % NS]), (k / NS) & 1, kDrainLimitCycles);
       if (items > 0) mbar_wait_limit(smem_u32(&c.q_full), (items - 1) & 1, kDrainLimitCycles);
@@ -329,77 +367,99 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     __syncwarp();
   } else if (warp == kPreMmaWarp) {
     // ============================ MMA issue ===============================
-    // (the whole warp takes every step, one elected lane issues)
+    // The whole warp takes every step, one elected lane issues. Row tile i's scores of key tile j + 1 go out
+    // after its P V of key tile j when there are two score buffers (one per row tile), so a warpgroup waits for
+    // both; with three buffers they go out half a step earlier and are there when it is done with its weights.
     constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile);
     constexpr uint32_t id_o = idesc_bf16_f32(kTile, D) | (1u << 16);   // V: MN-major
-    uint32_t kv = 0, pc = 0;             // pc: bit i, the phase of p_ready[i] to wait for
-    int items = 0;
-    auto scores = [&](int i, uint32_t s) {             // S_i = Q_i K^T, K in stage s
+    uint32_t kv = 0, st[2] = {0, 0}, pt[2] = {0, 0};   // ring tiles of the items before; key tiles by row tile: scores, P V
+    int items = 0, n0 = 0, n1 = 0, n = 0;
+    bool dead = false;
+    auto scores = [&](auto row_tile, int j) {          // S_i = Q_i K_j^T
+      constexpr int i = decltype(row_tile)::value;
+      const uint32_t k = kv + 2 * j, ks = k % NS;
+      if (Sh::bufs == 3 && (i == 0 || j >= n0)) {
+        dead |= pre_wait(c, c.full[ks], (k / NS) & 1);    // the key tile's first use
+        __syncwarp();
+        tc_fence_after();
+      }
       const uint64_t qa = smem_desc(q_s + i * Sh::tile_bytes, 1024, Swz::k128);
-      const uint64_t ka = smem_desc(ring + s * Sh::tile_bytes, 1024, Swz::k128);
+      const uint64_t ka = smem_desc(ring + ks * Sh::tile_bytes, 1024, Swz::k128);
+      const uint32_t to = tmem + Sh::buf(i, j) * kTile;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {            // (descriptors hold addresses in 16-byte units)
         const uint64_t o = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
-        umma_bf16_warp(tmem + i * kTile, qa + o, ka + o, id_s, kk != 0);
+        umma_bf16_warp(to, qa + o, ka + o, id_s, kk != 0);
       }
-      umma_commit_warp(smem_u32(&c.s_full[i]));
+      umma_commit_warp(smem_u32(&c.s_full[i][st[i] & 1]));
+      ++st[i];
+      if (i == 1 || j >= n1) {                         // and its last
+        umma_commit_warp(smem_u32(&c.empty[ks]));
+        if (j + 1 == n) umma_commit_warp(smem_u32(&c.q_empty));
+      }
     };
-    auto values = [&](int i, uint32_t s, int half, bool add) {   // O_i (+)= P_i V over half of the keys, V in stage s
-      const uint64_t va = smem_desc_mn128(ring + s * Sh::tile_bytes + half * (kTile / 2 * 128), kTile * 128, 1024);
+    auto values = [&](auto row_tile, int j, uint32_t vs) {   // O_i (+)= P_i V_j, as its halves of the keys come
+      constexpr int i = decltype(row_tile)::value;
+      const uint64_t va = smem_desc_mn128(ring + vs * Sh::tile_bytes, kTile * 128, 1024);
+      const uint32_t from = tmem + Sh::buf(i, j) * kTile;
 #pragma unroll
-      for (int kk = 0; kk < kTile / 32; ++kk)
-        umma_bf16_ts_warp(tmem + kColO + i * kTile, tmem + i * kTile + half * (kTile / 4) + kk * 8, va + kk * (2048 >> 4), id_o,
-                          kk != 0 || add);
+      for (int half = 0; half < 2; ++half) {
+        if (Sh::bufs == 2 || half == 0) {
+          dead |= pre_wait(c, c.p_ready[i][pt[i] & 1][Sh::bufs == 2 ? half : 1], (pt[i] >> 1) & 1);
+          __syncwarp();
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int kk = half * (kTile / 32); kk < (half + 1) * (kTile / 32); ++kk)
+          umma_bf16_ts_warp(tmem + Sh::col_o + i * D, from + kk * 8, va + kk * (2048 >> 4), id_o, kk != 0 || j != 0);
+      }
+      umma_commit_warp(smem_u32(&c.o_done[i][pt[i] & 1]));
+      ++pt[i];
     };
-    bool go = true;
-    for (int it = 0; go; ++it) {
+    constexpr std::integral_constant<int, 0> r0{};
+    constexpr std::integral_constant<int, 1> r1{};
+    for (int it = 0;; ++it) {
       const int sl = it % kItems;
-      go = warp_wait(c, c.item_full[sl], (it / kItems) & 1);
-      if (!go) break;
-      const bool valid = __shfl_sync(0xffffffffu, c.item[sl].valid, 0);
-      const int n0 = __shfl_sync(0xffffffffu, c.item[sl].n[0], 0), n1 = __shfl_sync(0xffffffffu, c.item[sl].n[1], 0), n = max(n0, n1);
+      pre_wait(c, c.item_full[sl], (it / kItems) & 1);
       __syncwarp();
+      const bool valid = __shfl_sync(0xffffffffu, c.item[sl].valid && !failed(c), 0);
+      n0 = __shfl_sync(0xffffffffu, c.item[sl].n[0], 0);
+      n1 = __shfl_sync(0xffffffffu, c.item[sl].n[1], 0);
+      n = max(n0, n1);
       if (lane == 0) mbar_arrive(smem_u32(&c.item_empty[sl]));
       __syncwarp();
       if (!valid) break;
       if (n == 0) continue;
-      go = warp_wait(c, c.q_full, items & 1) && warp_wait(c, c.full[kv % NS], (kv / NS) & 1);
+      pre_wait(c, c.q_full, items & 1);
       ++items;
-      if (!go) break;
-      tc_fence_after();
-      if (n0 > 0) scores(0, kv % NS);
-      if (n1 > 0) scores(1, kv % NS);
-      umma_commit_warp(smem_u32(&c.empty[kv % NS]));
-      ++kv;
-      if (n == 1) umma_commit_warp(smem_u32(&c.q_empty));
-      for (int j = 0; go && j < n; ++j) {
-        const uint32_t vs = kv % NS, ks = (kv + 1) % NS;
-        go = warp_wait(c, c.full[vs], (kv / NS) & 1) && (j + 1 == n || warp_wait(c, c.full[ks], ((kv + 1) / NS) & 1));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int ni = i ? n1 : n0;
-          if (go && j < ni) {
-            go = warp_wait(c, c.p_ready[i][0], (pc >> i) & 1);
-            if (!go) break;
-            tc_fence_after();
-            values(i, vs, 0, j != 0);
-            go = warp_wait(c, c.p_ready[i][1], (pc >> i) & 1);
-            if (!go) break;
-            tc_fence_after();
-            values(i, vs, 1, true);
-            pc ^= 1u << i;
-            if (j + 1 == ni) umma_commit_warp(smem_u32(&c.o_full[i]));
-          }
-          if (go && j + 1 < ni) scores(i, ks);
-        }
-        if (!go) break;
-        umma_commit_warp(smem_u32(&c.empty[vs]));
-        if (j + 1 < n) umma_commit_warp(smem_u32(&c.empty[ks]));
-        if (j + 2 == n) umma_commit_warp(smem_u32(&c.q_empty));   // the item's last scores are issued
-        kv += j + 1 < n ? 2 : 1;
+      if constexpr (Sh::bufs == 2) {
+        dead |= pre_wait(c, c.full[kv % NS], (kv / NS) & 1);
+        __syncwarp();
+        tc_fence_after();
       }
+      if (n0 > 0) scores(r0, 0);
+      if (n1 > 0) scores(r1, 0);
+      if (Sh::bufs == 3 && n0 > 1) scores(r0, 1);
+      for (int j = 0; j < n; ++j) {
+        const uint32_t v = kv + 2 * j + 1, vs = v % NS;
+        dead |= pre_wait(c, c.full[vs], (v / NS) & 1);
+        if (Sh::bufs == 2 && j + 1 < n) dead |= pre_wait(c, c.full[(v + 1) % NS], ((v + 1) / NS) & 1);
+        __syncwarp();
+        if (j < n0) values(r0, j, vs);
+        if (Sh::bufs == 2 ? j + 1 < n0 : j + 1 < n1) {
+          if constexpr (Sh::bufs == 2) scores(r0, j + 1); else scores(r1, j + 1);
+        }
+        if (j < n1) values(r1, j, vs);
+        umma_commit_warp(smem_u32(&c.empty[vs]));
+        if (Sh::bufs == 2 ? j + 1 < n1 : j + 2 < n0) {
+          if constexpr (Sh::bufs == 2) scores(r1, j + 1); else scores(r0, j + 2);
+        }
+        if (__any_sync(0xffffffffu, dead)) break;
+      }
+      kv += 2 * n;
     }
-    if (!go) {                           // let the MMAs in flight end
+    if (failed(c)) {                     // let the MMAs in flight end
+      __syncwarp();
       umma_commit_warp(smem_u32(&c.drain));
       mbar_wait_limit(smem_u32(&c.drain), 0, kDrainLimitCycles);
     }
@@ -410,27 +470,30 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     // ============================= softmax ================================
     const int i = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t col_s = lane_base + i * kTile, col_o = lane_base + kColO + i * kTile;
+    const uint32_t col_o = lane_base + Sh::col_o + i * D;
     const float sl2 = p.scale * kLog2e, grow = kRescale / sl2;
     const int t_in = row / GB, g = row - t_in * GB;
-    uint32_t sc = 0, oc = 0;
+    bool dead = false;
+    uint32_t t = 0;                      // key tiles of this row tile so far, over the items
     for (int it = 0;; ++it) {
       const int sl = it % kItems;
-      if (!warp_wait(c, c.item_full[sl], (it / kItems) & 1)) break;
-      const PrefillItem w = c.item[sl];
+      pre_wait(c, c.item_full[sl], (it / kItems) & 1);
       __syncwarp();
+      const PrefillItem w = c.item[sl];
+      const bool valid = __shfl_sync(0xffffffffu, w.valid && !failed(c), 0);
       if (lane == 0) mbar_arrive(smem_u32(&c.item_empty[sl]));
-      if (!w.valid) break;
+      if (!valid) break;
       const int tok = w.tok0 + i * TT + t_in, n = w.n[i];
       const bool live = t_in < TT && g < w.heads && tok < w.lq;
-      const int lim = live ? max(0, min(w.lk, tok + 1 + w.lk - w.lq)) : 0x7fffffff;   // keys the row sees
+      const int lim = live ? max(0, min(w.lk, tok + 1 + w.lk - w.lq)) - w.shift : 0x7fffffff;   // keys the row sees, from the first tile on
       const int least = __reduce_min_sync(0xffffffffu, lim);
+      uint32_t buf = Sh::buf(i, 0);
       float ref = -INFINITY, l = 0.f;      // exponents are relative to ref (in units of raw scores)
-      bool go = true;
-      for (int j = 0; j < n; ++j) {
-        go = warp_wait(c, c.s_full[i], sc & 1);
-        ++sc;
-        if (!go) break;
+      for (int j = 0; j < n; ++j, ++t) {
+        const uint32_t col_s = lane_base + buf * kTile;
+        if constexpr (Sh::bufs == 3) buf = buf == 0 ? 2 : buf - 1;   // (2 j + i) mod 3
+        dead |= pre_wait(c, c.s_full[i][t & 1], (t >> 1) & 1);
+        __syncwarp();
         tc_fence_after();
         uint32_t s[4][32];
 #pragma unroll
@@ -455,11 +518,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         if (j == 0) {
           ref = top;
-        } else if (__any_sync(0xffffffffu, top > ref + grow)) {
+        } else if (__any_sync(0xffffffffu, live && top > ref + grow)) {   // (rows of nobody hold anything: no say)
           const float nr = fmaxf(ref, top);
           const float f = nr == -INFINITY ? 1.f : exp2_fast((ref - nr) * sl2);
           ref = nr;
           l *= f;
+          // (with three score buffers the P V before may still run)
+          pre_wait(c, c.o_done[i][(t - 1) & 1], ((t - 1) >> 1) & 1);
+          __syncwarp();
+          tc_fence_after();
 #pragma unroll
           for (int q = 0; q < D / 32; ++q) {
             uint32_t o[32];
@@ -485,23 +552,105 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
             pk[e] = pack_bf16x2(w0, w1);
           }
           tmem_st32(col_s + h * 32, pk);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&c.p_ready[i][h]));
+          if (Sh::bufs == 2 || h == 1) {   // (with three score buffers nothing of this warpgroup waits for P V: one hand-over)
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c.p_ready[i][t & 1][h]));
+          }
         }
         const float2 all = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
         l += all.x + all.y;
+        if ((j & 15) == 15 && __any_sync(0xffffffffu, dead)) break;
       }
-      if (!go) break;
+      if constexpr (SPLIT) {
+        // This part's reference and sum of the row, then the row's over all parts.
+        if (n > 0) pre_wait(c, c.o_done[i][(t - 1) & 1], ((t - 1) >> 1) & 1);
+        __syncwarp();
+        float2* const stats = reinterpret_cast<float2*>(prefill_smem_raw + (out_s - raw)) + i * kTile + row;
+        *stats = make_float2(n > 0 ? ref : -INFINITY, l);
+        cluster.sync();
+        float all_ref = -INFINITY, all_l = 0.f;
+        for (int x = 0; x < parts; ++x) all_ref = fmaxf(all_ref, cluster.map_shared_rank(stats, x)->x);
+        const float base_ref = all_ref == -INFINITY ? 0.f : all_ref;
+        for (int x = 0; x < parts; ++x) {
+          const float2 st = *cluster.map_shared_rank(stats, x);
+          all_l += st.y * exp2_fast((st.x - base_ref) * sl2);
+        }
+        // This part's share of the result, fp32, over the key and value ring (nothing is in flight there any
+        // more): row tile after row tile, 16-byte chunks permuted by the row.
+        const float f = all_l == 0.f || n == 0 ? 0.f : exp2_fast((ref - base_ref) * sl2) / all_l;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32(col_o + q * 32, o);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (n > 0)
+              v = make_uint4(__float_as_uint(__uint_as_float(o[4 * e]) * f), __float_as_uint(__uint_as_float(o[4 * e + 1]) * f),
+                             __float_as_uint(__uint_as_float(o[4 * e + 2]) * f), __float_as_uint(__uint_as_float(o[4 * e + 3]) * f));
+            sts128(ring + ((i * kTile + row) * (D / 4) + ((q * 8 + e) ^ (row & (D / 4 - 1)))) * 16, v);
+          }
+        }
+        tc_fence_before();
+        if (p.lse && live && part == 0 && !failed(c))
+          p.lse[static_cast<long long>(w.q0 + i * TT + t_in) * p.q_heads + w.h0 + g] =
+              all_l == 0.f ? -INFINITY : (all_ref * sl2 + log2f(all_l)) * kLn2;
+        cluster.sync();
+        // Rows part, part + parts, ..: the sum over the parts, a warp a row.
+        constexpr int E = D / 32;
+        const float* const mine = reinterpret_cast<const float*>(prefill_smem_raw + (ring - raw));
+        for (int r = part + parts * warp; r < 2 * kTile; r += parts * kSoftmaxWarps) {
+          const int x_in = (r & (kTile - 1)) / GB, gg = (r & (kTile - 1)) - x_in * GB, ri = r >> 7;
+          const int tk = w.tok0 + ri * TT + x_in;
+          if (x_in >= TT || gg >= w.heads || tk >= w.lq || failed(c)) continue;
+          const int at = (r * (D / 4) + ((lane * E / 4) ^ (r & (D / 4 - 1)))) * 4 + lane * E % 4;
+          float sum[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) sum[e] = 0.f;
+#pragma unroll 4
+          for (int x = 0; x < parts; ++x) {
+            const float* const from = cluster.map_shared_rank(mine, x) + at;
+            if constexpr (E == 4) {
+              const float4 v = *reinterpret_cast<const float4*>(from);
+              sum[0] += v.x; sum[1] += v.y; sum[2] += v.z; sum[3] += v.w;
+            } else {
+              const float2 v = *reinterpret_cast<const float2*>(from);
+              sum[0] += v.x; sum[1] += v.y;
+            }
+          }
+          float check = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) check = __fmaf_rn(sum[e], 0.f, check);
+          const int q_row = w.q0 + ri * TT + x_in, h = w.h0 + gg;
+          if (__any_sync(0xffffffffu, !(check == 0.f))) {
+            row_again<D>(p, q_row, h, w.kvh, w.k0 - w.shift, max(0, min(w.lk, tk + 1 + w.lk - w.lq)), sl2, lane);
+          } else {
+            uint32_t v[E / 2];
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) v[e] = pack_bf16x2(sum[2 * e], sum[2 * e + 1]);
+            uint16_t* const out = p.out + q_row * p.out_stride + h * D + lane * E;
+            if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(v[0], v[1]);
+            else *reinterpret_cast<uint32_t*>(out) = v[0];
+          }
+        }
+        met = 2;
+        continue;
+      }
       // The row's result, through shared memory so that a store instruction writes 4 whole 128-byte lines
       // (one row per lane, 16 bytes each, wrote 32 and held up the SM's loads: 5000 clocks an item, now 1000).
       uint16_t* const to = p.out + static_cast<long long>(w.q0 + i * TT + t_in) * p.out_stride + (w.h0 + g) * D;
       const uint32_t lives = __ballot_sync(0xffffffffu, live);
       bool bad = false;
       if (n > 0) {
-        if (!warp_wait(c, c.o_full[i], oc & 1)) break;
-        ++oc;
+        pre_wait(c, c.o_done[i][(t - 1) & 1], ((t - 1) >> 1) & 1);
+        __syncwarp();
+        if (__any_sync(0xffffffffu, failed(c))) break;
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const uint64_t invp = pair(inv, inv);
@@ -551,23 +700,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         const int src = __ffs(left) - 1;
         const int r = w.q0 + i * TT + __shfl_sync(0xffffffffu, t_in, src), h = w.h0 + __shfl_sync(0xffffffffu, g, src);
         const int keys = __shfl_sync(0xffffffffu, lim, src);
-        RowState<D> st;
-        st.begin(p.q + r * p.q_stride + h * D, sl2, lane);
-        for (int j = 0; j < keys; ++j) {
-          constexpr int E = D / 32;
-          float k[E], v[E];
-          load_bf16<E>(p.k + (w.k0 + j) * p.k_stride + w.kvh * D + lane * E, k);
-          load_bf16<E>(p.v + (w.k0 + j) * p.v_stride + w.kvh * D + lane * E, v);
-          st.add(k, v);
-        }
-        for (int e = 0; e < D / 32; ++e)
-          p.out[r * p.out_stride + h * D + lane * (D / 32) + e] = f32_to_bf16_bits(st.l == 0.f ? 0.f : st.acc[e] / st.l);
-        if (p.lse && lane == 0)
-          p.lse[static_cast<long long>(r) * p.q_heads + h] = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
+        row_again<D>(p, r, h, w.kvh, w.k0, keys, sl2, lane);
       }
     }
   }
 
+  if constexpr (SPLIT) {   // every thread of the cluster meets three times, whatever became of its item
+    for (int x = met; x < 3; ++x) cluster.sync();
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == kPreMmaWarp) {
@@ -578,25 +718,44 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
 
 namespace {
 
-template <int D>
-int launch_one(const PrefillArgs& a, void* stream) {
+template <int D, bool SPLIT>
+int launch_grid(const PrefillArgs& a, long long items, int parts, void* stream) {
   // (set on every call: the attribute belongs to the current device, like the launch)
-  cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefillShape<D>::smem);
+  const auto kernel = prefill_kernel<D, SPLIT>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefillShape<D>::smem);
   if (e != cudaSuccess) return static_cast<int>(e);
-  // At most this many items: a sequence adds one more than its whole pairs of row tiles.
-  const long long subs = a.kv_heads * ((a.q_heads / a.kv_heads + a.head_block - 1) / a.head_block);
-  const long long most = (a.total_q / (2 * a.tile_tokens) + static_cast<long long>(a.batch)) * subs;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(most), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(items * parts), 1, 1);
   cfg.blockDim = dim3(kPreThreads, 1, 1);
   cfg.dynamicSmemBytes = PrefillShape<D>::smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(parts);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return static_cast<int>(cudaLaunchKernelEx(&cfg, prefill_kernel<D>, a));
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, a));
+}
+
+template <int D>
+int launch_one(const PrefillArgs& a, void* stream) {
+  // At most this many items: a sequence adds one more than its whole pairs of row tiles.
+  const long long subs = a.kv_heads * ((a.q_heads / a.kv_heads + a.head_block - 1) / a.head_block);
+  const long long items = (a.total_q / (2 * a.tile_tokens) + static_cast<long long>(a.batch)) * subs;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  // Few items over long keys: split the keys over up to 8 CTAs while the GPU has SMs for them and each part
+  // keeps at least two key tiles of the average sequence.
+  const long long tiles = a.total_k / a.batch / kTile;
+  int parts = 1;
+  while (parts < 8 && items * parts * 2 <= sms && tiles >= 4 * parts) parts *= 2;
+  return parts > 1 ? launch_grid<D, true>(a, items, parts, stream) : launch_grid<D, false>(a, items, 1, stream);
 }
 
 }  // namespace

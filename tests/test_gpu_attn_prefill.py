@@ -179,3 +179,34 @@ def test_cached_prefix_end_to_end():
     table = order[None, :-(-n // page)].int().contiguous()
     last = A.run_decode(q[n - 1:], cache, table, A.int32([n]), H, 0.1)
     R.check(last.view(1, H, d), want[n - 1:], bound[n - 1:])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kv,G,qk", [
+    (2, 4, [(5, 700)]), (1, 8, [(1, 2000)]), (2, 1, [(130, 1100)]), (1, 16, [(33, 9000)]), (3, 5, [(17, 4001)]),
+    (1, 4, [(3, 5000), (40, 60), (2, 1), (70, 3000)]),        # parts without a key tile, a row without keys
+    (2, 8, [(100, 1300), (0, 0), (9, 2600)]), (1, 130, [(2, 3000)]),
+])
+def test_few_rows_over_long_keys(d, kv, G, qk):
+    """Shapes whose keys are split over the CTAs of a cluster and joined."""
+    q, k, v, cu_q, cu_k = case(kv * 31 + G, qk, kv, G, d)
+    out = compare(q, k, v, cu_q, cu_k, kv, G, d, d ** -0.5)
+    again = A.run_prefill(q, k, v, A.int32(cu_q), A.int32(cu_k), kv * G, kv, d ** -0.5)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_rows_over_long_keys_bad_values(d):
+    """Split keys: scores that differ by thousands between the parts; NaN in keys that rows do not see."""
+    kv, G, qk = 1, 4, [(6, 3000), (4, 2500)]
+    q, k, v, cu_q, cu_k = case(77, qk, kv, G, d, spread=8.0)
+    ramp = torch.linspace(0.1, 2.0, k.shape[0], device="cuda")[:, None]
+    k = (k.float() * ramp).bfloat16()
+    compare(q, k, v, cu_q, cu_k, kv, G, d, 0.5)
+    k, v = k.clone(), v.clone()
+    k[2997:3000], v[2997:3000] = float("nan"), float("inf")     # rows 0 .. 2 of the first do not see them
+    out = A.run_prefill(q, k, v, A.int32(cu_q), A.int32(cu_k), G, kv, 0.5).view(-1, G, d)
+    want, _, bound, _ = A.prefill_want(q, k, v, cu_q, cu_k, G, kv, 0.5)
+    keep = [0, 1, 2, 6, 7, 8, 9]
+    R.check(out[keep], want[keep], bound[keep])
+    assert torch.isnan(out[3:6]).all()
