@@ -9,7 +9,8 @@
 // Split. The work unit is a tile of kTile tokens of one segment: a segment is (sequence, key-value
 // head, block of 16 query heads). All tiles of the batch, segment after segment, are cut into equal
 // contiguous ranges, one per CTA (two CTAs per SM; fewer CTAs when there would be less than one tile
-// for each warp). A range is walked piece by piece (a piece: its part of one segment). A piece that is
+// for each warp); ends that fall into a segment of at most kWhole tiles move to its nearer end, as
+// joining its parts takes longer than the few tiles. A range is walked piece by piece (a piece: its part of one segment). A piece that is
 // a whole segment is finished by its CTA; otherwise the CTA stores (maximum, sum, unnormalised output)
 // in the workspace and the last CTA of the segment to arrive joins them in CTA order, so the bits never
 // depend on who was last. Segments over many CTAs join in two levels (kJoinGroup).
@@ -41,6 +42,7 @@ constexpr int kHalfStage = 4096;                 // bytes of K (and of V) in a s
 constexpr int kCtasPerSm = 2;
 constexpr int kJoinGroup = 16;                   // partial results joined by one CTA
 constexpr int kMaxCtas = 512;                    // counters in the workspace
+constexpr int kWhole = 2 * kDecWarps;            // segments of at most this many tiles are not divided
 constexpr int kRows = 16;                        // query heads of a segment
 
 // Workspace: counters [3][kMaxCtas] (a segment's first join group, by its first CTA; its other groups, by
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
   constexpr int TOK = T::tokens, NT = TOK / 8, KS = D / 16, R = HALF ? 1 : 2;
   constexpr int PL = T::per_lane;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long s_sum[kDecWarps];
+  __shared__ long long s_sum[kDecWarps], s_u[2];
   __shared__ int s_b, s_sub, s_tiles, s_len, s_tile0, s_last;
   __shared__ float s_m[kDecWarps][kRows], s_l[kDecWarps][kRows];
   __shared__ float s_jm[kJoinGroup * kRows], s_jl[kJoinGroup * kRows];
@@ -234,33 +236,59 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
     zero_empty();
     return;
   }
-  const long long u0 = mul_div(c, total, n), u1 = mul_div(c + 1, total, n);
-  if (u0 >= before && u0 < before + mine) {   // this thread's sequences hold u0
+  // Ends of the range: equal shares, moved to the nearer end of a segment of at most kWhole tiles.
+  if (tid == 0) s_u[1] = total;              // (the last CTA's)
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    long long u = mul_div(c + e, total, n);
+    if (u < before || u >= before + mine) continue;   // another thread's sequences hold it
     long long at = before;
     for (int b = b0; b < b1; ++b) {
       int len;
       const int t = tiles_of<TOK>(p, b, len);
       const long long span = static_cast<long long>(t) * subs;
-      if (u0 < at + span) {
-        s_b = b;
-        s_tiles = t;
-        s_len = len;
-        s_sub = static_cast<int>(mul_div(u0 - at, 1, t));
-        s_tile0 = static_cast<int>(u0 - at - static_cast<long long>(s_sub) * t);
+      if (u < at + span) {
+        const int sub = static_cast<int>(mul_div(u - at, 1, t));
+        int tile = static_cast<int>(u - at - static_cast<long long>(sub) * t);
+        if (t <= kWhole) {
+          const int to = 2 * tile < t ? 0 : t;
+          u += to - tile;
+          tile = to;
+        }
+        s_u[e] = u;
+        if (e == 0) {
+          s_b = b;
+          s_tiles = t;
+          s_len = len;
+          s_sub = sub;
+          s_tile0 = tile;
+        }
         break;
       }
       at += span;
     }
   }
   __syncthreads();
+  const long long u0 = s_u[0], u1 = s_u[1];
+  if (u0 >= u1) {
+    zero_empty();
+    return;
+  }
+  Walk start{s_b, s_sub, s_tiles, s_len};
+  int start_tile = s_tile0;
+  if (start_tile == start.tiles) {
+    next_segment<TOK>(p, subs, start);
+    start_tile = 0;
+  }
 
   const uint32_t ring = smem_u32(smem) + warp * kStages * T::stage_bytes;
   const unsigned char* const ring_ptr = smem + warp * kStages * T::stage_bytes;
 
   // ---- loads: a cursor over this warp's tiles, one tile ahead of the copies in its page look-up
-  Walk lw{s_b, s_sub, s_tiles, s_len};
+  Walk lw = start;
   long long lu = u0;                       // first unit of the cursor's piece
-  int lt0 = s_tile0, lt1 = static_cast<int>(min(static_cast<long long>(lw.tiles), s_tile0 + (u1 - u0)));
+  int lt0 = start_tile, lt1 = static_cast<int>(min(static_cast<long long>(lw.tiles), start_tile + (u1 - u0)));
   int lt = lt0 + warp;
   bool more = true;
   int page[PL], slot[PL];
@@ -332,8 +360,8 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
   for (int s = 0; s < kStages - 1; ++s) load(s);
 
   // ---- pieces
-  Walk w{s_b, s_sub, s_tiles, s_len};
-  int ta = s_tile0, it = 0;
+  Walk w = start;
+  int ta = start_tile, it = 0;
   for (long long u = u0; u < u1;) {
     const int tb = static_cast<int>(min(static_cast<long long>(w.tiles), ta + (u1 - u)));
     const int head = w.sub / blocks, h0 = head * G + (w.sub - head * blocks) * kRows;

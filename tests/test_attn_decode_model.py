@@ -4,6 +4,7 @@ tile belongs to one CTA, no two parts share a workspace slot, no two joins share
 counter sees exactly the arrivals it waits for."""
 from __future__ import annotations
 
+import bisect
 import os
 import random
 import re
@@ -19,6 +20,7 @@ def const(name):
 
 
 WARPS, GROUP, MAX_CTAS, PER_SM = const("kDecWarps"), const("kJoinGroup"), const("kMaxCtas"), const("kCtasPerSm")
+WHOLE = int(re.search(r"constexpr int kWhole = (\d+) \* kDecWarps;", SRC).group(1)) * WARPS
 
 
 def plan(tiles, subs, grid, shared_counters=False):
@@ -33,9 +35,15 @@ def plan(tiles, subs, grid, shared_counters=False):
             segments.append((at, t))
             at += t
     covered, parts, i0 = 0, {}, 0
+
+    def end(u):
+        """An equal share's end, moved to the nearer end of a segment of at most WHOLE tiles."""
+        s0, t = segments[bisect.bisect_right(starts, u) - 1] if u < total else (total, 0)
+        return u if t > WHOLE or u == total else (s0 if 2 * (u - s0) < t else s0 + t)
+    starts = [s0 for s0, _ in segments]
     for c in range(n):
-        u0, u1 = c * total // n, (c + 1) * total // n
-        assert u0 == covered and u1 > u0
+        u0, u1 = end(c * total // n), end((c + 1) * total // n)
+        assert u0 == covered and u1 >= u0
         covered = u1
         u, i = u0, i0
         while u < u1:
@@ -45,6 +53,7 @@ def plan(tiles, subs, grid, shared_counters=False):
             ta = u - s0
             tb = min(t, ta + (u1 - u))
             if not (ta == 0 and tb == t):
+                assert t > WHOLE
                 parts.setdefault((s0, t), []).append((c, 2 * c + (ta == 0)))
             u += tb - ta
         i0 = i
@@ -88,4 +97,4 @@ def test_the_model_sees_a_shared_counter():
     """A segment's last group may start in the CTA where the next segment starts: one counter for both is
     the mistake the separate ones are there for."""
     with pytest.raises(AssertionError, match="two segments at one counter"):
-        plan([313, 3, 0, 57], 4, 152 * PER_SM, shared_counters=True)
+        plan([65, 9, 12], 4, 152 * PER_SM, shared_counters=True)
