@@ -285,13 +285,36 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
   const uint32_t ring = smem_u32(smem) + warp * kStages * T::stage_bytes;
   const unsigned char* const ring_ptr = smem + warp * kStages * T::stage_bytes;
 
-  // ---- loads: a cursor over this warp's tiles, one tile ahead of the copies in its page look-up
+  // Q of a segment as A fragments (raw BF16 pairs): loaded ahead of the copies, and for the next piece before
+  // the join of the one before.
+  uint32_t qa[KS][2 * R];
+  auto load_q = [&](const Walk& at) {
+    const int head = at.sub / blocks, first = head * G + (at.sub - head * blocks) * kRows, rows = min(kRows, head * G + G - first);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int row = g + 8 * r;
+      const uint16_t* q = p.q + at.b * p.q_stride + (first + row) * D;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int d = FMT == kKvBf16 ? k * 16 + j * 8 + qd * 2 : k * 16 + qd * 4 + j * 2;
+          qa[k][j * R + r] = row < rows ? __ldg(reinterpret_cast<const uint32_t*>(q + d)) : 0u;
+        }
+    }
+  };
+  load_q(start);
+
+  // ---- loads: a cursor over this warp's tiles, two tiles ahead of the copies in its page look-ups
   Walk lw = start;
   long long lu = u0;                       // first unit of the cursor's piece
   int lt0 = start_tile, lt1 = static_cast<int>(min(static_cast<long long>(lw.tiles), start_tile + (u1 - u0)));
   int lt = lt0 + warp;
   bool more = true;
-  int page[PL], slot[PL];
+  struct Ahead {                           // a tile to copy: its tokens' pages and slots, its head
+    int page[PL], slot[PL], head;
+    bool is;
+  } next{}, after{};
   auto settle = [&]() {                    // to the next tile of this warp, or the end
     while (lt >= lt1) {
       lu += lt1 - lt0;
@@ -305,33 +328,38 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
       lt = warp;
     }
   };
-  auto look_up = [&]() {
+  auto look_up = [&](Ahead& t) {            // the cursor's tile, then the cursor moves on
+    t.is = more;
     if (!more) return;
+    t.head = lw.sub / blocks;
 #pragma unroll
     for (int j = 0; j < PL; ++j) {
-      const int i = lane + 32 * j, t = lt * TOK + i;
-      page[j] = -1;
-      slot[j] = 0;
-      if (i < TOK && t < lw.len) {
-        const int e = p.page_shift >= 0 ? t >> p.page_shift : t / p.c.page_size;
-        slot[j] = t - e * p.c.page_size;
-        page[j] = __ldg(p.table + lw.b * p.table_stride + e);
+      const int i = lane + 32 * j, at = lt * TOK + i;
+      t.page[j] = -1;
+      t.slot[j] = 0;
+      if (i < TOK && at < lw.len) {
+        const int e = p.page_shift >= 0 ? at >> p.page_shift : at / p.c.page_size;
+        t.slot[j] = at - e * p.c.page_size;
+        t.page[j] = __ldg(p.table + lw.b * p.table_stride + e);
       }
     }
+    lt += kDecWarps;
+    settle();
   };
-  auto load = [&](int s) {                 // the cursor's tile into stage s, then the cursor moves on
-    if (more) {
+  auto load = [&](int s) {                 // the next tile into stage s
+    if (next.is) {
       const uint32_t st = ring + s * T::stage_bytes;
-      const int head = lw.sub / blocks;
+      const int head = next.head;
       long long off[PL];
       uint64_t live = 0;
 #pragma unroll
       for (int j = 0; j < PL; ++j) {
-        const bool ok = page[j] >= 0 && page[j] < p.c.num_pages;
-        off[j] = ok ? page[j] * p.c.page_bytes + head * p.c.head_bytes + slot[j] * p.c.token_bytes : -1;
+        const int page = next.page[j], slot = next.slot[j];
+        const bool ok = page >= 0 && page < p.c.num_pages;
+        off[j] = ok ? page * p.c.page_bytes + head * p.c.head_bytes + slot * p.c.token_bytes : -1;
         live |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << (32 * j);
         if constexpr (FMT != kKvBf16) {
-          const long long si = ok ? scale_index(p.c, page[j], head, slot[j]) : 0;
+          const long long si = ok ? scale_index(p.c, page, head, slot) : 0;
           const uint32_t to = st + 2 * kHalfStage + (lane + 32 * j) * 4;
           cp_async4_n(to, p.c.ks + si, ok ? 4 : 0);
           cp_async4_n(to + TOK * 4, p.c.vs + si, ok ? 4 : 0);
@@ -348,14 +376,14 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
         cp_async16_n(to, p.c.k + from, o < 0 ? 0 : 16);
         cp_async16_n(to + kHalfStage, p.c.v + from, o < 0 ? 0 : 16);
       }
-      lt += kDecWarps;
-      settle();
-      look_up();
+      next = after;
+      look_up(after);
     }
     cp_async_commit();
   };
   settle();
-  look_up();
+  look_up(next);
+  look_up(after);
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) load(s);
 
@@ -367,21 +395,11 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
     const int head = w.sub / blocks, h0 = head * G + (w.sub - head * blocks) * kRows;
     const int rows = min(kRows, head * G + G - h0);
 
-    // Q as A fragments; scores come out in units of zscale (base-2 exponents).
-    uint32_t qa[KS][2 * R];
+    // Scores come out in units of zscale (base-2 exponents).
     float zscale[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int row = g + 8 * r;
-      const uint16_t* q = p.q + w.b * p.q_stride + (h0 + row) * D;
       zscale[r] = p.scale * kLog2e;
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int d = FMT == kKvBf16 ? k * 16 + j * 8 + qd * 2 : k * 16 + qd * 4 + j * 2;
-          qa[k][j * R + r] = row < rows ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
-        }
       if constexpr (FMT != kKvBf16) {      // BF16 -> f16, the row's largest magnitude at 2^14 .. 2^15
         uint32_t top = 0;
 #pragma unroll
@@ -535,10 +553,18 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
         }
       }
     }
-    // (lora_kv_write makes no NaN codes; a cache that holds them gives NaN, as a scale of NaN does)
+    // lora_kv_write makes no NaN codes; a cache that holds them gives NaN, as a scale of NaN does (the
+    // conversion above would take them for 480).
     if (FMT == kKvE4m3 && __any_sync(0xffffffffu, (nan_codes & 0x80808080u) != 0))
 #pragma unroll
       for (int r = 0; r < R; ++r) l[r] = __int_as_float(0x7fffffff);
+
+    u += tb - ta;
+    Walk nw = w;
+    if (u < u1) {
+      next_segment<TOK>(p, subs, nw);
+      load_q(nw);
+    }
 
     // ---- join the warps: (m, l) of each row, then O in two steps through two buffers
 #pragma unroll
@@ -641,7 +667,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
       }
       // The segment's CTAs c0 .. c1, in groups of kJoinGroup; slot of CTA x: its part either starts
       // the segment (x == c0: slot 2 x + 1) or goes on with it (slot 2 x).
-      const long long s0 = u - ta, s1 = s0 + w.tiles - 1;
+      const long long s0 = u - tb, s1 = s0 + w.tiles - 1;
       auto cta_of = [&](long long unit) {   // the last x with x * total / n <= unit: ((unit + 1) n - 1) / total
         const long long v = (unit + 1) * n - 1;
         return static_cast<int>(mul_div(v, 1, total));
@@ -717,8 +743,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
         if (groups > 1 && last_of(counters + 2 * kMaxCtas + c0, groups)) join(c0, groups, kJoinGroup, true);
       }
     }
-    u += tb - ta;
-    if (u < u1) next_segment<TOK>(p, subs, w);
+    w = nw;
     ta = 0;
     __syncthreads();
   }

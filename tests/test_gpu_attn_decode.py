@@ -167,6 +167,21 @@ def test_a_token_that_is_not_finite():
         assert hurt[:, 5].all() if fmt == "bf16" else hurt.all()
 
 
+def test_nan_codes_in_a_foreign_cache():
+    """E4M3 NaN codes, which lora_kv_write never makes: one in K or in V of a token makes the outputs
+    that read it NaN, those of other sequences and heads stay."""
+    lens, page, d = [50, 60], 16, 128
+    for which in (0, 1):
+        for byte in (0x7F, 0xFF):
+            cache, kval, vval, table, q = case(25, lens, 2, 2, d, page, "e4m3")
+            cache.tensors[which].view(torch.uint8)[int(table[0, 2]), 1, 9, 77] = byte
+            out = A.run_decode(q, cache, table, A.int32(lens), 4, 0.1).view(2, 4, d)
+            want, _, bound = A.decode_want(q, kval, vval, table, lens, page, 0.1, 4)
+            R.check(out[1], want[1], bound[1])
+            R.check(out[0, :2], want[0, :2], bound[0, :2])
+            assert torch.isnan(out[0, 2:]).all()
+
+
 def test_lengths_are_clamped():
     """Negative lengths are empty, lengths past the table end with the table."""
     page, d = 16, 64
