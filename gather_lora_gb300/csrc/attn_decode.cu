@@ -117,13 +117,13 @@ __device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t&
 template <int FMT>
 __device__ __forceinline__ void codes_to_bf16(uint32_t c, uint32_t& even, uint32_t& odd) {
   if constexpr (FMT == kKvE4m3) {
-    // Sign, then the 4 + 3 bits in BF16's lowest exponent and highest mantissa bits: the value times
-    // 2^-120 (E4M3's subnormals are BF16's there), multiplied back up.
-    const __nv_bfloat162 up = __halves2bfloat162(__ushort_as_bfloat16(0x7b80), __ushort_as_bfloat16(0x7b80));
-    uint32_t e = ((c << 4) & 0x07f007f0u) | ((c << 8) & 0x80008000u), o = ((c >> 4) & 0x07f007f0u) | (c & 0x80008000u);
-    const __nv_bfloat162 a = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&e), up), b = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o), up);
-    even = *reinterpret_cast<const uint32_t*>(&a);
-    odd = *reinterpret_cast<const uint32_t*>(&b);
+    // Through f16 and fp32 (every step exact, NaN stays NaN): the unpacking adds run beside the ALU, which
+    // shifts and masks of the codes' bits would fill.
+    uint32_t e, o;
+    e4m3x4_to_f16(__byte_perm(c, 0, 0x3120), e, o);
+    const float2 x = f16x2_to_f32(e), y = f16x2_to_f32(o);
+    even = pack_bf16x2(x.x, x.y);
+    odd = pack_bf16x2(y.x, y.y);
   } else {
     // 0x4300 | low 7 bits is 128 + them; minus 128 or, for a set sign bit, 256
     const uint32_t x = __byte_perm(c, 0x43434343u, 0x4240), y = __byte_perm(c, 0x43434343u, 0x4341);
@@ -426,7 +426,6 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
       }
     }
 
-    uint32_t nan_codes = 0;
     float o[D / 8][4], m[R], l[R];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
@@ -546,19 +545,11 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
               codes_to_bf16<FMT>(c[2 * j + 1], e1, f1);
               mma_k16(o[2 * (i + j)], a0, a1, a2, a3, e0, e1);
               mma_k16(o[2 * (i + j) + 1], a0, a1, a2, a3, f0, f1);
-              if constexpr (FMT == kKvE4m3)   // a NaN code (0x7f, 0xff) carries into its byte's top bit
-                nan_codes |= ((c[2 * j] & 0x7f7f7f7fu) + 0x01010101u) | ((c[2 * j + 1] & 0x7f7f7f7fu) + 0x01010101u);
             }
           }
         }
       }
     }
-    // lora_kv_write makes no NaN codes; a cache that holds them gives NaN, as a scale of NaN does (the
-    // conversion above would take them for 480).
-    if (FMT == kKvE4m3 && __any_sync(0xffffffffu, (nan_codes & 0x80808080u) != 0))
-#pragma unroll
-      for (int r = 0; r < R; ++r) l[r] = __int_as_float(0x7fffffff);
-
     u += tb - ta;
     Walk nw = w;
     if (u < u1) {
