@@ -21,14 +21,15 @@
 // layout of A in the product with V. Running maximum m and sum l per row as usual.
 //
 // 8-bit formats. K's codes become f16 pairs in registers (exact: E4M3 and integers to 127 fit f16's 11
-// bits; Q is scaled by a power of two into f16's range), V's become BF16 pairs (exact too), because K's scale
-// multiplies the score but V's the weight, p_t s_t, and scales may differ by any factor from token to
-// token: BF16 has fp32's range. A lane's 4 consecutive code bytes of K are 4 consecutive dimensions, so the
-// dimensions of Q are dealt to the MMA's k index in that order; V is read transposed as byte pairs and
-// split into even and odd dimensions.
+// bits; Q is scaled by a power of two into f16's range). V's become TF32, exact too, with the weights: K's scale
+// multiplies the score but V's the weight, p_t s_t, so weights may span any range (TF32 has fp32's) and even
+// a single token's must not be rounded to 8 bits (BF16 weights measured 1.5 times the error of rounding the
+// result alone, and more instructions: the codes come out of their conversions in fp32). A lane's 4
+// consecutive code bytes of K are 4 consecutive dimensions, so the dimensions of Q are dealt to the MMA's k
+// index in that order; V is read transposed as byte pairs and split into even and odd dimensions.
 //
-// Rounding to fewer bits: softmax weights to BF16 before they multiply V, as the tensor cores take 16-bit
-// operands; sums and statistics are fp32; the output rounds once to BF16.
+// Rounding to fewer bits: softmax weights before they multiply V, to BF16 (BF16 cache: the tensor cores take
+// operands of one type) or TF32 (8-bit); sums and statistics are fp32; the output rounds once to BF16.
 #include "attn_common.cuh"
 
 namespace glora {
@@ -112,27 +113,30 @@ __device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t&
   }
 }
 
-// V's codes of tokens t0, t1 and dimensions d0, d1, as bytes (t0 d0, t0 d1, t1 d0, t1 d1) -> BF16 pairs
-// (t0, t1) of d0 and of d1, exact.
+// Four codes -> fp32 (low byte first), by way of f16: its unpacking runs beside the ALU (INT8 144.9 -> 140.9 us).
 template <int FMT>
-__device__ __forceinline__ void codes_to_bf16(uint32_t c, uint32_t& even, uint32_t& odd) {
-  if constexpr (FMT == kKvE4m3) {
-    // Through f16 and fp32 (every step exact, NaN stays NaN): the unpacking adds run beside the ALU, which
-    // shifts and masks of the codes' bits would fill.
-    uint32_t e, o;
-    e4m3x4_to_f16(__byte_perm(c, 0, 0x3120), e, o);
-    const float2 x = f16x2_to_f32(e), y = f16x2_to_f32(o);
-    even = pack_bf16x2(x.x, x.y);
-    odd = pack_bf16x2(y.x, y.y);
-  } else {
-    // 0x4300 | low 7 bits is 128 + them; minus 128 or, for a set sign bit, 256
-    const uint32_t x = __byte_perm(c, 0x43434343u, 0x4240), y = __byte_perm(c, 0x43434343u, 0x4341);
-    const uint32_t xl = x & 0xff7fff7fu, xs = x & 0xff80ff80u, yl = y & 0xff7fff7fu, ys = y & 0xff80ff80u;
-    const __nv_bfloat162 a = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&xl), *reinterpret_cast<const __nv_bfloat162*>(&xs));
-    const __nv_bfloat162 b = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&yl), *reinterpret_cast<const __nv_bfloat162*>(&ys));
-    even = *reinterpret_cast<const uint32_t*>(&a);
-    odd = *reinterpret_cast<const uint32_t*>(&b);
-  }
+__device__ __forceinline__ void codes_to_tf32(uint32_t c, uint32_t (&v)[4]) {
+  uint32_t lo, hi;
+  codes_to_f16<FMT>(c, lo, hi);
+  const float2 x = f16x2_to_f32(lo), y = f16x2_to_f32(hi);
+  v[0] = __float_as_uint(x.x);
+  v[1] = __float_as_uint(x.y);
+  v[2] = __float_as_uint(y.x);
+  v[3] = __float_as_uint(y.y);
+}
+// fp32 rounded to TF32's 11 significant bits.
+__device__ __forceinline__ uint32_t to_tf32(float f) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(r) : "f"(f));
+  return r;
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ float quad_max(float v) {
@@ -521,10 +525,10 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
       // O += P V
 #pragma unroll
       for (int k = 0; k < TOK / 16; ++k) {
-        const uint32_t a0 = pack_bf16x2(z[2 * k][0], z[2 * k][1]), a2 = pack_bf16x2(z[2 * k + 1][0], z[2 * k + 1][1]);
-        const uint32_t a1 = HALF ? 0u : pack_bf16x2(z[2 * k][2], z[2 * k][3]);
-        const uint32_t a3 = HALF ? 0u : pack_bf16x2(z[2 * k + 1][2], z[2 * k + 1][3]);
         if constexpr (FMT == kKvBf16) {
+          const uint32_t a0 = pack_bf16x2(z[2 * k][0], z[2 * k][1]), a2 = pack_bf16x2(z[2 * k + 1][0], z[2 * k + 1][1]);
+          const uint32_t a1 = HALF ? 0u : pack_bf16x2(z[2 * k][2], z[2 * k][3]);
+          const uint32_t a3 = HALF ? 0u : pack_bf16x2(z[2 * k + 1][2], z[2 * k + 1][3]);
 #pragma unroll
           for (int i = 0; i < D / 8; i += 2) {
             uint32_t b0, b1, b2, b3;
@@ -533,18 +537,25 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
             mma_k16(o[i + 1], a0, a1, a2, a3, b2, b3);
           }
         } else {
+          // The MMA's k index q, q + 4 is token 2q, 2q + 1 of a group of 8: the scores' own layout.
+          uint32_t a[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)      // (row g, g + 8) x (token 2q, 2q + 1)
+              a[h][x] = HALF && (x & 1) ? 0u : to_tf32(z[2 * k + h][2 * (x & 1) + (x >> 1)]);
 #pragma unroll
           for (int i = 0; i < D / 16; i += 2) {
-            uint32_t c[4];               // (tokens 0-7, 8-15) of 16-dimension blocks i and i + 1
+            uint32_t c[4];                   // (tokens 0-7, 8-15) of 16-dimension blocks i and i + 1
             ldsm_x4_t(sv + T::at(k * 16 + (lane & 15), i + (lane >> 4)), c[0], c[1], c[2], c[3]);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 4; ++j) {
               // bytes of a register: token 2 qd: dimensions 2g, 2g + 1; token 2 qd + 1: the same
-              uint32_t e0, e1, f0, f1;
-              codes_to_bf16<FMT>(c[2 * j], e0, f0);
-              codes_to_bf16<FMT>(c[2 * j + 1], e1, f1);
-              mma_k16(o[2 * (i + j)], a0, a1, a2, a3, e0, e1);
-              mma_k16(o[2 * (i + j) + 1], a0, a1, a2, a3, f0, f1);
+              uint32_t v[4];
+              codes_to_tf32<FMT>(c[j], v);
+              const uint32_t(&w)[4] = a[j & 1];
+              mma_tf32(o[2 * (i + (j >> 1))], w[0], w[1], w[2], w[3], v[0], v[2]);
+              mma_tf32(o[2 * (i + (j >> 1)) + 1], w[0], w[1], w[2], w[3], v[1], v[3]);
             }
           }
         }
