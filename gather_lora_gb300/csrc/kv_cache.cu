@@ -9,7 +9,12 @@
 // rows. A thread holds 8 values (16 bytes of BF16) of a K row and the same 8 of the V row, so the slot is
 // divided into page and slot once for both; the 8 or 16 threads of a head row find its largest magnitude by
 // shuffles. Large calls give a thread kMany such pieces, whose loads are all in flight before the first is
-// used (with one, the wait for the slot number left half of the memory system idle).
+// used (with one, the wait for the slot number left half of the memory system idle). The write's four
+// divisions a row go to four threads and its maxima to packed BF16: it was bound by issue, 315 instructions a
+// warp and piece, 85 us in the case below.
+//
+// Measured on a GB300: 65536 tokens of 8 x 128 in E4M3 written in 67.7 us and read back in 65.4, 6.0 and 6.2
+// TB/s; 32 tokens of 4 x 128 in 1.7 and 1.5 us.
 #include "attn_common.cuh"
 
 namespace glora {
