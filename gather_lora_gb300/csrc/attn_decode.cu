@@ -5,11 +5,11 @@
 // Every cached byte is used once per call (2 G multiply-adds per element), so HBM bandwidth
 // bounds the kernel; what it needs is enough bytes in flight on every SM and an even share of the
 // batch's tokens for each, whatever the lengths are. The 8-bit formats are bound by instruction issue before
-// that: 900 a warp and 8 KB tile, 450 in BF16, with two warps a scheduler (registers).
+// that: 850 a warp and 8 KB tile, 440 in BF16, with two warps a scheduler (registers).
 //
 // Measured on a GB300: 128 contexts to 16384 (8 key-value heads of 128, BF16) 733 us, 6.9 TB/s; 32 to 4096
-// 58.6 us, 5.8 TB/s; 64 to 8191 (4 heads, E4M3) 72.8 us, 4.8 TB/s; 5 to 100003 (16 heads of 64, INT8) 141 us,
-// 4.3 TB/s; one of 700 tokens 9.0 us, all latency: plan 1.2, first loads 1, tile 0.6, joins 3.
+// 58.9 us, 5.8 TB/s; 64 to 8191 (4 heads, E4M3) 66.2 us, 5.3 TB/s; 5 to 100003 (16 heads of 64, INT8) 127 us,
+// 4.8 TB/s; one of 700 tokens 9.1 us, all latency: plan 1.2, first loads 1, tile 0.6, joins 3.
 //
 // Split. The work unit is a tile of kTile tokens of one segment: a segment is (sequence, key-value
 // head, block of 16 query heads). All tiles of the batch, segment after segment, are cut into equal
@@ -118,7 +118,7 @@ __device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t&
   }
 }
 
-// Four codes -> fp32 (low byte first), by way of f16: its unpacking runs beside the ALU (INT8 144.9 -> 140.9 us).
+// Four codes -> fp32 (low byte first), by way of f16: its unpacking runs beside the ALU (INT8, 5 contexts to 100003, 144.9 -> 140.9 us).
 template <int FMT>
 __device__ __forceinline__ void codes_to_tf32(uint32_t c, uint32_t (&v)[4]) {
   uint32_t lo, hi;
@@ -435,9 +435,10 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
       }
     }
 
-    float o[D / 8][4], m[R], l[R];
+    constexpr int OT = HALF ? D / 16 : D / 8;
+    float o[OT][4], m[R], l[R];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int i = 0; i < OT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
 #pragma unroll
@@ -522,12 +523,20 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
         l[r] = l[r] * keep[r] + sum;
       }
       if (__any_sync(0xffffffffu, keep[0] != 1.f || (!HALF && keep[R - 1] != 1.f))) {
+        // (HALF: accumulator columns are heads 2 qd, 2 qd + 1, whose factors lanes 8 qd, 8 qd + 4 hold)
+        float kx[2] = {keep[0], keep[R - 1]};
+        if constexpr (HALF) {
+          kx[0] = __shfl_sync(0xffffffffu, keep[0], qd * 8);
+          kx[1] = __shfl_sync(0xffffffffu, keep[0], qd * 8 + 4);
+        }
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+        for (int i = 0; i < OT; ++i)
 #pragma unroll
-          for (int j = 0; j < 2 * R; ++j) o[i][j] *= keep[j >> 1];
+          for (int j = 0; j < 4; ++j) o[i][j] *= kx[HALF ? j & 1 : j >> 1];
       }
-      // O += P V
+      // O += P V; with at most 8 heads O^T += V^T P^T instead, the same registers the other way round: dimensions
+      // are the MMA's 16 rows and the heads its 8 columns, half as many MMAs and accumulators (E4M3 72.9 -> 66.2 us, INT8
+      // 141 -> 126.6 in the cases above).
 #pragma unroll
       for (int k = 0; k < TOK / 16; ++k) {
         if constexpr (FMT == kKvBf16) {
@@ -538,8 +547,12 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
           for (int i = 0; i < D / 8; i += 2) {
             uint32_t b0, b1, b2, b3;
             ldsm_x4_t(sv + T::at(k * 16 + (lane & 15), i + (lane >> 4)), b0, b1, b2, b3);
-            mma_k16(o[i], a0, a1, a2, a3, b0, b1);
-            mma_k16(o[i + 1], a0, a1, a2, a3, b2, b3);
+            if constexpr (HALF) {
+              mma_k16(o[i / 2], b0, b2, b1, b3, a0, a2);
+            } else {
+              mma_k16(o[i], a0, a1, a2, a3, b0, b1);
+              mma_k16(o[i + 1], a0, a1, a2, a3, b2, b3);
+            }
           }
         } else {
           // The MMA's k index q, q + 4 is token 2q, 2q + 1 of a group of 8: the scores' own layout.
@@ -559,8 +572,12 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
               uint32_t v[4];
               codes_to_tf32<FMT>(c[j], v);
               const uint32_t(&w)[4] = a[j & 1];
-              mma_tf32(o[2 * (i + (j >> 1))], w[0], w[1], w[2], w[3], v[0], v[2]);
-              mma_tf32(o[2 * (i + (j >> 1)) + 1], w[0], w[1], w[2], w[3], v[1], v[3]);
+              if constexpr (HALF) {
+                mma_tf32(o[i + (j >> 1)], v[0], v[1], v[2], v[3], w[0], w[2]);
+              } else {
+                mma_tf32(o[2 * (i + (j >> 1))], w[0], w[1], w[2], w[3], v[0], v[2]);
+                mma_tf32(o[2 * (i + (j >> 1)) + 1], w[0], w[1], w[2], w[3], v[1], v[3]);
+              }
             }
           }
         }
@@ -583,26 +600,29 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
       }
     }
     __syncthreads();
-    float mj[R], lj[R];
+    // Joined maximum and sum of this lane's two accumulator rows (HALF: columns), and this warp's factor.
+    float mj[2], lj[2];
+    int own[2];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < 2; ++r) {
+      own[r] = HALF ? 2 * qd + r : g + 8 * r;
       mj[r] = -INFINITY;
       lj[r] = 0.f;
 #pragma unroll
-      for (int x = 0; x < kDecWarps; ++x) mj[r] = fmaxf(mj[r], s_m[x][g + 8 * r]);
+      for (int x = 0; x < kDecWarps; ++x) mj[r] = fmaxf(mj[r], s_m[x][own[r]]);
       const float ref = mj[r] == -INFINITY ? 0.f : mj[r];
 #pragma unroll
-      for (int x = 0; x < kDecWarps; ++x) lj[r] += s_l[x][g + 8 * r] * exp2_fast(s_m[x][g + 8 * r] - ref);
-      const float f = exp2_fast(m[r] - ref);
+      for (int x = 0; x < kDecWarps; ++x) lj[r] += s_l[x][own[r]] * exp2_fast(s_m[x][own[r]] - ref);
+      const float f = exp2_fast(s_m[warp][own[r]] - ref);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][2 * r] *= f;
-        o[i][2 * r + 1] *= f;
-      }
+      for (int i = 0; i < OT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if ((HALF ? j & 1 : j >> 1) == r) o[i][j] *= f;
     }
     // (16 rows go through the buffers in two halves of the dimensions)
-    constexpr int NB = D / 8 / R;
-    auto buffer = [&](int x, int i, int j) -> float& { return s_o[(x * NB * 2 * R + i * 2 * R + j) * 32 + lane]; };
+    constexpr int NB = D / 16;
+    auto buffer = [&](int x, int i, int j) -> float& { return s_o[(x * NB * 4 + i * 4 + j) * 32 + lane]; };
 #pragma unroll
     for (int h = 0; h < R; ++h) {
 #pragma unroll
@@ -611,67 +631,62 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
 #pragma unroll
           for (int i = 0; i < NB; ++i)
 #pragma unroll
-            for (int j = 0; j < 2 * R; ++j) buffer(warp - step, i, j) = o[h * NB + i][j];
+            for (int j = 0; j < 4; ++j) buffer(warp - step, i, j) = o[h * NB + i][j];
         __syncthreads();
         if (warp < step)
 #pragma unroll
           for (int i = 0; i < NB; ++i)
 #pragma unroll
-            for (int j = 0; j < 2 * R; ++j) o[h * NB + i][j] += buffer(warp, i, j);
+            for (int j = 0; j < 4; ++j) o[h * NB + i][j] += buffer(warp, i, j);
         if (step > 1 || h + 1 < R) __syncthreads();
       }
     }
 
-    // ---- the piece's result (warp 0 holds it)
-    // The dimensions of accumulator pair i: BF16 8 i + 2 qd, + 1; 8-bit, blocks of 16 as (even, odd) pairs.
-    auto dim = [&](int i, int j) { return FMT == kKvBf16 ? 8 * i + 2 * qd + j : 16 * (i >> 1) + 4 * qd + 2 * j + (i & 1); };
+    // ---- the piece's result: from warp 0 to [rows][D] fp32 in shared memory, then all threads take it
+    if (warp == 0) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < OT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = own[HALF ? j & 1 : j >> 1];
+          // HALF: dimensions g, g + 8 of block i (8-bit: 2g, 2g + 1); else 8 i + 2 qd, + 1 (8-bit: blocks of 16 as
+          // (even, odd) pairs)
+          int d;
+          if constexpr (HALF) d = FMT == kKvBf16 ? 16 * i + g + 8 * (j >> 1) : 16 * i + 2 * g + (j >> 1);
+          else d = FMT == kKvBf16 ? 8 * i + 2 * qd + (j & 1) : 16 * (i >> 1) + 4 * qd + 2 * (j & 1) + (i & 1);
+          s_o[row * D + d] = o[i][j];
+        }
+      if (HALF ? g == 0 : qd == 0)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          s_jm[own[r]] = mj[r];
+          s_jl[own[r]] = lj[r];
+        }
+    }
+    __syncthreads();
     const bool complete = ta == 0 && tb == w.tiles;
     if (complete) {
-      if (warp == 0) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const int row = g + 8 * r;
-          if (row >= rows) continue;
-          const float f = lj[r] == 0.f ? 0.f : 1.f / lj[r];
-          uint16_t* const to = p.out + w.b * p.out_stride + (h0 + row) * D;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            if constexpr (FMT == kKvBf16) {
-              *reinterpret_cast<uint32_t*>(to + 8 * i + 2 * qd) = pack_bf16x2(o[i][2 * r] * f, o[i][2 * r + 1] * f);
-            } else if ((i & 1) == 0) {
-              *reinterpret_cast<uint2*>(to + 8 * i + 4 * qd) =
-                  make_uint2(pack_bf16x2(o[i][2 * r] * f, o[i + 1][2 * r] * f), pack_bf16x2(o[i][2 * r + 1] * f, o[i + 1][2 * r + 1] * f));
-            }
-          }
-          if (p.lse && qd == 0)
-            p.lse[static_cast<long long>(w.b) * p.q_heads + h0 + row] = lj[r] == 0.f ? -INFINITY : (mj[r] + log2f(lj[r])) * kLn2;
-        }
+      for (int i = tid; i < rows * D / 4; i += kDecThreads) {
+        const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
+        const float4 v = *reinterpret_cast<const float4*>(s_o + row * D + d);
+        const float lr = s_jl[row], f = lr == 0.f ? 0.f : 1.f / lr;
+        *reinterpret_cast<uint2*>(p.out + w.b * p.out_stride + (h0 + row) * D + d) =
+            make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+        if (p.lse && d == 0)
+          p.lse[static_cast<long long>(w.b) * p.q_heads + h0 + row] = lr == 0.f ? -INFINITY : (s_jm[row] + log2f(lr)) * kLn2;
       }
     } else {
       int* const counters = static_cast<int*>(p.workspace);
       float* const slots = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kCounterBytes);
       constexpr int SF = kSlotFloats<D>;
-      if (warp == 0) {
-        float* const to = slots + static_cast<long long>(2 * c + (ta == 0)) * SF;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const int row = g + 8 * r;
-          if (row >= rows) continue;
-          if (qd == 0) {
-            to[row] = mj[r];
-            to[kRows + row] = lj[r];
-          }
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            if constexpr (FMT == kKvBf16) {
-              *reinterpret_cast<float2*>(to + 2 * kRows + row * D + dim(i, 0)) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
-            } else if ((i & 1) == 0) {
-              *reinterpret_cast<float4*>(to + 2 * kRows + row * D + dim(i, 0)) =
-                  make_float4(o[i][2 * r], o[i + 1][2 * r], o[i][2 * r + 1], o[i + 1][2 * r + 1]);
-            }
-          }
-        }
+      float* const to = slots + static_cast<long long>(2 * c + (ta == 0)) * SF;
+      if (tid < rows) {
+        to[tid] = s_jm[tid];
+        to[kRows + tid] = s_jl[tid];
       }
+      for (int i = tid; i < rows * D / 4; i += kDecThreads)
+        *reinterpret_cast<float4*>(to + 2 * kRows + 4 * i) = *reinterpret_cast<const float4*>(s_o + 4 * i);
       // The segment's CTAs c0 .. c1, in groups of kJoinGroup; slot of CTA x: its part either starts
       // the segment (x == c0: slot 2 x + 1) or goes on with it (slot 2 x).
       const long long s0 = u - tb, s1 = s0 + w.tiles - 1;
