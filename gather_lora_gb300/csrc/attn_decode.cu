@@ -5,7 +5,7 @@
 // Every cached byte is used once per call (2 G multiply-adds per element), so HBM bandwidth
 // bounds the kernel; what it needs is enough bytes in flight on every SM and an even share of the
 // batch's tokens for each, whatever the lengths are. The 8-bit formats are bound by instruction issue before
-// that: 850 a warp and 8 KB tile, 440 in BF16, with two warps a scheduler (registers).
+// that: 840 a warp and 8 KB tile (E4M3), 470 in BF16, with two warps a scheduler (registers).
 //
 // Measured on a GB300: 128 contexts to 16384 (8 key-value heads of 128, BF16) 733 us, 6.9 TB/s; 32 to 4096
 // 58.9 us, 5.8 TB/s; 64 to 8191 (4 heads, E4M3) 66.2 us, 5.3 TB/s; 5 to 100003 (16 heads of 64, INT8) 127 us,
