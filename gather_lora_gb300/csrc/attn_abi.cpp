@@ -143,8 +143,8 @@ int lora_attn_decode(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* ou
   if (int rc = check_heads(q_heads, cache->kv_heads)) return rc;
   if (int rc = check_scale(scale)) return rc;
   if (max_pages < 0) return fail(LORA_ERR_SIZE, "max_pages %d < 0", max_pages);
-  if (static_cast<int64_t>(max_pages) * cache->page_size > INT32_MAX)
-    return fail(LORA_ERR_SIZE, "max_pages %d x page_size %d passes 2^31 - 1 tokens", max_pages, cache->page_size);
+  if (static_cast<int64_t>(max_pages) * cache->page_size > LORA_MAX_SEQ_TOKENS)
+    return fail(LORA_ERR_SIZE, "max_pages %d x page_size %d passes %d tokens", max_pages, cache->page_size, LORA_MAX_SEQ_TOKENS);
   const int64_t width = static_cast<int64_t>(q_heads) * cache->head_dim;
   if (int rc = check_rows("q", q_row_stride, width)) return rc;
   if (int rc = check_rows("out", out_row_stride, width)) return rc;

@@ -246,8 +246,6 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
     return;
   }
   // Ends of the range: equal shares, moved to the nearer end of a segment of at most kWhole tiles.
-  if (tid == 0) s_u[1] = total;              // (the last CTA's)
-  __syncthreads();
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     long long u = mul_div(c + e, total, n);
@@ -279,7 +277,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
     }
   }
   __syncthreads();
-  const long long u0 = s_u[0], u1 = s_u[1];
+  const long long u0 = s_u[0], u1 = c + 1 < n ? s_u[1] : total;
   if (u0 >= u1) {
     zero_empty();
     return;

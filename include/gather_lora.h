@@ -393,6 +393,7 @@ typedef struct lora_kv_cache {
 
 #define LORA_MAX_HEADS 1024        /* q_heads and kv_heads in [1, 1024] */
 #define LORA_MAX_KV_ROWS (1 << 24) /* n of lora_kv_write / lora_kv_read, total rows of lora_attn_prefill */
+#define LORA_MAX_SEQ_TOKENS ((1 << 30) + ((1 << 30) - 64)) /* max_pages * page_size of lora_attn_decode: 2^31 - 64 */
 #define LORA_MAX_SEQS 8192         /* batch of lora_attn_decode / lora_attn_prefill in [0, 8192] */
                                    /* head_dim is 64 or 128 */
 

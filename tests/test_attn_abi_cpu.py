@@ -85,6 +85,9 @@ def test_decode_refusals():
     for kw, code in CACHE_FAULTS:
         assert _decode(cache=_cache(**kw)) == code, kw
     assert _decode(cache=0) == -1
+    # the longest sequence a table may describe: 2^31 - 64 tokens
+    assert _decode(cache=_cache(page=2 ** 30 - 32, pages=1), mp=2, ts=2, q=None) == -1      # allowed: on to the next check
+    assert _decode(cache=_cache(page=2 ** 31 - 63, pages=1), mp=1, ts=1, q=None) == -2
     assert _decode(b=0, q=None, out=None, lens=None, ws=None, table=None) == 0
 
 
