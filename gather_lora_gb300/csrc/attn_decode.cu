@@ -46,8 +46,10 @@ constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kStages = 3;
 constexpr int kHalfStage = 4096;                 // bytes of K (and of V) in a stage
 constexpr int kCtasPerSm = 2;
-constexpr int kJoinGroup = 16;                   // partial results joined by one CTA
+constexpr int kJoinGroup = 16;                   // partial results in a group of the first level, in flight together in a join
 constexpr int kMaxCtas = 512;                    // counters in the workspace
+constexpr int kJoinMost = kMaxCtas / kJoinGroup; // parts of one join: the groups of a segment over all CTAs
+static_assert(kMaxCtas % kJoinGroup == 0 && kJoinMost >= kJoinGroup, "a join holds a whole group, and all groups of a segment");
 constexpr int kWhole = 2 * kDecWarps;            // segments of at most this many tiles are not divided
 constexpr int kRows = 16;                        // query heads of a segment
 
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
   __shared__ long long s_sum[kDecWarps], s_u[2];
   __shared__ int s_b, s_sub, s_tiles, s_len, s_tile0, s_last;
   __shared__ float s_m[kDecWarps][kRows], s_l[kDecWarps][kRows];
-  __shared__ float s_jm[kJoinGroup * kRows], s_jl[kJoinGroup * kRows];
+  __shared__ float s_jm[kJoinMost * kRows], s_jl[kJoinMost * kRows];
   __shared__ uint64_t s_live[kDecWarps][kStages];     // valid tokens of each stage
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3;
   float* const s_o = reinterpret_cast<float*>(smem + kDecWarps * kStages * T::stage_bytes);   // two buffers of D / 8 / R accumulator tiles
@@ -694,8 +696,9 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
       };
       const int c0 = cta_of(s0), c1 = cta_of(s1);
       const int groups = (c1 - c0) / kJoinGroup + 1, gi = (c - c0) / kJoinGroup;
-      // Joins slots first, first + step, ..; the result goes to the output, or in place into slot `first`.
-      // All loads of a thread are in flight together: one trip to L2 for up to kJoinGroup parts.
+      // Joins slots first, first + step, .. (at most kJoinMost); the result goes to the output, or in place into
+      // slot `first`. A thread's loads of kJoinGroup parts are in flight together: one trip to L2 for a group, two
+      // for the groups of a segment over more than kJoinGroup^2 CTAs.
       auto join = [&](int first_cta, int count, int step, bool last) {
         auto slot_of = [&](int x) { return slots + static_cast<long long>(2 * x + (x == c0)) * SF; };
         for (int i = tid; i < count * kRows; i += kDecThreads) {
@@ -707,26 +710,31 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
         // thread: 4 consecutive dimensions of one row at a time
         for (int i = tid; i < rows * D / 4; i += kDecThreads) {
           const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
-          float4 v[kJoinGroup];
-#pragma unroll
-          for (int x = 0; x < kJoinGroup; ++x) {
-            v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (x < count) v[x] = __ldcg(reinterpret_cast<const float4*>(slot_of(first_cta + x * step) + 2 * kRows + row * D + d));
-          }
-          float mm = -INFINITY;
-          for (int x = 0; x < count; ++x) mm = fmaxf(mm, s_jm[x * kRows + row]);
-          const float ref = mm == -INFINITY ? 0.f : mm;
-          float ll = 0.f;
+          float mm = -INFINITY, ref = 0.f, ll = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int x0 = 0; x0 < count; x0 += kJoinGroup) {
+            float4 v[kJoinGroup];
 #pragma unroll
-          for (int x = 0; x < kJoinGroup; ++x) {
-            if (x < count) {
-              const float f = exp2_fast(s_jm[x * kRows + row] - ref);
-              ll += s_jl[x * kRows + row] * f;
-              acc.x += v[x].x * f;
-              acc.y += v[x].y * f;
-              acc.z += v[x].z * f;
-              acc.w += v[x].w * f;
+            for (int x = 0; x < kJoinGroup; ++x) {
+              v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (x0 + x < count)
+                v[x] = __ldcg(reinterpret_cast<const float4*>(slot_of(first_cta + (x0 + x) * step) + 2 * kRows + row * D + d));
+            }
+            if (x0 == 0) {   // (while the first loads are under way)
+              for (int x = 0; x < count; ++x) mm = fmaxf(mm, s_jm[x * kRows + row]);
+              ref = mm == -INFINITY ? 0.f : mm;
+            }
+#pragma unroll
+            for (int x = 0; x < kJoinGroup; ++x) {
+              if (x0 + x < count) {
+                const float f = exp2_fast(s_jm[(x0 + x) * kRows + row] - ref);
+                ll += s_jl[(x0 + x) * kRows + row] * f;
+                acc.x += v[x].x * f;
+                acc.y += v[x].y * f;
+                acc.z += v[x].z * f;
+                acc.w += v[x].w * f;
+              }
             }
           }
           if (last) {
