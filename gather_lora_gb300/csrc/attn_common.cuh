@@ -19,6 +19,23 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// The pair m with the largest magnitudes of 8 BF16 values taken in.
+__device__ __forceinline__ uint32_t abs_max2(uint32_t m, const uint4& x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  __nv_bfloat162 r = *reinterpret_cast<const __nv_bfloat162*>(&m);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r = __hmax2_nan(r, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Of a pair of largest magnitudes: neither is an infinity or NaN.
+__device__ __forceinline__ bool all_finite(uint32_t m) { return (m & 0xffffu) < 0x7f80u && (m >> 16) < 0x7f80u; }
+// A BF16 pair with what is not finite set to zero.
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t x) {
+  if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+  if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+  return x;
+}
+
 // Four E4M3 codes -> two pairs of f16 (low byte first). Every E4M3 value is exact in f16.
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
   asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"

@@ -21,23 +21,28 @@
 // CTA: one per SM, persistent over the items. Two warpgroups each own one row tile: thread = row, with its
 // running reference and sum in registers. They alternate on the tensor pipe: while one does its softmax,
 // the other's P V and the next Q K^T run. Warp 8 issues the MMAs, warp 9 picks the items and issues TMA: K and
-// V tiles of 128 keys through one ring of stages, the next item's Q as soon as the last Q K^T has read the old
-// (warps 10 and 11 only complete the warpgroup that gives its registers to the softmax).
+// V tiles of 128 keys through one ring of stages, the next item's Q as soon as the last Q K^T has read the old.
+// Warps 10 and 11 look through V tiles (below).
 // Tensor memory: two (D = 128) or three (D = 64) score buffers of 128 columns, P as BF16 pairs over the first
 // half of its scores, and O0, O1.
 //
 // Softmax: exponents are base 2. The reference that exponents are relative to follows the running maximum
 // only when that has grown by more than 2^8 (one vote per warp): then l and O are multiplied by
-// 2^(old - new); otherwise weights up to 2^8 are kept as they are, which BF16 and fp32 hold alike.
+// 2^(old - new); otherwise weights are kept as they are. Exponents are 8 less than the reference says, so
+// weights stay at most 1 (O overflows only where sums of V itself would) and BF16 and fp32 hold them alike.
 //
 // Rounding to fewer bits: the weights to BF16 before P V (the tensor cores' operand type), the output once.
 // Keys that a row does not see get weight zero, but zero times NaN or infinity in their V rows is NaN in
-// an MMA: a row whose result is not finite is computed again key by key over its own keys (attn_row.cuh).
+// an MMA. Only the last key tiles of an item (at most three) hold keys that some row does not see: warps 10 and 11
+// look through the V of those, beside the scores' MMAs and the softmax. What is not finite they set to zero for
+// the P V, and add to the result rows that do see it once those are stored: a price by the tile, whatever the
+// length of the context (NaN throughout a prompt of 8192: 0.41 ms against 0.35). On clean data the look costs 12 packed
+// prompts 75 -> 78 us, a prompt of 8192 1%; with the waits or the additions in the other warps' loops it was 80 to 91.
 #include <cooperative_groups.h>
 
 #include <type_traits>
 
-#include "attn_row.cuh"
+#include "attn_common.cuh"
 #include "tc05.cuh"
 
 namespace cg = cooperative_groups;
@@ -51,13 +56,14 @@ namespace {
 constexpr unsigned kPrefillTimeoutBit = 0x2u;   // LORA_DEV_TIMEOUT
 constexpr int kTile = 128;                      // rows of a tile, keys of a tile
 constexpr int kSoftmaxWarps = 8;
-constexpr int kPreMmaWarp = 8, kPreTmaWarp = 9;
+constexpr int kPreMmaWarp = 8, kPreTmaWarp = 9, kPreScanWarp = 10, kScanWarps = 2;
 constexpr int kPreThreads = 384;
 // Registers a thread: 168 at launch (65536 over 12 warps); the helper warpgroup gives 96 away, the softmax
 // warpgroups hold a whole row of scores: 2 * 216 + 72 = 3 * 168.
 constexpr int kHelperRegs = 72, kSoftmaxRegs = 216;
 constexpr int kOutBytes = 4096;                 // staging of a warp's results: 32 rows x 64 columns
 constexpr int kItems = 4;                       // depth of the item ring
+constexpr int kJobs = 8;                        // V tiles to look through: at most 4 in the ring's stages, and the end
 constexpr float kRescale = 8.f;                 // reference moves when the maximum grew by 2^8
 
 template <int D>
@@ -79,16 +85,21 @@ struct PrefillItem {
   int n[2];            // key tiles of each row tile (split: of this CTA's part of the keys)
   int shift;           // keys of the sequence before the first of them (0 unless split)
   int h0, heads, kvh;  // first query head, how many, key-value head
+  int whole;           // keys that every row sees (of this CTA's part): key tiles from whole / 128 on are looked through
 };
 
 struct PrefillCtl {
-  unsigned long long full[8], empty[8];
+  unsigned long long full[8], empty[8];   // (K tiles lie in even stages, V tiles in odd ones, whose `full` takes two arrivals)
   unsigned long long q_full, q_empty;
   unsigned long long s_full[2][2], p_ready[2][2][2], o_done[2][2];   // [row tile][parity of its key tile] ([half])
   unsigned long long item_full[kItems], item_empty[kItems];
   unsigned long long drain, next_full;
+  unsigned long long landed[kJobs];    // the V tile of a job is there; `full` follows when it has been looked through
   uint4 next;                          // the answer to ask_next_block
-  PrefillItem item[kItems];
+  PrefillItem item[2 * kItems];        // (twice the ring's depth: an item can be read until its rows are stored)
+  int2 job[kJobs];                     // a V tile to look through: (item, stage + 16 (first row + 256 if the item's last)); item -1: the end
+  int stored[kSoftmaxWarps];           // items whose result rows the warp has stored
+  int bad[kScanWarps];                 // (split) a part's V held values that are not finite, by halves of the columns
   uint32_t tmem;
   int failed;
 };
@@ -175,21 +186,76 @@ __device__ __forceinline__ long long next_block(uint32_t from) {
 
 }  // namespace
 
-// Query row r, head h, over its first `keys` keys from row k0 on, by one warp: result and lse.
+// What was set to zero in half `half` of the columns of an item's V (its keys from w.whole on, rounded down to 8) is added to the
+// stored result rows that see it, as it is, since their weights are positive. By a warp.
 template <int D>
-__device__ __noinline__ void row_again(const PrefillArgs& p, int r, int h, int kvh, int k0, int keys, float sl2, int lane) {
-  constexpr int E = D / 32;
-  RowState<D> st;
-  st.begin(p.q + r * p.q_stride + h * D, sl2, lane);
-  for (int j = 0; j < keys; ++j) {
-    float k[E], v[E];
-    load_bf16<E>(p.k + (k0 + j) * p.k_stride + kvh * D + lane * E, k);
-    load_bf16<E>(p.v + (k0 + j) * p.v_stride + kvh * D + lane * E, v);
-    st.add(k, v);
+__device__ __forceinline__ void add_not_finite(const PrefillArgs& p, const PrefillItem& w, int half, int lane) {
+  const int col = half * (D / 2) + 2 * lane;           // two columns a lane
+  const bool mine = lane < D / 4;
+  const uint16_t* const v = p.v + w.k0 * p.v_stride + w.kvh * D + col;
+  float s0 = 0.f, s1 = 0.f;                            // of the keys so far; 0: nothing
+  int k = w.whole & ~7;
+  for (int tok = w.tok0; tok < min(w.tok0 + 2 * p.tile_tokens, w.lq); ++tok) {
+    for (const int seen = min(w.lk, tok + 1 + w.lk - w.lq); k < seen; ++k) {
+      const uint32_t x = mine ? __ldg(reinterpret_cast<const uint32_t*>(v + k * p.v_stride)) : 0u;
+      if ((x & 0x7f80u) == 0x7f80u) s0 += __uint_as_float(x << 16);
+      if ((x & 0x7f800000u) == 0x7f800000u) s1 += __uint_as_float(x & 0xffff0000u);
+    }
+    if (!__any_sync(0xffffffffu, s0 != 0.f || s1 != 0.f)) continue;
+    uint16_t* const out = p.out + (w.q0 + tok - w.tok0) * p.out_stride + w.h0 * D + col;
+#pragma unroll 4
+    for (int g = 0; g < w.heads; ++g) {
+      uint32_t* const at = reinterpret_cast<uint32_t*>(out + g * D);
+      if (!mine) continue;
+      const uint32_t x = *at;
+      *at = pack_bf16x2(__uint_as_float(x << 16) + s0, __uint_as_float(x & 0xffff0000u) + s1);
+    }
   }
-  for (int e = 0; e < E; ++e)
-    p.out[r * p.out_stride + h * D + lane * E + e] = f32_to_bf16_bits(st.l == 0.f ? 0.f : st.acc[e] / st.l);
-  if (p.lse && lane == 0) p.lse[static_cast<long long>(r) * p.q_heads + h] = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
+}
+
+// Sets what is not finite in half `half` of the columns of a V tile (rows first .. 127, first a multiple of 8) to zero, for
+// the tensor cores; true if there was any. By a warp: 16-byte chunks, 8 of half a row by D = 128 (4 rows at a time),
+// 4 by D = 64 (8 rows).
+template <int D>
+__device__ __forceinline__ bool zero_not_finite(uint32_t tile, int first, int half, int lane) {
+  constexpr int across = D / 16, rows = 32 / across;
+  const int r0 = lane / across, ch = lane % across + (D == 64 ? half * 4 : 0);
+  const uint32_t from = tile + (D == 128 ? half * (kTile * 128) : 0) + r0 * 128;
+  auto at = [&](int row) { return from + row * 128 + ((ch ^ ((row + r0) & 7)) << 4); };
+  uint32_t m = 0;
+#pragma unroll 2
+  for (int row = first; row < kTile; row += rows) m = abs_max2(m, lds128(at(row)));
+  if (!__any_sync(0xffffffffu, !all_finite(m))) return false;
+  for (int row = first; row < kTile; row += rows) {
+    const uint4 x = lds128(at(row));
+    sts128(at(row), make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w)));
+  }
+  fence_proxy_async_smem();
+  return true;
+}
+
+// How many items each softmax warp has stored: behind the rows themselves.
+__device__ __forceinline__ void publish(int* at, int v) {
+  asm volatile("st.release.cta.shared::cta.s32 [%0], %1;\n" ::"r"(smem_u32(at)), "r"(v) : "memory");
+}
+__device__ __forceinline__ int published(const int* at) {
+  int v;
+  asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];\n" : "=r"(v) : "r"(smem_u32(at)) : "memory");
+  return v;
+}
+// Wait (bounded) until all of them have stored `items` items.
+__device__ __forceinline__ bool wait_stored(PrefillCtl& c, int items, int lane) {
+  const long long t0 = clock64();
+  while (!__all_sync(0xffffffffu, published(&c.stored[lane % kSoftmaxWarps]) >= items)) {
+    if (__any_sync(0xffffffffu, failed(c))) return false;
+    if (__any_sync(0xffffffffu, clock64() - t0 > kWaitLimitCycles)) {
+      *reinterpret_cast<volatile int*>(&c.failed) = 1;
+      atomicOr(&g_prefill_status, kPrefillTimeoutBit);
+      return false;
+    }
+    __nanosleep(100);
+  }
+  return true;
 }
 
 // SPLIT: a cluster of CTAs takes one item, each an equal part of its key tiles, and joins through the others'
@@ -198,6 +264,7 @@ template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs p) {
   using Sh = PrefillShape<D>;
   constexpr int NS = Sh::stages;
+  static_assert(NS % 2 == 0 && NS / 2 + 1 <= kJobs && NS <= 16 && 2 * kItems <= 16 && kScanWarps == 2, "jobs");
   extern __shared__ unsigned char prefill_smem_raw[];
   const uint32_t raw = smem_u32(prefill_smem_raw), pad = ((raw + 1023u) & ~1023u) - raw;
   const uint32_t q_s = raw + pad, ring = q_s + 2 * Sh::tile_bytes;
@@ -209,7 +276,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(smem_u32(&c.full[s]), 1);
+      mbar_init(smem_u32(&c.full[s]), 1 + (s & 1));
       mbar_init(smem_u32(&c.empty[s]), 1);
     }
     mbar_init(smem_u32(&c.q_full), 1);
@@ -224,9 +291,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       mbar_init(smem_u32(&c.item_full[i]), 1);
       mbar_init(smem_u32(&c.item_empty[i]), kSoftmaxWarps + 1);
     }
+    for (int i = 0; i < kJobs; ++i) mbar_init(smem_u32(&c.landed[i]), 1);
     mbar_init(smem_u32(&c.drain), 1);
     mbar_init(smem_u32(&c.next_full), 1);
     c.failed = 0;
+    for (int i = 0; i < kSoftmaxWarps; ++i) c.stored[i] = 0;
+    for (int i = 0; i < kScanWarps; ++i) c.bad[i] = 0;
     mbar_fence_init();
   }
   if (warp == kPreMmaWarp) {
@@ -246,10 +316,39 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
 
   if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kHelperRegs));
-  if (warp == kPreTmaWarp) {
+  if (warp >= kPreScanWarp) {
+    // ================ V tiles that not every row sees whole ================
+    // Each warp takes half of the columns, from the first key on that not every row sees: what is not finite is set to
+    // zero, then the tile is `full`. A job's barrier is used again only when its stage is, which is after that.
+    const int half = warp - kPreScanWarp;
+    bool bad = false;                    // in this item
+    for (uint32_t job = 0;; ++job) {
+      pre_wait(c, c.landed[job % kJobs], (job / kJobs) & 1);
+      __syncwarp();
+      const int it = __shfl_sync(0xffffffffu, failed(c) ? -1 : c.job[job % kJobs].x, 0);
+      if (it < 0) break;
+      const int what = __shfl_sync(0xffffffffu, c.job[job % kJobs].y, 0), vs = what & 15, first = ((what >> 4) & 127) & ~7;
+      bad |= zero_not_finite<D>(ring + vs * Sh::tile_bytes, first, half, lane);
+      const bool add = !SPLIT && bad && (what >> 12);
+      PrefillItem w;
+      if (add) w = c.item[it % (2 * kItems)];          // (its slot is safe until the tile is `full`)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c.full[vs]));
+      if (add) {
+        bad = false;
+        if (wait_stored(c, it + 1, lane)) add_not_finite<D>(p, w, half, lane);
+      }
+    }
+    if constexpr (SPLIT) {               // the first part is told, and adds them when all have stored their rows
+      cluster.sync();
+      met = 1;
+      if (lane == 0 && bad && !failed(c)) *cluster.map_shared_rank(&c.bad[half], 0) = 1;
+    }
+  } else if (warp == kPreTmaWarp) {
     // ======================= items and TMA loads ==========================
     int b0 = 0, it = 0, items = 0;      // chunk of 32 sequences under search; items, those with keys
     uint32_t kv = 0;                    // ring tiles issued
+    uint32_t jobs = 0, by_job = 0;      // V tiles given to the look; stages whose last tile was one
     long long base = 0;                 // row-tile pairs before sequence b0
     bool go = true;
     auto ask = [&]() {                  // (lane 0) the next item, once the current one's loads are nearly out
@@ -321,10 +420,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
           w.shift = 0;
         }
         w.k0 = k0 + w.shift;
+        w.whole = max(0, min(lk, w.tok0 + 1 + lk - lq) - w.shift);   // (the first row sees the fewest)
         w.kvh = sub / blocks;
         w.h0 = w.kvh * G + (sub - w.kvh * blocks) * GB;
         w.heads = min(GB, w.kvh * G + G - w.h0);
-        c.item[sl] = w;
+        c.item[it % (2 * kItems)] = w;
         mbar_arrive(smem_u32(&c.item_full[sl]));
         const int n = max(w.n[0], w.n[1]);
         bool asked = !SPLIT && go && n == 0;
@@ -347,7 +447,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
             const uint32_t s = kv % NS;
             if (kv >= NS && pre_wait(c, c.empty[s], ((kv / NS) - 1) & 1)) break;
             ++kv;
-            const uint32_t fb = smem_u32(&c.full[s]), to = ring + s * Sh::tile_bytes;
+            const bool look = (j & 1) && (j >> 1) >= w.whole / kTile;
+            const uint32_t fb = smem_u32(look ? &c.landed[jobs % kJobs] : &c.full[s]), to = ring + s * Sh::tile_bytes;
+            by_job &= ~(1u << s);
+            if ((j & 1) && !look) mbar_arrive(fb);
+            if (look) {
+              const int row = (j >> 1) == w.whole / kTile ? w.whole % kTile : 0;
+              c.job[jobs++ % kJobs] = make_int2(it, s + 16 * (row + (j == 2 * n - 1 ? 256 : 0)));
+              by_job |= 1u << s;
+            }
             mbar_arrive_expect_tx(fb, Sh::tile_bytes);
 #pragma unroll
             for (int a = 0; a < Sh::atoms; ++a)
@@ -365,9 +473,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       idx = __shfl_sync(0xffffffffu, idx, 0);
       go = __shfl_sync(0xffffffffu, go, 0);
     }
+    if (lane == 0) {                     // no more jobs
+      c.job[jobs % kJobs].x = -1;
+      mbar_arrive(smem_u32(&c.landed[jobs % kJobs]));
+    }
     if (lane == 0 && failed(c)) {        // let the loads in flight land
-      for (uint32_t k = kv > NS ? kv - NS : 0; k < kv; ++k)
-        mbar_wait_limit(smem_u32(&c.full[k % NS]), (k / NS) & 1, kDrainLimitCycles);
+      for (uint32_t k = kv > NS ? kv - NS : 0; k < kv; ++k) {
+        if (!((by_job >> (k % NS)) & 1)) mbar_wait_limit(smem_u32(&c.full[k % NS]), (k / NS) & 1, kDrainLimitCycles);
+      }
+      for (uint32_t k = jobs > NS / 2 ? jobs - NS / 2 : 0; k < jobs; ++k)
+        mbar_wait_limit(smem_u32(&c.landed[k % kJobs]), (k / kJobs) & 1, kDrainLimitCycles);
       if (items > 0) mbar_wait_limit(smem_u32(&c.q_full), (items - 1) & 1, kDrainLimitCycles);
     }
     __syncwarp();
@@ -425,12 +540,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     constexpr std::integral_constant<int, 0> r0{};
     constexpr std::integral_constant<int, 1> r1{};
     for (int it = 0;; ++it) {
-      const int sl = it % kItems;
+      const int sl = it % kItems, si = it % (2 * kItems);
       pre_wait(c, c.item_full[sl], (it / kItems) & 1);
       __syncwarp();
-      const bool valid = __shfl_sync(0xffffffffu, c.item[sl].valid && !failed(c), 0);
-      n0 = __shfl_sync(0xffffffffu, c.item[sl].n[0], 0);
-      n1 = __shfl_sync(0xffffffffu, c.item[sl].n[1], 0);
+      const bool valid = __shfl_sync(0xffffffffu, c.item[si].valid && !failed(c), 0);
+      n0 = __shfl_sync(0xffffffffu, c.item[si].n[0], 0);
+      n1 = __shfl_sync(0xffffffffu, c.item[si].n[1], 0);
       n = max(n0, n1);
       if (lane == 0) mbar_arrive(smem_u32(&c.item_empty[sl]));
       __syncwarp();
@@ -485,7 +600,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       const int sl = it % kItems;
       pre_wait(c, c.item_full[sl], (it / kItems) & 1);
       __syncwarp();
-      const PrefillItem w = c.item[sl];
+      const PrefillItem w = c.item[it % (2 * kItems)];
       const bool valid = __shfl_sync(0xffffffffu, w.valid && !failed(c), 0);
       if (lane == 0) mbar_arrive(smem_u32(&c.item_empty[sl]));
       if (!valid) break;
@@ -494,7 +609,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       const int lim = live ? max(0, min(w.lk, tok + 1 + w.lk - w.lq)) - w.shift : 0x7fffffff;   // keys the row sees, from the first tile on
       const int least = __reduce_min_sync(0xffffffffu, lim);
       uint32_t buf = Sh::buf(i, 0);
-      float ref = -INFINITY, l = 0.f;      // exponents are relative to ref (in units of raw scores)
+      float ref = -INFINITY, l = 0.f;      // exponents are relative to ref (in units of raw scores), less kRescale
       for (int j = 0; j < n; ++j, ++t) {
         const uint32_t col_s = lane_base + buf * kTile;
         if constexpr (Sh::bufs == 3) buf = buf == 0 ? 2 : buf - 1;   // (2 j + i) mod 3
@@ -543,7 +658,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
             tmem_st32(col_o + q * 32, o);
           }
         }
-        const float off = ref == -INFINITY ? 0.f : -ref * sl2;   // (nothing seen: every weight is 0)
+        const float off = ref == -INFINITY ? 0.f : __fmaf_rn(-ref, sl2, -kRescale);   // (nothing seen: every weight is 0)
         const uint64_t sl2p = pair(sl2, sl2), offp = pair(off, off);
         uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -606,7 +721,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         tc_fence_before();
         if (p.lse && live && part == 0 && !failed(c))
           p.lse[static_cast<long long>(w.q0 + i * TT + t_in) * p.q_heads + w.h0 + g] =
-              all_l == 0.f ? -INFINITY : (all_ref * sl2 + log2f(all_l)) * kLn2;
+              all_l == 0.f ? -INFINITY : (all_ref * sl2 + kRescale + log2f(all_l)) * kLn2;
         cluster.sync();
         // Rows part, part + parts, ..: the sum over the parts, a warp a row.
         constexpr int E = D / 32;
@@ -630,20 +745,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
               sum[0] += v.x; sum[1] += v.y;
             }
           }
-          float check = 0.f;
+          uint32_t v[E / 2];
 #pragma unroll
-          for (int e = 0; e < E; ++e) check = __fmaf_rn(sum[e], 0.f, check);
-          const int q_row = w.q0 + ri * TT + x_in, h = w.h0 + gg;
-          if (__any_sync(0xffffffffu, !(check == 0.f))) {
-            row_again<D>(p, q_row, h, w.kvh, w.k0 - w.shift, max(0, min(w.lk, tk + 1 + w.lk - w.lq)), sl2, lane);
-          } else {
-            uint32_t v[E / 2];
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) v[e] = pack_bf16x2(sum[2 * e], sum[2 * e + 1]);
-            uint16_t* const out = p.out + q_row * p.out_stride + h * D + lane * E;
-            if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(v[0], v[1]);
-            else *reinterpret_cast<uint32_t*>(out) = v[0];
-          }
+          for (int e = 0; e < E / 2; ++e) v[e] = pack_bf16x2(sum[2 * e], sum[2 * e + 1]);
+          uint16_t* const out = p.out + (w.q0 + ri * TT + x_in) * p.out_stride + (w.h0 + gg) * D + lane * E;
+          if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(v[0], v[1]);
+          else *reinterpret_cast<uint32_t*>(out) = v[0];
         }
         met = 2;
         continue;
@@ -652,7 +759,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       // (one row per lane, 16 bytes each, wrote 32 and held up the SM's loads: 5000 clocks an item, now 1000).
       uint16_t* const to = p.out + static_cast<long long>(w.q0 + i * TT + t_in) * p.out_stride + (w.h0 + g) * D;
       const uint32_t lives = __ballot_sync(0xffffffffu, live);
-      bool bad = false;
       if (n > 0) {
         pre_wait(c, c.o_done[i][(t - 1) & 1], ((t - 1) >> 1) & 1);
         __syncwarp();
@@ -661,7 +767,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const uint64_t invp = pair(inv, inv);
         const uint32_t stage = out_s + warp * kOutBytes;
-        uint64_t check[2] = {0, 0};          // stays 0 while all results are finite
 #pragma unroll
         for (int half = 0; half < D / 64; ++half) {
           uint32_t o[2][32];
@@ -675,9 +780,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
               uint32_t r[4];
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
-                const uint64_t f = mul2(pair(__uint_as_float(o[q][e + 2 * x]), __uint_as_float(o[q][e + 2 * x + 1])), invp);
-                check[x & 1] = fma2(f, 0, check[x & 1]);
-                const float2 v = unpair(f);
+                const float2 v = unpair(mul2(pair(__uint_as_float(o[q][e + 2 * x]), __uint_as_float(o[q][e + 2 * x + 1])), invp));
                 r[x] = pack_bf16x2(v.x, v.y);
               }
               sts128(stage + lane * 128 + (((q * 4 + e / 8) ^ (lane & 7)) << 4), make_uint4(r[0], r[1], r[2], r[3]));
@@ -693,26 +796,23 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
           __syncwarp();
         }
         tc_fence_before();
-        const float2 sum0 = unpair(add2(check[0], check[1]));
-        bad = live && !(sum0.x + sum0.y == 0.f);
       } else if (live) {
 #pragma unroll
         for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(to + e) = make_uint4(0, 0, 0, 0);
       }
       const long long out_row = w.q0 + i * TT + t_in;
-      if (p.lse && live) p.lse[out_row * p.q_heads + w.h0 + g] = l == 0.f ? -INFINITY : (ref * sl2 + log2f(l)) * kLn2;
-      // Rows that are not finite: once more, over their own keys alone.
-      for (uint32_t left = __ballot_sync(0xffffffffu, bad); left; left &= left - 1) {
-        const int src = __ffs(left) - 1;
-        const int r = w.q0 + i * TT + __shfl_sync(0xffffffffu, t_in, src), h = w.h0 + __shfl_sync(0xffffffffu, g, src);
-        const int keys = __shfl_sync(0xffffffffu, lim, src);
-        row_again<D>(p, r, h, w.kvh, w.k0, keys, sl2, lane);
-      }
+      if (p.lse && live) p.lse[out_row * p.q_heads + w.h0 + g] = l == 0.f ? -INFINITY : (ref * sl2 + kRescale + log2f(l)) * kLn2;
+      __syncwarp();
+      if (lane == 0) publish(&c.stored[warp], it + 1);
     }
   }
 
   if constexpr (SPLIT) {   // every thread of the cluster meets three times, whatever became of its item
     for (int x = met; x < 3; ++x) cluster.sync();
+    if (part == 0 && warp >= kPreScanWarp && !failed(c)) {
+      const int half = warp - kPreScanWarp;
+      if (*const_cast<const volatile int*>(&c.bad[half])) add_not_finite<D>(p, c.item[0], half, lane);
+    }
   }
   tc_fence_before();
   __syncthreads();
