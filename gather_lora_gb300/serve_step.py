@@ -77,7 +77,7 @@ class AttentionLayer:
         while len(pages) * self.page_size < first + n:
             pages.append(self.free.pop())
         t = torch.arange(first, first + n)
-        return torch.tensor(pages)[t // self.page_size] * self.page_size + t % self.page_size
+        return torch.tensor(pages, dtype=torch.int64)[t // self.page_size] * self.page_size + t % self.page_size
 
     def _write(self, qkv, slots):
         q, k, _ = self.widths
