@@ -71,6 +71,20 @@ class AttentionLayer:
         self._fold("o", a, y, 0, seq_slot)
         return y
 
+    def _check(self, x, seqs, counts, seq_slot):
+        """Refuse a call before any of it changes the layer: rows that do not fit, a sequence twice, too few free pages."""
+        if (x.dim() != 2 or x.shape != (sum(counts), self.hidden) or x.stride(1) != 1 or len(seqs) != len(counts) or
+                min(counts, default=0) < 0):
+            raise ValueError(f"rows {tuple(x.shape)} for {len(seqs)} sequences with {list(counts)} rows of {self.hidden}")
+        if seq_slot.shape != (x.shape[0],) or seq_slot.dtype != torch.int32:
+            raise ValueError(f"seq_slot is int32 [{x.shape[0]}]: got {seq_slot.dtype} {tuple(seq_slot.shape)}")
+        if len(set(seqs)) != len(seqs):
+            raise ValueError(f"a sequence is there twice: {list(seqs)}")
+        need = sum(max(0, -(-(self.lengths.get(s, 0) + n) // self.page_size) - len(self.tables.get(s, [])))
+                   for s, n in zip(seqs, counts))
+        if need > len(self.free):
+            raise RuntimeError(f"{need} pages are needed, {len(self.free)} are free: release a sequence first")
+
     def _slots(self, seq, first, n):
         """Cache slots of tokens first .. first + n of a sequence, pages taken as they are needed."""
         pages = self.tables.setdefault(seq, [])
@@ -86,6 +100,7 @@ class AttentionLayer:
 
     def prefill(self, x, seqs, counts, seq_slot):
         """Rows x [sum(counts), hidden] of the sequences `seqs`, each after what of it is cached already."""
+        self._check(x, seqs, counts, seq_slot)
         before = [self.lengths.get(s, 0) for s in seqs]
         slots = torch.cat([self._slots(s, b, n) for s, b, n in zip(seqs, before, counts)]).to(self.device)
         qkv = self._qkv(x, seq_slot)
@@ -111,6 +126,7 @@ class AttentionLayer:
 
     def decode(self, x, seqs, seq_slot):
         """One new token per sequence: x [len(seqs), hidden]."""
+        self._check(x, seqs, [1] * len(seqs), seq_slot)
         slots = torch.cat([self._slots(s, self.lengths.get(s, 0), 1) for s in seqs]).to(self.device)
         qkv = self._qkv(x, seq_slot)
         self._write(qkv, slots)
