@@ -235,7 +235,7 @@ def lora_moe_gather_bgmv(x, x_row_stride, base_out, out_row_stride, indices, n_r
 
 def lora_kv_write(k, k_row_stride, v, v_row_stride, slots, n, cache, stream=None):
     """K and V rows into their cache slots (see lora_kv_write in include/gather_lora.h). slots:
-    int64 [n]; cache: a KvCache."""
+    int64 [n], no slot twice; cache: a KvCache."""
     return _check(load().lora_kv_write(_addr(k), k_row_stride, _addr(v), v_row_stride, _addr(slots), n,
                                        _cache(cache), _stream(stream)))
 

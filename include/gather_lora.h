@@ -402,8 +402,9 @@ typedef struct lora_kv_cache {
  *
  * Row i of k and of v holds kv_heads * head_dim BF16 values (row strides in
  * elements, multiples of 8); slots[i] = page * page_size + slot in the page, any
- * value outside [0, num_pages * page_size) skips the row. Two rows of one call
- * with the same slot leave one of the two, which one is not defined.
+ * value outside [0, num_pages * page_size) skips the row (padding wants one). Two
+ * rows of one call with the same slot leave that slot undefined: codes of one may
+ * stand beside the scale or another head of the other. No other slot is touched.
  * E4M3 and INT8, per row and head, Q = 448 or 127, a = the largest magnitude:
  *   scale = a / Q,  code = round(x * (Q / a))    (f32 operations, ties to even);
  *   a < 2^-100: scale 0 and codes 0; a value that is not finite: scale NaN and
