@@ -465,7 +465,8 @@ int lora_attn_decode(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* ou
  *   q, out    [total_q, row stride] BF16, q_heads * head_dim values used
  *   k, v      [total_k, row stride] BF16, kv_heads * head_dim values used
  *   cu_q, cu_k  [batch + 1] int32, non-decreasing, in [0, total_q] / [0, total_k]
- *             (a sequence whose offsets are not is left out); query rows of no
+ *             (a sequence whose own two fall or leave that range is left out;
+ *             rows of sequences that overlap are not defined); query rows of no
  *             sequence stay unchanged
  *   lse       optional [total_q, q_heads] f32: ln sum_j exp(z_j)
  *   scale     positive and finite
