@@ -2,14 +2,15 @@
 //
 // For sequence b and the G query heads that share key-value head h:
 //   z[g, t] = scale (q_g . k_t),  out_g = sum_t softmax(z_g)_t v_t.
-// Every cached byte is used once per call (2 G multiply-adds per element), so HBM bandwidth
-// bounds the kernel; what it needs is enough bytes in flight on every SM and an even share of the
-// batch's tokens for each, whatever the lengths are. The 8-bit formats are bound by instruction issue before
+// With up to 16 query heads a group every cached byte is read once per call (2 G multiply-adds per element), so
+// HBM bandwidth bounds the kernel; what it needs is enough bytes in flight on every SM and an even share of the
+// batch's tokens for each, whatever the lengths are. Larger groups read it once for each block of 16 heads. The 8-bit formats are bound by instruction issue before
 // that: 840 a warp and 8 KB tile (E4M3), 470 in BF16, with two warps a scheduler (registers).
 //
 // Measured on a GB300: 128 contexts to 16384 (8 key-value heads of 128, BF16) 733 us, 6.9 TB/s; 32 to 4096
-// 58.9 us, 5.8 TB/s; 64 to 8191 (4 heads, E4M3) 66.2 us, 5.3 TB/s; 5 to 100003 (16 heads of 64, INT8) 127 us,
-// 4.8 TB/s; one of 700 tokens 9.1 us, all latency: plan 1.2, first loads 1, tile 0.6, joins 3.
+// 58.8 us, 5.8 TB/s; 64 to 8191 (4 heads, E4M3) 65.7 us, 5.3 TB/s; 5 to 100003 (16 heads of 64, INT8) 128 us,
+// 4.8 TB/s; one of 100000 with one key-value head (BF16, 304 parts in 19 groups) 20.4 us; one of 700 tokens 9.2 us,
+// all latency: plan 1.2, first loads 1, tile 0.6, join 3.
 //
 // Split. The work unit is a tile of kTile tokens of one segment: a segment is (sequence, key-value
 // head, block of 16 query heads). All tiles of the batch, segment after segment, are cut into equal

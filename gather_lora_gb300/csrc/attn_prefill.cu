@@ -9,9 +9,9 @@
 // warpgroup's chain per block: softmax 1300 clocks, then its P V and next Q K^T; two warpgroups hide most
 // of each other's.
 //
-// Measured on a GB300 (32 heads over 4, head_dim 128): a prompt of 8192 340 us in a burst, 1.62 PFLOP/s, and
-// 370 held under the 1400 W limit; 12 packed prompts to 1100 (32 over 8) 75 us; chunks of up to 513 rows after
-// 6000 keys at head_dim 64 50 us; one prompt of 37 rows 6.7 us.
+// Measured on a GB300 (32 heads over 4, head_dim 128): a prompt of 8192 345 us in a burst, 1.59 PFLOP/s, and
+// 370 held under the 1400 W limit; 12 packed prompts to 1100 (32 over 8) 78 us; chunks of up to 513 rows after
+// 6000 keys at head_dim 64 50 us; one prompt of 37 rows 6.9 us.
 //
 // Rows of a tile. The G query heads that share a key-value head read the same keys, so a 128-row tile
 // holds TT = 128 / G tokens x G heads (row = token * G + head; one 3-D TMA box): short prompts and
