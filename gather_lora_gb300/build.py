@@ -18,7 +18,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgather_lora.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-Xcompiler", "-Wall"]
-SOURCES = ["kernels.cu", "dense.cu", "kv_cache.cu", "attn_decode.cu", "attn_prefill.cu", "abi.cpp", "attn_abi.cpp"]
+SOURCES = ["kernels.cu", "dense.cu", "kv_cache.cu", "attn_decode.cu", "attn_decode_window.cu",
+           "attn_prefill.cu", "attn_chunk.cu", "rope.cu", "abi.cpp", "attn_abi.cpp"]
 
 
 def nvcc() -> str:

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <cstring>
 
 #include "abi_common.h"
 #include "attn_types.h"
@@ -106,6 +107,103 @@ int kv_rows(const void* k, int64_t k_row_stride, const void* v, int64_t v_row_st
   return LORA_OK;
 }
 
+int check_table(int32_t max_pages, int64_t table_stride, const lora_kv_cache* cache) {
+  if (max_pages < 0) return fail(LORA_ERR_SIZE, "max_pages %d < 0", max_pages);
+  if (static_cast<int64_t>(max_pages) * cache->page_size > LORA_MAX_SEQ_TOKENS)
+    return fail(LORA_ERR_SIZE, "max_pages %d x page_size %d passes %d tokens", max_pages, cache->page_size, LORA_MAX_SEQ_TOKENS);
+  if (table_stride < max_pages) return fail(LORA_ERR_STRIDE, "table_stride %lld < max_pages %d", (long long)table_stride, max_pages);
+  return LORA_OK;
+}
+
+int check_window(int32_t window, int32_t sinks) {
+  if (window < 1) return fail(LORA_ERR_SIZE, "window %d < 1", window);
+  return sinks >= 0 ? LORA_OK : fail(LORA_ERR_SIZE, "sinks %d < 0", sinks);
+}
+
+// What lora_qk_rope and lora_kv_append share: the rotation, positions and norms, and a pair of q rows.
+int rope_args(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* q_out, int64_t q_out_row_stride, int32_t n, int32_t q_heads,
+              const lora_rope* rope, const int32_t* positions, int64_t position_stride, const lora_bf16_t* q_norm,
+              const lora_bf16_t* k_norm, float eps, glora::RopeArgs& a) {
+  if (n < 0 || n > LORA_MAX_KV_ROWS) return fail(LORA_ERR_SIZE, "n %d outside [0, %d]", n, LORA_MAX_KV_ROWS);
+  if (q_heads < 0 || q_heads > LORA_MAX_HEADS) return fail(LORA_ERR_SIZE, "q_heads %d outside [0, %d]", q_heads, LORA_MAX_HEADS);
+  if (!rope) return fail(LORA_ERR_NULL, "rope is NULL");
+  if (int rc = check_head_dim(rope->head_dim)) return rc;
+  if (rope->rotary_dim < 0 || rope->rotary_dim > rope->head_dim || rope->rotary_dim % 8)
+    return fail(LORA_ERR_SIZE, "rotary_dim %d is not a multiple of 8 in [0, %d]", rope->rotary_dim, rope->head_dim);
+  if (rope->axes < 1 || rope->axes > LORA_MAX_ROPE_AXES)
+    return fail(LORA_ERR_SIZE, "axes %d outside [1, %d]", rope->axes, LORA_MAX_ROPE_AXES);
+  for (int j = 0; j < rope->rotary_dim / 2; ++j)
+    if (rope->axis[j] >= rope->axes) return fail(LORA_ERR_SIZE, "axis %d of pair %d is not below axes %d", rope->axis[j], j, rope->axes);
+  if (position_stride < n) return fail(LORA_ERR_STRIDE, "position_stride %lld < n %d", (long long)position_stride, n);
+  if ((q_norm || k_norm) && !(std::isfinite(eps) && eps >= 0.f)) return fail(LORA_ERR_SIZE, "eps %g is not finite and >= 0", (double)eps);
+  if (q_heads) {
+    const int64_t width = static_cast<int64_t>(q_heads) * rope->head_dim;
+    if (int rc = check_rows("q", q_row_stride, width)) return rc;
+    if (int rc = check_rows("q_out", q_out_row_stride, width)) return rc;
+  }
+  if (n > 0 && q_heads && (!q || !q_out)) return fail(LORA_ERR_NULL, "a required pointer is NULL (q, q_out)");
+  if (n > 0 && rope->rotary_dim && !positions) return fail(LORA_ERR_NULL, "positions is NULL");
+  if (q_heads && (!aligned16(q) || !aligned16(q_out))) return fail(LORA_ERR_ALIGN, "q and q_out must be 16-byte aligned");
+  if (!aligned16(q_norm) || !aligned16(k_norm)) return fail(LORA_ERR_ALIGN, "q_norm and k_norm must be 16-byte aligned");
+  std::memcpy(a.rope.turns, rope->turns, sizeof a.rope.turns);
+  std::memcpy(a.rope.axis, rope->axis, sizeof a.rope.axis);
+  a.rope.rotary = rope->rotary_dim;
+  a.rope.axes = rope->axes;
+  a.rope.interleaved = rope->interleaved != 0;
+  a.q = q;
+  a.q_stride = q_row_stride;
+  a.q_out = q_out;
+  a.q_out_stride = q_out_row_stride;
+  a.positions = positions;
+  a.position_stride = position_stride;
+  a.q_norm = q_norm;
+  a.k_norm = k_norm;
+  a.eps = eps;
+  a.n = n;
+  a.q_heads = q_heads;
+  a.head_dim = rope->head_dim;
+  return LORA_OK;
+}
+
+// What lora_attn_decode and lora_attn_decode_window share: `a` checked and filled in (batch > 0 if `a.batch` is).
+int decode_args(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* out, int64_t out_row_stride, int32_t batch,
+                int32_t q_heads, float scale, const lora_kv_cache* cache, const int32_t* block_table, int64_t table_stride,
+                int32_t max_pages, const int32_t* seq_lens, float* lse, void* workspace, int64_t workspace_bytes,
+                glora::DecodeArgs& a) {
+  if (batch < 0 || batch > LORA_MAX_SEQS) return fail(LORA_ERR_SIZE, "batch %d outside [0, %d]", batch, LORA_MAX_SEQS);
+  if (int rc = check_cache(cache, a.c)) return rc;
+  if (int rc = check_heads(q_heads, cache->kv_heads)) return rc;
+  if (int rc = check_scale(scale)) return rc;
+  if (int rc = check_table(max_pages, table_stride, cache)) return rc;
+  const int64_t width = static_cast<int64_t>(q_heads) * cache->head_dim;
+  if (int rc = check_rows("q", q_row_stride, width)) return rc;
+  if (int rc = check_rows("out", out_row_stride, width)) return rc;
+  if (workspace_bytes < LORA_ATTN_WORKSPACE)
+    return fail(LORA_ERR_SIZE, "workspace of %lld bytes, %d are needed", (long long)workspace_bytes, LORA_ATTN_WORKSPACE);
+  if (batch == 0) return LORA_OK;
+  if (!q || !out || !seq_lens || !workspace || (max_pages > 0 && !block_table))
+    return fail(LORA_ERR_NULL, "a required pointer is NULL (q, out, block_table, seq_lens, workspace)");
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace))
+    return fail(LORA_ERR_ALIGN, "q, out and workspace must be 16-byte aligned");
+  a.q = q;
+  a.q_stride = q_row_stride;
+  a.out = out;
+  a.out_stride = out_row_stride;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.max_pages = max_pages;
+  a.lens = seq_lens;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.batch = batch;
+  a.q_heads = q_heads;
+  a.head_dim = cache->head_dim;
+  a.format = cache->format;
+  a.page_shift = log2_or(cache->page_size);
+  a.scale = scale;
+  return LORA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -138,28 +236,59 @@ int lora_attn_decode(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* ou
                      const int32_t* seq_lens, float* lse, void* workspace, int64_t workspace_bytes,
                      void* stream) {
   glora::DecodeArgs a{};
+  if (int rc = decode_args(q, q_row_stride, out, out_row_stride, batch, q_heads, scale, cache, block_table, table_stride, max_pages,
+                           seq_lens, lse, workspace, workspace_bytes, a)) return rc;
+  if (batch == 0) return ok();
+  const int rc = glora::launch_decode(a, stream);
+  return rc ? cuda_fail(rc, "lora_attn_decode launch") : ok();
+}
+
+int lora_attn_decode_window(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* out, int64_t out_row_stride,
+                            int32_t batch, int32_t q_heads, float scale, const lora_kv_cache* cache,
+                            const int32_t* block_table, int64_t table_stride, int32_t max_pages,
+                            const int32_t* seq_lens, int32_t window, int32_t sinks, float* lse,
+                            void* workspace, int64_t workspace_bytes, void* stream) {
+  glora::DecodeArgs a{};
+  if (int rc = check_window(window, sinks)) return rc;
+  if (int rc = decode_args(q, q_row_stride, out, out_row_stride, batch, q_heads, scale, cache, block_table, table_stride, max_pages,
+                           seq_lens, lse, workspace, workspace_bytes, a)) return rc;
+  if (batch == 0) return ok();
+  a.window = window;
+  a.sinks = sinks;
+  // A window that holds all that the block table can name hides nothing.
+  const bool all = window >= static_cast<int64_t>(max_pages) * cache->page_size;
+  const int rc = all ? glora::launch_decode(a, stream) : glora::launch_decode_window(a, stream);
+  return rc ? cuda_fail(rc, "lora_attn_decode_window launch") : ok();
+}
+
+int lora_attn_chunk(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* out, int64_t out_row_stride,
+                    const int32_t* cu_q, int32_t batch, int32_t total_q, int32_t q_heads, float scale,
+                    const lora_kv_cache* cache, const int32_t* block_table, int64_t table_stride,
+                    int32_t max_pages, const int32_t* seq_lens, int32_t window, int32_t sinks, float* lse,
+                    void* workspace, int64_t workspace_bytes, void* stream) {
+  glora::ChunkArgs a{};
   if (batch < 0 || batch > LORA_MAX_SEQS) return fail(LORA_ERR_SIZE, "batch %d outside [0, %d]", batch, LORA_MAX_SEQS);
+  if (total_q < 0 || total_q > LORA_MAX_KV_ROWS) return fail(LORA_ERR_SIZE, "total_q %d outside [0, %d]", total_q, LORA_MAX_KV_ROWS);
   if (int rc = check_cache(cache, a.c)) return rc;
   if (int rc = check_heads(q_heads, cache->kv_heads)) return rc;
   if (int rc = check_scale(scale)) return rc;
-  if (max_pages < 0) return fail(LORA_ERR_SIZE, "max_pages %d < 0", max_pages);
-  if (static_cast<int64_t>(max_pages) * cache->page_size > LORA_MAX_SEQ_TOKENS)
-    return fail(LORA_ERR_SIZE, "max_pages %d x page_size %d passes %d tokens", max_pages, cache->page_size, LORA_MAX_SEQ_TOKENS);
+  if (int rc = check_window(window, sinks)) return rc;
+  if (int rc = check_table(max_pages, table_stride, cache)) return rc;
   const int64_t width = static_cast<int64_t>(q_heads) * cache->head_dim;
   if (int rc = check_rows("q", q_row_stride, width)) return rc;
   if (int rc = check_rows("out", out_row_stride, width)) return rc;
-  if (table_stride < max_pages) return fail(LORA_ERR_STRIDE, "table_stride %lld < max_pages %d", (long long)table_stride, max_pages);
-  if (workspace_bytes < LORA_ATTN_WORKSPACE)
-    return fail(LORA_ERR_SIZE, "workspace of %lld bytes, %d are needed", (long long)workspace_bytes, LORA_ATTN_WORKSPACE);
-  if (batch == 0) return ok();
-  if (!q || !out || !seq_lens || !workspace || (max_pages > 0 && !block_table))
-    return fail(LORA_ERR_NULL, "a required pointer is NULL (q, out, block_table, seq_lens, workspace)");
+  if (workspace_bytes < LORA_CHUNK_WORKSPACE)
+    return fail(LORA_ERR_SIZE, "workspace of %lld bytes, %d are needed", (long long)workspace_bytes, LORA_CHUNK_WORKSPACE);
+  if (batch == 0 || total_q == 0) return ok();
+  if (!q || !out || !cu_q || !seq_lens || !workspace || (max_pages > 0 && !block_table))
+    return fail(LORA_ERR_NULL, "a required pointer is NULL (q, out, cu_q, block_table, seq_lens, workspace)");
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace))
     return fail(LORA_ERR_ALIGN, "q, out and workspace must be 16-byte aligned");
   a.q = q;
   a.q_stride = q_row_stride;
   a.out = out;
   a.out_stride = out_row_stride;
+  a.cu_q = cu_q;
   a.table = block_table;
   a.table_stride = table_stride;
   a.max_pages = max_pages;
@@ -167,13 +296,94 @@ int lora_attn_decode(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* ou
   a.lse = lse;
   a.workspace = workspace;
   a.batch = batch;
+  a.total_q = total_q;
   a.q_heads = q_heads;
   a.head_dim = cache->head_dim;
   a.format = cache->format;
   a.page_shift = log2_or(cache->page_size);
   a.scale = scale;
-  const int rc = glora::launch_decode(a, stream);
-  return rc ? cuda_fail(rc, "lora_attn_decode launch") : ok();
+  a.window = window;
+  a.sinks = sinks;
+  const int rc = glora::launch_chunk(a, stream);
+  return rc ? cuda_fail(rc, "lora_attn_chunk launch") : ok();
+}
+
+int lora_rope_init(lora_rope* rope, int32_t head_dim, int32_t rotary_dim, const double* freqs, const uint8_t* axis,
+                   int32_t axes, int32_t interleaved) {
+  if (!rope) return fail(LORA_ERR_NULL, "rope is NULL");
+  if (int rc = check_head_dim(head_dim)) return rc;
+  if (rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 8)
+    return fail(LORA_ERR_SIZE, "rotary_dim %d is not a multiple of 8 in [0, %d]", rotary_dim, head_dim);
+  if (axes < 1 || axes > LORA_MAX_ROPE_AXES) return fail(LORA_ERR_SIZE, "axes %d outside [1, %d]", axes, LORA_MAX_ROPE_AXES);
+  if (rotary_dim && !freqs) return fail(LORA_ERR_NULL, "freqs is NULL");
+  lora_rope r{};
+  for (int j = 0; j < rotary_dim / 2; ++j) {
+    if (!std::isfinite(freqs[j])) return fail(LORA_ERR_SIZE, "freqs[%d] is not finite", j);
+    if (axis && axis[j] >= axes) return fail(LORA_ERR_SIZE, "axis %d of pair %d is not below axes %d", axis[j], j, axes);
+    // (taken of the magnitude: there the difference is exact; 63 bits of it, which double's 53 do not pass)
+    const double t = std::fabs(freqs[j]) * 0.15915494309189535;    // 1 / (2 pi)
+    const uint64_t part = static_cast<uint64_t>(std::ldexp(t - std::floor(t), 63)) << 1;
+    r.turns[j] = freqs[j] < 0 ? 0 - part : part;
+    r.axis[j] = axis ? axis[j] : 0;
+  }
+  r.head_dim = head_dim;
+  r.rotary_dim = rotary_dim;
+  r.axes = axes;
+  r.interleaved = interleaved != 0;
+  *rope = r;
+  return ok();
+}
+
+int lora_qk_rope(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* q_out, int64_t q_out_row_stride,
+                 const lora_bf16_t* k, int64_t k_row_stride, lora_bf16_t* k_out, int64_t k_out_row_stride,
+                 int32_t n, int32_t q_heads, int32_t kv_heads, const lora_rope* rope,
+                 const int32_t* positions, int64_t position_stride, const lora_bf16_t* q_norm,
+                 const lora_bf16_t* k_norm, float eps, void* stream) {
+  glora::RopeArgs a{};
+  if (kv_heads < 0 || kv_heads > LORA_MAX_HEADS || (q_heads == 0 && kv_heads == 0))
+    return fail(LORA_ERR_SIZE, "kv_heads %d outside [0, %d], or no heads at all", kv_heads, LORA_MAX_HEADS);
+  if (int rc = rope_args(q, q_row_stride, q_out, q_out_row_stride, n, q_heads, rope, positions, position_stride, q_norm, k_norm, eps, a)) return rc;
+  if (kv_heads) {
+    const int64_t width = static_cast<int64_t>(kv_heads) * rope->head_dim;
+    if (int rc = check_rows("k", k_row_stride, width)) return rc;
+    if (int rc = check_rows("k_out", k_out_row_stride, width)) return rc;
+    if (n > 0 && (!k || !k_out)) return fail(LORA_ERR_NULL, "a required pointer is NULL (k, k_out)");
+    if (!aligned16(k) || !aligned16(k_out)) return fail(LORA_ERR_ALIGN, "k and k_out must be 16-byte aligned");
+  }
+  if (n == 0) return ok();
+  a.k = k;
+  a.k_stride = k_row_stride;
+  a.k_out = k_out;
+  a.k_out_stride = k_out_row_stride;
+  a.kv_heads = kv_heads;
+  a.format = glora::kRopeRows;
+  const int rc = glora::launch_rope(a, stream);
+  return rc ? cuda_fail(rc, "lora_qk_rope launch") : ok();
+}
+
+int lora_kv_append(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* q_out, int64_t q_out_row_stride,
+                   int32_t q_heads, const lora_bf16_t* k, int64_t k_row_stride, const lora_bf16_t* v,
+                   int64_t v_row_stride, const int64_t* slots, int32_t n, const lora_kv_cache* cache,
+                   const lora_rope* rope, const int32_t* positions, int64_t position_stride,
+                   const lora_bf16_t* q_norm, const lora_bf16_t* k_norm, float eps, void* stream) {
+  glora::RopeArgs a{};
+  glora::KvRowsArgs rows{};
+  if (int rc = kv_rows(k, k_row_stride, v, v_row_stride, slots, n, cache, rows)) return rc;
+  if (int rc = rope_args(q, q_row_stride, q_out, q_out_row_stride, n, q_heads, rope, positions, position_stride, q_norm, k_norm, eps, a)) return rc;
+  if (rope->head_dim != cache->head_dim)
+    return fail(LORA_ERR_SIZE, "the rotation is for head_dim %d, the cache has %d", rope->head_dim, cache->head_dim);
+  if (n == 0) return ok();
+  a.c = rows.c;
+  a.k = k;
+  a.k_stride = k_row_stride;
+  a.v = v;
+  a.v_stride = v_row_stride;
+  a.slots = rows.slots;
+  a.kv_heads = cache->kv_heads;
+  a.format = cache->format;
+  a.page_shift = rows.page_shift;
+  const int rc = glora::launch_rope(a, stream);
+  return rc ? cuda_fail(rc, "lora_kv_append launch") : ok();
 }
 
 int lora_attn_prefill(const lora_bf16_t* q, int64_t q_row_stride, const lora_bf16_t* k, int64_t k_row_stride,

@@ -59,6 +59,46 @@ __device__ __forceinline__ long long scale_index(const KvView& c, int page, int 
   return (static_cast<long long>(page) * c.kv_heads + head) * c.page_size + slot;
 }
 
+// Page and slot of a cache-wide slot number; false outside the cache. page_shift: log2 of page_size, or -1.
+__device__ __forceinline__ bool locate(const KvView& c, int page_shift, long long at, int& page, int& slot) {
+  if (at < 0 || at >= static_cast<long long>(c.num_pages) * c.page_size) return false;
+  if (page_shift >= 0) {
+    page = static_cast<int>(at >> page_shift);
+    slot = static_cast<int>(at) & (c.page_size - 1);
+  } else if ((at >> 32) == 0) {   // 32-bit division where it is enough
+    const uint32_t q = static_cast<uint32_t>(at) / static_cast<uint32_t>(c.page_size);
+    page = static_cast<int>(q);
+    slot = static_cast<int>(static_cast<uint32_t>(at) - q * static_cast<uint32_t>(c.page_size));
+  } else {
+    page = static_cast<int>(at / c.page_size);
+    slot = static_cast<int>(at - static_cast<long long>(page) * c.page_size);
+  }
+  return true;
+}
+
+constexpr float kZeroRow = 7.888609052210118e-31f;   // 2^-100: a row whose magnitudes are below it is stored as zeros
+
+// Four values times `inv`, rounded to codes.
+template <int FMT>
+__device__ __forceinline__ uint32_t quantise4(const float (&x)[4], float inv) {
+  float f[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = __fmul_rn(x[j], inv);
+  if constexpr (FMT == kKvE4m3) {
+    uint32_t code;
+    asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n"
+        " mov.b32 %0, {l, h};\n}\n"
+        : "=r"(code)
+        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]));
+    return code;
+  } else {   // at most 127 (1 + 2^-23) in magnitude: 1.5 * 2^23 + f holds the rounded integer in its low byte
+    uint32_t t[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] = __float_as_uint(__fadd_rn(f[j], 12582912.f));
+    return __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+  }
+}
+
 // Four codes of an 8-bit format as f32.
 template <int FMT>
 __device__ __forceinline__ void codes_to_f32(uint32_t c, float (&f)[4]) {

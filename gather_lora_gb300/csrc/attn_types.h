@@ -33,6 +33,33 @@ struct KvRowsArgs {
   uint32_t heads_magic;      // ceil(2^32 / kv_heads): x / kv_heads = hi(x * magic) for x * kv_heads < 2^32, kv_heads > 1
 };
 
+// lora_rope as the kernels take it.
+struct RopeTable {
+  unsigned long long turns[64];
+  unsigned char axis[64];
+  int rotary, axes, interleaved;
+};
+
+constexpr int kRopeRows = -1;   // `format` of RopeArgs when k goes to k_out; otherwise k and v go to the cache
+
+struct RopeArgs {
+  KvView c;
+  RopeTable rope;
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  long long q_stride, q_out_stride, k_stride, k_out_stride, v_stride;
+  const int32_t* positions;
+  long long position_stride;
+  const long long* slots;
+  const uint16_t* q_norm;    // or NULL
+  const uint16_t* k_norm;
+  float eps;
+  int n, q_heads, kv_heads, head_dim, format, page_shift;
+};
+
 struct DecodeArgs {
   KvView c;
   const uint16_t* q;
@@ -48,6 +75,25 @@ struct DecodeArgs {
   int batch, q_heads, head_dim, format;
   int page_shift;            // log2 of page_size, or -1: not a power of two
   float scale;
+  int window, sinks;         // (windowed decode)
+};
+
+struct ChunkArgs {
+  KvView c;
+  const uint16_t* q;
+  long long q_stride;
+  uint16_t* out;
+  long long out_stride;
+  const int32_t* cu_q;
+  const int32_t* table;
+  long long table_stride;
+  const int32_t* lens;
+  float* lse;
+  void* workspace;
+  int max_pages, batch, total_q, q_heads, head_dim, format;
+  int page_shift;            // log2 of page_size, or -1: not a power of two
+  float scale;
+  int window, sinks;
 };
 
 struct PrefillArgs {
@@ -71,7 +117,10 @@ struct PrefillArgs {
 // Launchers. Return 0 or a cudaError_t value.
 int launch_kv_write(const KvRowsArgs& a, void* stream);
 int launch_kv_read(const KvRowsArgs& a, void* stream);
+int launch_rope(const RopeArgs& a, void* stream);
 int launch_decode(const DecodeArgs& a, void* stream);
+int launch_decode_window(const DecodeArgs& a, void* stream);
+int launch_chunk(const ChunkArgs& a, void* stream);
 int launch_prefill(const PrefillArgs& a, void* stream);
 // OR of the prefill kernel's device status bits since the last clear (synchronizes `stream`).
 int read_prefill_status(void* stream, uint32_t* out, int clear);

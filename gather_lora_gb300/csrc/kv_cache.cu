@@ -23,25 +23,6 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kMany = 4;          // pieces of a thread in large calls
-constexpr float kZeroRow = 7.888609052210118e-31f;   // 2^-100: below it a row is stored as zeros
-
-// Page and slot of slots[i]; false outside the cache.
-__device__ __forceinline__ bool locate(const KvRowsArgs& p, long long at, int& page, int& slot) {
-  const KvView& c = p.c;
-  if (at < 0 || at >= static_cast<long long>(c.num_pages) * c.page_size) return false;
-  if (p.page_shift >= 0) {
-    page = static_cast<int>(at >> p.page_shift);
-    slot = static_cast<int>(at) & (c.page_size - 1);
-  } else if ((at >> 32) == 0) {   // 32-bit division where it is enough
-    const uint32_t q = static_cast<uint32_t>(at) / static_cast<uint32_t>(c.page_size);
-    page = static_cast<int>(q);
-    slot = static_cast<int>(static_cast<uint32_t>(at) - q * static_cast<uint32_t>(c.page_size));
-  } else {
-    page = static_cast<int>(at / c.page_size);
-    slot = static_cast<int>(at - static_cast<long long>(page) * c.page_size);
-  }
-  return true;
-}
 
 // Larger of two BF16 pairs, NaN if either is.
 __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
@@ -63,20 +44,10 @@ __device__ __forceinline__ uint2 quantise8(const uint4& x, float inv) {
     float f[4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      f[2 * j] = __fmul_rn(__uint_as_float(w[2 * h + j] << 16), inv);
-      f[2 * j + 1] = __fmul_rn(__uint_as_float(w[2 * h + j] & 0xffff0000u), inv);
+      f[2 * j] = __uint_as_float(w[2 * h + j] << 16);
+      f[2 * j + 1] = __uint_as_float(w[2 * h + j] & 0xffff0000u);
     }
-    if constexpr (FMT == kKvE4m3) {
-      asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n"
-          " mov.b32 %0, {l, h};\n}\n"
-          : "=r"(code[h])
-          : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]));
-    } else {   // at most 127 (1 + 2^-23) in magnitude: 1.5 * 2^23 + f holds the rounded integer in its low byte
-      uint32_t t[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) t[j] = __float_as_uint(__fadd_rn(f[j], 12582912.f));
-      code[h] = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
-    }
+    code[h] = quantise4<FMT>(f, inv);
   }
   return make_uint2(code[0], code[1]);
 }
@@ -117,7 +88,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const KvRowsArgs 
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     int page = 0, slot = 0;
-    const bool live = locate(p, at[j], page, slot);
+    const bool live = locate(p.c, p.page_shift, at[j], page, slot);
     const long long to = page * p.c.page_bytes + head[j] * p.c.head_bytes + slot * p.c.token_bytes;
     if constexpr (FMT == kKvBf16) {
       if (live) {
@@ -165,7 +136,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const KvRowsArgs p
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     int page = 0, slot = 0;
-    const bool live = locate(p, at[j], page, slot);
+    const bool live = locate(p.c, p.page_shift, at[j], page, slot);
     const long long from0 = page * p.c.page_bytes + head[j] * p.c.head_bytes + slot * p.c.token_bytes;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {

@@ -25,9 +25,11 @@ TMAP_MIN_RANK = 32         # LORA_TMAP_MIN_RANK: a_tmaps are used from this max_
 DELTA_DENSE_MIN_ROWS = 256  # LORA_DELTA_DENSE_MIN_ROWS: lora_delta's tensor-core path from this m up
 
 
-# enum lora_kv_format, and the scratch lora_attn_decode wants (zero-filled once)
+# enum lora_kv_format, and the scratch lora_attn_decode and lora_attn_chunk want (zero-filled once)
 KV_BF16, KV_E4M3, KV_INT8 = 0, 1, 2
 ATTN_WORKSPACE = 16 << 20   # LORA_ATTN_WORKSPACE
+CHUNK_WORKSPACE = 48 << 20  # LORA_CHUNK_WORKSPACE
+NO_WINDOW = 0x7fffffff      # LORA_NO_WINDOW: a window that holds every token
 
 
 class _KvCacheStruct(ctypes.Structure):
@@ -59,6 +61,44 @@ class KvCache:
         self.tensors = (k_pages, v_pages, k_scale, v_scale)
         self.struct = _KvCacheStruct(_addr(k_pages), _addr(v_pages), _addr(k_scale), _addr(v_scale),
                                      *k_pages.stride()[:3], *k_pages.shape, fmt)
+
+
+class _RopeStruct(ctypes.Structure):
+    """lora_rope of include/gather_lora.h."""
+    _fields_ = [("turns", ctypes.c_uint64 * 64), ("axis", ctypes.c_uint8 * 64), ("head_dim", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("axes", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class Rope:
+    """A rotation by positions (lora_rope), set up once. Pair j of the first rotary_dim elements of a head
+    (all of them by default; a multiple of 8) turns by position * freqs[j], freqs being base ** (-2 j /
+    rotary_dim) unless given (radians per position). `sections` (pairs of each position axis, in order) or
+    `axis` (the axis of each pair) for several axes. Pairs are elements j and j + rotary_dim / 2, or 2 j
+    and 2 j + 1 if `interleaved`."""
+
+    def __init__(self, head_dim, rotary_dim=None, base=10000.0, freqs=None, sections=None, axis=None, interleaved=False):
+        rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        pairs = max(0, rotary_dim) // 2
+        if freqs is None:
+            freqs = [base ** (-2.0 * j / rotary_dim) for j in range(pairs)]
+        freqs = [float(f) for f in freqs]
+        if sections is not None and axis is not None:
+            raise ValueError("sections or axis, not both")
+        if sections is not None:
+            if any(m < 0 for m in sections):
+                raise ValueError(f"a section has no fewer than 0 pairs: got {list(sections)}")
+            axis = [a for a, m in enumerate(sections) for _ in range(m)]
+        axes = len(sections) if sections is not None else max([0, *axis]) + 1 if axis is not None else 1
+        axis = [0] * pairs if axis is None else [int(a) for a in axis]
+        if len(freqs) != pairs or len(axis) != pairs or any(not 0 <= a < 256 for a in axis):
+            raise ValueError(f"rotary_dim {rotary_dim} has {pairs} pairs: got {len(freqs)} frequencies and axes of {len(axis)} pairs {axis}")
+        self.struct = _RopeStruct()
+        _check(load().lora_rope_init(ctypes.byref(self.struct), head_dim, rotary_dim, (ctypes.c_double * max(pairs, 1))(*freqs),
+                                     (ctypes.c_uint8 * max(pairs, 1))(*axis), axes, int(bool(interleaved))))
+
+
+def _rope(r):
+    return r if r is None else ctypes.byref(r.struct if isinstance(r, Rope) else r)
 
 
 def _cache(c):
@@ -110,6 +150,17 @@ def load():
     lib.lora_attn_prefill.restype = ctypes.c_int
     lib.lora_attn_prefill.argtypes = [P, I64, P, I64, P, I64, P, I64, P, P, I32, I32, I32, I32, I32, I32,
                                       ctypes.c_float, P, P]
+    F32, RP = ctypes.c_float, ctypes.POINTER(_RopeStruct)
+    lib.lora_attn_decode_window.restype = ctypes.c_int
+    lib.lora_attn_decode_window.argtypes = [P, I64, P, I64, I32, I32, F32, KV, P, I64, I32, P, I32, I32, P, P, I64, P]
+    lib.lora_attn_chunk.restype = ctypes.c_int
+    lib.lora_attn_chunk.argtypes = [P, I64, P, I64, P, I32, I32, I32, F32, KV, P, I64, I32, P, I32, I32, P, P, I64, P]
+    lib.lora_rope_init.restype = ctypes.c_int
+    lib.lora_rope_init.argtypes = [RP, I32, I32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_uint8), I32, I32]
+    lib.lora_qk_rope.restype = ctypes.c_int
+    lib.lora_qk_rope.argtypes = [P, I64, P, I64, P, I64, P, I64, I32, I32, I32, RP, P, I64, P, P, F32, P]
+    lib.lora_kv_append.restype = ctypes.c_int
+    lib.lora_kv_append.argtypes = [P, I64, P, I64, I32, P, I64, P, I64, P, I32, KV, RP, P, I64, P, P, F32, P]
     lib.lora_last_error.restype = ctypes.c_char_p
     lib.lora_last_error.argtypes = []
     lib.lora_read_device_status.restype = ctypes.c_int
@@ -254,6 +305,42 @@ def lora_attn_decode(q, q_row_stride, out, out_row_stride, batch, q_heads, scale
                                           _cache(cache), _addr(block_table), table_stride, max_pages,
                                           _addr(seq_lens), _addr(lse), _addr(workspace), workspace_bytes,
                                           _stream(stream)))
+
+
+def lora_qk_rope(q, q_row_stride, q_out, q_out_row_stride, k, k_row_stride, k_out, k_out_row_stride, n, q_heads, kv_heads,
+                 rope, positions, position_stride, q_norm=None, k_norm=None, eps=1e-6, stream=None):
+    """q and k rows normed per head (optional) and rotated (see lora_qk_rope in include/gather_lora.h).
+    rope: a Rope; positions: int32 [axes, position_stride]; q_norm, k_norm: BF16 [head_dim]."""
+    return _check(load().lora_qk_rope(_addr(q), q_row_stride, _addr(q_out), q_out_row_stride, _addr(k), k_row_stride,
+                                      _addr(k_out), k_out_row_stride, n, q_heads, kv_heads, _rope(rope), _addr(positions),
+                                      position_stride, _addr(q_norm), _addr(k_norm), eps, _stream(stream)))
+
+
+def lora_kv_append(q, q_row_stride, q_out, q_out_row_stride, q_heads, k, k_row_stride, v, v_row_stride, slots, n, cache,
+                   rope, positions, position_stride, q_norm=None, k_norm=None, eps=1e-6, stream=None):
+    """lora_qk_rope with k, and v as it is, going into their cache slots (see lora_kv_append in
+    include/gather_lora.h). slots: int64 [n], no slot twice; cache: a KvCache."""
+    return _check(load().lora_kv_append(_addr(q), q_row_stride, _addr(q_out), q_out_row_stride, q_heads, _addr(k), k_row_stride,
+                                        _addr(v), v_row_stride, _addr(slots), n, _cache(cache), _rope(rope), _addr(positions),
+                                        position_stride, _addr(q_norm), _addr(k_norm), eps, _stream(stream)))
+
+
+def lora_attn_decode_window(q, q_row_stride, out, out_row_stride, batch, q_heads, scale, cache, block_table, table_stride,
+                            max_pages, seq_lens, window, sinks, workspace, workspace_bytes, lse=None, stream=None):
+    """lora_attn_decode for a layer that sees the last `window` tokens and the first `sinks` (see
+    lora_attn_decode_window in include/gather_lora.h)."""
+    return _check(load().lora_attn_decode_window(_addr(q), q_row_stride, _addr(out), out_row_stride, batch, q_heads, scale,
+                                                 _cache(cache), _addr(block_table), table_stride, max_pages, _addr(seq_lens),
+                                                 window, sinks, _addr(lse), _addr(workspace), workspace_bytes, _stream(stream)))
+
+
+def lora_attn_chunk(q, q_row_stride, out, out_row_stride, cu_q, batch, total_q, q_heads, scale, cache, block_table,
+                    table_stride, max_pages, seq_lens, window, sinks, workspace, workspace_bytes, lse=None, stream=None):
+    """Attention of chunks of new tokens over the cache (see lora_attn_chunk in include/gather_lora.h).
+    workspace: at least CHUNK_WORKSPACE bytes, zero-filled once; window: NO_WINDOW for none."""
+    return _check(load().lora_attn_chunk(_addr(q), q_row_stride, _addr(out), out_row_stride, _addr(cu_q), batch, total_q, q_heads,
+                                         scale, _cache(cache), _addr(block_table), table_stride, max_pages, _addr(seq_lens),
+                                         window, sinks, _addr(lse), _addr(workspace), workspace_bytes, _stream(stream)))
 
 
 def lora_attn_prefill(q, q_row_stride, k, k_row_stride, v, v_row_stride, out, out_row_stride, cu_q, cu_k, batch,

@@ -12,7 +12,11 @@
  * the attention beside them in a serving step (the section further down):
  *
  *   lora_kv_write, lora_kv_read   a paged key-value cache in BF16 or 8 bits
+ *   lora_qk_rope                  queries and keys normed per head and rotated by their positions
+ *   lora_kv_append                the same, keys and values going into their cache slots
  *   lora_attn_decode              one new token per sequence over that cache
+ *   lora_attn_decode_window       the same, seeing a sliding window and some first tokens
+ *   lora_attn_chunk               chunks of new tokens over that cache, with or without a window
  *   lora_attn_prefill             causal attention over packed prompts
  *
  * plus lora_encode_a_tmaps (TMA tensor maps of the A matrices, encoded once on
@@ -357,7 +361,9 @@ int lora_launch_geometry(int moe, int32_t rows, int32_t max_loras, int32_t max_r
  * (lora_kv_write), and attention reads them: one new token per sequence over the
  * cache (lora_attn_decode), or whole prompts and prompt chunks over packed K and
  * V rows (lora_attn_prefill), a cached prefix being read back into such rows
- * first (lora_kv_read). The conventions above hold: device pointers owned by
+ * first (lora_kv_read). Rows with positions are rotated, and their heads normed,
+ * by lora_qk_rope or on their way into the cache (lora_kv_append); chunks attend
+ * over the cache itself in lora_attn_chunk. The conventions above hold: device pointers owned by
  * the caller, strides in elements, checks on the host before any launch, no
  * allocation, no synchronization, launch shapes from host integers alone
  * (capture-safe), bad device data is never a fault. q_heads query heads share
@@ -478,6 +484,120 @@ int lora_attn_prefill(const lora_bf16_t* q, int64_t q_row_stride, const lora_bf1
                       const int32_t* cu_q, const int32_t* cu_k, int32_t batch, int32_t total_q,
                       int32_t total_k, int32_t q_heads, int32_t kv_heads, int32_t head_dim, float scale,
                       float* lse, void* stream);
+
+/*
+ * A rotation of queries and keys by their positions, set up once by
+ * lora_rope_init (host memory; the calls take it by value). Pair j of a head,
+ * j < rotary_dim / 2, is turned by the angle position[axis j] * freqs[j]:
+ *   (y0, y1) = (x0 cos - x1 sin, x1 cos + x0 sin),
+ * its elements j and j + rotary_dim / 2, or (interleaved) 2 j and 2 j + 1.
+ * Elements from rotary_dim on are not turned. Angles are reduced exactly: the
+ * turns a position makes are held as a fraction of 2^64, so positions may be
+ * any int32, however far.
+ */
+#define LORA_MAX_ROPE_AXES 4
+typedef struct lora_rope {
+    uint64_t turns[64];            /* freqs[j] / (2 pi), less its whole part, in units of 2^-64 */
+    uint8_t axis[64];              /* which position turns pair j */
+    int32_t head_dim, rotary_dim, axes, interleaved;
+} lora_rope;
+
+/*
+ * lora_rope_init — host helper: fills *rope. head_dim 64 or 128, rotary_dim a
+ * multiple of 8 in [0, head_dim], freqs [rotary_dim / 2] finite angles (radians)
+ * per position, axis [rotary_dim / 2] with values below axes (NULL: all 0),
+ * axes in [1, LORA_MAX_ROPE_AXES].
+ */
+int lora_rope_init(lora_rope* rope, int32_t head_dim, int32_t rotary_dim, const double* freqs,
+                   const uint8_t* axis, int32_t axes, int32_t interleaved);
+
+/*
+ * lora_qk_rope — every head of the q and k rows normed (optional) and rotated.
+ *
+ * Row i of q holds q_heads * head_dim BF16 values, of k kv_heads * head_dim (one
+ * of the two counts may be 0, its pointers then ignored). Per head x, in f32,
+ * rounded to BF16 once:
+ *   with a norm:  x <- x * rsqrt(mean(x^2) + eps) * norm     (q_norm for q, k_norm for k;
+ *                 [head_dim] BF16, 16-byte aligned, NULL: none; the squares are
+ *                 summed in f32: magnitudes up to 2^63 / head_dim, others are not defined)
+ *   then the rotation by the row's positions.
+ * The results go to q_out and k_out, which may be q and k themselves (with the
+ * same strides) but must not overlap them otherwise.
+ *   positions  [axes, position_stride] int32, n used per axis (row i: positions[a *
+ *              position_stride + i]); ignored for rotary_dim 0
+ *   eps        finite, >= 0 (used with a norm)
+ * All rows 16-byte aligned, their strides multiples of 8; n in [0, LORA_MAX_KV_ROWS].
+ */
+int lora_qk_rope(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* q_out, int64_t q_out_row_stride,
+                 const lora_bf16_t* k, int64_t k_row_stride, lora_bf16_t* k_out, int64_t k_out_row_stride,
+                 int32_t n, int32_t q_heads, int32_t kv_heads, const lora_rope* rope,
+                 const int32_t* positions, int64_t position_stride, const lora_bf16_t* q_norm,
+                 const lora_bf16_t* k_norm, float eps, void* stream);
+
+/*
+ * lora_kv_append — lora_qk_rope and lora_kv_write in one pass: q rows normed and
+ * rotated into q_out, k rows normed and rotated into their cache slots, v rows
+ * into theirs as they are. q_heads may be 0 (q and q_out ignored); k rows are
+ * left as they are.
+ * The rotated keys are quantised from f32, without a rounding to BF16 before (a
+ * BF16 cache: rounded once), with lora_kv_write's formulas and its rules for
+ * slots: a row whose slot is outside the cache is stored nowhere (its q row is
+ * rotated all the same), a slot named twice is left undefined.
+ */
+int lora_kv_append(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* q_out, int64_t q_out_row_stride,
+                   int32_t q_heads, const lora_bf16_t* k, int64_t k_row_stride, const lora_bf16_t* v,
+                   int64_t v_row_stride, const int64_t* slots, int32_t n, const lora_kv_cache* cache,
+                   const lora_rope* rope, const int32_t* positions, int64_t position_stride,
+                   const lora_bf16_t* q_norm, const lora_bf16_t* k_norm, float eps, void* stream);
+
+/*
+ * A window: the row at position p sees the cached tokens t <= p with t > p - window
+ * (itself and the window - 1 before it) or t < sinks (the first tokens, which stay
+ * visible). window in [1, LORA_NO_WINDOW], which holds every token; sinks >= 0.
+ */
+#define LORA_NO_WINDOW 0x7fffffff
+
+/*
+ * lora_attn_decode_window — lora_attn_decode for a layer with a sliding window:
+ * the token of sequence b stands at position seq_lens[b] - 1 and sees what the
+ * window above says. Tokens that it does not see are not read. Everything else,
+ * the workspace too, is lora_attn_decode's.
+ */
+int lora_attn_decode_window(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* out, int64_t out_row_stride,
+                            int32_t batch, int32_t q_heads, float scale, const lora_kv_cache* cache,
+                            const int32_t* block_table, int64_t table_stride, int32_t max_pages,
+                            const int32_t* seq_lens, int32_t window, int32_t sinks, float* lse,
+                            void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * lora_attn_chunk — attention of chunks of new tokens over the cache.
+ *
+ * Sequence b has query rows [cu_q[b], cu_q[b+1]) of q (n of them: a prompt, a
+ * later part of one, a few drafted tokens or a single one) and L = seq_lens[b]
+ * cached tokens, the chunk's own (already written) included and last: row i
+ * stands at position p = L - n + i and sees the tokens t <= p that the window
+ * above leaves it. Per row and head
+ *   z_t = scale * (q_i . k_t),   out_i = sum_t softmax(z)_t v_t;
+ * a row that sees no token (p < 0) gives zeros and lse = -infinity. Tokens that a
+ * row does not see have no influence on it, whatever they hold; a token whose
+ * page is outside [0, num_pages) is left out. L is clamped as in lora_attn_decode.
+ *   q, out      [total_q, row stride] BF16, q_heads * head_dim values used, 16-byte
+ *               aligned, strides multiples of 8
+ *   cu_q        [batch + 1] int32, non-decreasing, in [0, total_q] (a sequence whose
+ *               own two fall or leave that range is left out; rows of sequences that
+ *               overlap are not defined); rows of no sequence stay unchanged
+ *   block_table, table_stride, max_pages, seq_lens, scale   as in lora_attn_decode
+ *   lse         optional [total_q, q_heads] f32: ln sum_t exp(z_t)
+ *   workspace   as in lora_attn_decode, LORA_CHUNK_WORKSPACE bytes, its own
+ * An E4M3 code that is NaN makes its whole token NaN to the rows that see it.
+ * How the work is split follows the whole batch: the same call gives the same bits.
+ */
+#define LORA_CHUNK_WORKSPACE (48 << 20)
+int lora_attn_chunk(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* out, int64_t out_row_stride,
+                    const int32_t* cu_q, int32_t batch, int32_t total_q, int32_t q_heads, float scale,
+                    const lora_kv_cache* cache, const int32_t* block_table, int64_t table_stride,
+                    int32_t max_pages, const int32_t* seq_lens, int32_t window, int32_t sinks, float* lse,
+                    void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ---- pure host helpers (no GPU) ------------------------------------------ */
 
