@@ -686,11 +686,12 @@ int lora_selftest_wait_timeout(int64_t limit_cycles, void* stream) {
 
 int lora_read_device_status(void* stream, uint32_t* status_out, int clear) {
   if (!status_out) return fail(LORA_ERR_NULL, "status_out is NULL");
-  uint32_t a = 0, b = 0, c = 0;
+  uint32_t a = 0, b = 0, c = 0, d = 0;
   int rc = glora::read_device_status(stream, &a, clear);
   if (!rc) rc = glora::read_dense_status(stream, &b, clear);
   if (!rc) rc = glora::read_prefill_status(stream, &c, clear);
-  *status_out = a | b | c;
+  if (!rc) rc = glora::read_chunk_status(stream, &d, clear);
+  *status_out = a | b | c | d;
   return rc ? cuda_fail(rc, "lora_read_device_status") : ok();
 }
 

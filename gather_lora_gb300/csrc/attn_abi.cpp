@@ -107,6 +107,13 @@ int kv_rows(const void* k, int64_t k_row_stride, const void* v, int64_t v_row_st
   return LORA_OK;
 }
 
+// Heads of a group in equal blocks of at most 128 (one block up to 128), as many whole tokens as fit 128 rows.
+void row_tiles(int group, int& head_block, int& tile_tokens) {
+  const int blocks = (group + 127) / 128;
+  head_block = (group + blocks - 1) / blocks;
+  tile_tokens = 128 / head_block;
+}
+
 int check_table(int32_t max_pages, int64_t table_stride, const lora_kv_cache* cache) {
   if (max_pages < 0) return fail(LORA_ERR_SIZE, "max_pages %d < 0", max_pages);
   if (static_cast<int64_t>(max_pages) * cache->page_size > LORA_MAX_SEQ_TOKENS)
@@ -304,6 +311,7 @@ int lora_attn_chunk(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* out
   a.scale = scale;
   a.window = window;
   a.sinks = sinks;
+  row_tiles(q_heads / cache->kv_heads, a.head_block, a.tile_tokens);
   const int rc = glora::launch_chunk(a, stream);
   return rc ? cuda_fail(rc, "lora_attn_chunk launch") : ok();
 }
@@ -426,10 +434,7 @@ int lora_attn_prefill(const lora_bf16_t* q, int64_t q_row_stride, const lora_bf1
   a.head_dim = head_dim;
   a.scale = scale;
   a.lse = lse;
-  // Heads of a group in equal blocks of at most 128 (one block up to 128), as many whole tokens as fit 128 rows.
-  const int group = q_heads / kv_heads, blocks = (group + 127) / 128;
-  a.head_block = (group + blocks - 1) / blocks;
-  a.tile_tokens = 128 / a.head_block;
+  row_tiles(q_heads / kv_heads, a.head_block, a.tile_tokens);
   const uint64_t qd[3] = {static_cast<uint64_t>(head_dim), static_cast<uint64_t>(q_heads), static_cast<uint64_t>(total_q)};
   const uint64_t qs[2] = {static_cast<uint64_t>(head_dim) * 2, static_cast<uint64_t>(q_row_stride) * 2};
   const uint32_t qb[3] = {64, static_cast<uint32_t>(a.head_block), static_cast<uint32_t>(a.tile_tokens)};

@@ -4,77 +4,1292 @@
 // t > p - window or t < sinks:
 //   z_t = scale (q_i . k_t),   out_i = sum_t softmax(z)_t v_t.
 //
-// One warp a row and head, a token at a time, everything in fp32: running maximum, sum and result.
+// Both products run on tcgen05 (M = 128 rows, fp32 accumulators in tensor memory) with a running softmax between them,
+// as in the prefill attention: rows of a tile are TT tokens x the G heads of a key-value head, a work item is two such row
+// tiles of one sequence and key-value head, each owned by a softmax warpgroup (thread = row), and a key tile is 128 tokens.
+//
+// Split. The work unit is a key tile of an item. A window's tiles are numbered without the gap between the first
+// tokens' and the window's. All units of the batch, item after item, are cut into equal contiguous ranges, one per CTA (one
+// CTA per SM), so that any mix of long and short chunks and contexts takes equal time everywhere; ends within kSnap units of
+// an item's end move there. A range is walked piece by piece (its part of one item). A piece that is a whole item is
+// finished by its CTA; otherwise its rows' sums go to the workspace and the last CTA of the item to arrive joins them in CTA
+// order (in two levels beyond kJoinGroup), so the bits never depend on who was last.
+//
+// Roles of a CTA's 16 warps: 0-7 softmax, 8 issues the MMAs, 9 plans and loads Q, 10 loads Q, 11-15 load K and V. The loaders
+// take groups of 16 tokens in turn: one lane a token looks its page up, then the rows go to the swizzled tiles by cp.async
+// (BF16) or through registers (8 bits), whatever the page size and the strides are. What nobody in the item sees is not
+// read but zero-filled.
+//
+// 8-bit formats run in f16: the codes of both formats are exact in it, Q is brought into its range by a power of two a
+// row, and the weights have 11 bits. K's scale multiplies the score, V's the weight: to keep weights of any scale in f16's
+// range the running reference is that of y_t = z_t + log2 s_t, the weight w = 2^(y - ref) multiplies the codes and the sum of
+// the softmax is that of w_t / s_t.
+//
+// Rounding to fewer bits: the weights (BF16 over a BF16 cache, else f16: the tensor cores' operand types), the result.
+//
+// Zero weight times what is not finite is NaN in an MMA. The loaders look through what some rows of the item see and others
+// do not (its last tokens, and the first ones of its windows), set what is not finite in V to zero, and the softmax
+// warps add it to the stored rows that see it.
+#include <type_traits>
+
 #include "attn_common.cuh"
+#include "tc05.cuh"
 
 namespace glora {
 
+__device__ unsigned int g_chunk_status = 0;
+
 namespace {
 
-constexpr int kChunkWarps = 8;
+constexpr unsigned kChunkTimeoutBit = 0x2u;     // LORA_DEV_TIMEOUT
+constexpr int kTile = 128;                      // rows of a tile, tokens of a key tile
+constexpr int kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
+constexpr int kMmaWarp = 8, kPlanWarp = 9, kQWarps = 2, kLoadWarp = 11, kLoaders = 5;
+constexpr int kChunkThreads = 512, kChunkWarps = kChunkThreads / 32;
+// Registers a thread: 128 at launch; two warpgroups give away what the softmax's rows of scores need: 2 * 64 + 2 * 192 = 4 * 128.
+constexpr int kHelperRegs = 64, kSoftRegs = 192;
+constexpr int kPieces = 4;                      // depth of the ring of pieces
+constexpr int kMeta = 4;                        // depth of the ring of tokens' masks and scales
+constexpr int kGroup = 16, kGroups = kTile / kGroup;   // tokens of a loader's group; groups of a tile
+constexpr int kLag = 3;                         // groups of copies that a loader has in flight behind the newest
+constexpr int kStageBytes = 2048;               // staging of a warp's results: 32 rows of 64 bytes
+constexpr float kGrow = 8.f;                    // the reference moves when the maximum grew by 2^8
+constexpr float kTop = 7.f;                     // 8 bits: a weight at the reference is 2^7, at most 2^15
+constexpr float kSumUnit = 6.103515625e-05f;    // 8 bits: 2^-14, so that weight / scale stays in range
+constexpr int kMostCtas = 160;                  // slots in the workspace
+constexpr int kJoinGroup = 16;                  // parts of a join
+constexpr int kSnap = 2;
+constexpr int kMostSeqs = 8192;                 // LORA_MAX_SEQS
+constexpr int kFewPairs = 8;                    // sequences of more row-tile pairs are summed by a warp
+static_assert(kMostCtas <= kJoinGroup * kJoinGroup, "two levels of joins");
+
+// Workspace: counters [3][kMostCtas] (an item's first join group, by its first CTA; its other groups, by theirs; its
+// groups together), then 2 slots per CTA of exponent[256], sum[256], O[256][D], 4 words of flags.
+constexpr int kCounterBytes = 4096;
+template <int D>
+constexpr int kSlotFloats = 2 * 2 * kTile + 2 * kTile * D + 4;
+static_assert(3 * kMostCtas * 4 <= kCounterBytes && kCounterBytes + 2LL * kMostCtas * kSlotFloats<128> * 4 <= (48 << 20), "workspace");
+
+template <int D>
+struct ChunkShape {
+  static constexpr int tile_bytes = kTile * D * 2;              // Q row tile, K tile or V tile
+  static constexpr int pairs = D == 128 ? 2 : 4;                // ring: stages of K and V
+  static constexpr int bufs = D == 128 ? 2 : 3;                 // score buffers in tensor memory: what O0 and O1 leave
+  static constexpr uint32_t col_o = 512 - 2 * D;
+  static __device__ __forceinline__ uint32_t buf(int i, int j) { return bufs == 2 ? i : (2u * j + i) % 3u; }
+  // Byte of 16-byte chunk c of row r: 64-column blocks, 128-byte swizzle.
+  static __device__ __forceinline__ uint32_t at(int r, int c) { return (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
+};
+
+struct ChunkMeta {           // of a key tile
+  float a[kTile];            // 8 bits: scale log2(e) times K's scale
+  float b[kTile];            // log2 of V's scale
+  float iv[kTile];           // kSumUnit / V's scale
+  uint16_t live[kGroups];    // tokens that are there and that some row sees
+};
+
+struct ChunkPiece {
+  int valid;
+  int b, row0;               // sequence; first query row
+  int first, end;            // positions of its first token (may be negative) and of its last
+  int kvh, h0, heads;
+  int low, kept, skip;       // first token in any row's window; tiles from `kept` on stand `skip` further
+  int ta, n, tiles;          // first tile, tiles; the item's
+  int ni[2];                 // tiles of each row tile
+  int c0, c1;                // the item's CTAs
+};
+
+struct ChunkCtl {
+  unsigned long long full[8], empty[8];              // K stages even, V stages odd
+  unsigned long long meta_full[kMeta], meta_empty[kMeta];
+  unsigned long long q_full, q_empty;
+  unsigned long long s_full[2][2], p_ready[2][2][2], o_done[2][2];   // [row tile][parity of its key tile] ([half])
+  unsigned long long piece_full[kPieces], piece_empty[kPieces];
+  unsigned long long drain;
+  ChunkPiece piece[kPieces];
+  int bad[kPieces];                                  // something in V was set to zero
+  uint32_t tmem;
+  int failed, last;
+  // the plan
+  long long warp_sum[kChunkWarps], total, sum[2], rem[2];
+  int seq[2];
+};
+
+template <int D>
+struct ChunkSmem {
+  using Sh = ChunkShape<D>;
+  static constexpr int q = 0, ring = 2 * Sh::tile_bytes, stage = ring + 2 * Sh::pairs * Sh::tile_bytes;
+  static constexpr int meta = stage + kSoftWarps * kStageBytes;
+  static constexpr int qf = meta + kMeta * static_cast<int>(sizeof(ChunkMeta));
+  static constexpr int ctl = qf + kPieces * 2 * kTile * 4;
+  static constexpr int bytes = ctl + static_cast<int>(sizeof(ChunkCtl)) + 1024;    // (+ alignment)
+  static_assert(sizeof(ChunkMeta) % 16 == 0 && bytes <= 232448, "shared memory");
+  static_assert(kMostSeqs * 8 <= 2 * Sh::pairs * Sh::tile_bytes, "the plan's sums lie in the ring");
+};
+
+__device__ __forceinline__ bool failed(const ChunkCtl& c) { return *reinterpret_cast<const volatile int*>(&c.failed) != 0; }
+
+// Bounded wait; true if it ran out. Once one has, all others of the CTA end at once, the roles leave their loops and nothing
+// more is stored (what runs on until then stays in bounds).
+__device__ __forceinline__ bool wait(ChunkCtl& c, unsigned long long& bar, uint32_t parity) {
+  const uint32_t b = smem_u32(&bar);
+  if (mbar_try_wait(b, parity, 100000)) return false;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(b, parity, 100000)) {
+    if (failed(c)) return true;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      *reinterpret_cast<volatile int*>(&c.failed) = 1;
+      atomicOr(&g_chunk_status, kChunkTimeoutBit);
+      return true;
+    }
+  }
+  return false;
+}
+__device__ __forceinline__ bool passed(unsigned long long& bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(done)
+               : "r"(smem_u32(&bar)), "r"(parity)
+               : "memory");
+  return done != 0;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_left() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(kSoftThreads) : "memory"); }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Four codes as f16 pairs.
+template <int FMT>
+__device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
+  if constexpr (FMT == kKvE4m3) {
+    e4m3x4_to_f16(c, lo, hi);
+  } else {   // 0x6400 | (code + 128) is the f16 number 1152 + code
+    c ^= 0x80808080u;
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    uint32_t l = __byte_perm(c, 0x64646464u, 0x4140), h = __byte_perm(c, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&l), off), y = __hsub2(*reinterpret_cast<__half2*>(&h), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
+// ---- the plan ---------------------------------------------------------------
+
+struct Seq {
+  int q0, n, len;            // first row, rows (0: left out), cached tokens
+};
+__device__ __forceinline__ Seq sequence(const ChunkArgs& p, int b) {
+  Seq s{};
+  const int a0 = __ldg(p.cu_q + b), a1 = __ldg(p.cu_q + b + 1);
+  if (a0 < 0 || a1 <= a0 || a1 > p.total_q) return s;
+  s.q0 = a0;
+  s.n = a1 - a0;
+  const long long most = static_cast<long long>(p.max_pages) * p.c.page_size;
+  s.len = static_cast<int>(min(static_cast<long long>(max(__ldg(p.lens + b), 0)), most));
+  return s;
+}
+
+// What the rows at positions first .. end see between them, as key tiles.
+struct Span {
+  int low, kept, skip, tiles;
+};
+__device__ __forceinline__ Span span(const ChunkArgs& p, int first, int end) {
+  Span s{};
+  if (end < 0) return s;
+  s.low = first >= p.window ? first - p.window + 1 : 0;
+  const int sinks = min(p.sinks, s.low);
+  s.kept = sinks / kTile + (sinks % kTile ? 1 : 0);
+  s.skip = max(0, s.low / kTile - s.kept);
+  s.tiles = end / kTile + 1 - s.skip;
+  return s;
+}
+// Key tiles of row-tile pair x of a sequence (0 where all its rows stand before the first token).
+__device__ __forceinline__ int pair_tiles(const ChunkArgs& p, const Seq& s, int step, int x) {
+  const int t0 = x * step;
+  return span(p, s.len - s.n + t0, s.len - s.n + min(t0 + step, s.n) - 1).tiles;
+}
+
+// Unit at which CTA c's range begins, before ends move.
+__device__ __forceinline__ long long cut(long long c, long long total, long long n) { return c * total / n; }
 
 }  // namespace
 
+// What was set to zero in V is added to the stored result rows of this warp that see it, as it is, since their weights are
+// positive: per token of the warp, over the tokens that it sees and others of the item do not.
 template <int FMT, int D>
-__global__ void __launch_bounds__(kChunkWarps * 32) chunk_kernel(const ChunkArgs p) {
-  constexpr int E = D / 32;            // consecutive dimensions of a lane
+__device__ __noinline__ void add_not_finite(const ChunkArgs& p, const ChunkPiece& w, int warp, int lane) {
+  constexpr int E = D / 32;
+  const int i = warp >> 2, r0 = (warp & 3) * 32, GB = p.head_block, TT = p.tile_tokens;
+  const int32_t* const table = p.table + w.b * p.table_stride;
+  for (int t_in = r0 / GB; t_in <= (r0 + 31) / GB && t_in < TT; ++t_in) {
+    const int pos = w.first + i * TT + t_in;
+    if (pos > w.end) break;
+    if (pos < 0) continue;
+    float s[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) s[e] = 0.f;
+    // ends of the two ranges of such tokens: before the last row's window, and behind the first row
+    const int low_end = min(pos, w.end - p.window);
+    for (int part = 0; part < 2; ++part) {
+      const int from = part ? max(max(w.first + 1, 0), low_end + 1) : max(0, pos - p.window + 1), to = part ? pos : low_end;
+      for (int t = from; t <= to; ++t) {
+        const bool sees = t > pos - p.window || t < p.sinks;
+        const bool all_see = t <= w.first && (t > w.end - p.window || t < p.sinks);
+        if (!sees || all_see) continue;
+        const int entry = p.page_shift >= 0 ? t >> p.page_shift : t / p.c.page_size, page = __ldg(table + entry);
+        if (page < 0 || page >= p.c.num_pages) continue;
+        const unsigned char* const v = p.c.v + page * p.c.page_bytes + w.kvh * p.c.head_bytes + (t - entry * p.c.page_size) * p.c.token_bytes;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if constexpr (FMT == kKvBf16) {
+            const uint32_t x = reinterpret_cast<const uint16_t*>(v)[lane * E + e];
+            if ((x & 0x7f80u) == 0x7f80u) s[e] += __uint_as_float(x << 16);
+          } else {
+            if ((v[lane * E + e] & 0x7f) == 0x7f) s[e] = __int_as_float(0x7fffffff);
+          }
+        }
+        bool all_nan = true;               // nothing more can change
+#pragma unroll
+        for (int e = 0; e < E; ++e) all_nan = all_nan && s[e] != s[e];
+        if (__all_sync(0xffffffffu, all_nan)) {
+          t = to;
+          part = 1;
+        }
+      }
+    }
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) any = any || s[e] != 0.f;
+    if (!__any_sync(0xffffffffu, any)) continue;
+    for (int r = max(r0, t_in * GB); r < min(r0 + 32, t_in * GB + GB); ++r) {
+      const int g = r - t_in * GB;
+      if (g >= w.heads) break;
+      uint16_t* const out = p.out + (static_cast<long long>(w.row0) + i * TT + t_in) * p.out_stride + (w.h0 + g) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        uint32_t* const at = reinterpret_cast<uint32_t*>(out + e);
+        const uint32_t x = *at;
+        *at = pack_bf16x2(__uint_as_float(x << 16) + s[e], __uint_as_float(x & 0xffff0000u) + s[e + 1]);
+      }
+    }
+  }
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_constant__ ChunkArgs p) {
+  using Sh = ChunkShape<D>;
+  using Sm = ChunkSmem<D>;
+  constexpr int NP = Sh::pairs;
+  constexpr bool CODED = FMT != kKvBf16;
+  extern __shared__ unsigned char chunk_smem_raw[];
+  const uint32_t raw = smem_u32(chunk_smem_raw), pad = ((raw + 1023u) & ~1023u) - raw;
+  unsigned char* const base = chunk_smem_raw + pad;
+  const uint32_t q_s = raw + pad + Sm::q, ring = raw + pad + Sm::ring;
+  ChunkMeta* const metas = reinterpret_cast<ChunkMeta*>(base + Sm::meta);
+  float* const q_factor = reinterpret_cast<float*>(base + Sm::qf);           // [kPieces][256]
+  ChunkCtl& c = *reinterpret_cast<ChunkCtl*>(base + Sm::ctl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < 2 * NP; ++s) {
+      mbar_init(smem_u32(&c.full[s]), kGroups);
+      mbar_init(smem_u32(&c.empty[s]), 1);
+    }
+    for (int s = 0; s < kMeta; ++s) {
+      mbar_init(smem_u32(&c.meta_full[s]), kGroups);
+      mbar_init(smem_u32(&c.meta_empty[s]), kSoftWarps);
+    }
+    mbar_init(smem_u32(&c.q_full), kQWarps);
+    mbar_init(smem_u32(&c.q_empty), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&c.s_full[i >> 1][i & 1]), 1);
+      mbar_init(smem_u32(&c.p_ready[i >> 1][i & 1][0]), 4);
+      mbar_init(smem_u32(&c.p_ready[i >> 1][i & 1][1]), 4);
+      mbar_init(smem_u32(&c.o_done[i >> 1][i & 1]), 1);
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(smem_u32(&c.piece_full[i]), 1);
+      mbar_init(smem_u32(&c.piece_empty[i]), kSoftWarps + 1 + (kQWarps - 1) + kLoaders);
+    }
+    mbar_init(smem_u32(&c.drain), 1);
+    c.failed = 0;
+    mbar_fence_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&c.tmem), 512);
+    tmem_relinquish();
+  }
   pdl_wait_then_release();
-  const int lane = threadIdx.x & 31, b = blockIdx.y;
-  const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
-  if (q0 < 0 || q1 > p.total_q || q1 <= q0) return;
-  const int n = q1 - q0, G = p.q_heads / p.c.kv_heads;
-  const long long most = static_cast<long long>(p.max_pages) * p.c.page_size;
-  const int len = static_cast<int>(min(static_cast<long long>(max(__ldg(p.lens + b), 0)), most));
-  const float sl2 = p.scale * kLog2e;
-  for (long long unit = static_cast<long long>(blockIdx.x) * kChunkWarps + threadIdx.x / 32; unit < static_cast<long long>(n) * p.q_heads;
-       unit += static_cast<long long>(gridDim.x) * kChunkWarps) {
-    const int i = static_cast<int>(unit / p.q_heads), h = static_cast<int>(unit - static_cast<long long>(i) * p.q_heads), kvh = h / G;
-    const long long row = q0 + i;
-    float q[E], o[E], m = -INFINITY, l = 0.f;
+
+  // ---- the batch's units, and where this CTA's range begins and ends
+  const int TT = p.tile_tokens, step = 2 * TT, GB = p.head_block;
+  const int G = p.q_heads / p.c.kv_heads, blocks = (G + GB - 1) / GB, subs = p.c.kv_heads * blocks;
+  {
+    long long* const sums = reinterpret_cast<long long*>(base + Sm::ring);               // units of a sequence and key-value head
+    const int per = (p.batch + kChunkThreads - 1) / kChunkThreads;
+    const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+    long long mine = 0;
+    for (int k = 0; k < per; ++k) {
+      const int b = b0 + k;
+      Seq s{};
+      if (b < b1) s = sequence(p, b);
+      const int np = s.n > 0 ? (s.n - 1) / step + 1 : 0;
+      long long sum = 0;
+      if (np <= kFewPairs)
+        for (int x = 0; x < np; ++x) sum += pair_tiles(p, s, step, x);
+      uint32_t many = __ballot_sync(0xffffffffu, np > kFewPairs);
+      while (many) {
+        const int src = __ffs(many) - 1;
+        many &= many - 1;
+        Seq o;
+        o.q0 = 0;
+        o.n = __shfl_sync(0xffffffffu, s.n, src);
+        o.len = __shfl_sync(0xffffffffu, s.len, src);
+        const int onp = (o.n - 1) / step + 1;
+        long long part = 0;
+        for (int x = lane; x < onp; x += 32) part += pair_tiles(p, o, step, x);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      q[e] = bf16_bits_to_f32(p.q[row * p.q_stride + h * D + lane * E + e]) * sl2;
-      o[e] = 0.f;
+        for (int y = 16; y > 0; y >>= 1) part += __shfl_xor_sync(0xffffffffu, part, y);
+        if (lane == src) sum = part;
+      }
+      if (b < b1) sums[b] = sum;
+      mine += sum;
     }
-    const int pos = len - n + i, low = max(0, pos - min(p.window - 1, pos));
-    auto value = [&](const unsigned char* at, int e, const float* scales, long long si) {
-      if constexpr (FMT == kKvBf16) return bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(at)[lane * E + e]);
-      float f[4];
-      codes_to_f32<FMT>(at[lane * E + e], f);
-      return f[0] * scales[si];
+    mine *= subs;
+    long long before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += t;
+    }
+    if (lane == 31) c.warp_sum[warp] = before;
+    before -= mine;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    long long total = 0;
+    for (int w = 0; w < kChunkWarps; ++w) {
+      if (w < warp) before += c.warp_sum[w];
+      total += c.warp_sum[w];
+    }
+    const long long n = min(static_cast<long long>(gridDim.x), (total + 1) / 2);     // CTAs with work
+    if (tid == 0) c.total = total;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (blockIdx.x >= n) break;
+      const long long u = cut(blockIdx.x + e, total, n);
+      if (u < before || u >= before + mine) continue;                        // another thread's sequences hold it
+      long long at = before;
+      for (int b = b0; b < b1; ++b) {
+        const long long all = sums[b] * subs;
+        if (u < at + all) {
+          c.seq[e] = b;
+          c.sum[e] = sums[b];
+          c.rem[e] = u - at;
+          break;
+        }
+        at += all;
+      }
+    }
+    __syncthreads();
+  }
+  const uint32_t tmem = c.tmem;
+  const long long total = c.total, ctas = min(static_cast<long long>(gridDim.x), (total + 1) / 2);
+  const bool works = blockIdx.x < ctas;
+
+  if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kHelperRegs));
+  if (warp == kPlanWarp || warp == kPlanWarp + 1) {
+    // ===================== pieces, and the rows of Q ======================
+    // Warp 9 walks the range; both load half of a piece's rows.
+    int b = 0, sub = 0, x = 0, tile = 0, tiles = 0;       // the item under the walk, and its next tile
+    long long s0 = 0, u = 0, u1 = 0;                      // its first unit; the walk's position and end
+    Seq s{};
+    const int snap = static_cast<int>(min(static_cast<long long>(kSnap), total / max(ctas, 1LL) / 4));
+    auto first_pair = [&]() { return max(0, (s.n - s.len) / step); };       // the first with a tile (s.len > 0)
+    auto next_item = [&]() {                              // (there is one)
+      s0 += tiles;
+      if ((x + 1) * step < s.n) {
+        ++x;
+      } else {
+        if (++sub == subs) {
+          sub = 0;
+          do s = sequence(p, ++b);
+          while (s.n == 0 || s.len == 0);
+        }
+        x = first_pair();
+      }
+      tile = 0;
+      tiles = pair_tiles(p, s, step, x);
     };
-    for (int t = 0; t <= pos; ++t) {
-      if (t >= p.sinks && t < low) t = low;
-      const int entry = p.page_shift >= 0 ? t >> p.page_shift : t / p.c.page_size, slot = t - entry * p.c.page_size;
-      const int page = __ldg(p.table + b * p.table_stride + entry);
-      if (page < 0 || page >= p.c.num_pages) continue;
-      const long long off = page * p.c.page_bytes + kvh * p.c.head_bytes + slot * p.c.token_bytes, si = scale_index(p.c, page, kvh, slot);
-      float z = 0.f;
+    if (warp == kPlanWarp && works) {
+      // The item that holds a cut, by prefix sums over its sequence's pairs; 0: this CTA's first unit, 1: the next one's.
+      for (int e = 1; e >= 0; --e) {
+        const long long r = cut(blockIdx.x + e, total, ctas);
+        if (r >= total) {
+          u1 = total;
+          continue;
+        }
+        b = c.seq[e];
+        s = sequence(p, b);
+        const long long su = c.sum[e];
+        sub = static_cast<int>(c.rem[e] / su);
+        const long long rest = c.rem[e] - sub * su;
+        const int np = (s.n - 1) / step + 1;
+        long long before = 0;
+        for (int x0 = 0; x0 < np; x0 += 32) {
+          const int mine = x0 + lane < np ? pair_tiles(p, s, step, x0 + lane) : 0;
+          long long incl = mine;
 #pragma unroll
-      for (int e = 0; e < E; ++e) z += q[e] * value(p.c.k + off, e, p.c.ks, si);
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-      const float mn = fmaxf(m, z), ref = mn == -INFINITY ? 0.f : mn, keep = exp2_fast(m - ref), w = exp2_fast(z - ref);
-      m = mn;
-      l = l * keep + w;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * keep + w * value(p.c.v + off, e, p.c.vs, si);
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
+          }
+          const uint32_t hit = __ballot_sync(0xffffffffu, rest < before + incl);
+          if (hit) {
+            const int src = __ffs(hit) - 1;
+            x = x0 + src;
+            tiles = __shfl_sync(0xffffffffu, mine, src);
+            tile = static_cast<int>(rest - before - (__shfl_sync(0xffffffffu, incl, src) - tiles));
+            break;
+          }
+          before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        s0 = r - tile;
+        if (tile <= snap) tile = 0;
+        else if (tiles - tile <= snap) tile = tiles;
+        if (e == 1) u1 = s0 + tile;
+        else u = s0 + tile;
+      }
+      if (u < u1 && tile == tiles) next_item();
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t loads = 0;
+    for (int it = 0;; ++it) {
+      const int sl = it % kPieces;
+      if (warp == kPlanWarp) {
+        // (a slot is written again only when all have left it, after a failure too: nobody stops before the last piece)
+        if (it >= kPieces && wait(c, c.piece_empty[sl], ((it / kPieces) - 1) & 1))
+          mbar_wait_limit(smem_u32(&c.piece_empty[sl]), ((it / kPieces) - 1) & 1, kDrainLimitCycles);
+        __syncwarp();
+        const bool go = u < u1 && !__any_sync(0xffffffffu, failed(c));
+        if (lane == 0) {
+          ChunkPiece w;
+          w.valid = go;
+          if (go) {
+            const int t0 = x * step, t1 = min(t0 + step, s.n);
+            w.b = b;
+            w.row0 = s.q0 + t0;
+            w.first = s.len - s.n + t0;
+            w.end = s.len - s.n + t1 - 1;
+            w.kvh = sub / blocks;
+            w.h0 = w.kvh * G + (sub - w.kvh * blocks) * GB;
+            w.heads = min(GB, w.kvh * G + G - w.h0);
+            const Span v = span(p, w.first, w.end);
+            w.low = v.low;
+            w.kept = v.kept;
+            w.skip = v.skip;
+            w.tiles = tiles;
+            w.ta = tile;
+            w.n = static_cast<int>(min(static_cast<long long>(tiles), tile + (u1 - u))) - tile;
 #pragma unroll
-    for (int e = 0; e < E; ++e) p.out[row * p.out_stride + h * D + lane * E + e] = f32_to_bf16_bits(o[e] * inv);
-    if (p.lse && lane == 0) p.lse[row * p.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            for (int i = 0; i < 2; ++i) {                 // tiles that hold a token its last row may see
+              const int last = min(w.first + (i + 1) * TT - 1, w.end), any = w.first + i * TT <= w.end && last >= 0;
+              w.ni[i] = any ? max(0, min(w.ta + w.n, last / kTile + 1 - w.skip) - w.ta) : 0;
+            }
+            w.c0 = static_cast<int>(((s0 + snap + 1) * ctas + total - 1) / total) - 1;
+            w.c1 = static_cast<int>(((s0 + tiles - snap) * ctas + total - 1) / total) - 1;
+          }
+          c.piece[sl] = w;
+          *reinterpret_cast<volatile int*>(&c.bad[sl]) = 0;
+          mbar_arrive(smem_u32(&c.piece_full[sl]));
+        }
+        __syncwarp();
+        if (go) {
+          const int m = static_cast<int>(min(static_cast<long long>(tiles), tile + (u1 - u))) - tile;
+          u += m;
+          tile += m;
+          if (u < u1) next_item();
+        }
+      }
+      wait(c, c.piece_full[sl], (it / kPieces) & 1);
+      __syncwarp();
+      const ChunkPiece& w = c.piece[sl];
+      const bool valid = __shfl_sync(0xffffffffu, w.valid, 0);
+      if (valid && !__any_sync(0xffffffffu, failed(c))) {
+        if (loads > 0) wait(c, c.q_empty, (loads - 1) & 1);
+        ++loads;
+        __syncwarp();
+        // Rows of Q: 128 of each row tile, by 16-byte chunks; rows of nobody are zero.
+        constexpr int CH = D / 8, RPI = 32 / CH;          // chunks of a row; rows of an instruction
+        const int ch = lane % CH, tokens = w.end - w.first + 1;
+        const uint16_t* const q = p.q + w.h0 * D + ch * 8;
+        for (int r = (warp - kPlanWarp) * kTile + lane / CH; r < (warp - kPlanWarp + 1) * kTile; r += RPI) {
+          const int i = r >> 7, rr = r & 127, t_in = rr / GB, g = rr - t_in * GB, tok = i * TT + t_in;
+          const bool live = t_in < TT && g < w.heads && tok < tokens;
+          const uint16_t* const from = live ? q + (static_cast<long long>(w.row0) + tok) * p.q_stride + g * D : p.q;
+          copy16(q_s + i * Sh::tile_bytes + Sh::at(rr, ch), from, live);
+        }
+        cp_async_commit();
+        copies_left<0>();
+        if constexpr (CODED) {
+          // BF16 -> f16, each row's largest magnitude at 2^14 .. 2^15, by a power of two
+          for (int r = (warp - kPlanWarp) * kTile + lane / CH; r < (warp - kPlanWarp + 1) * kTile; r += RPI) {
+            const uint32_t at = q_s + (r >> 7) * Sh::tile_bytes + Sh::at(r & 127, ch);
+            const uint4 v = lds128(at);
+            const uint32_t m2 = abs_max2(0, v);
+            uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+            for (int o = CH / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int e = static_cast<int>(top >> 7) - 127;
+            const int up = top == 0 || e == 128 ? 0 : max(-126, min(126, 14 - e));
+            const float f = __int_as_float((127 + up) << 23);
+            const uint32_t x4[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = pack_f16x2(__uint_as_float(x4[j] << 16) * f, __uint_as_float(x4[j] & 0xffff0000u) * f);
+            sts128(at, make_uint4(h[0], h[1], h[2], h[3]));
+            if (ch == 0) q_factor[sl * 2 * kTile + r] = __int_as_float((127 - up) << 23);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.q_full));
+      }
+      if (warp != kPlanWarp) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.piece_empty[sl]));
+      }
+      if (!valid) break;
+    }
+  } else if (warp >= kLoadWarp) {
+    // =========================== K and V tiles ============================
+    const int lw = warp - kLoadWarp;
+    uint32_t kt = 0, gg = 0;             // key tiles and groups of the pieces before
+    const float sl2 = p.scale * kLog2e;
+    constexpr int CH = (CODED ? D : 2 * D) / 16, TPI = 32 / CH, NI = kGroup / TPI;   // 16-byte chunks of a token; tokens of an instruction; instructions
+    const int ch = lane % CH, sub_t = lane / CH;
+    for (int it = 0;; ++it) {
+      const int sl = it % kPieces;
+      wait(c, c.piece_full[sl], (it / kPieces) & 1);
+      __syncwarp();
+      const ChunkPiece& w = c.piece[sl];
+      if (!w.valid) break;
+      const int32_t* const table = p.table + w.b * p.table_stride;
+      const int groups = w.n * kGroups;
+      bool bad = false;
+      // First token of group g of the piece.
+      auto token0 = [&](int g) {
+        const int t = w.ta + g / kGroups;
+        return (t < w.kept ? t : t + w.skip) * kTile + (g % kGroups) * kGroup;
+      };
+      // Page of this lane's token (lanes 16 .. 31 as lanes 0 .. 15) and its slot; -1: nobody sees it.
+      auto look_up = [&](int g, int& slot) {
+        const int t = token0(g) + (lane & 15);
+        slot = 0;
+        if (t > w.end || (t < w.low && t >= p.sinks)) return -1;
+        const int entry = p.page_shift >= 0 ? t >> p.page_shift : t / p.c.page_size;
+        slot = t - entry * p.c.page_size;
+        return __ldg(table + entry);
+      };
+      // Of a group: some of its tokens are seen by some rows and not by others.
+      auto partly = [&](int g) {
+        const int t = token0(g);
+        return !(t + kGroup - 1 <= w.first && (t > w.end - p.window || t + kGroup - 1 < p.sinks));
+      };
+      auto part_seen = [&](int t) { return !(t <= w.first && (t > w.end - p.window || t < p.sinks)); };
+      const int g0 = static_cast<int>((lw + kLoaders - gg % kLoaders) % kLoaders);   // this warp's first group
+      // The stages and the masks of group g's tile are free; false: it has to be waited for.
+      auto ready = [&](int g, bool block) {
+        const uint32_t k = kt + g / kGroups, ks = 2 * (k % NP);
+        bool ok = true;
+        if (k >= NP) {
+          const uint32_t ph = ((k / NP) - 1) & 1;
+          if (block) {
+            wait(c, c.empty[ks], ph);
+            wait(c, c.empty[ks + 1], ph);
+          } else {
+            ok = passed(c.empty[ks], ph) && passed(c.empty[ks + 1], ph);
+          }
+        }
+        if (k >= kMeta) {
+          const uint32_t ph = ((k / kMeta) - 1) & 1;
+          if (block) wait(c, c.meta_empty[k % kMeta], ph);
+          else ok = ok && passed(c.meta_empty[k % kMeta], ph);
+        }
+        return __all_sync(0xffffffffu, ok);
+      };
+      auto arrive = [&](int g) {
+        const uint32_t k = kt + g / kGroups, ks = 2 * (k % NP);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&c.meta_full[k % kMeta]));
+          mbar_arrive(smem_u32(&c.full[ks]));
+          mbar_arrive(smem_u32(&c.full[ks + 1]));
+        }
+      };
+      if constexpr (!CODED) {
+        int next = g0;                   // the oldest group that has not been handed over
+        auto hand_over = [&]() {         // its copies have landed
+          if (partly(next)) {
+            const uint32_t k = kt + next / kGroups, at = ring + (2 * (k % NP) + 1) * Sh::tile_bytes;
+            const int t0 = token0(next), r0 = (next % kGroups) * kGroup;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+              const int t = i * TPI + sub_t;
+              const uint32_t to = at + Sh::at(r0 + t, ch);
+              const uint4 v = lds128(to);
+              if (part_seen(t0 + t) && !all_finite(abs_max2(0, v))) {
+                bad = true;
+                sts128(to, make_uint4(finite_or_zero(v.x), finite_or_zero(v.y), finite_or_zero(v.z), finite_or_zero(v.w)));
+              }
+            }
+            if (__any_sync(0xffffffffu, bad) && lane == 0) *reinterpret_cast<volatile int*>(&c.bad[sl]) = 1;
+          }
+          arrive(next);
+          next += kLoaders;
+        };
+        int slot = 0, page = g0 < groups ? look_up(g0, slot) : -1;
+        for (int g = g0; g < groups; g += kLoaders) {
+          const bool there = page >= 0 && page < p.c.num_pages;
+          const long long off = there ? page * p.c.page_bytes + w.kvh * p.c.head_bytes + slot * p.c.token_bytes : -1;
+          const uint32_t live = __ballot_sync(0xffffffffu, there) & 0xffffu;
+          if (g + kLoaders < groups) page = look_up(g + kLoaders, slot);     // (while this group is on its way)
+          if (!ready(g, false)) {        // (what is in flight may be what it waits for)
+            copies_left<0>();
+            while (next < g) hand_over();
+            ready(g, true);
+            if (__any_sync(0xffffffffu, failed(c))) break;
+          }
+          const uint32_t k = kt + g / kGroups, at = ring + 2 * (k % NP) * Sh::tile_bytes;
+          const int r0 = (g % kGroups) * kGroup;
+          if (lane == 0) metas[k % kMeta].live[g % kGroups] = static_cast<uint16_t>(live);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const int t = i * TPI + sub_t;
+            const long long o = __shfl_sync(0xffffffffu, off, t);
+            const uint32_t to = at + Sh::at(r0 + t, ch);
+            const long long from = (o < 0 ? 0 : o) + ch * 16;
+            copy16(to, p.c.k + from, o >= 0);
+            copy16(to + Sh::tile_bytes, p.c.v + from, o >= 0);
+          }
+          cp_async_commit();
+          if (next + kLag * kLoaders <= g) {
+            copies_left<kLag>();
+            hand_over();
+          }
+        }
+        copies_left<0>();
+        while (next < groups && !__any_sync(0xffffffffu, failed(c))) hand_over();
+      } else {
+        // K of the next group is loaded while V of this one is converted: half of a group at least is always in flight.
+        uint4 kx[NI], vx[NI];
+        long long off = -1;
+        bool there = false;
+        float ks = 0.f, vs = 0.f;
+        int slot = 0, page = g0 < groups ? look_up(g0, slot) : -1;
+        auto locate = [&]() {            // of the group whose page was looked up; its scales
+          there = page >= 0 && page < p.c.num_pages;
+          off = there ? page * p.c.page_bytes + w.kvh * p.c.head_bytes + slot * p.c.token_bytes : -1;
+          ks = vs = 0.f;
+          if (there) {
+            const long long si = scale_index(p.c, page, w.kvh, slot);
+            ks = __ldg(p.c.ks + si);
+            vs = __ldg(p.c.vs + si);
+          }
+        };
+        auto fetch = [&](const unsigned char* from, uint4 (&to)[NI]) {
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const long long o = __shfl_sync(0xffffffffu, off, i * TPI + sub_t);
+            to[i] = make_uint4(0, 0, 0, 0);
+            if (o >= 0) to[i] = __ldg(reinterpret_cast<const uint4*>(from + o + ch * 16));
+          }
+        };
+        // 16 codes -> two chunks of f16 (lanes of the upper half of a row store them in the other order: no bank twice).
+        auto put = [&](uint32_t at, int r, const uint4& v) {
+          uint32_t h[8];
+          codes_to_f16<FMT>(v.x, h[0], h[1]);
+          codes_to_f16<FMT>(v.y, h[2], h[3]);
+          codes_to_f16<FMT>(v.z, h[4], h[5]);
+          codes_to_f16<FMT>(v.w, h[6], h[7]);
+          const bool swap = CH == 8 && ch >= 4;
+          const uint4 first = swap ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+          const uint4 second = swap ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(h[4], h[5], h[6], h[7]);
+          sts128(at + Sh::at(r, 2 * ch + swap), first);
+          sts128(at + Sh::at(r, 2 * ch + !swap), second);
+        };
+        if (g0 < groups) {
+          locate();
+          fetch(p.c.k, kx);
+        }
+        for (int g = g0; g < groups; g += kLoaders) {
+          fetch(p.c.v, vx);
+          const float k_scale = ks, v_scale = vs;
+          const bool was_there = there;
+          if (g + kLoaders < groups) page = look_up(g + kLoaders, slot);
+          ready(g, true);
+          if (__any_sync(0xffffffffu, failed(c))) break;
+          const uint32_t k = kt + g / kGroups, at = ring + 2 * (k % NP) * Sh::tile_bytes;
+          const int r0 = (g % kGroups) * kGroup, t0 = token0(g);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) put(at, r0 + i * TPI + sub_t, kx[i]);
+          if (g + kLoaders < groups) {
+            locate();
+            fetch(p.c.k, kx);
+          }
+          // Masks and scales. A scale of 0 stands for codes whose weight only counts in the sum: 2^-64 there, with the codes
+          // zero; a negative one changes the codes' signs. (Below 2^-110, under what lora_kv_write stores: 2^-110.)
+          ChunkMeta& m = metas[k % kMeta];
+          const uint32_t live = __ballot_sync(0xffffffffu, was_there) & 0xffffu;
+          if (lane == 0) m.live[g % kGroups] = static_cast<uint16_t>(live);
+          if (lane < kGroup) {
+            const float mag = v_scale == 0.f ? 5.421010862427522e-20f : fmaxf(fabsf(v_scale), 7.703719777548943e-34f);
+            const float s = v_scale != v_scale ? v_scale : mag;       // (fmaxf drops NaN)
+            m.a[r0 + lane] = k_scale * sl2;
+            m.b[r0 + lane] = log2f(s);
+            m.iv[r0 + lane] = v_scale != v_scale ? 0.f : kSumUnit / s;   // (times the weight 0 of a row that does not see it: 0)
+          }
+          const uint32_t odd = __ballot_sync(0xffffffffu, was_there && v_scale <= 0.f);
+          const bool look = FMT == kKvE4m3 && partly(g);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const int t = i * TPI + sub_t;
+            uint4 v = vx[i];
+            if (odd || look) {
+              uint32_t x4[4] = {v.x, v.y, v.z, v.w};
+              const float sc = __shfl_sync(0xffffffffu, v_scale, t);
+              const bool part = look && part_seen(t0 + t);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (part) {                // NaN codes (magnitude 0x7f) to zero
+                  const uint32_t nan = (((x4[j] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+                  if (nan) bad = true;
+                  x4[j] &= ~(nan * 0xffu);
+                }
+                if (sc == 0.f) x4[j] = 0;
+                if (sc < 0.f) {
+                  if constexpr (FMT == kKvE4m3) x4[j] ^= 0x80808080u;
+                  else x4[j] = __vneg4(x4[j]);
+                }
+              }
+              v = make_uint4(x4[0], x4[1], x4[2], x4[3]);
+            }
+            put(at + Sh::tile_bytes, r0 + t, v);
+          }
+          if (__any_sync(0xffffffffu, bad) && lane == 0) *reinterpret_cast<volatile int*>(&c.bad[sl]) = 1;
+          arrive(g);
+        }
+      }
+      kt += w.n;
+      gg += groups;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c.piece_empty[sl]));
+    }
+    copies_left<0>();
+  } else if (warp == kMmaWarp) {
+    // ============================ MMA issue ===============================
+    // The whole warp takes every step, one elected lane issues. Row tile i's scores of key tile j + 1 go out
+    // after its P V of key tile j when there are two score buffers (one per row tile), so a warpgroup waits for
+    // both; with three buffers they go out half a step earlier and are there when it is done with its weights.
+    constexpr uint32_t type = CODED ? (1u << 7) | (1u << 10) : 0u;     // f16 instead of BF16
+    constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile) & ~type;
+    constexpr uint32_t id_o = (idesc_bf16_f32(kTile, D) & ~type) | (1u << 16);   // V: MN-major
+    uint32_t kt = 0, st[2] = {0, 0}, pt[2] = {0, 0};   // key tiles of the pieces before; by row tile: scores, P V
+    int loads = 0, n0 = 0, n1 = 0, n = 0;
+    bool dead = false;
+    auto scores = [&](auto row_tile, int j) {          // S_i = Q_i K_j^T
+      constexpr int i = decltype(row_tile)::value;
+      const uint32_t k = kt + j, ks = 2 * (k % NP);
+      if (Sh::bufs == 3 && (i == 0 || j >= n0)) {
+        dead |= wait(c, c.full[ks], (k / NP) & 1);        // the key tile's first use
+        __syncwarp();
+        tc_fence_after();
+      }
+      const uint64_t qa = smem_desc(q_s + i * Sh::tile_bytes, 1024, Swz::k128);
+      const uint64_t ka = smem_desc(ring + ks * Sh::tile_bytes, 1024, Swz::k128);
+      const uint32_t to = tmem + Sh::buf(i, j) * kTile;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {            // (descriptors hold addresses in 16-byte units)
+        const uint64_t o = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+        umma_bf16_warp(to, qa + o, ka + o, id_s, kk != 0);
+      }
+      umma_commit_warp(smem_u32(&c.s_full[i][st[i] & 1]));
+      ++st[i];
+    };
+    // After the last use of K tile j.
+    auto keys_done = [&](int j) {
+      umma_commit_warp(smem_u32(&c.empty[2 * ((kt + j) % NP)]));
+      if (j + 1 == n) umma_commit_warp(smem_u32(&c.q_empty));
+    };
+    auto values = [&](auto row_tile, int j, uint32_t vs) {   // O_i (+)= P_i V_j, as its halves of the keys come
+      constexpr int i = decltype(row_tile)::value;
+      const uint64_t va = smem_desc_mn128(ring + vs * Sh::tile_bytes, kTile * 128, 1024);
+      const uint32_t from = tmem + Sh::buf(i, j) * kTile;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (Sh::bufs == 2 || half == 0) {
+          dead |= wait(c, c.p_ready[i][pt[i] & 1][Sh::bufs == 2 ? half : 1], (pt[i] >> 1) & 1);
+          __syncwarp();
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int kk = half * (kTile / 32); kk < (half + 1) * (kTile / 32); ++kk)
+          umma_bf16_ts_warp(tmem + Sh::col_o + i * D, from + kk * 8, va + kk * (2048 >> 4), id_o, kk != 0 || j != 0);
+      }
+      umma_commit_warp(smem_u32(&c.o_done[i][pt[i] & 1]));
+      ++pt[i];
+    };
+    constexpr std::integral_constant<int, 0> r0{};
+    constexpr std::integral_constant<int, 1> r1{};
+    for (int it = 0;; ++it) {
+      const int sl = it % kPieces;
+      wait(c, c.piece_full[sl], (it / kPieces) & 1);
+      __syncwarp();
+      const bool valid = __shfl_sync(0xffffffffu, c.piece[sl].valid, 0);
+      n0 = __shfl_sync(0xffffffffu, c.piece[sl].ni[0], 0);
+      n1 = __shfl_sync(0xffffffffu, c.piece[sl].ni[1], 0);
+      n = __shfl_sync(0xffffffffu, c.piece[sl].n, 0);
+      if (lane == 0) mbar_arrive(smem_u32(&c.piece_empty[sl]));
+      __syncwarp();
+      if (!valid) break;
+      dead |= wait(c, c.q_full, loads & 1);
+      ++loads;
+      if (__any_sync(0xffffffffu, dead)) continue;
+      // Scores of key tile j for both row tiles, in the order of use, with the release of K behind the last one.
+      auto keys = [&](auto row_tile, int j) {
+        constexpr int i = decltype(row_tile)::value;
+        scores(row_tile, j);
+        if (i == 1 || j >= n1) keys_done(j);
+      };
+      if constexpr (Sh::bufs == 2) {
+        dead |= wait(c, c.full[2 * (kt % NP)], (kt / NP) & 1);
+        __syncwarp();
+        tc_fence_after();
+      }
+      if (n0 > 0) keys(r0, 0);
+      if (n1 > 0) keys(r1, 0);
+      if (Sh::bufs == 3 && n0 > 1) keys(r0, 1);
+      for (int j = 0; j < n; ++j) {
+        const uint32_t k = kt + j, vs = 2 * (k % NP) + 1;
+        dead |= wait(c, c.full[vs], (k / NP) & 1);
+        if (Sh::bufs == 2 && j + 1 < n) dead |= wait(c, c.full[2 * ((k + 1) % NP)], ((k + 1) / NP) & 1);
+        __syncwarp();
+        tc_fence_after();
+        if (j < n0) values(r0, j, vs);
+        if (Sh::bufs == 2 ? j + 1 < n0 : j + 1 < n1) {
+          if constexpr (Sh::bufs == 2) keys(r0, j + 1); else keys(r1, j + 1);
+        }
+        if (j < n1) values(r1, j, vs);
+        umma_commit_warp(smem_u32(&c.empty[vs]));
+        if (Sh::bufs == 2 ? j + 1 < n1 : j + 2 < n0) {
+          if constexpr (Sh::bufs == 2) keys(r1, j + 1); else keys(r0, j + 2);
+        }
+        if (j >= n0 && j >= n1) {          // (a tile that no row of the piece needs: its K is let go here)
+          if constexpr (Sh::bufs == 3) dead |= wait(c, c.full[vs - 1], (k / NP) & 1);
+          keys_done(j);
+        }
+        if (__any_sync(0xffffffffu, dead)) break;
+      }
+      kt += n;
+    }
+    if (failed(c)) {                     // let the MMAs in flight end
+      __syncwarp();
+      umma_commit_warp(smem_u32(&c.drain));
+      mbar_wait_limit(smem_u32(&c.drain), 0, kDrainLimitCycles);
+    }
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
+    // ============================= softmax ================================
+    const int i = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t col_o = lane_base + Sh::col_o + i * D;
+    const float sl2 = p.scale * kLog2e, grow = CODED ? kGrow : kGrow / sl2;
+    const int t_in = row / GB, g = row - t_in * GB;
+    const uint32_t stage = raw + pad + Sm::stage + warp * kStageBytes;
+    bool dead = false;
+    uint32_t t = 0, kt = 0;              // key tiles of this row tile so far; of the pieces before
+    for (int it = 0;; ++it) {
+      const int sl = it % kPieces;
+      wait(c, c.piece_full[sl], (it / kPieces) & 1);
+      __syncwarp();
+      const ChunkPiece& w = c.piece[sl];
+      if (!w.valid) break;               // (the only way out: all eight warps meet at the joins' barriers)
+      const int pos = w.first + i * TT + t_in, n = w.ni[i];
+      const bool live = t_in < TT && g < w.heads && pos <= w.end;
+      float qf = 1.f;                      // 8 bits: Q was divided by it
+      bool plain_q = true;
+      uint32_t buf = Sh::buf(i, 0);
+      float ref = -INFINITY, l = 0.f;      // exponents are relative to ref (BF16: in units of raw scores, less kGrow)
+      for (int j = 0; j < n; ++j, ++t) {
+        const uint32_t col_s = lane_base + buf * kTile;
+        if constexpr (Sh::bufs == 3) buf = buf == 0 ? 2 : buf - 1;   // (2 j + i) mod 3
+        const uint32_t k = kt + j;
+        const ChunkMeta& m = metas[k % kMeta];
+        dead |= wait(c, c.meta_full[k % kMeta], (k / kMeta) & 1);
+        dead |= wait(c, c.s_full[i][t & 1], (t >> 1) & 1);
+        __syncwarp();
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(col_s + q * 32, s[q]);
+        tmem_ld_wait();
+        if constexpr (CODED) {             // y = score * K's scale + log2 of V's
+          if (j == 0) {
+            qf = q_factor[sl * 2 * kTile + i * kTile + row];
+            plain_q = __all_sync(0xffffffffu, qf == 1.f);
+          }
+          const uint64_t qf2 = pair(qf, qf);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 a = *reinterpret_cast<const float4*>(m.a + q * 32 + e), b = *reinterpret_cast<const float4*>(m.b + q * 32 + e);
+              uint64_t a01 = pair(a.x, a.y), a23 = pair(a.z, a.w);
+              if (!plain_q) {
+                a01 = mul2(a01, qf2);
+                a23 = mul2(a23, qf2);
+              }
+              const float2 y0 = unpair(fma2(pair(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), a01, pair(b.x, b.y)));
+              const float2 y1 = unpair(fma2(pair(__uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3])), a23, pair(b.z, b.w)));
+              s[q][e] = __float_as_uint(y0.x);
+              s[q][e + 1] = __float_as_uint(y0.y);
+              s[q][e + 2] = __float_as_uint(y1.x);
+              s[q][e + 3] = __float_as_uint(y1.y);
+            }
+        }
+        // What the row sees of the tile.
+        const int tile = w.ta + j, t0 = (tile < w.kept ? tile : tile + w.skip) * kTile;
+        const uint4 there = *reinterpret_cast<const uint4*>(m.live);
+        const int hi = pos - t0, lo = hi - min(p.window - 1, max(pos, 0)), sk = p.sinks - t0;    // sees x <= hi with x >= lo or x < sk
+        const bool whole = hi >= kTile - 1 && (lo <= 0 || sk >= kTile) && (there.x & there.y & there.z & there.w) == 0xffffffffu;
+        if (__any_sync(0xffffffffu, live && !whole)) {
+          const uint32_t there4[4] = {there.x, there.y, there.z, there.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            auto below = [&](int x) { return x <= q * 32 ? 0u : x >= q * 32 + 32 ? 0xffffffffu : (1u << (x - q * 32)) - 1; };   // bits under x
+            const uint32_t see = there4[q] & (hi >= kTile - 1 ? 0xffffffffu : below(hi + 1)) & (~below(lo) | below(sk));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1)) s[q][e] = 0xff800000u;
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mx[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+          for (int e = 1; e < 31; e += 2) mx[q] = max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+          mx[q] = fmaxf(mx[q], __uint_as_float(s[q][31]));
+        }
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        if (j == 0) {
+          ref = top;
+        } else if (__any_sync(0xffffffffu, live && top > ref + grow)) {   // (rows of nobody hold anything: no say)
+          const float nr = top > ref + grow ? top : ref;                  // (a row's bits do not go by its neighbours')
+          const float f = nr == -INFINITY ? 1.f : exp2_fast(CODED ? ref - nr : (ref - nr) * sl2);
+          ref = nr;
+          l *= f;
+          // (with three score buffers the P V before may still run)
+          dead |= wait(c, c.o_done[i][(t - 1) & 1], ((t - 1) >> 1) & 1);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32(col_o + q * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(col_o + q * 32, o);
+          }
+        }
+        // (nothing seen: every weight is 0)
+        const float off = ref == -INFINITY ? 0.f : CODED ? kTop - ref : __fmaf_rn(-ref, sl2, -kGrow);
+        const uint64_t sl2p = pair(sl2, sl2), offp = pair(off, off);
+        uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int q = 2 * h + (e >> 4), f = (e & 15) * 2;
+            const uint64_t z = pair(__uint_as_float(s[q][f]), __uint_as_float(s[q][f + 1]));
+            const float2 x = unpair(CODED ? add2(z, offp) : fma2(z, sl2p, offp));
+            const float w0 = exp2_fast(x.x), w1 = exp2_fast(x.y);
+            if constexpr (CODED) {
+              const float2 iv = *reinterpret_cast<const float2*>(m.iv + q * 32 + f);
+              sum[e & 3] = fma2(pair(w0, w1), pair(iv.x, iv.y), sum[e & 3]);
+              pk[e] = pack_f16x2(w0, w1);
+            } else {
+              sum[e & 3] = add2(sum[e & 3], pair(w0, w1));
+              pk[e] = pack_bf16x2(w0, w1);
+            }
+          }
+          tmem_st32(col_s + h * 32, pk);
+          if (Sh::bufs == 2 || h == 1) {   // (with three score buffers nothing of this warpgroup waits for P V: one hand-over)
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c.p_ready[i][t & 1][h]));
+          }
+        }
+        const float2 all = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+        l += all.x + all.y;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.meta_empty[k % kMeta]));
+        if ((j & 15) == 15 && __any_sync(0xffffffffu, dead)) break;
+      }
+      for (int j = n; j < w.n; ++j) {      // tiles that this row tile has no use for
+        const uint32_t k = kt + j;
+        wait(c, c.meta_full[k % kMeta], (k / kMeta) & 1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.meta_empty[k % kMeta]));
+      }
+      kt += w.n;
+      if (n > 0) dead |= wait(c, c.o_done[i][(t - 1) & 1], ((t - 1) >> 1) & 1);
+      __syncwarp();
+      tc_fence_after();
+
+      // Stored weights stand for weight * 2^-exponent, their sum l likewise (8 bits: times kSumUnit).
+      const float exponent = ref == -INFINITY ? -INFINITY : CODED ? ref - kTop : __fmaf_rn(ref, sl2, kGrow);
+      const long long out_row = static_cast<long long>(w.row0) + i * TT + t_in;
+      auto log_sum = [&](float e, float sum) { return sum == 0.f ? -INFINITY : (e + log2f(sum) + (CODED ? 14.f : 0.f)) * kLn2; };
+      auto inverse = [&](float sum) {      // of the sum without kSumUnit
+        if (!CODED) return sum == 0.f ? 0.f : 1.f / sum;
+        return sum == 0.f ? 0.f : sum > 1.f ? 1.f / sum * kSumUnit : 1.f / (sum / kSumUnit);
+      };
+      if (w.ta == 0 && w.n == w.tiles) {
+        // The whole item: its rows, through shared memory so that a store instruction writes whole 64-byte pieces.
+        uint16_t* const to = p.out + out_row * p.out_stride + (w.h0 + g) * D;
+        const uint32_t lives = __ballot_sync(0xffffffffu, live);
+        const float inv = n > 0 ? inverse(l) : 0.f;
+        const uint64_t invp = pair(inv, inv);
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32(col_o + q * 32, o);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t r[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float2 v = unpair(mul2(pair(__uint_as_float(o[e + 2 * y]), __uint_as_float(o[e + 2 * y + 1])), invp));
+              r[y] = n > 0 ? pack_bf16x2(v.x, v.y) : 0u;
+            }
+            sts128(stage + lane * 64 + (((e / 8) ^ ((lane >> 1) & 3)) << 4), make_uint4(r[0], r[1], r[2], r[3]));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int r = y * 8 + lane / 4, ch = lane % 4;
+            const uint4 v = lds128(stage + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+            uint16_t* const at = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), r));
+            if (((lives >> r) & 1) && !failed(c)) *reinterpret_cast<uint4*>(at + q * 32 + ch * 8) = v;
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        if (p.lse && live && !failed(c)) p.lse[out_row * p.q_heads + w.h0 + g] = n > 0 ? log_sum(exponent, l) : -INFINITY;
+        if (*reinterpret_cast<volatile int*>(&c.bad[sl]) && !failed(c)) {
+          __syncwarp();
+          add_not_finite<FMT, D>(p, w, warp, lane);
+        }
+      } else {
+        // A part: exponent, sum and O of its rows into this CTA's slot; the last CTA of the item joins them.
+        int* const counters = static_cast<int*>(p.workspace);
+        float* const slots = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kCounterBytes);
+        constexpr int SF = kSlotFloats<D>, FLAG = SF - 4;
+        const int me = blockIdx.x, tokens = w.end - w.first + 1;
+        const int rows = tokens > TT ? kTile + min(kTile, (tokens - TT) * GB) : min(kTile, tokens * GB);   // rows up to the last live one
+        float* const mine = slots + static_cast<long long>(2 * me + (w.ta == 0)) * SF;
+        const int rr = i * kTile + row;
+        if (rr < rows) {
+          mine[rr] = n > 0 ? exponent : -INFINITY;
+          mine[2 * kTile + rr] = n > 0 ? l : 0.f;
+        }
+        if (i * kTile + (warp & 3) * 32 < rows) {
+#pragma unroll
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t o[16];
+            if (n > 0) {
+              tmem_ld16(col_o + q * 16, o);
+              tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sts128(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4), make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+            __syncwarp();
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int r = y * 8 + lane / 4, ch = lane % 4, ra = i * kTile + (warp & 3) * 32 + r;
+              const uint4 v = lds128(stage + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+              if (ra < rows) *reinterpret_cast<uint4*>(mine + 4 * kTile + static_cast<long long>(ra) * D + q * 16 + ch * 4) = v;
+            }
+            __syncwarp();
+          }
+        }
+        tc_fence_before();
+        if (tid == 0) mine[FLAG] = __int_as_float(*reinterpret_cast<volatile int*>(&c.bad[sl]));
+
+        float* const factors = reinterpret_cast<float*>(base + Sm::stage);    // [kJoinGroup][256] over all warps' staging
+        static_assert(kJoinGroup * 2 * kTile * 4 <= kSoftWarps * kStageBytes, "factors of a join");
+        // Joins slots of CTAs first, first + by, .. (at most kJoinGroup): into the rows, or in place into the first's.
+        auto join = [&](int first_cta, int count, int by, bool last) {
+          auto slot_of = [&](int y) { return slots + static_cast<long long>(2 * (first_cta + y * by) + (first_cta + y * by == w.c0)) * SF; };
+          float e_all = -INFINITY, l_all = 0.f;
+          if (tid < rows) {
+            float es[kJoinGroup], ls[kJoinGroup];
+#pragma unroll
+            for (int y = 0; y < kJoinGroup; ++y) {
+              es[y] = y < count ? __ldcg(slot_of(y) + tid) : -INFINITY;
+              ls[y] = y < count ? __ldcg(slot_of(y) + 2 * kTile + tid) : 0.f;
+            }
+#pragma unroll
+            for (int y = 0; y < kJoinGroup; ++y) e_all = fmaxf(e_all, es[y]);
+            const float from = e_all == -INFINITY ? 0.f : e_all;
+#pragma unroll
+            for (int y = 0; y < kJoinGroup; ++y) {
+              es[y] = exp2_fast(es[y] - from);
+              l_all += ls[y] * es[y];
+            }
+            const float inv = last ? inverse(l_all) : 1.f;
+#pragma unroll
+            for (int y = 0; y < kJoinGroup; ++y) factors[y * 2 * kTile + tid] = es[y] * inv;
+          }
+          bool bad = false;
+          for (int y = 0; y < count; ++y) bad = bad || __float_as_int(__ldcg(slot_of(y) + FLAG)) != 0;
+          soft_sync();
+          // thread: 4 consecutive dimensions of one row at a time, all parts' loads in flight
+          for (int task = tid; task < rows * (D / 4); task += kSoftThreads) {
+            const int r = task / (D / 4), d = task % (D / 4) * 4;
+            float4 v[kJoinGroup];
+#pragma unroll
+            for (int y = 0; y < kJoinGroup; ++y) {
+              v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (y < count) v[y] = __ldcg(reinterpret_cast<const float4*>(slot_of(y) + 4 * kTile + r * D + d));
+            }
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int y = 0; y < kJoinGroup; ++y)
+              if (y < count) {
+                const float f = factors[y * 2 * kTile + r];
+                acc.x += v[y].x * f;
+                acc.y += v[y].y * f;
+                acc.z += v[y].z * f;
+                acc.w += v[y].w * f;
+              }
+            if (last) {
+              const int ri = r / kTile, rt = r % kTile / GB, rg = r % kTile - rt * GB, tok = ri * TT + rt;
+              if (rt < TT && rg < w.heads && tok < tokens && !failed(c))
+                *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(w.row0) + tok) * p.out_stride + (w.h0 + rg) * D + d) =
+                    make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+            } else {
+              *reinterpret_cast<float4*>(slot_of(0) + 4 * kTile + r * D + d) = acc;
+            }
+          }
+          if (last) {
+            const int rt = tid % kTile / GB, rg = tid % kTile - rt * GB, tok = tid / kTile * TT + rt;
+            if (p.lse && tid < rows && rt < TT && rg < w.heads && tok < tokens && !failed(c))
+              p.lse[(static_cast<long long>(w.row0) + tok) * p.q_heads + w.h0 + rg] = log_sum(e_all, l_all);
+          } else {
+            if (tid < rows) {
+              slot_of(0)[tid] = e_all;
+              slot_of(0)[2 * kTile + tid] = l_all;
+            }
+            if (tid == 0) slot_of(0)[FLAG] = __int_as_float(bad);
+          }
+          soft_sync();                     // (the factors lie where the warps stage their results)
+          if (last && bad && !failed(c)) add_not_finite<FMT, D>(p, w, warp, lane);
+        };
+        // Arrive at a counter; true in the CTA that is the last of `count`, which sets it back to 0.
+        auto last_of = [&](int* counter, int count) {
+          soft_sync();
+          if (tid == 0) {   // releases the CTA's writes before the barrier, acquires those of the CTAs before it
+            int seen;
+            asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;\n" : "=r"(seen) : "l"(counter) : "memory");
+            c.last = seen == count - 1;
+            if (c.last) *counter = 0;
+          }
+          soft_sync();
+          return *const_cast<const volatile int*>(&c.last) != 0;
+        };
+        const int groups = (w.c1 - w.c0) / kJoinGroup + 1, gi = (me - w.c0) / kJoinGroup;
+        const int head = w.c0 + gi * kJoinGroup, count = min(kJoinGroup, w.c1 - head + 1);
+        if (last_of(counters + (gi ? kMostCtas : 0) + head, count)) {
+          join(head, count, 1, groups == 1);
+          if (groups > 1 && last_of(counters + 2 * kMostCtas + w.c0, groups)) join(w.c0, groups, kJoinGroup, true);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c.piece_empty[sl]));
+    }
+    // Rows that stand before the first token, in whole pairs of row tiles (others are rows of an item): zeros.
+    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+      const Seq s = sequence(p, b);
+      const int none = s.n == 0 ? 0 : s.len == 0 ? s.n : max(0, s.n - s.len) / step * step;
+      for (int r = warp; r < none; r += kSoftWarps) {
+        uint16_t* const to = p.out + (static_cast<long long>(s.q0) + r) * p.out_stride;
+        for (int x = lane; x < p.q_heads * D / 8; x += 32) *reinterpret_cast<uint4*>(to + x * 8) = make_uint4(0, 0, 0, 0);
+        if (p.lse)
+          for (int x = lane; x < p.q_heads; x += 32) p.lse[(static_cast<long long>(s.q0) + r) * p.q_heads + x] = -INFINITY;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
 namespace {
 
+template <int FMT, int D>
+int launch_one(const ChunkArgs& a, void* stream) {
+  const auto kernel = chunk_kernel<FMT, D>;
+  // (set on every call: the attribute belongs to the current device, like the launch)
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkSmem<D>::bytes);
+  int dev = 0, sms = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(sms < kMostCtas ? sms : kMostCtas), 1, 1);
+  cfg.blockDim = dim3(kChunkThreads, 1, 1);
+  cfg.dynamicSmemBytes = ChunkSmem<D>::bytes;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, a));
+}
+
 template <int FMT>
 int launch_format(const ChunkArgs& a, void* stream) {
-  const unsigned per = static_cast<unsigned>(152 * 8 / a.batch + 1);
-  if (a.head_dim == 128) chunk_kernel<FMT, 128><<<dim3(per, a.batch), kChunkWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  else chunk_kernel<FMT, 64><<<dim3(per, a.batch), kChunkWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return static_cast<int>(cudaGetLastError());
+  return a.head_dim == 128 ? launch_one<FMT, 128>(a, stream) : launch_one<FMT, 64>(a, stream);
 }
 
 }  // namespace
@@ -85,6 +1300,19 @@ int launch_chunk(const ChunkArgs& a, void* stream) {
     case kKvE4m3: return launch_format<kKvE4m3>(a, stream);
     default: return launch_format<kKvInt8>(a, stream);
   }
+}
+
+int read_chunk_status(void* stream, uint32_t* out, int clear) {
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint32_t v = 0;
+  cudaError_t err = cudaMemcpyFromSymbolAsync(&v, g_chunk_status, sizeof v, 0, cudaMemcpyDeviceToHost, s);
+  if (err == cudaSuccess && clear) {
+    static const uint32_t z = 0;
+    err = cudaMemcpyToSymbolAsync(g_chunk_status, &z, sizeof z, 0, cudaMemcpyHostToDevice, s);
+  }
+  if (err == cudaSuccess) err = cudaStreamSynchronize(s);
+  *out = v;
+  return static_cast<int>(err);
 }
 
 }  // namespace glora

@@ -94,6 +94,8 @@ struct ChunkArgs {
   int page_shift;            // log2 of page_size, or -1: not a power of two
   float scale;
   int window, sinks;
+  int head_block;            // query heads of a row tile: the group's, in blocks of at most 128
+  int tile_tokens;           // tokens of a row tile: 128 / head_block
 };
 
 struct PrefillArgs {
@@ -122,7 +124,8 @@ int launch_decode(const DecodeArgs& a, void* stream);
 int launch_decode_window(const DecodeArgs& a, void* stream);
 int launch_chunk(const ChunkArgs& a, void* stream);
 int launch_prefill(const PrefillArgs& a, void* stream);
-// OR of the prefill kernel's device status bits since the last clear (synchronizes `stream`).
+// OR of the prefill (chunk) kernel's device status bits since the last clear (synchronizes `stream`).
 int read_prefill_status(void* stream, uint32_t* out, int clear);
+int read_chunk_status(void* stream, uint32_t* out, int clear);
 
 }  // namespace glora

@@ -3,7 +3,7 @@
 //
 //   x <- x * rsqrt(mean(x^2) + eps) * w          per head (optional)
 //   (y0, y1) = (x0 cos a - x1 sin a, x1 cos a + x0 sin a),   a = position[axis_j] * freq_j, pair j
-//   cache: k after that, v as it is: scale = max |y| / Q, code = round(y * (Q / max |y|)), Q = 448 or 127
+//   cache: k after that, v as it is: scale = a (1 / Q), code = round(y (Q (1 / a))), a = max |y|, Q = 448 or 127
 //
 // Every value is read and written once, with some 12 operations on it between: HBM bandwidth bounds it, latency at a
 // few rows. All of a value's work is done in fp32 registers and rounded once.
@@ -181,13 +181,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             for (int o = TPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(team, m, o));
             const bool finite = m < 0x7f800000u;
             const float amax = __uint_as_float(m);
-            // Lane 0 of the team divides Q / a, lane 1 a / Q.
-            const float quot = finite && amax >= kZeroRow ? ((i & 1) ? __fdiv_rn(amax, kv_qmax<FMT>()) : __fdiv_rn(kv_qmax<FMT>(), amax)) : 0.f;
-            const float inv = __shfl_sync(team, quot, 0, TPR);
+            // The divisions Q / a and a / Q as a reciprocal and products: every lane has the factor, without a division.
+            const float inv = finite && amax >= kZeroRow ? __fmul_rn(kv_qmax<FMT>(), __frcp_rn(amax)) : 0.f;
             if (stored) {
               *reinterpret_cast<uint32_t*>(to + lo) = inv != 0.f ? quantise4<FMT>(f, inv) : 0u;   // (not finite, or all but zero: codes of zero)
               *reinterpret_cast<uint32_t*>(to + hi) = inv != 0.f ? quantise4<FMT>(g, inv) : 0u;
-              if (i == 1) (kind[u] == 1 ? p.c.ks : p.c.vs)[scale_index(p.c, page, head[u], slot)] = finite ? quot : __int_as_float(0x7fffffff);
+              if (i == 0)
+                (kind[u] == 1 ? p.c.ks : p.c.vs)[scale_index(p.c, page, head[u], slot)] =
+                    !finite ? __int_as_float(0x7fffffff) : inv != 0.f ? __fmul_rn(amax, 1.f / kv_qmax<FMT>()) : 0.f;
             }
           }
         }

@@ -540,9 +540,13 @@ int lora_qk_rope(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* q_out,
  * into theirs as they are. q_heads may be 0 (q and q_out ignored); k rows are
  * left as they are.
  * The rotated keys are quantised from f32, without a rounding to BF16 before (a
- * BF16 cache: rounded once), with lora_kv_write's formulas and its rules for
- * slots: a row whose slot is outside the cache is stored nowhere (its q row is
- * rotated all the same), a slot named twice is left undefined.
+ * BF16 cache: rounded once). E4M3 and INT8 as in lora_kv_write, its two divisions
+ * as a reciprocal and products:
+ *   scale = a * (1 / Q),  code = round(y * (Q * (1 / a)))    (f32 operations, ties to even),
+ * so a scale may differ from lora_kv_write's in its last bit and a code beside a
+ * tie be the neighbour. Its rules for slots hold: a row whose slot is outside the
+ * cache is stored nowhere (its q row is rotated all the same), a slot named twice
+ * is left undefined.
  */
 int lora_kv_append(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* q_out, int64_t q_out_row_stride,
                    int32_t q_heads, const lora_bf16_t* k, int64_t k_row_stride, const lora_bf16_t* v,
@@ -589,7 +593,6 @@ int lora_attn_decode_window(const lora_bf16_t* q, int64_t q_row_stride, lora_bf1
  *   block_table, table_stride, max_pages, seq_lens, scale   as in lora_attn_decode
  *   lse         optional [total_q, q_heads] f32: ln sum_t exp(z_t)
  *   workspace   as in lora_attn_decode, LORA_CHUNK_WORKSPACE bytes, its own
- * An E4M3 code that is NaN makes its whole token NaN to the rows that see it.
  * How the work is split follows the whole batch: the same call gives the same bits.
  */
 #define LORA_CHUNK_WORKSPACE (48 << 20)

@@ -55,11 +55,20 @@ def run(cache, table, q, cu, lens, h, scale, window=S.EVERY, sinks=0, ws=None, o
     return out
 
 
+def f16_floor(vval, lens):
+    """Over 8-bit caches the weights w_t s_t are kept in f16, the largest of a row between 2^7 and 2^15: one whose f16 is
+    subnormal is off by at most half of 2^-24 whatever its own size, 2^-32 of the largest. With s the scale of the token
+    with the largest and codes c_t, the result is off by at most 2^-32 s sum_t |c_t| <= 2^-32 (tokens) max |v|."""
+    return 2.0 ** -32 * max(lens, default=0) * vval.abs().nan_to_num(0, 0, 0).amax()
+
+
 def compare(cache, kval, vval, table, q, cu, lens, h, scale=0.1, window=S.EVERY, sinks=0, ws=None):
     page = cache.struct.page_size
     lse = torch.full((q.shape[0], h), 5.0, device="cuda")
     out = run(cache, table, q, cu, lens, h, scale, window, sinks, ws=ws, lse=lse)
     want, wl, bound, covered = S.chunk_want(q, kval, vval, table, cu, lens, page, scale, h, window, sinks)
+    if cache.struct.format != L.KV_BF16:
+        bound = bound + f16_floor(vval, lens)
     R.check(out.view(want.shape)[covered], want[covered], bound[covered], ("out", window, sinks))
     mag = scale * q.shape[1] / h * q.double().abs().nan_to_num(0, 0, 0).amax() * kval.abs().nan_to_num(0, 0, 0).amax() if q.shape[0] else 0
     R.check_lse(lse[covered], wl[covered], mag, "lse")

@@ -2,6 +2,7 @@
 derived in tests/step_refs.py (-m gpu)."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
@@ -148,11 +149,19 @@ def fresh(num, kv, page, d, fmt, layout):
     return pages, sc, L.KvCache(*pages, *sc)
 
 
+def product_codes(x, fmt):
+    """float32 rows [..., D] -> (code values float64, scale float32) by a reciprocal and products, each rounded to float32."""
+    q = np.float32(R.QMAX[fmt])
+    a = np.abs(x).max(-1)
+    y = (x * (q * (np.float32(1) / a))[..., None]).astype(np.float64)
+    return R.round_e4m3(y) if fmt == "e4m3" else np.clip(np.rint(y), -127, 127), a * (np.float32(1) / q)
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
 @pytest.mark.parametrize("d,rot,inter,axes,layout", [(128, 128, False, 1, "hnd"), (64, 64, True, 3, "nhd"), (128, 64, False, 2, "kv"), (64, 24, False, 1, "hnd")])
 @pytest.mark.parametrize("n,hq,hkv,page", [(1, 2, 1, 1), (3, 0, 2, 7), (37, 8, 4, 16), (515, 9, 3, 64), (4100, 8, 8, 20)])
 def test_append(fmt, d, rot, inter, axes, layout, n, hq, hkv, page):
-    """q as lora_qk_rope gives it, bit for bit; v as lora_kv_write stores it, bit for bit; k within the bounds of one
+    """q as lora_qk_rope gives it, bit for bit; v by the stated formulas, bit for bit; k within the bounds of one
     rounding to the format; skipped slots and everything else untouched."""
     g = A.gen(n + rot + d)
     freqs, axis, rope = rotation(d, rot, axes, inter)
@@ -172,17 +181,21 @@ def test_append(fmt, d, rot, inter, axes, layout, n, hq, hkv, page):
         assert torch.equal(q[:n], want_q)
     live = (slots >= 0) & (slots < num * page)
     pg, sl = slots[live] // page, slots[live] % page
-    # v, and the slots that were not named, as lora_kv_write leaves them
-    pages2, sc2, cache2 = fresh(num, hkv, page, d, fmt, layout)
-    v = rows[:, (hq + hkv) * d:]
-    L.lora_kv_write(v, v.stride(0), v, v.stride(0), slots, n, cache2)
-    byte = [t.view(torch.uint8) if fmt != "bf16" else t.contiguous().view(torch.uint8) for t in (*pages, *pages2)]
-    assert torch.equal(byte[1], byte[3])
+    # the slots that were not named
     hit = torch.zeros(num, page, dtype=torch.bool, device="cuda")
     hit[pg, sl] = True
-    assert (byte[0].transpose(1, 2)[~hit] == 0x5A).all()
-    if fmt != "bf16":
-        assert torch.equal(sc[1], sc2[1]) and (sc[0].transpose(1, 2)[~hit] == 7).all()
+    for x in pages:
+        assert ((x.view(torch.uint8) if fmt != "bf16" else x.contiguous().view(torch.uint8)).transpose(1, 2)[~hit] == 0x5A).all()
+    for x in sc if fmt != "bf16" else ():
+        assert (x.transpose(1, 2)[~hit] == 7).all()
+    # v: the formulas, operation by operation
+    v = rows[:, (hq + hkv) * d:].reshape(n, hkv, d)[live]
+    if fmt == "bf16":
+        assert torch.equal(pages[1][pg, :, sl], v)
+    else:
+        code, scale = product_codes(v.float().cpu().numpy(), fmt)
+        assert np.array_equal(pages[1].view(torch.uint8)[pg, :, sl].view(R.DTYPE[fmt]).double().cpu().numpy(), code)
+        assert np.array_equal(sc[1][pg, :, sl].cpu().numpy(), scale)
     # k
     y, mag = S.turned(rows[:, hq * d:(hq + hkv) * d].double().reshape(n, hkv, d), pos, freqs, axis, rot, inter, kn, EPS)
     y, mag = y[live], mag[live]
