@@ -46,8 +46,8 @@ constexpr int kTile = 128;                      // rows of a tile, tokens of a k
 constexpr int kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
 constexpr int kMmaWarp = 8, kPlanWarp = 9, kQWarps = 2, kLoadWarp = 11, kLoaders = 5;
 constexpr int kChunkThreads = 512, kChunkWarps = kChunkThreads / 32;
-// Registers a thread: 128 at launch; two warpgroups give away what the softmax's rows of scores need: 2 * 64 + 2 * 192 = 4 * 128.
-constexpr int kHelperRegs = 64, kSoftRegs = 192;
+// Registers a thread: 128 at launch; two warpgroups give away what the softmax's rows of scores need: 2 * 104 + 2 * 152 = 4 * 128.
+constexpr int kHelperRegs = 104, kSoftRegs = 152;
 constexpr int kPieces = 4;                      // depth of the ring of pieces
 constexpr int kMeta = 4;                        // depth of the ring of tokens' masks and scales
 constexpr int kGroup = 16, kGroups = kTile / kGroup;   // tokens of a loader's group; groups of a tile
@@ -122,7 +122,7 @@ struct ChunkSmem {
   static constexpr int meta = stage + kSoftWarps * kStageBytes;
   static constexpr int qf = meta + kMeta * static_cast<int>(sizeof(ChunkMeta));
   static constexpr int ctl = qf + kPieces * 2 * kTile * 4;
-  static constexpr int bytes = ctl + static_cast<int>(sizeof(ChunkCtl)) + 1024;    // (+ alignment)
+  static constexpr int bytes = ctl + static_cast<int>(sizeof(ChunkCtl));
   static_assert(sizeof(ChunkMeta) % 16 == 0 && bytes <= 232448, "shared memory");
   static_assert(kMostSeqs * 8 <= 2 * Sh::pairs * Sh::tile_bytes, "the plan's sums lie in the ring");
 };
@@ -183,6 +183,18 @@ __device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t&
   }
 }
 
+// 32 columns of scores, in two blocks: register blocks of 16 leave the allocator room where one of 32 made it spill.
+__device__ __forceinline__ void scores32(uint32_t at, uint32_t (&v)[32]) {
+  uint32_t x[16], y[16];
+  tmem_ld16(at, x);
+  tmem_ld16(at + 16, y);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    v[e] = x[e];
+    v[16 + e] = y[e];
+  }
+}
+
 // ---- the plan ---------------------------------------------------------------
 
 struct Seq {
@@ -221,6 +233,23 @@ __device__ __forceinline__ int pair_tiles(const ChunkArgs& p, const Seq& s, int 
 
 // Unit at which CTA c's range begins, before ends move.
 __device__ __forceinline__ long long cut(long long c, long long total, long long n) { return c * total / n; }
+
+// Rows of an item up to the last that is somebody's.
+__device__ __forceinline__ int rows_of(const ChunkArgs& p, const ChunkPiece& w) {
+  const int tokens = w.end - w.first + 1, TT = p.tile_tokens, GB = p.head_block;
+  return tokens > TT ? kTile + min(kTile, (tokens - TT) * GB) : min(kTile, tokens * GB);
+}
+
+// A row's stored weights stand for weight * 2^-exponent, their sum likewise (8 bits: times kSumUnit as well).
+template <bool CODED>
+__device__ __forceinline__ float log_sum(float exponent, float sum) {
+  return sum == 0.f ? -INFINITY : (exponent + log2f(sum) + (CODED ? 14.f : 0.f)) * kLn2;
+}
+template <bool CODED>
+__device__ __forceinline__ float inverse(float sum) {
+  if (!CODED) return sum == 0.f ? 0.f : 1.f / sum;
+  return sum == 0.f ? 0.f : sum > 1.f ? 1.f / sum * kSumUnit : 1.f / (sum / kSumUnit);
+}
 
 }  // namespace
 
@@ -285,16 +314,86 @@ __device__ __noinline__ void add_not_finite(const ChunkArgs& p, const ChunkPiece
   }
 }
 
+// Joins an item's parts in the slots of CTAs first, first + by, .. (at most kJoinGroup): into the result rows, or in place
+// into the first's slot. By the softmax warps. (Not inlined: its registers are not the softmax loop's.)
+template <int FMT, int D>
+__device__ __noinline__ void join(const ChunkArgs& p, ChunkCtl& c, const ChunkPiece& w, float* factors, int first, int count, int by, bool last) {
+  constexpr bool CODED = FMT != kKvBf16;
+  constexpr int SF = kSlotFloats<D>, FLAG = SF - 4, AT = 8;        // parts whose loads are in flight together
+  const int tid = threadIdx.x, rows = rows_of(p, w), tokens = w.end - w.first + 1, TT = p.tile_tokens, GB = p.head_block;
+  float* const slots = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kCounterBytes);
+  // (the item's first CTA has its part in the second of its slots)
+  auto slot_of = [&](int y) { return slots + static_cast<long long>(2 * (first + y * by) + (first + y * by == w.c0)) * SF; };
+  float e_all = -INFINITY, l_all = 0.f;
+  if (tid < rows) {
+    for (int y = 0; y < count; ++y) {
+      const float e = __ldcg(slot_of(y) + tid);
+      factors[y * 2 * kTile + tid] = e;
+      e_all = fmaxf(e_all, e);
+    }
+    const float from = e_all == -INFINITY ? 0.f : e_all;
+    for (int y = 0; y < count; ++y) l_all += __ldcg(slot_of(y) + 2 * kTile + tid) * exp2_fast(factors[y * 2 * kTile + tid] - from);
+    const float inv = last ? inverse<CODED>(l_all) : 1.f;
+    for (int y = 0; y < count; ++y) factors[y * 2 * kTile + tid] = exp2_fast(factors[y * 2 * kTile + tid] - from) * inv;
+  }
+  bool bad = false;
+  for (int y = 0; y < count; ++y) bad = bad || __float_as_int(__ldcg(slot_of(y) + FLAG)) != 0;
+  soft_sync();
+  // thread: 4 consecutive dimensions of one row at a time
+  for (int task = tid; task < rows * (D / 4); task += kSoftThreads) {
+    const int r = task / (D / 4), d = task % (D / 4) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int y0 = 0; y0 < count; y0 += AT) {
+      float4 v[AT];
+#pragma unroll
+      for (int y = 0; y < AT; ++y) {
+        v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (y0 + y < count) v[y] = __ldcg(reinterpret_cast<const float4*>(slot_of(y0 + y) + 4 * kTile + r * D + d));
+      }
+#pragma unroll
+      for (int y = 0; y < AT; ++y)
+        if (y0 + y < count) {
+          const float f = factors[(y0 + y) * 2 * kTile + r];
+          acc.x += v[y].x * f;
+          acc.y += v[y].y * f;
+          acc.z += v[y].z * f;
+          acc.w += v[y].w * f;
+        }
+    }
+    if (last) {
+      const int ri = r / kTile, rt = r % kTile / GB, rg = r % kTile - rt * GB, tok = ri * TT + rt;
+      if (rt < TT && rg < w.heads && tok < tokens && !failed(c))
+        *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(w.row0) + tok) * p.out_stride + (w.h0 + rg) * D + d) =
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    } else {
+      *reinterpret_cast<float4*>(slot_of(0) + 4 * kTile + r * D + d) = acc;
+    }
+  }
+  if (last) {
+    const int rt = tid % kTile / GB, rg = tid % kTile - rt * GB, tok = tid / kTile * TT + rt;
+    if (p.lse && tid < rows && rt < TT && rg < w.heads && tok < tokens && !failed(c))
+      p.lse[(static_cast<long long>(w.row0) + tok) * p.q_heads + w.h0 + rg] = log_sum<CODED>(e_all, l_all);
+  } else {
+    if (tid < rows) {
+      slot_of(0)[tid] = e_all;
+      slot_of(0)[2 * kTile + tid] = l_all;
+    }
+    if (tid == 0) slot_of(0)[FLAG] = __int_as_float(bad);
+  }
+  soft_sync();                       // (the factors lie where the warps stage their results)
+  if (last && bad && !failed(c)) add_not_finite<FMT, D>(p, w, tid >> 5, tid & 31);
+}
+
 template <int FMT, int D>
 __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_constant__ ChunkArgs p) {
   using Sh = ChunkShape<D>;
   using Sm = ChunkSmem<D>;
   constexpr int NP = Sh::pairs;
   constexpr bool CODED = FMT != kKvBf16;
-  extern __shared__ unsigned char chunk_smem_raw[];
-  const uint32_t raw = smem_u32(chunk_smem_raw), pad = ((raw + 1023u) & ~1023u) - raw;
-  unsigned char* const base = chunk_smem_raw + pad;
-  const uint32_t q_s = raw + pad + Sm::q, ring = raw + pad + Sm::ring;
+  extern __shared__ __align__(1024) unsigned char chunk_smem[];             // (aligned by its declaration, so that offsets are constants)
+  unsigned char* const base = chunk_smem;
+  const uint32_t q_s = smem_u32(chunk_smem) + Sm::q, ring = smem_u32(chunk_smem) + Sm::ring;
   ChunkMeta* const metas = reinterpret_cast<ChunkMeta*>(base + Sm::meta);
   float* const q_factor = reinterpret_cast<float*>(base + Sm::qf);           // [kPieces][256]
   ChunkCtl& c = *reinterpret_cast<ChunkCtl*>(base + Sm::ctl);
@@ -573,6 +672,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     }
   } else if (warp >= kLoadWarp) {
     // =========================== K and V tiles ============================
+    // Groups of 16 tokens of K, then of V, tile by tile (K0 V0 K1 V1 ..), dealt to the warps in turn: every warp has one or two of
+    // each tile.
     const int lw = warp - kLoadWarp;
     uint32_t kt = 0, gg = 0;             // key tiles and groups of the pieces before
     const float sl2 = p.scale * kLog2e;
@@ -585,64 +686,58 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       const ChunkPiece& w = c.piece[sl];
       if (!w.valid) break;
       const int32_t* const table = p.table + w.b * p.table_stride;
-      const int groups = w.n * kGroups;
+      const int groups = w.n * 2 * kGroups, ta = w.ta, kept = w.kept, skip = w.skip, end = w.end, low = w.low;
+      const long long head_off = w.kvh * p.c.head_bytes;
       bool bad = false;
       // First token of group g of the piece.
       auto token0 = [&](int g) {
-        const int t = w.ta + g / kGroups;
-        return (t < w.kept ? t : t + w.skip) * kTile + (g % kGroups) * kGroup;
+        const int t = ta + g / (2 * kGroups);
+        return (t < kept ? t : t + skip) * kTile + (g % kGroups) * kGroup;
       };
       // Page of this lane's token (lanes 16 .. 31 as lanes 0 .. 15) and its slot; -1: nobody sees it.
       auto look_up = [&](int g, int& slot) {
         const int t = token0(g) + (lane & 15);
         slot = 0;
-        if (t > w.end || (t < w.low && t >= p.sinks)) return -1;
+        if (t > end || (t < low && t >= p.sinks)) return -1;
         const int entry = p.page_shift >= 0 ? t >> p.page_shift : t / p.c.page_size;
         slot = t - entry * p.c.page_size;
         return __ldg(table + entry);
       };
+      auto stage_of = [&](int g) { return 2 * ((kt + g / (2 * kGroups)) % NP) + (g / kGroups) % 2; };
       // Of a group: some of its tokens are seen by some rows and not by others.
       auto partly = [&](int g) {
         const int t = token0(g);
-        return !(t + kGroup - 1 <= w.first && (t > w.end - p.window || t + kGroup - 1 < p.sinks));
+        return !(t + kGroup - 1 <= w.first && (t > end - p.window || t + kGroup - 1 < p.sinks));
       };
-      auto part_seen = [&](int t) { return !(t <= w.first && (t > w.end - p.window || t < p.sinks)); };
+      auto part_seen = [&](int t) { return !(t <= w.first && (t > end - p.window || t < p.sinks)); };
       const int g0 = static_cast<int>((lw + kLoaders - gg % kLoaders) % kLoaders);   // this warp's first group
-      // The stages and the masks of group g's tile are free; false: it has to be waited for.
+      // Group g's stage (K: and the masks of its tile) is free; false: it has to be waited for.
       auto ready = [&](int g, bool block) {
-        const uint32_t k = kt + g / kGroups, ks = 2 * (k % NP);
-        bool ok = true;
-        if (k >= NP) {
-          const uint32_t ph = ((k / NP) - 1) & 1;
-          if (block) {
-            wait(c, c.empty[ks], ph);
-            wait(c, c.empty[ks + 1], ph);
-          } else {
-            ok = passed(c.empty[ks], ph) && passed(c.empty[ks + 1], ph);
-          }
+        const uint32_t k = kt + g / (2 * kGroups);
+        unsigned long long& stage = c.empty[stage_of(g)];
+        unsigned long long& meta = c.meta_empty[k % kMeta];
+        const uint32_t ph = ((k / NP) - 1) & 1, mph = ((k / kMeta) - 1) & 1;
+        const bool has = k >= NP, keys = k >= kMeta && (g / kGroups) % 2 == 0;
+        if (block) {
+          if (has) wait(c, stage, ph);
+          if (keys) wait(c, meta, mph);
+          return true;
         }
-        if (k >= kMeta) {
-          const uint32_t ph = ((k / kMeta) - 1) & 1;
-          if (block) wait(c, c.meta_empty[k % kMeta], ph);
-          else ok = ok && passed(c.meta_empty[k % kMeta], ph);
-        }
-        return __all_sync(0xffffffffu, ok);
+        return static_cast<bool>(__all_sync(0xffffffffu, (!has || passed(stage, ph)) && (!keys || passed(meta, mph))));
       };
       auto arrive = [&](int g) {
-        const uint32_t k = kt + g / kGroups, ks = 2 * (k % NP);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&c.meta_full[k % kMeta]));
-          mbar_arrive(smem_u32(&c.full[ks]));
-          mbar_arrive(smem_u32(&c.full[ks + 1]));
+          if ((g / kGroups) % 2 == 0) mbar_arrive(smem_u32(&c.meta_full[(kt + g / (2 * kGroups)) % kMeta]));
+          mbar_arrive(smem_u32(&c.full[stage_of(g)]));
         }
       };
       if constexpr (!CODED) {
         int next = g0;                   // the oldest group that has not been handed over
         auto hand_over = [&]() {         // its copies have landed
-          if (partly(next)) {
-            const uint32_t k = kt + next / kGroups, at = ring + (2 * (k % NP) + 1) * Sh::tile_bytes;
+          if ((next / kGroups) % 2 && partly(next)) {
+            const uint32_t at = ring + stage_of(next) * Sh::tile_bytes;
             const int t0 = token0(next), r0 = (next % kGroups) * kGroup;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
@@ -662,7 +757,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         int slot = 0, page = g0 < groups ? look_up(g0, slot) : -1;
         for (int g = g0; g < groups; g += kLoaders) {
           const bool there = page >= 0 && page < p.c.num_pages;
-          const long long off = there ? page * p.c.page_bytes + w.kvh * p.c.head_bytes + slot * p.c.token_bytes : -1;
+          const long long off = there ? page * p.c.page_bytes + head_off + slot * p.c.token_bytes : -1;
           const uint32_t live = __ballot_sync(0xffffffffu, there) & 0xffffu;
           if (g + kLoaders < groups) page = look_up(g + kLoaders, slot);     // (while this group is on its way)
           if (!ready(g, false)) {        // (what is in flight may be what it waits for)
@@ -671,17 +766,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             ready(g, true);
             if (__any_sync(0xffffffffu, failed(c))) break;
           }
-          const uint32_t k = kt + g / kGroups, at = ring + 2 * (k % NP) * Sh::tile_bytes;
+          const bool keys = (g / kGroups) % 2 == 0;
+          const unsigned char* const from = keys ? p.c.k : p.c.v;
+          const uint32_t at = ring + stage_of(g) * Sh::tile_bytes;
           const int r0 = (g % kGroups) * kGroup;
-          if (lane == 0) metas[k % kMeta].live[g % kGroups] = static_cast<uint16_t>(live);
+          if (keys && lane == 0) metas[(kt + g / (2 * kGroups)) % kMeta].live[g % kGroups] = static_cast<uint16_t>(live);
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
             const int t = i * TPI + sub_t;
             const long long o = __shfl_sync(0xffffffffu, off, t);
-            const uint32_t to = at + Sh::at(r0 + t, ch);
-            const long long from = (o < 0 ? 0 : o) + ch * 16;
-            copy16(to, p.c.k + from, o >= 0);
-            copy16(to + Sh::tile_bytes, p.c.v + from, o >= 0);
+            copy16(at + Sh::at(r0 + t, ch), from + (o < 0 ? 0 : o) + ch * 16, o >= 0);
           }
           cp_async_commit();
           if (next + kLag * kLoaders <= g) {
@@ -692,28 +786,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         copies_left<0>();
         while (next < groups && !__any_sync(0xffffffffu, failed(c))) hand_over();
       } else {
-        // K of the next group is loaded while V of this one is converted: half of a group at least is always in flight.
-        uint4 kx[NI], vx[NI];
-        long long off = -1;
+        // A group's codes are loaded while the one before it is converted, its pages looked up one ahead of that.
+        uint4 cur[NI], ahead[NI];
+        float ks = 0.f, vs = 0.f;        // scales of the group loaded last (K groups: of both; V groups: V's)
         bool there = false;
-        float ks = 0.f, vs = 0.f;
         int slot = 0, page = g0 < groups ? look_up(g0, slot) : -1;
-        auto locate = [&]() {            // of the group whose page was looked up; its scales
+        auto fetch = [&](int g) {        // the group whose page was looked up
           there = page >= 0 && page < p.c.num_pages;
-          off = there ? page * p.c.page_bytes + w.kvh * p.c.head_bytes + slot * p.c.token_bytes : -1;
+          const long long off = there ? page * p.c.page_bytes + head_off + slot * p.c.token_bytes : -1;
+          const bool keys = (g / kGroups) % 2 == 0;
           ks = vs = 0.f;
           if (there) {
             const long long si = scale_index(p.c, page, w.kvh, slot);
-            ks = __ldg(p.c.ks + si);
+            if (keys) ks = __ldg(p.c.ks + si);
             vs = __ldg(p.c.vs + si);
           }
-        };
-        auto fetch = [&](const unsigned char* from, uint4 (&to)[NI]) {
+          const unsigned char* const from = keys ? p.c.k : p.c.v;
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
             const long long o = __shfl_sync(0xffffffffu, off, i * TPI + sub_t);
-            to[i] = make_uint4(0, 0, 0, 0);
-            if (o >= 0) to[i] = __ldg(reinterpret_cast<const uint4*>(from + o + ch * 16));
+            ahead[i] = make_uint4(0, 0, 0, 0);
+            if (o >= 0) ahead[i] = __ldg(reinterpret_cast<const uint4*>(from + o + ch * 16));
           }
         };
         // 16 codes -> two chunks of f16 (lanes of the upper half of a row store them in the other order: no bank twice).
@@ -729,45 +822,40 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           sts128(at + Sh::at(r, 2 * ch + swap), first);
           sts128(at + Sh::at(r, 2 * ch + !swap), second);
         };
-        if (g0 < groups) {
-          locate();
-          fetch(p.c.k, kx);
-        }
+        if (g0 < groups) fetch(g0);
         for (int g = g0; g < groups; g += kLoaders) {
-          fetch(p.c.v, vx);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) cur[i] = ahead[i];
           const float k_scale = ks, v_scale = vs;
-          const bool was_there = there;
-          if (g + kLoaders < groups) page = look_up(g + kLoaders, slot);
+          const uint32_t live = __ballot_sync(0xffffffffu, there) & 0xffffu, odd = __ballot_sync(0xffffffffu, there && v_scale <= 0.f);
+          if (g + kLoaders < groups) {
+            page = look_up(g + kLoaders, slot);
+            fetch(g + kLoaders);
+          }
           ready(g, true);
           if (__any_sync(0xffffffffu, failed(c))) break;
-          const uint32_t k = kt + g / kGroups, at = ring + 2 * (k % NP) * Sh::tile_bytes;
-          const int r0 = (g % kGroups) * kGroup, t0 = token0(g);
+          const bool keys = (g / kGroups) % 2 == 0;
+          const uint32_t at = ring + stage_of(g) * Sh::tile_bytes;
+          const int r0 = (g % kGroups) * kGroup;
+          if (keys) {
+            // Masks and scales. A scale of 0 stands for codes whose weight only counts in the sum: 2^-64 there, with V's codes
+            // zero; a negative one changes the codes' signs. (Below 2^-110, under what lora_kv_write stores: 2^-110.)
+            ChunkMeta& m = metas[(kt + g / (2 * kGroups)) % kMeta];
+            if (lane == 0) m.live[g % kGroups] = static_cast<uint16_t>(live);
+            if (lane < kGroup) {
+              const float mag = v_scale == 0.f ? 5.421010862427522e-20f : fmaxf(fabsf(v_scale), 7.703719777548943e-34f);
+              const float s = v_scale != v_scale ? v_scale : mag;       // (fmaxf drops NaN)
+              m.a[r0 + lane] = k_scale * sl2;
+              m.b[r0 + lane] = log2f(s);
+              m.iv[r0 + lane] = v_scale != v_scale ? 0.f : kSumUnit / s;   // (times the weight 0 of a row that does not see it: 0)
+            }
+          } else if (odd || (FMT == kKvE4m3 && partly(g))) {
+            const bool look = FMT == kKvE4m3 && partly(g);
+            const int t0 = token0(g);
 #pragma unroll
-          for (int i = 0; i < NI; ++i) put(at, r0 + i * TPI + sub_t, kx[i]);
-          if (g + kLoaders < groups) {
-            locate();
-            fetch(p.c.k, kx);
-          }
-          // Masks and scales. A scale of 0 stands for codes whose weight only counts in the sum: 2^-64 there, with the codes
-          // zero; a negative one changes the codes' signs. (Below 2^-110, under what lora_kv_write stores: 2^-110.)
-          ChunkMeta& m = metas[k % kMeta];
-          const uint32_t live = __ballot_sync(0xffffffffu, was_there) & 0xffffu;
-          if (lane == 0) m.live[g % kGroups] = static_cast<uint16_t>(live);
-          if (lane < kGroup) {
-            const float mag = v_scale == 0.f ? 5.421010862427522e-20f : fmaxf(fabsf(v_scale), 7.703719777548943e-34f);
-            const float s = v_scale != v_scale ? v_scale : mag;       // (fmaxf drops NaN)
-            m.a[r0 + lane] = k_scale * sl2;
-            m.b[r0 + lane] = log2f(s);
-            m.iv[r0 + lane] = v_scale != v_scale ? 0.f : kSumUnit / s;   // (times the weight 0 of a row that does not see it: 0)
-          }
-          const uint32_t odd = __ballot_sync(0xffffffffu, was_there && v_scale <= 0.f);
-          const bool look = FMT == kKvE4m3 && partly(g);
-#pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            const int t = i * TPI + sub_t;
-            uint4 v = vx[i];
-            if (odd || look) {
-              uint32_t x4[4] = {v.x, v.y, v.z, v.w};
+            for (int i = 0; i < NI; ++i) {
+              const int t = i * TPI + sub_t;
+              uint32_t x4[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
               const float sc = __shfl_sync(0xffffffffu, v_scale, t);
               const bool part = look && part_seen(t0 + t);
 #pragma unroll
@@ -783,11 +871,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                   else x4[j] = __vneg4(x4[j]);
                 }
               }
-              v = make_uint4(x4[0], x4[1], x4[2], x4[3]);
+              cur[i] = make_uint4(x4[0], x4[1], x4[2], x4[3]);
             }
-            put(at + Sh::tile_bytes, r0 + t, v);
+            if (__any_sync(0xffffffffu, bad) && lane == 0) *reinterpret_cast<volatile int*>(&c.bad[sl]) = 1;
           }
-          if (__any_sync(0xffffffffu, bad) && lane == 0) *reinterpret_cast<volatile int*>(&c.bad[sl]) = 1;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) put(at, r0 + i * TPI + sub_t, cur[i]);
           arrive(g);
         }
       }
@@ -918,7 +1007,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const uint32_t col_o = lane_base + Sh::col_o + i * D;
     const float sl2 = p.scale * kLog2e, grow = CODED ? kGrow : kGrow / sl2;
     const int t_in = row / GB, g = row - t_in * GB;
-    const uint32_t stage = raw + pad + Sm::stage + warp * kStageBytes;
+    const uint32_t stage = smem_u32(chunk_smem) + Sm::stage + warp * kStageBytes;
     bool dead = false;
     uint32_t t = 0, kt = 0;              // key tiles of this row tile so far; of the pieces before
     for (int it = 0;; ++it) {
@@ -942,18 +1031,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         dead |= wait(c, c.s_full[i][t & 1], (t >> 1) & 1);
         __syncwarp();
         tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(col_s + q * 32, s[q]);
-        tmem_ld_wait();
-        if constexpr (CODED) {             // y = score * K's scale + log2 of V's
-          if (j == 0) {
-            qf = q_factor[sl * 2 * kTile + i * kTile + row];
-            plain_q = __all_sync(0xffffffffu, qf == 1.f);
-          }
-          const uint64_t qf2 = pair(qf, qf);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
+        if (CODED && j == 0) {
+          qf = q_factor[sl * 2 * kTile + i * kTile + row];
+          plain_q = __all_sync(0xffffffffu, qf == 1.f);
+        }
+        // What the row sees of the tile.
+        const int tile = w.ta + j, t0 = (tile < w.kept ? tile : tile + w.skip) * kTile;
+        const uint4 there = *reinterpret_cast<const uint4*>(m.live);
+        const int hi = pos - t0, lo = hi - min(p.window - 1, max(pos, 0)), sk = p.sinks - t0;    // sees x <= hi with x >= lo or x < sk
+        const bool whole = hi >= kTile - 1 && (lo <= 0 || sk >= kTile) && (there.x & there.y & there.z & there.w) == 0xffffffffu;
+        const bool cuts = __any_sync(0xffffffffu, live && !whole);
+        // A quarter of the scores at a time, the next one on its way from tensor memory: as they are (8 bits: y), what is not
+        // seen at -infinity.
+        uint32_t sa[32], sb[32];
+        auto shape = [&](auto which, uint32_t (&s)[32]) {
+          constexpr int q = decltype(which)::value;
+          if constexpr (CODED) {           // y = score * K's scale + log2 of V's
+            const uint64_t qf2 = pair(qf, qf);
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               const float4 a = *reinterpret_cast<const float4*>(m.a + q * 32 + e), b = *reinterpret_cast<const float4*>(m.b + q * 32 + e);
@@ -962,39 +1056,49 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                 a01 = mul2(a01, qf2);
                 a23 = mul2(a23, qf2);
               }
-              const float2 y0 = unpair(fma2(pair(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), a01, pair(b.x, b.y)));
-              const float2 y1 = unpair(fma2(pair(__uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3])), a23, pair(b.z, b.w)));
-              s[q][e] = __float_as_uint(y0.x);
-              s[q][e + 1] = __float_as_uint(y0.y);
-              s[q][e + 2] = __float_as_uint(y1.x);
-              s[q][e + 3] = __float_as_uint(y1.y);
+              const float2 y0 = unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), a01, pair(b.x, b.y)));
+              const float2 y1 = unpair(fma2(pair(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), a23, pair(b.z, b.w)));
+              s[e] = __float_as_uint(y0.x);
+              s[e + 1] = __float_as_uint(y0.y);
+              s[e + 2] = __float_as_uint(y1.x);
+              s[e + 3] = __float_as_uint(y1.y);
             }
-        }
-        // What the row sees of the tile.
-        const int tile = w.ta + j, t0 = (tile < w.kept ? tile : tile + w.skip) * kTile;
-        const uint4 there = *reinterpret_cast<const uint4*>(m.live);
-        const int hi = pos - t0, lo = hi - min(p.window - 1, max(pos, 0)), sk = p.sinks - t0;    // sees x <= hi with x >= lo or x < sk
-        const bool whole = hi >= kTile - 1 && (lo <= 0 || sk >= kTile) && (there.x & there.y & there.z & there.w) == 0xffffffffu;
-        if (__any_sync(0xffffffffu, live && !whole)) {
-          const uint32_t there4[4] = {there.x, there.y, there.z, there.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          }
+          if (cuts) {
             auto below = [&](int x) { return x <= q * 32 ? 0u : x >= q * 32 + 32 ? 0xffffffffu : (1u << (x - q * 32)) - 1; };   // bits under x
-            const uint32_t see = there4[q] & (hi >= kTile - 1 ? 0xffffffffu : below(hi + 1)) & (~below(lo) | below(sk));
+            const uint32_t see = (q == 0 ? there.x : q == 1 ? there.y : q == 2 ? there.z : there.w) & below(min(hi, kTile) + 1) & (~below(lo) | below(sk));
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!((see >> e) & 1)) s[q][e] = 0xff800000u;
+              if (!((see >> e) & 1)) s[e] = 0xff800000u;
           }
-        }
-        float mx[4];
+        };
+        auto most = [&](const uint32_t (&s)[32], float top) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          mx[q] = __uint_as_float(s[q][0]);
-#pragma unroll
-          for (int e = 1; e < 31; e += 2) mx[q] = max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
-          mx[q] = fmaxf(mx[q], __uint_as_float(s[q][31]));
-        }
-        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          for (int e = 0; e < 32; e += 4)
+            top = max3(top, max3(__uint_as_float(s[e]), __uint_as_float(s[e + 1]), __uint_as_float(s[e + 2])), __uint_as_float(s[e + 3]));
+          return top;
+        };
+        constexpr std::integral_constant<int, 0> q0{};
+        constexpr std::integral_constant<int, 1> q1{};
+        constexpr std::integral_constant<int, 2> q2{};
+        constexpr std::integral_constant<int, 3> q3{};
+        // The maximum over all four (the first two stay), then their weights.
+        scores32(col_s + 96, sa);
+        tmem_ld_wait();
+        scores32(col_s + 64, sb);
+        shape(q3, sa);
+        float top = most(sa, -INFINITY);
+        tmem_ld_wait();
+        scores32(col_s + 32, sa);
+        shape(q2, sb);
+        top = most(sb, top);
+        tmem_ld_wait();
+        scores32(col_s, sb);
+        shape(q1, sa);
+        top = most(sa, top);
+        tmem_ld_wait();
+        shape(q0, sb);
+        top = most(sb, top);
         if (j == 0) {
           ref = top;
         } else if (__any_sync(0xffffffffu, live && top > ref + grow)) {   // (rows of nobody hold anything: no say)
@@ -1006,31 +1110,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           dead |= wait(c, c.o_done[i][(t - 1) & 1], ((t - 1) >> 1) & 1);
           __syncwarp();
           tc_fence_after();
-#pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            tmem_ld32(col_o + q * 32, o);
+#pragma unroll 1
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t o[16];
+            tmem_ld16(col_o + q * 16, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(col_o + q * 32, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(col_o + q * 16, o);
           }
         }
         // (nothing seen: every weight is 0)
         const float off = ref == -INFINITY ? 0.f : CODED ? kTop - ref : __fmaf_rn(-ref, sl2, -kGrow);
         const uint64_t sl2p = pair(sl2, sl2), offp = pair(off, off);
         uint64_t sum[4] = {0, 0, 0, 0};
+        auto weights = [&](auto which, const uint32_t (&s)[32]) {
+          constexpr int q = decltype(which)::value;
+          uint32_t pk[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int q = 2 * h + (e >> 4), f = (e & 15) * 2;
-            const uint64_t z = pair(__uint_as_float(s[q][f]), __uint_as_float(s[q][f + 1]));
+          for (int e = 0; e < 16; ++e) {
+            const uint64_t z = pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
             const float2 x = unpair(CODED ? add2(z, offp) : fma2(z, sl2p, offp));
             const float w0 = exp2_fast(x.x), w1 = exp2_fast(x.y);
             if constexpr (CODED) {
-              const float2 iv = *reinterpret_cast<const float2*>(m.iv + q * 32 + f);
+              const float2 iv = *reinterpret_cast<const float2*>(m.iv + q * 32 + 2 * e);
               sum[e & 3] = fma2(pair(w0, w1), pair(iv.x, iv.y), sum[e & 3]);
               pk[e] = pack_f16x2(w0, w1);
             } else {
@@ -1038,14 +1141,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
               pk[e] = pack_bf16x2(w0, w1);
             }
           }
-          tmem_st32(col_s + h * 32, pk);
-          if (Sh::bufs == 2 || h == 1) {   // (with three score buffers nothing of this warpgroup waits for P V: one hand-over)
+          tmem_st16(col_s + q * 16, pk);   // (over scores that are in registers or done with)
+          if (Sh::bufs == 2 ? q & 1 : q == 3) {   // (with three score buffers nothing of this warpgroup waits for P V: one hand-over)
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&c.p_ready[i][t & 1][h]));
+            if (lane == 0) mbar_arrive(smem_u32(&c.p_ready[i][t & 1][q >> 1]));
           }
-        }
+        };
+        weights(q0, sb);
+        scores32(col_s + 64, sb);
+        weights(q1, sa);
+        tmem_ld_wait();
+        scores32(col_s + 96, sa);
+        shape(q2, sb);
+        weights(q2, sb);
+        tmem_ld_wait();
+        shape(q3, sa);
+        weights(q3, sa);
         const float2 all = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
         l += all.x + all.y;
         __syncwarp();
@@ -1063,19 +1176,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       __syncwarp();
       tc_fence_after();
 
-      // Stored weights stand for weight * 2^-exponent, their sum l likewise (8 bits: times kSumUnit).
       const float exponent = ref == -INFINITY ? -INFINITY : CODED ? ref - kTop : __fmaf_rn(ref, sl2, kGrow);
       const long long out_row = static_cast<long long>(w.row0) + i * TT + t_in;
-      auto log_sum = [&](float e, float sum) { return sum == 0.f ? -INFINITY : (e + log2f(sum) + (CODED ? 14.f : 0.f)) * kLn2; };
-      auto inverse = [&](float sum) {      // of the sum without kSumUnit
-        if (!CODED) return sum == 0.f ? 0.f : 1.f / sum;
-        return sum == 0.f ? 0.f : sum > 1.f ? 1.f / sum * kSumUnit : 1.f / (sum / kSumUnit);
-      };
       if (w.ta == 0 && w.n == w.tiles) {
         // The whole item: its rows, through shared memory so that a store instruction writes whole 64-byte pieces.
         uint16_t* const to = p.out + out_row * p.out_stride + (w.h0 + g) * D;
         const uint32_t lives = __ballot_sync(0xffffffffu, live);
-        const float inv = n > 0 ? inverse(l) : 0.f;
+        const float inv = n > 0 ? inverse<CODED>(l) : 0.f;
         const uint64_t invp = pair(inv, inv);
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
@@ -1105,7 +1212,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           __syncwarp();
         }
         tc_fence_before();
-        if (p.lse && live && !failed(c)) p.lse[out_row * p.q_heads + w.h0 + g] = n > 0 ? log_sum(exponent, l) : -INFINITY;
+        if (p.lse && live && !failed(c)) p.lse[out_row * p.q_heads + w.h0 + g] = n > 0 ? log_sum<CODED>(exponent, l) : -INFINITY;
         if (*reinterpret_cast<volatile int*>(&c.bad[sl]) && !failed(c)) {
           __syncwarp();
           add_not_finite<FMT, D>(p, w, warp, lane);
@@ -1115,8 +1222,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         int* const counters = static_cast<int*>(p.workspace);
         float* const slots = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kCounterBytes);
         constexpr int SF = kSlotFloats<D>, FLAG = SF - 4;
-        const int me = blockIdx.x, tokens = w.end - w.first + 1;
-        const int rows = tokens > TT ? kTile + min(kTile, (tokens - TT) * GB) : min(kTile, tokens * GB);   // rows up to the last live one
+        const int me = blockIdx.x, rows = rows_of(p, w);
         float* const mine = slots + static_cast<long long>(2 * me + (w.ta == 0)) * SF;
         const int rr = i * kTile + row;
         if (rr < rows) {
@@ -1150,76 +1256,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         tc_fence_before();
         if (tid == 0) mine[FLAG] = __int_as_float(*reinterpret_cast<volatile int*>(&c.bad[sl]));
 
-        float* const factors = reinterpret_cast<float*>(base + Sm::stage);    // [kJoinGroup][256] over all warps' staging
-        static_assert(kJoinGroup * 2 * kTile * 4 <= kSoftWarps * kStageBytes, "factors of a join");
-        // Joins slots of CTAs first, first + by, .. (at most kJoinGroup): into the rows, or in place into the first's.
-        auto join = [&](int first_cta, int count, int by, bool last) {
-          auto slot_of = [&](int y) { return slots + static_cast<long long>(2 * (first_cta + y * by) + (first_cta + y * by == w.c0)) * SF; };
-          float e_all = -INFINITY, l_all = 0.f;
-          if (tid < rows) {
-            float es[kJoinGroup], ls[kJoinGroup];
-#pragma unroll
-            for (int y = 0; y < kJoinGroup; ++y) {
-              es[y] = y < count ? __ldcg(slot_of(y) + tid) : -INFINITY;
-              ls[y] = y < count ? __ldcg(slot_of(y) + 2 * kTile + tid) : 0.f;
-            }
-#pragma unroll
-            for (int y = 0; y < kJoinGroup; ++y) e_all = fmaxf(e_all, es[y]);
-            const float from = e_all == -INFINITY ? 0.f : e_all;
-#pragma unroll
-            for (int y = 0; y < kJoinGroup; ++y) {
-              es[y] = exp2_fast(es[y] - from);
-              l_all += ls[y] * es[y];
-            }
-            const float inv = last ? inverse(l_all) : 1.f;
-#pragma unroll
-            for (int y = 0; y < kJoinGroup; ++y) factors[y * 2 * kTile + tid] = es[y] * inv;
-          }
-          bool bad = false;
-          for (int y = 0; y < count; ++y) bad = bad || __float_as_int(__ldcg(slot_of(y) + FLAG)) != 0;
-          soft_sync();
-          // thread: 4 consecutive dimensions of one row at a time, all parts' loads in flight
-          for (int task = tid; task < rows * (D / 4); task += kSoftThreads) {
-            const int r = task / (D / 4), d = task % (D / 4) * 4;
-            float4 v[kJoinGroup];
-#pragma unroll
-            for (int y = 0; y < kJoinGroup; ++y) {
-              v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (y < count) v[y] = __ldcg(reinterpret_cast<const float4*>(slot_of(y) + 4 * kTile + r * D + d));
-            }
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int y = 0; y < kJoinGroup; ++y)
-              if (y < count) {
-                const float f = factors[y * 2 * kTile + r];
-                acc.x += v[y].x * f;
-                acc.y += v[y].y * f;
-                acc.z += v[y].z * f;
-                acc.w += v[y].w * f;
-              }
-            if (last) {
-              const int ri = r / kTile, rt = r % kTile / GB, rg = r % kTile - rt * GB, tok = ri * TT + rt;
-              if (rt < TT && rg < w.heads && tok < tokens && !failed(c))
-                *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(w.row0) + tok) * p.out_stride + (w.h0 + rg) * D + d) =
-                    make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-            } else {
-              *reinterpret_cast<float4*>(slot_of(0) + 4 * kTile + r * D + d) = acc;
-            }
-          }
-          if (last) {
-            const int rt = tid % kTile / GB, rg = tid % kTile - rt * GB, tok = tid / kTile * TT + rt;
-            if (p.lse && tid < rows && rt < TT && rg < w.heads && tok < tokens && !failed(c))
-              p.lse[(static_cast<long long>(w.row0) + tok) * p.q_heads + w.h0 + rg] = log_sum(e_all, l_all);
-          } else {
-            if (tid < rows) {
-              slot_of(0)[tid] = e_all;
-              slot_of(0)[2 * kTile + tid] = l_all;
-            }
-            if (tid == 0) slot_of(0)[FLAG] = __int_as_float(bad);
-          }
-          soft_sync();                     // (the factors lie where the warps stage their results)
-          if (last && bad && !failed(c)) add_not_finite<FMT, D>(p, w, warp, lane);
-        };
         // Arrive at a counter; true in the CTA that is the last of `count`, which sets it back to 0.
         auto last_of = [&](int* counter, int count) {
           soft_sync();
@@ -1232,11 +1268,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           soft_sync();
           return *const_cast<const volatile int*>(&c.last) != 0;
         };
+        float* const factors = reinterpret_cast<float*>(base + Sm::stage);    // over all warps' staging
+        static_assert(kJoinGroup * 2 * kTile * 4 <= kSoftWarps * kStageBytes, "factors of a join");
         const int groups = (w.c1 - w.c0) / kJoinGroup + 1, gi = (me - w.c0) / kJoinGroup;
         const int head = w.c0 + gi * kJoinGroup, count = min(kJoinGroup, w.c1 - head + 1);
         if (last_of(counters + (gi ? kMostCtas : 0) + head, count)) {
-          join(head, count, 1, groups == 1);
-          if (groups > 1 && last_of(counters + 2 * kMostCtas + w.c0, groups)) join(w.c0, groups, kJoinGroup, true);
+          join<FMT, D>(p, c, w, factors, head, count, 1, groups == 1);
+          if (groups > 1 && last_of(counters + 2 * kMostCtas + w.c0, groups)) join<FMT, D>(p, c, w, factors, w.c0, groups, kJoinGroup, true);
         }
       }
       __syncwarp();
