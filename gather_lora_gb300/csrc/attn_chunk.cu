@@ -61,6 +61,7 @@ constexpr int kJoinGroup = 16;                  // parts of a join
 constexpr int kSnap = 2;
 constexpr int kMostSeqs = 8192;                 // LORA_MAX_SEQS
 constexpr int kFewPairs = 8;                    // sequences of more row-tile pairs are summed by a warp
+static_assert(kWaitLimitCycles < (1LL << 32), "waits are limited by a 32-bit clock");
 static_assert(kMostCtas <= kJoinGroup * kJoinGroup, "two levels of joins");
 
 // Workspace: counters [3][kMostCtas] (an item's first join group, by its first CTA; its other groups, by theirs; its
@@ -131,17 +132,15 @@ __device__ __forceinline__ bool failed(const ChunkCtl& c) { return *reinterpret_
 
 // Bounded wait; true if it ran out. Once one has, all others of the CTA end at once, the roles leave their loops and nothing
 // more is stored (what runs on until then stays in bounds).
+// (Small, as it is inlined at every wait: the roles' loops share the instruction caches. The status word is set at the end.)
 __device__ __forceinline__ bool wait(ChunkCtl& c, unsigned long long& bar, uint32_t parity) {
   const uint32_t b = smem_u32(&bar);
   if (mbar_try_wait(b, parity, 100000)) return false;
-  const long long t0 = clock64();
+  const uint32_t t0 = static_cast<uint32_t>(clock());
+#pragma unroll 1
   while (!mbar_try_wait(b, parity, 100000)) {
+    if (static_cast<uint32_t>(clock()) - t0 > static_cast<uint32_t>(kWaitLimitCycles)) *reinterpret_cast<volatile int*>(&c.failed) = 1;
     if (failed(c)) return true;
-    if (clock64() - t0 > kWaitLimitCycles) {
-      *reinterpret_cast<volatile int*>(&c.failed) = 1;
-      atomicOr(&g_chunk_status, kChunkTimeoutBit);
-      return true;
-    }
   }
   return false;
 }
@@ -183,16 +182,21 @@ __device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t&
   }
 }
 
-// 32 columns of scores, in two blocks: register blocks of 16 leave the allocator room where one of 32 made it spill.
+// 32 columns of scores (valid after tmem_ld_wait), in two blocks: register blocks of 16 leave the allocator room where one of 32
+// made it spill.
 __device__ __forceinline__ void scores32(uint32_t at, uint32_t (&v)[32]) {
-  uint32_t x[16], y[16];
-  tmem_ld16(at, x);
-  tmem_ld16(at + 16, y);
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    v[e] = x[e];
-    v[16 + e] = y[e];
-  }
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(at)
+      : "memory");
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(at + 16)
+      : "memory");
 }
 
 // ---- the plan ---------------------------------------------------------------
@@ -1042,10 +1046,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         const bool whole = hi >= kTile - 1 && (lo <= 0 || sk >= kTile) && (there.x & there.y & there.z & there.w) == 0xffffffffu;
         const bool cuts = __any_sync(0xffffffffu, live && !whole);
         // A quarter of the scores at a time, the next one on its way from tensor memory: as they are (8 bits: y), what is not
-        // seen at -infinity.
+        // seen at -infinity. (Loops over the halves, not unrolled: see wait() on code size.)
         uint32_t sa[32], sb[32];
-        auto shape = [&](auto which, uint32_t (&s)[32]) {
-          constexpr int q = decltype(which)::value;
+        auto shape = [&](int q, uint32_t (&s)[32]) {
           if constexpr (CODED) {           // y = score * K's scale + log2 of V's
             const uint64_t qf2 = pair(qf, qf);
 #pragma unroll
@@ -1065,8 +1068,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             }
           }
           if (cuts) {
-            auto below = [&](int x) { return x <= q * 32 ? 0u : x >= q * 32 + 32 ? 0xffffffffu : (1u << (x - q * 32)) - 1; };   // bits under x
-            const uint32_t see = (q == 0 ? there.x : q == 1 ? there.y : q == 2 ? there.z : there.w) & below(min(hi, kTile) + 1) & (~below(lo) | below(sk));
+            auto below = [&](int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1; };   // bits under x
+            const uint32_t see = reinterpret_cast<const uint32_t*>(m.live)[q] & below(min(hi, kTile) + 1 - q * 32) & (~below(lo - q * 32) | below(sk - q * 32));
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!((see >> e) & 1)) s[e] = 0xff800000u;
@@ -1078,27 +1081,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             top = max3(top, max3(__uint_as_float(s[e]), __uint_as_float(s[e + 1]), __uint_as_float(s[e + 2])), __uint_as_float(s[e + 3]));
           return top;
         };
-        constexpr std::integral_constant<int, 0> q0{};
-        constexpr std::integral_constant<int, 1> q1{};
-        constexpr std::integral_constant<int, 2> q2{};
-        constexpr std::integral_constant<int, 3> q3{};
         // The maximum over all four (the first two stay), then their weights.
-        scores32(col_s + 96, sa);
-        tmem_ld_wait();
-        scores32(col_s + 64, sb);
-        shape(q3, sa);
-        float top = most(sa, -INFINITY);
-        tmem_ld_wait();
-        scores32(col_s + 32, sa);
-        shape(q2, sb);
-        top = most(sb, top);
-        tmem_ld_wait();
-        scores32(col_s, sb);
-        shape(q1, sa);
-        top = most(sa, top);
-        tmem_ld_wait();
-        shape(q0, sb);
-        top = most(sb, top);
+        float top = -INFINITY;
+        scores32(col_s + 96, sb);
+#pragma unroll 1
+        for (int h = 1; h >= 0; --h) {
+          tmem_ld_wait();
+          scores32(col_s + h * 64, sa);
+          shape(2 * h + 1, sb);
+          top = most(sb, top);
+          tmem_ld_wait();
+          if (h) scores32(col_s + 32, sb);
+          shape(2 * h, sa);
+          top = most(sa, top);
+        }
         if (j == 0) {
           ref = top;
         } else if (__any_sync(0xffffffffu, live && top > ref + grow)) {   // (rows of nobody hold anything: no say)
@@ -1124,8 +1120,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         const float off = ref == -INFINITY ? 0.f : CODED ? kTop - ref : __fmaf_rn(-ref, sl2, -kGrow);
         const uint64_t sl2p = pair(sl2, sl2), offp = pair(off, off);
         uint64_t sum[4] = {0, 0, 0, 0};
-        auto weights = [&](auto which, const uint32_t (&s)[32]) {
-          constexpr int q = decltype(which)::value;
+        auto weights = [&](int q, const uint32_t (&s)[32]) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -1142,23 +1137,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             }
           }
           tmem_st16(col_s + q * 16, pk);   // (over scores that are in registers or done with)
-          if (Sh::bufs == 2 ? q & 1 : q == 3) {   // (with three score buffers nothing of this warpgroup waits for P V: one hand-over)
+        };
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          weights(2 * h, sa);
+          if (h == 0) scores32(col_s + 64, sa);
+          weights(2 * h + 1, sb);
+          if (Sh::bufs == 2 || h == 1) {   // (with three score buffers nothing of this warpgroup waits for P V: one hand-over)
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&c.p_ready[i][t & 1][q >> 1]));
+            if (lane == 0) mbar_arrive(smem_u32(&c.p_ready[i][t & 1][h]));
           }
-        };
-        weights(q0, sb);
-        scores32(col_s + 64, sb);
-        weights(q1, sa);
-        tmem_ld_wait();
-        scores32(col_s + 96, sa);
-        shape(q2, sb);
-        weights(q2, sb);
-        tmem_ld_wait();
-        shape(q3, sa);
-        weights(q3, sa);
+          if (h == 0) {
+            tmem_ld_wait();
+            scores32(col_s + 96, sb);
+            shape(2, sa);
+            tmem_ld_wait();
+            shape(3, sb);
+          }
+        }
         const float2 all = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
         l += all.x + all.y;
         __syncwarp();
@@ -1295,6 +1293,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && failed(c)) atomicOr(&g_chunk_status, kChunkTimeoutBit);
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
