@@ -81,6 +81,18 @@ int encode_bf16_map(TensorMapBytes* out, const void* ptr, int rank, const uint64
   return r == CUDA_SUCCESS ? LORA_OK : fail(LORA_ERR_CUDA, "cuTensorMapEncodeTiled failed for %s (%d)", what, static_cast<int>(r));
 }
 
+int encode_page_map(TensorMapBytes* out, const void* ptr, bool bf16, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box, const char* what) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_tiled();
+  if (!enc) return fail(LORA_ERR_CUDA, "cuTensorMapEncodeTiled is not available (no CUDA driver)");
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(reinterpret_cast<CUtensorMap*>(out), bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+                         const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? LORA_OK : fail(LORA_ERR_CUDA, "cuTensorMapEncodeTiled failed for %s (%d)", what, static_cast<int>(r));
+}
+
 }  // namespace glora
 
 namespace {

@@ -19,6 +19,10 @@ int device_sm_count_or(int fallback);
 int encode_bf16_map(TensorMapBytes* out, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
                     const uint32_t* box, CUtensorMapSwizzle swz, const char* what);
 
+// A tensor map of cache pages, 4 dimensions: BF16 with the 128-byte swizzle, or bytes without one.
+int encode_page_map(TensorMapBytes* out, const void* ptr, bool bf16, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box, const char* what);
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace glora

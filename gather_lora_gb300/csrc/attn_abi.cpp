@@ -107,6 +107,36 @@ int kv_rows(const void* k, int64_t k_row_stride, const void* v, int64_t v_row_st
   return LORA_OK;
 }
 
+// TMA boxes over the cache's pages, where their size and strides allow: slots in eights (the swizzle's period), every stride a
+// multiple of the one before it. Otherwise a.box_tokens stays 0.
+int page_boxes(const lora_kv_cache* cache, glora::ChunkArgs& a) {
+  a.box_tokens = 0;
+  if (cache->num_pages == 0 || cache->page_size % 8) return LORA_OK;
+  int tokens = 8;
+  while (tokens < 128 && cache->page_size % (2 * tokens) == 0) tokens *= 2;
+  const bool bf16 = cache->format == LORA_KV_BF16;
+  const int64_t row = static_cast<int64_t>(cache->head_dim) * (bf16 ? 2 : 1);
+  // (a dimension of one may have any stride: it gets the one that follows from those inside it)
+  const bool inside = cache->kv_heads > 1 && a.c.head_bytes < a.c.token_bytes;
+  const int64_t count[2] = {inside ? cache->kv_heads : cache->page_size, inside ? cache->page_size : cache->kv_heads};
+  int64_t stride[3] = {inside ? a.c.head_bytes : a.c.token_bytes, inside ? a.c.token_bytes : a.c.head_bytes, a.c.page_bytes};
+  if (count[1] == 1) stride[1] = stride[0] * count[0];
+  if (cache->num_pages == 1) stride[2] = stride[1] * count[1];
+  if (stride[0] < row || stride[1] % stride[0] || stride[1] < stride[0] * count[0] || stride[2] % stride[1] ||
+      stride[2] < stride[1] * count[1] || stride[2] >= (int64_t{1} << 40))
+    return LORA_OK;
+  const uint64_t dims[4] = {static_cast<uint64_t>(cache->head_dim), static_cast<uint64_t>(count[0]), static_cast<uint64_t>(count[1]),
+                            static_cast<uint64_t>(cache->num_pages)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(stride[0]), static_cast<uint64_t>(stride[1]), static_cast<uint64_t>(stride[2])};
+  const uint32_t t = static_cast<uint32_t>(tokens), inner = bf16 ? 64 : static_cast<uint32_t>(cache->head_dim);
+  const uint32_t box[4] = {inner, inside ? 1 : t, inside ? t : 1, 1};
+  if (int rc = glora::encode_page_map(&a.map_k, a.c.k, bf16, dims, strides, box, "k_pages")) return rc;
+  if (int rc = glora::encode_page_map(&a.map_v, a.c.v, bf16, dims, strides, box, "v_pages")) return rc;
+  a.box_tokens = tokens;
+  a.heads_inside = inside;
+  return LORA_OK;
+}
+
 // Heads of a group in equal blocks of at most 128 (one block up to 128), as many whole tokens as fit 128 rows.
 void row_tiles(int group, int& head_block, int& tile_tokens) {
   const int blocks = (group + 127) / 128;
@@ -312,6 +342,7 @@ int lora_attn_chunk(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* out
   a.window = window;
   a.sinks = sinks;
   row_tiles(q_heads / cache->kv_heads, a.head_block, a.tile_tokens);
+  if (int rc = page_boxes(cache, a)) return rc;
   const int rc = glora::launch_chunk(a, stream);
   return rc ? cuda_fail(rc, "lora_attn_chunk launch") : ok();
 }

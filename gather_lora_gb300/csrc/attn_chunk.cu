@@ -15,15 +15,17 @@
 // finished by its CTA; otherwise its rows' sums go to the workspace and the last CTA of the item to arrive joins them in CTA
 // order (in two levels beyond kJoinGroup), so the bits never depend on who was last.
 //
-// Roles of a CTA's 16 warps: 0-7 softmax, 8 issues the MMAs, 9 plans and loads Q, 10 loads Q, 11-15 load K and V. The loaders
-// take groups of 16 tokens in turn: one lane a token looks its page up, then the rows go to the swizzled tiles by cp.async
-// (BF16) or through registers (8 bits), whatever the page size and the strides are. What nobody in the item sees is not
-// read but zero-filled.
+// Roles of a CTA's 16 warps: 0-7 softmax, 8 issues the MMAs, 9 plans and loads Q, 10 loads Q, 11-15 bring K and V. Where the pages'
+// size and strides allow (BOXED: sizes in eights), warp 11 looks the pages up, a lane four tokens, and issues TMA, a box a page,
+// and warps 12-15 take what has landed over: codes are converted in place in their stage, V that some rows see and others do
+// not is looked through. Otherwise the five warps take groups of 16 tokens in turn by cp.async (BF16) or through registers.
 //
-// 8-bit formats run in f16: the codes of both formats are exact in it, Q is brought into its range by a power of two a
-// row, and the weights have 11 bits. K's scale multiplies the score, V's the weight: to keep weights of any scale in f16's
-// range the running reference is that of y_t = z_t + log2 s_t, the weight w = 2^(y - ref) multiplies the codes and the sum of
-// the softmax is that of w_t / s_t.
+// 8-bit formats run in f16: the codes of both formats are exact in it, times their scale over a power of two that a group of 16
+// tokens shares (a product rounded once, to 11 bits), so that the softmax meets scales once in 16 columns: with one a token,
+// read from shared memory by every row, it took 2.8 times as long, as the MMAs leave little of that memory's bandwidth. K's
+// power of two multiplies the scores; V's the weight: to keep weights of any scale in f16's range the running reference is that of
+// y_t = z_t + log2 of V's, the weight w = 2^(y - ref) multiplies V and the softmax's own sum is that of w over V's. Q is brought
+// into f16's range by a power of two a row.
 //
 // Rounding to fewer bits: the weights (BF16 over a BF16 cache, else f16: the tensor cores' operand types), the result.
 //
@@ -44,7 +46,7 @@ namespace {
 constexpr unsigned kChunkTimeoutBit = 0x2u;     // LORA_DEV_TIMEOUT
 constexpr int kTile = 128;                      // rows of a tile, tokens of a key tile
 constexpr int kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
-constexpr int kMmaWarp = 8, kPlanWarp = 9, kQWarps = 2, kLoadWarp = 11, kLoaders = 5;
+constexpr int kMmaWarp = 8, kPlanWarp = 9, kQWarps = 2, kLoadWarp = 11, kLoaders = 5, kTakers = 4;
 constexpr int kChunkThreads = 512, kChunkWarps = kChunkThreads / 32;
 // Registers a thread: 128 at launch; two warpgroups give away what the softmax's rows of scores need: 2 * 104 + 2 * 152 = 4 * 128.
 constexpr int kHelperRegs = 104, kSoftRegs = 152;
@@ -59,6 +61,7 @@ constexpr float kSumUnit = 6.103515625e-05f;    // 8 bits: 2^-14, so that weight
 constexpr int kMostCtas = 160;                  // slots in the workspace
 constexpr int kJoinGroup = 16;                  // parts of a join
 constexpr int kSnap = 2;
+constexpr int kItemCost = 2;                    // what an item costs besides its key tiles, in key tiles
 constexpr int kMostSeqs = 8192;                 // LORA_MAX_SEQS
 constexpr int kFewPairs = 8;                    // sequences of more row-tile pairs are summed by a warp
 static_assert(kWaitLimitCycles < (1LL << 32), "waits are limited by a 32-bit clock");
@@ -83,10 +86,10 @@ struct ChunkShape {
 };
 
 struct ChunkMeta {           // of a key tile
-  float a[kTile];            // 8 bits: scale log2(e) times K's scale
-  float b[kTile];            // log2 of V's scale
-  float iv[kTile];           // kSumUnit / V's scale
-  uint16_t live[kGroups];    // tokens that are there and that some row sees
+  uint32_t live[4];          // tokens that are there and that some row sees
+  float4 group[kGroups];     // 8 bits, of 16 tokens: scale log2(e) times K's power of two, log2 of V's, kSumUnit over V's
+  uint32_t mk[kTile];        // (BOXED) a token's K scale over the group's, as two f16 whose sum it is
+  uint32_t mv[kTile];        // V's
 };
 
 struct ChunkPiece {
@@ -102,6 +105,7 @@ struct ChunkPiece {
 
 struct ChunkCtl {
   unsigned long long full[8], empty[8];              // K stages even, V stages odd
+  unsigned long long landed[8];                      // (BOXED) full but for the look or the conversion
   unsigned long long meta_full[kMeta], meta_empty[kMeta];
   unsigned long long q_full, q_empty;
   unsigned long long s_full[2][2], p_ready[2][2][2], o_done[2][2];   // [row tile][parity of its key tile] ([half])
@@ -181,6 +185,72 @@ __device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t&
     hi = *reinterpret_cast<const uint32_t*>(&y);
   }
 }
+// A scale over its group's power of two as f16 hi + lo (hi in the low half): 22 bits of it.
+__device__ __forceinline__ uint32_t split_f16(float m) {
+  const __half hi = __float2half_rn(m), lo = __float2half_rn(m - __half2float(hi));
+  return static_cast<uint32_t>(__half_as_ushort(hi)) | static_cast<uint32_t>(__half_as_ushort(lo)) << 16;
+}
+// Eight codes times such a scale, rounded once.
+template <int FMT>
+__device__ __forceinline__ uint4 scaled8(uint32_t c0, uint32_t c1, uint32_t m) {
+  uint32_t h[4];
+  codes_to_f16<FMT>(c0, h[0], h[1]);
+  codes_to_f16<FMT>(c1, h[2], h[3]);
+  const uint32_t m0 = __byte_perm(m, m, 0x1010), m1 = __byte_perm(m, m, 0x3232);
+  const __half2 hi = *reinterpret_cast<const __half2*>(&m0), lo = *reinterpret_cast<const __half2*>(&m1);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __half2 x = *reinterpret_cast<const __half2*>(&h[j]), r = __hfma2(x, hi, __hmul2(x, lo));
+    h[j] = *reinterpret_cast<const uint32_t*>(&r);
+  }
+  return make_uint4(h[0], h[1], h[2], h[3]);
+}
+// Exponent of the power of two of a group whose largest finite scale is `most`: codes times scales are below 2^15 of it.
+template <int FMT>
+__device__ __forceinline__ int group_exponent(float most) {
+  constexpr int bits = FMT == kKvE4m3 ? 9 : 7;             // codes are below 2^bits
+  return max(-120, (__float_as_int(most) >> 23) - 127 + 1 + bits - 15);
+}
+__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + e) << 23); }
+__device__ __forceinline__ float finite_magnitude(float s) { return fabsf(s) < INFINITY ? fabsf(s) : 0.f; }
+// What the softmax needs of a group. (One whose scales are all 0 only counts in the sums: 2^-64 keeps it from raising the reference.)
+template <int FMT>
+__device__ __forceinline__ float4 group_of(float most_k, float most_v, float sl2) {
+  const int ev = most_v == 0.f ? -64 : group_exponent<FMT>(most_v);
+  return make_float4(most_k == 0.f ? sl2 : exp2_int(group_exponent<FMT>(most_k)) * sl2, static_cast<float>(ev), kSumUnit * exp2_int(-ev), 0.f);
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_of(float s, float most) {
+  return split_f16(most == 0.f && s == s ? 0.f : s * exp2_int(-group_exponent<FMT>(most == 0.f ? 1.f : most)));
+}
+
+// Chunks of V: whether all is finite, and with what is not set to zero.
+template <bool CODED>
+__device__ __forceinline__ bool chunk_finite(const uint4& x) {
+  if (!CODED) return all_finite(abs_max2(0, x));
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  bool ok = true;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) ok = ok && (w[j] & 0x7c00u) != 0x7c00u && (w[j] & 0x7c000000u) != 0x7c000000u;
+  return ok;
+}
+template <bool CODED>
+__device__ __forceinline__ uint4 chunk_or_zero(const uint4& x) {
+  if (!CODED) return make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if ((w[j] & 0x7c00u) == 0x7c00u) w[j] &= 0xffff0000u;
+    if ((w[j] & 0x7c000000u) == 0x7c000000u) w[j] &= 0xffffu;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int c0, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n"
+               ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+               : "memory");
+}
 
 // 32 columns of scores (valid after tmem_ld_wait), in two blocks: register blocks of 16 leave the allocator room where one of 32
 // made it spill.
@@ -229,12 +299,22 @@ __device__ __forceinline__ Span span(const ChunkArgs& p, int first, int end) {
   s.tiles = end / kTile + 1 - s.skip;
   return s;
 }
-// Key tiles of row-tile pair x of a sequence (0 where all its rows stand before the first token).
+// Key tiles of row-tile pair x of a sequence (0 where all its rows stand before the first token); its units: kItemCost more.
 __device__ __forceinline__ int pair_tiles(const ChunkArgs& p, const Seq& s, int step, int x) {
   const int t0 = x * step;
   return span(p, s.len - s.n + t0, s.len - s.n + min(t0 + step, s.n) - 1).tiles;
 }
 
+__device__ __forceinline__ int pair_units(const ChunkArgs& p, const Seq& s, int step, int x) {
+  const int t = pair_tiles(p, s, step, x);
+  return t ? t + kItemCost : 0;
+}
+
+// CTAs with work: at least this many units each.
+constexpr int kLeast = 4;
+__device__ __forceinline__ long long working(long long total, unsigned grid) {
+  return min(static_cast<long long>(grid), (total + kLeast - 1) / kLeast);
+}
 // Unit at which CTA c's range begins, before ends move.
 __device__ __forceinline__ long long cut(long long c, long long total, long long n) { return c * total / n; }
 
@@ -288,7 +368,10 @@ __device__ __noinline__ void add_not_finite(const ChunkArgs& p, const ChunkPiece
             const uint32_t x = reinterpret_cast<const uint16_t*>(v)[lane * E + e];
             if ((x & 0x7f80u) == 0x7f80u) s[e] += __uint_as_float(x << 16);
           } else {
-            if ((v[lane * E + e] & 0x7f) == 0x7f) s[e] = __int_as_float(0x7fffffff);
+            float f[4];
+            codes_to_f32<FMT>(v[lane * E + e], f);
+            const float x = f[0] * __ldg(p.c.vs + scale_index(p.c, page, w.kvh, t - entry * p.c.page_size));
+            if (!(fabsf(x) < INFINITY)) s[e] = __int_as_float(0x7fffffff);
           }
         }
         bool all_nan = true;               // nothing more can change
@@ -323,7 +406,7 @@ __device__ __noinline__ void add_not_finite(const ChunkArgs& p, const ChunkPiece
 template <int FMT, int D>
 __device__ __noinline__ void join(const ChunkArgs& p, ChunkCtl& c, const ChunkPiece& w, float* factors, int first, int count, int by, bool last) {
   constexpr bool CODED = FMT != kKvBf16;
-  constexpr int SF = kSlotFloats<D>, FLAG = SF - 4, AT = 8;        // parts whose loads are in flight together
+  constexpr int SF = kSlotFloats<D>, FLAG = SF - 4;
   const int tid = threadIdx.x, rows = rows_of(p, w), tokens = w.end - w.first + 1, TT = p.tile_tokens, GB = p.head_block;
   float* const slots = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kCounterBytes);
   // (the item's first CTA has its part in the second of its slots)
@@ -343,37 +426,62 @@ __device__ __noinline__ void join(const ChunkArgs& p, ChunkCtl& c, const ChunkPi
   bool bad = false;
   for (int y = 0; y < count; ++y) bad = bad || __float_as_int(__ldcg(slot_of(y) + FLAG)) != 0;
   soft_sync();
-  // thread: 4 consecutive dimensions of one row at a time
-  for (int task = tid; task < rows * (D / 4); task += kSoftThreads) {
-    const int r = task / (D / 4), d = task % (D / 4) * 4;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // A thread's task: 4 consecutive dimensions of a row. It takes T of them and Y parts of each at a time, their loads in flight
+  // together: many rows have few parts as a rule, few rows many.
+  auto tasks = [&](auto t_at_once, auto y_at_once) {
+    constexpr int T = decltype(t_at_once)::value, Y = decltype(y_at_once)::value;
+    const int all = rows * (D / 4);
 #pragma unroll 1
-    for (int y0 = 0; y0 < count; y0 += AT) {
-      float4 v[AT];
+    for (int first_task = tid; first_task < all; first_task += T * kSoftThreads) {
+      float4 acc[T];
 #pragma unroll
-      for (int y = 0; y < AT; ++y) {
-        v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (y0 + y < count) v[y] = __ldcg(reinterpret_cast<const float4*>(slot_of(y0 + y) + 4 * kTile + r * D + d));
+      for (int x = 0; x < T; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int y0 = 0; y0 < count; y0 += Y) {
+        float4 v[T][Y];
+#pragma unroll
+        for (int x = 0; x < T; ++x)
+#pragma unroll
+          for (int y = 0; y < Y; ++y) {
+            const int task = first_task + x * kSoftThreads;
+            v[x][y] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (task < all && y0 + y < count) v[x][y] = __ldcg(reinterpret_cast<const float4*>(slot_of(y0 + y) + 4 * kTile) + task);
+          }
+#pragma unroll
+        for (int x = 0; x < T; ++x)
+#pragma unroll
+          for (int y = 0; y < Y; ++y) {
+            const int task = first_task + x * kSoftThreads;
+            if (task < all && y0 + y < count) {
+              const float f = factors[(y0 + y) * 2 * kTile + task / (D / 4)];
+              acc[x].x += v[x][y].x * f;
+              acc[x].y += v[x][y].y * f;
+              acc[x].z += v[x][y].z * f;
+              acc[x].w += v[x][y].w * f;
+            }
+          }
       }
+#pragma unroll 1
+      for (int x = 0; x < T; ++x) {
+        const int task = first_task + x * kSoftThreads, r = task / (D / 4), d = task % (D / 4) * 4;
+        if (task >= all) break;
+        float4 a = acc[0];
 #pragma unroll
-      for (int y = 0; y < AT; ++y)
-        if (y0 + y < count) {
-          const float f = factors[(y0 + y) * 2 * kTile + r];
-          acc.x += v[y].x * f;
-          acc.y += v[y].y * f;
-          acc.z += v[y].z * f;
-          acc.w += v[y].w * f;
+        for (int z = 1; z < T; ++z)
+          if (x == z) a = acc[z];
+        if (last) {
+          const int ri = r / kTile, rt = r % kTile / GB, rg = r % kTile - rt * GB, tok = ri * TT + rt;
+          if (rt < TT && rg < w.heads && tok < tokens && !failed(c))
+            *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(w.row0) + tok) * p.out_stride + (w.h0 + rg) * D + d) =
+                make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+        } else {
+          *(reinterpret_cast<float4*>(slot_of(0) + 4 * kTile) + task) = a;
         }
+      }
     }
-    if (last) {
-      const int ri = r / kTile, rt = r % kTile / GB, rg = r % kTile - rt * GB, tok = ri * TT + rt;
-      if (rt < TT && rg < w.heads && tok < tokens && !failed(c))
-        *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(w.row0) + tok) * p.out_stride + (w.h0 + rg) * D + d) =
-            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-    } else {
-      *reinterpret_cast<float4*>(slot_of(0) + 4 * kTile + r * D + d) = acc;
-    }
-  }
+  };
+  if (rows * (D / 4) > 2 * kSoftThreads) tasks(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+  else tasks(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
   if (last) {
     const int rt = tid % kTile / GB, rg = tid % kTile - rt * GB, tok = tid / kTile * TT + rt;
     if (p.lse && tid < rows && rt < TT && rg < w.heads && tok < tokens && !failed(c))
@@ -389,7 +497,7 @@ __device__ __noinline__ void join(const ChunkArgs& p, ChunkCtl& c, const ChunkPi
   if (last && bad && !failed(c)) add_not_finite<FMT, D>(p, w, tid >> 5, tid & 31);
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool BOXED>
 __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_constant__ ChunkArgs p) {
   using Sh = ChunkShape<D>;
   using Sm = ChunkSmem<D>;
@@ -405,12 +513,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 
   if (tid == 0) {
     for (int s = 0; s < 2 * NP; ++s) {
-      mbar_init(smem_u32(&c.full[s]), kGroups);
+      mbar_init(smem_u32(&c.full[s]), !BOXED ? kGroups : CODED || (s & 1) ? kTakers : 1);
+      mbar_init(smem_u32(&c.landed[s]), 1);
       mbar_init(smem_u32(&c.empty[s]), 1);
     }
     for (int s = 0; s < kMeta; ++s) {
-      mbar_init(smem_u32(&c.meta_full[s]), kGroups);
-      mbar_init(smem_u32(&c.meta_empty[s]), kSoftWarps);
+      mbar_init(smem_u32(&c.meta_full[s]), BOXED ? 1 : kGroups);
+      mbar_init(smem_u32(&c.meta_empty[s]), kSoftWarps + (BOXED && CODED ? kTakers : 0));
     }
     mbar_init(smem_u32(&c.q_full), kQWarps);
     mbar_init(smem_u32(&c.q_empty), 1);
@@ -449,7 +558,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       const int np = s.n > 0 ? (s.n - 1) / step + 1 : 0;
       long long sum = 0;
       if (np <= kFewPairs)
-        for (int x = 0; x < np; ++x) sum += pair_tiles(p, s, step, x);
+        for (int x = 0; x < np; ++x) sum += pair_units(p, s, step, x);
       uint32_t many = __ballot_sync(0xffffffffu, np > kFewPairs);
       while (many) {
         const int src = __ffs(many) - 1;
@@ -460,7 +569,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         o.len = __shfl_sync(0xffffffffu, s.len, src);
         const int onp = (o.n - 1) / step + 1;
         long long part = 0;
-        for (int x = lane; x < onp; x += 32) part += pair_tiles(p, o, step, x);
+        for (int x = lane; x < onp; x += 32) part += pair_units(p, o, step, x);
 #pragma unroll
         for (int y = 16; y > 0; y >>= 1) part += __shfl_xor_sync(0xffffffffu, part, y);
         if (lane == src) sum = part;
@@ -485,7 +594,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       if (w < warp) before += c.warp_sum[w];
       total += c.warp_sum[w];
     }
-    const long long n = min(static_cast<long long>(gridDim.x), (total + 1) / 2);     // CTAs with work
+    const long long n = working(total, gridDim.x);
     if (tid == 0) c.total = total;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -507,7 +616,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     __syncthreads();
   }
   const uint32_t tmem = c.tmem;
-  const long long total = c.total, ctas = min(static_cast<long long>(gridDim.x), (total + 1) / 2);
+  const long long total = c.total, ctas = working(total, gridDim.x);
   const bool works = blockIdx.x < ctas;
 
   if (warp >= kSoftWarps) {
@@ -521,7 +630,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const int snap = static_cast<int>(min(static_cast<long long>(kSnap), total / max(ctas, 1LL) / 4));
     auto first_pair = [&]() { return max(0, (s.n - s.len) / step); };       // the first with a tile (s.len > 0)
     auto next_item = [&]() {                              // (there is one)
-      s0 += tiles;
+      s0 += kItemCost + tiles;
       if ((x + 1) * step < s.n) {
         ++x;
       } else {
@@ -551,7 +660,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         const int np = (s.n - 1) / step + 1;
         long long before = 0;
         for (int x0 = 0; x0 < np; x0 += 32) {
-          const int mine = x0 + lane < np ? pair_tiles(p, s, step, x0 + lane) : 0;
+          const int mine = x0 + lane < np ? pair_units(p, s, step, x0 + lane) : 0;
           long long incl = mine;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -562,20 +671,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           if (hit) {
             const int src = __ffs(hit) - 1;
             x = x0 + src;
-            tiles = __shfl_sync(0xffffffffu, mine, src);
-            tile = static_cast<int>(rest - before - (__shfl_sync(0xffffffffu, incl, src) - tiles));
+            const int units = __shfl_sync(0xffffffffu, mine, src);
+            tile = static_cast<int>(rest - before - (__shfl_sync(0xffffffffu, incl, src) - units));     // (in units so far)
+            tiles = units - kItemCost;
             break;
           }
           before += __shfl_sync(0xffffffffu, incl, 31);
         }
         s0 = r - tile;
+        tile -= kItemCost;
         if (tile <= snap) tile = 0;
         else if (tiles - tile <= snap) tile = tiles;
-        if (e == 1) u1 = s0 + tile;
-        else u = s0 + tile;
+        const long long at = s0 + (tile ? kItemCost + tile : 0);
+        if (e == 1) u1 = at;
+        else u = at;
       }
       if (u < u1 && tile == tiles) next_item();
     }
+    auto tiles_here = [&]() { return static_cast<int>(min(static_cast<long long>(tiles), u1 - s0 - kItemCost)) - tile; };   // of the item, in this range
     uint32_t loads = 0;
     for (int it = 0;; ++it) {
       const int sl = it % kPieces;
@@ -603,14 +716,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             w.skip = v.skip;
             w.tiles = tiles;
             w.ta = tile;
-            w.n = static_cast<int>(min(static_cast<long long>(tiles), tile + (u1 - u))) - tile;
+            w.n = tiles_here();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {                 // tiles that hold a token its last row may see
               const int last = min(w.first + (i + 1) * TT - 1, w.end), any = w.first + i * TT <= w.end && last >= 0;
               w.ni[i] = any ? max(0, min(w.ta + w.n, last / kTile + 1 - w.skip) - w.ta) : 0;
             }
-            w.c0 = static_cast<int>(((s0 + snap + 1) * ctas + total - 1) / total) - 1;
-            w.c1 = static_cast<int>(((s0 + tiles - snap) * ctas + total - 1) / total) - 1;
+            w.c0 = static_cast<int>(((s0 + kItemCost + snap + 1) * ctas + total - 1) / total) - 1;
+            w.c1 = static_cast<int>(((s0 + kItemCost + tiles - snap) * ctas + total - 1) / total) - 1;
           }
           c.piece[sl] = w;
           *reinterpret_cast<volatile int*>(&c.bad[sl]) = 0;
@@ -618,9 +731,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         }
         __syncwarp();
         if (go) {
-          const int m = static_cast<int>(min(static_cast<long long>(tiles), tile + (u1 - u))) - tile;
-          u += m;
-          tile += m;
+          tile += tiles_here();
+          u = s0 + kItemCost + tile;
           if (u < u1) next_item();
         }
       }
@@ -673,6 +785,193 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         if (lane == 0) mbar_arrive(smem_u32(&c.piece_empty[sl]));
       }
       if (!valid) break;
+    }
+  } else if (BOXED && warp == kLoadWarp) {
+    // ==================== pages looked up, TMA of K and V ====================
+    // A lane has 4 consecutive tokens of a tile (of one page: boxes are of 8 slots or more); the first lane of a box issues it. A
+    // page that is not there is asked for behind the last: its rows are filled with zeros.
+    const int BT = p.box_tokens;
+    const float sl2 = p.scale * kLog2e;
+    constexpr uint32_t bytes = CODED ? kTile * D : Sh::tile_bytes;
+    uint32_t kt = 0, tiles = 0;          // key tiles of the pieces before; issued
+    for (int it = 0;; ++it) {
+      const int sl = it % kPieces;
+      wait(c, c.piece_full[sl], (it / kPieces) & 1);
+      __syncwarp();
+      const ChunkPiece& w = c.piece[sl];
+      if (!w.valid) break;
+      const int32_t* const table = p.table + w.b * p.table_stride;
+      auto first_token = [&](int j) {
+        const int t = w.ta + j;
+        return (t < w.kept ? t : t + w.skip) * kTile;
+      };
+      int slot = 0, page = -1;           // of this lane's tokens of the tile to issue next
+      auto look_up = [&](int j) {
+        const int t = first_token(j) + lane * 4, box = t & ~(BT - 1);
+        page = -1;
+        if (box > w.end || (box + BT - 1 < w.low && box >= p.sinks)) return;      // (nobody sees any of the box)
+        const int entry = p.page_shift >= 0 ? t >> p.page_shift : t / p.c.page_size;
+        slot = t - entry * p.c.page_size;
+        page = __ldg(table + entry);
+      };
+      look_up(0);
+      for (int j = 0; j < w.n; ++j) {
+        const uint32_t k = kt + j, ks = 2 * (k % NP);
+        const int t = first_token(j) + lane * 4, my_slot = slot;
+        const bool there = page >= 0 && page < p.c.num_pages;
+        const int my_page = there ? page : p.c.num_pages;
+        uint32_t seen = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (there && t + x <= w.end && (t + x >= w.low || t + x < p.sinks)) seen |= 1u << x;
+        float sk[4], sv[4];
+        if constexpr (CODED) {
+          const long long si = there ? scale_index(p.c, my_page, w.kvh, my_slot) : 0;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            sk[x] = there ? __ldg(p.c.ks + si + x) : 0.f;
+            sv[x] = there ? __ldg(p.c.vs + si + x) : 0.f;
+          }
+        }
+        if (j + 1 < w.n) look_up(j + 1);
+        ChunkMeta& m = metas[k % kMeta];
+        if (k >= kMeta) wait(c, c.meta_empty[k % kMeta], ((k / kMeta) - 1) & 1);
+        if (k >= NP) wait(c, c.empty[ks], ((k / NP) - 1) & 1);
+        __syncwarp();
+        // Copies first, then the masks and scales.
+        auto copies = [&](uint32_t stage, const TensorMapBytes& map) {
+          const uint32_t bar = smem_u32(!CODED && !(stage & 1) ? &c.full[stage] : &c.landed[stage]);
+          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+          __syncwarp();
+          if ((lane * 4) % BT == 0) {
+            const int c1 = p.heads_inside ? w.kvh : my_slot, c2 = p.heads_inside ? my_slot : w.kvh;
+            const uint32_t to = ring + stage * Sh::tile_bytes;
+            if constexpr (CODED) {
+              tma_load_4d(to + Sh::tile_bytes / 2 + lane * 4 * D, &map, 0, c1, c2, my_page, bar);
+            } else {
+#pragma unroll
+              for (int a = 0; a < D / 64; ++a) tma_load_4d(to + a * (kTile * 128) + lane * 4 * 128, &map, a * 64, c1, c2, my_page, bar);
+            }
+          }
+        };
+        if (__any_sync(0xffffffffu, failed(c))) break;
+        copies(ks, p.map_k);
+        uint32_t live = seen << (4 * (lane & 7));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) live |= __shfl_xor_sync(0xffffffffu, live, o);
+        if ((lane & 7) == 0) m.live[lane >> 3] = live;
+        if constexpr (CODED) {
+          float mk = 0.f, mv = 0.f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            mk = fmaxf(mk, finite_magnitude(sk[x]));
+            mv = fmaxf(mv, finite_magnitude(sv[x]));
+          }
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) {
+            mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+          }
+          if ((lane & 3) == 0) m.group[lane >> 2] = group_of<FMT>(mk, mv, sl2);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            m.mk[lane * 4 + x] = scale_of<FMT>(sk[x], mk);
+            m.mv[lane * 4 + x] = scale_of<FMT>(sv[x], mv);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.meta_full[k % kMeta]));
+        if (k >= NP) wait(c, c.empty[ks + 1], ((k / NP) - 1) & 1);
+        __syncwarp();
+        copies(ks + 1, p.map_v);
+        tiles = k + 1;
+      }
+      kt += w.n;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c.piece_empty[sl]));
+    }
+    if (lane == 0 && failed(c)) {        // let the copies in flight land
+      for (uint32_t k = tiles > NP ? tiles - NP : 0; k <= tiles; ++k)
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t st = 2 * (k % NP) + x;
+          mbar_wait_limit(smem_u32(!CODED && !x ? &c.full[st] : &c.landed[st]), (k / NP) & 1, k < tiles ? kDrainLimitCycles : kDrainLimitCycles / 16);
+        }
+    }
+    __syncwarp();
+  } else if (BOXED && warp > kLoadWarp) {
+    // ================= what has landed: converted, looked through =================
+    // Warp q of the four has rows 32 q .. of every tile. 8 bits: a tile's codes lie in the upper half of its stage; at head_dim 128 a row's
+    // are where the second half of its f16 goes, so that a warp's rows are its own; at 64 all four have read theirs before any writes.
+    const int q = warp - kLoadWarp - 1;
+    uint32_t kt = 0;
+    for (int it = 0;; ++it) {
+      const int sl = it % kPieces;
+      wait(c, c.piece_full[sl], (it / kPieces) & 1);
+      __syncwarp();
+      const ChunkPiece& w = c.piece[sl];
+      if (!w.valid) break;
+      for (int j = 0; j < w.n; ++j) {
+        const uint32_t k = kt + j;
+        const int tile = w.ta + j, t0 = (tile < w.kept ? tile : tile + w.skip) * kTile + q * 32;
+        const bool partly = !(t0 + 31 <= w.first && (t0 > w.end - p.window || t0 + 31 < p.sinks));   // some rows see some of it, others not
+        auto part_seen = [&](int t) { return !(t <= w.first && (t > w.end - p.window || t < p.sinks)); };
+        bool bad = false;
+#pragma unroll 1
+        for (int x = CODED ? 0 : 1; x < 2; ++x) {
+          const uint32_t st = 2 * (k % NP) + x, at = ring + st * Sh::tile_bytes;
+          wait(c, c.landed[st], (k / NP) & 1);
+          __syncwarp();
+          if constexpr (CODED) {
+            if (x == 0) wait(c, c.meta_full[k % kMeta], (k / kMeta) & 1);
+            const uint32_t* const mult = x ? metas[k % kMeta].mv : metas[k % kMeta].mk;
+            constexpr int CH = D / 16, RPI = 32 / CH, NI = 32 / RPI;
+            const int ch = lane % CH, r0 = q * 32 + lane / CH;
+            uint4 v[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) v[i] = lds128(at + Sh::tile_bytes / 2 + (r0 + i * RPI) * D + ch * 16);
+            if constexpr (D == 64) asm volatile("bar.sync 2, %0;\n" ::"n"(kTakers * 32) : "memory");
+            else __syncwarp();
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+              const int r = r0 + i * RPI;
+              const uint32_t m = mult[r];
+              uint4 a = scaled8<FMT>(v[i].x, v[i].y, m), b = scaled8<FMT>(v[i].z, v[i].w, m);
+              if (x && partly && part_seen(t0 - q * 32 + r) && !(chunk_finite<true>(a) && chunk_finite<true>(b))) {
+                bad = true;
+                a = chunk_or_zero<true>(a);
+                b = chunk_or_zero<true>(b);
+              }
+              // (lanes of the upper half of a row store their chunks in the other order: no bank twice)
+              const bool swap = CH == 8 && ch >= 4;
+              sts128(at + Sh::at(r, 2 * ch + swap), swap ? b : a);
+              sts128(at + Sh::at(r, 2 * ch + !swap), swap ? a : b);
+            }
+            fence_proxy_async_smem();
+          } else if (partly) {
+            constexpr int CH = D / 8, RPI = 32 / CH;
+            const int ch = lane % CH;
+#pragma unroll 4
+            for (int r = q * 32 + lane / CH; r < q * 32 + 32; r += RPI) {
+              const uint32_t to = at + Sh::at(r, ch);
+              const uint4 v = lds128(to);
+              if (part_seen(t0 - q * 32 + r) && !chunk_finite<false>(v)) {
+                bad = true;
+                sts128(to, chunk_or_zero<false>(v));
+              }
+            }
+            fence_proxy_async_smem();
+          }
+          if (x && partly && __any_sync(0xffffffffu, bad) && lane == 0) *reinterpret_cast<volatile int*>(&c.bad[sl]) = 1;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&c.full[st]));
+            if (CODED && x) mbar_arrive(smem_u32(&c.meta_empty[k % kMeta]));
+          }
+        }
+      }
+      kt += w.n;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c.piece_empty[sl]));
     }
   } else if (warp >= kLoadWarp) {
     // =========================== K and V tiles ============================
@@ -748,9 +1047,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
               const int t = i * TPI + sub_t;
               const uint32_t to = at + Sh::at(r0 + t, ch);
               const uint4 v = lds128(to);
-              if (part_seen(t0 + t) && !all_finite(abs_max2(0, v))) {
+              if (part_seen(t0 + t) && !chunk_finite<false>(v)) {
                 bad = true;
-                sts128(to, make_uint4(finite_or_zero(v.x), finite_or_zero(v.y), finite_or_zero(v.z), finite_or_zero(v.w)));
+                sts128(to, chunk_or_zero<false>(v));
               }
             }
             if (__any_sync(0xffffffffu, bad) && lane == 0) *reinterpret_cast<volatile int*>(&c.bad[sl]) = 1;
@@ -774,7 +1073,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           const unsigned char* const from = keys ? p.c.k : p.c.v;
           const uint32_t at = ring + stage_of(g) * Sh::tile_bytes;
           const int r0 = (g % kGroups) * kGroup;
-          if (keys && lane == 0) metas[(kt + g / (2 * kGroups)) % kMeta].live[g % kGroups] = static_cast<uint16_t>(live);
+          if (keys && lane == 0) reinterpret_cast<uint16_t*>(metas[(kt + g / (2 * kGroups)) % kMeta].live)[g % kGroups] = static_cast<uint16_t>(live);
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
             const int t = i * TPI + sub_t;
@@ -813,25 +1112,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             if (o >= 0) ahead[i] = __ldg(reinterpret_cast<const uint4*>(from + o + ch * 16));
           }
         };
-        // 16 codes -> two chunks of f16 (lanes of the upper half of a row store them in the other order: no bank twice).
-        auto put = [&](uint32_t at, int r, const uint4& v) {
-          uint32_t h[8];
-          codes_to_f16<FMT>(v.x, h[0], h[1]);
-          codes_to_f16<FMT>(v.y, h[2], h[3]);
-          codes_to_f16<FMT>(v.z, h[4], h[5]);
-          codes_to_f16<FMT>(v.w, h[6], h[7]);
-          const bool swap = CH == 8 && ch >= 4;
-          const uint4 first = swap ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
-          const uint4 second = swap ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(h[4], h[5], h[6], h[7]);
-          sts128(at + Sh::at(r, 2 * ch + swap), first);
-          sts128(at + Sh::at(r, 2 * ch + !swap), second);
-        };
         if (g0 < groups) fetch(g0);
         for (int g = g0; g < groups; g += kLoaders) {
 #pragma unroll
           for (int i = 0; i < NI; ++i) cur[i] = ahead[i];
           const float k_scale = ks, v_scale = vs;
-          const uint32_t live = __ballot_sync(0xffffffffu, there) & 0xffffu, odd = __ballot_sync(0xffffffffu, there && v_scale <= 0.f);
+          const uint32_t live = __ballot_sync(0xffffffffu, there) & 0xffffu;
           if (g + kLoaders < groups) {
             page = look_up(g + kLoaders, slot);
             fetch(g + kLoaders);
@@ -840,47 +1126,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           if (__any_sync(0xffffffffu, failed(c))) break;
           const bool keys = (g / kGroups) % 2 == 0;
           const uint32_t at = ring + stage_of(g) * Sh::tile_bytes;
-          const int r0 = (g % kGroups) * kGroup;
-          if (keys) {
-            // Masks and scales. A scale of 0 stands for codes whose weight only counts in the sum: 2^-64 there, with V's codes
-            // zero; a negative one changes the codes' signs. (Below 2^-110, under what lora_kv_write stores: 2^-110.)
-            ChunkMeta& m = metas[(kt + g / (2 * kGroups)) % kMeta];
-            if (lane == 0) m.live[g % kGroups] = static_cast<uint16_t>(live);
-            if (lane < kGroup) {
-              const float mag = v_scale == 0.f ? 5.421010862427522e-20f : fmaxf(fabsf(v_scale), 7.703719777548943e-34f);
-              const float s = v_scale != v_scale ? v_scale : mag;       // (fmaxf drops NaN)
-              m.a[r0 + lane] = k_scale * sl2;
-              m.b[r0 + lane] = log2f(s);
-              m.iv[r0 + lane] = v_scale != v_scale ? 0.f : kSumUnit / s;   // (times the weight 0 of a row that does not see it: 0)
-            }
-          } else if (odd || (FMT == kKvE4m3 && partly(g))) {
-            const bool look = FMT == kKvE4m3 && partly(g);
-            const int t0 = token0(g);
+          const int r0 = (g % kGroups) * kGroup, t0 = token0(g);
+          // The group's powers of two (lanes 16 .. 31 as lanes 0 .. 15), a token's scale over them.
+          float most_k = finite_magnitude(k_scale), most_v = finite_magnitude(v_scale);
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-              const int t = i * TPI + sub_t;
-              uint32_t x4[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
-              const float sc = __shfl_sync(0xffffffffu, v_scale, t);
-              const bool part = look && part_seen(t0 + t);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (part) {                // NaN codes (magnitude 0x7f) to zero
-                  const uint32_t nan = (((x4[j] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
-                  if (nan) bad = true;
-                  x4[j] &= ~(nan * 0xffu);
-                }
-                if (sc == 0.f) x4[j] = 0;
-                if (sc < 0.f) {
-                  if constexpr (FMT == kKvE4m3) x4[j] ^= 0x80808080u;
-                  else x4[j] = __vneg4(x4[j]);
-                }
-              }
-              cur[i] = make_uint4(x4[0], x4[1], x4[2], x4[3]);
-            }
-            if (__any_sync(0xffffffffu, bad) && lane == 0) *reinterpret_cast<volatile int*>(&c.bad[sl]) = 1;
+          for (int o = 1; o < kGroup; o <<= 1) {
+            most_k = fmaxf(most_k, __shfl_xor_sync(0xffffffffu, most_k, o));
+            most_v = fmaxf(most_v, __shfl_xor_sync(0xffffffffu, most_v, o));
           }
+          if (keys && lane == 0) {
+            ChunkMeta& m = metas[(kt + g / (2 * kGroups)) % kMeta];
+            reinterpret_cast<uint16_t*>(m.live)[g % kGroups] = static_cast<uint16_t>(live);
+            m.group[g % kGroups] = group_of<FMT>(most_k, most_v, sl2);
+          }
+          const uint32_t mult = keys ? scale_of<FMT>(k_scale, most_k) : scale_of<FMT>(v_scale, most_v);
+          const bool look = !keys && partly(g);
 #pragma unroll
-          for (int i = 0; i < NI; ++i) put(at, r0 + i * TPI + sub_t, cur[i]);
+          for (int i = 0; i < NI; ++i) {
+            const int t = i * TPI + sub_t, r = r0 + t;
+            const uint32_t m = __shfl_sync(0xffffffffu, mult, t);
+            uint4 a = scaled8<FMT>(cur[i].x, cur[i].y, m), b = scaled8<FMT>(cur[i].z, cur[i].w, m);
+            if (look && part_seen(t0 + t) && !(chunk_finite<true>(a) && chunk_finite<true>(b))) {
+              bad = true;
+              a = chunk_or_zero<true>(a);
+              b = chunk_or_zero<true>(b);
+            }
+            const bool swap = CH == 8 && ch >= 4;
+            sts128(at + Sh::at(r, 2 * ch + swap), swap ? b : a);
+            sts128(at + Sh::at(r, 2 * ch + !swap), swap ? a : b);
+          }
+          if (look && __any_sync(0xffffffffu, bad) && lane == 0) *reinterpret_cast<volatile int*>(&c.bad[sl]) = 1;
           arrive(g);
         }
       }
@@ -1023,7 +1298,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       const int pos = w.first + i * TT + t_in, n = w.ni[i];
       const bool live = t_in < TT && g < w.heads && pos <= w.end;
       float qf = 1.f;                      // 8 bits: Q was divided by it
-      bool plain_q = true;
       uint32_t buf = Sh::buf(i, 0);
       float ref = -INFINITY, l = 0.f;      // exponents are relative to ref (BF16: in units of raw scores, less kGrow)
       for (int j = 0; j < n; ++j, ++t) {
@@ -1035,51 +1309,48 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         dead |= wait(c, c.s_full[i][t & 1], (t >> 1) & 1);
         __syncwarp();
         tc_fence_after();
-        if (CODED && j == 0) {
-          qf = q_factor[sl * 2 * kTile + i * kTile + row];
-          plain_q = __all_sync(0xffffffffu, qf == 1.f);
-        }
+        if (CODED && j == 0) qf = q_factor[sl * 2 * kTile + i * kTile + row];
         // What the row sees of the tile.
         const int tile = w.ta + j, t0 = (tile < w.kept ? tile : tile + w.skip) * kTile;
         const uint4 there = *reinterpret_cast<const uint4*>(m.live);
         const int hi = pos - t0, lo = hi - min(p.window - 1, max(pos, 0)), sk = p.sinks - t0;    // sees x <= hi with x >= lo or x < sk
         const bool whole = hi >= kTile - 1 && (lo <= 0 || sk >= kTile) && (there.x & there.y & there.z & there.w) == 0xffffffffu;
         const bool cuts = __any_sync(0xffffffffu, live && !whole);
-        // A quarter of the scores at a time, the next one on its way from tensor memory: as they are (8 bits: y), what is not
-        // seen at -infinity. (Loops over the halves, not unrolled: see wait() on code size.)
+        // A quarter of the scores at a time, the next one on its way from tensor memory; what is not seen at -infinity. (Loops over
+        // the halves, not unrolled: see wait() on code size.)
         uint32_t sa[32], sb[32];
-        auto shape = [&](int q, uint32_t (&s)[32]) {
-          if constexpr (CODED) {           // y = score * K's scale + log2 of V's
-            const uint64_t qf2 = pair(qf, qf);
+        auto mask = [&](int q, uint32_t (&s)[32]) {
+          if (!cuts) return;
+          auto below = [&](int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1; };   // bits under x
+          const uint32_t see = m.live[q] & below(min(hi, kTile) + 1 - q * 32) & (~below(lo - q * 32) | below(sk - q * 32));
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 a = *reinterpret_cast<const float4*>(m.a + q * 32 + e), b = *reinterpret_cast<const float4*>(m.b + q * 32 + e);
-              uint64_t a01 = pair(a.x, a.y), a23 = pair(a.z, a.w);
-              if (!plain_q) {
-                a01 = mul2(a01, qf2);
-                a23 = mul2(a23, qf2);
-              }
-              const float2 y0 = unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), a01, pair(b.x, b.y)));
-              const float2 y1 = unpair(fma2(pair(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), a23, pair(b.z, b.w)));
-              s[e] = __float_as_uint(y0.x);
-              s[e + 1] = __float_as_uint(y0.y);
-              s[e + 2] = __float_as_uint(y1.x);
-              s[e + 3] = __float_as_uint(y1.y);
-            }
-          }
-          if (cuts) {
-            auto below = [&](int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1; };   // bits under x
-            const uint32_t see = reinterpret_cast<const uint32_t*>(m.live)[q] & below(min(hi, kTile) + 1 - q * 32) & (~below(lo - q * 32) | below(sk - q * 32));
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((see >> e) & 1)) s[e] = 0xff800000u;
+          for (int e = 0; e < 32; ++e)
+            if (!((see >> e) & 1)) s[e] = 0xff800000u;
+        };
+        // Factor of the scores and what is added to them (8 bits: of 16 columns; the factor is never 0, -infinity stays itself).
+        auto factor = [&](int g16, float& f, float& add, float& unit) {
+          if constexpr (CODED) {
+            const float4 g4 = m.group[g16];
+            f = fmaxf(g4.x * qf, 1e-37f);
+            add = g4.y;
+            unit = g4.z;
           }
         };
-        auto most = [&](const uint32_t (&s)[32], float top) {
+        auto most = [&](int q, const uint32_t (&s)[32], float top) {
+          float a[2];
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            top = max3(top, max3(__uint_as_float(s[e]), __uint_as_float(s[e + 1]), __uint_as_float(s[e + 2])), __uint_as_float(s[e + 3]));
-          return top;
+          for (int h = 0; h < 2; ++h) {
+            a[h] = __uint_as_float(s[16 * h]);
+#pragma unroll
+            for (int e = 1; e < 15; e += 2) a[h] = max3(a[h], __uint_as_float(s[16 * h + e]), __uint_as_float(s[16 * h + e + 1]));
+            a[h] = fmaxf(a[h], __uint_as_float(s[16 * h + 15]));
+            if constexpr (CODED) {
+              float f, add, unit;
+              factor(2 * q + h, f, add, unit);
+              a[h] = __fmaf_rn(a[h], f, add);
+            }
+          }
+          return max3(top, a[0], a[1]);
         };
         // The maximum over all four (the first two stay), then their weights.
         float top = -INFINITY;
@@ -1088,12 +1359,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         for (int h = 1; h >= 0; --h) {
           tmem_ld_wait();
           scores32(col_s + h * 64, sa);
-          shape(2 * h + 1, sb);
-          top = most(sb, top);
+          mask(2 * h + 1, sb);
+          top = most(2 * h + 1, sb, top);
           tmem_ld_wait();
           if (h) scores32(col_s + 32, sb);
-          shape(2 * h, sa);
-          top = most(sa, top);
+          mask(2 * h, sa);
+          top = most(2 * h, sa, top);
         }
         if (j == 0) {
           ref = top;
@@ -1118,23 +1389,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         }
         // (nothing seen: every weight is 0)
         const float off = ref == -INFINITY ? 0.f : CODED ? kTop - ref : __fmaf_rn(-ref, sl2, -kGrow);
-        const uint64_t sl2p = pair(sl2, sl2), offp = pair(off, off);
-        uint64_t sum[4] = {0, 0, 0, 0};
+        uint64_t sum[2] = {0, 0};
         auto weights = [&](int q, const uint32_t (&s)[32]) {
           uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint64_t z = pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-            const float2 x = unpair(CODED ? add2(z, offp) : fma2(z, sl2p, offp));
-            const float w0 = exp2_fast(x.x), w1 = exp2_fast(x.y);
-            if constexpr (CODED) {
-              const float2 iv = *reinterpret_cast<const float2*>(m.iv + q * 32 + 2 * e);
-              sum[e & 3] = fma2(pair(w0, w1), pair(iv.x, iv.y), sum[e & 3]);
-              pk[e] = pack_f16x2(w0, w1);
-            } else {
-              sum[e & 3] = add2(sum[e & 3], pair(w0, w1));
-              pk[e] = pack_bf16x2(w0, w1);
+          for (int h = 0; h < 2; ++h) {
+            float f = sl2, add = 0.f, unit = 0.f;
+            factor(2 * q + h, f, add, unit);
+            add += off;
+            const uint64_t fp = pair(f, f), addp = pair(add, add);
+            uint64_t mine[2] = {0, 0};     // 8 bits: the group's sum
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 x = unpair(fma2(pair(__uint_as_float(s[16 * h + 2 * e]), __uint_as_float(s[16 * h + 2 * e + 1])), fp, addp));
+              const float w0 = exp2_fast(x.x), w1 = exp2_fast(x.y);
+              uint64_t& to = CODED ? mine[e & 1] : sum[e & 1];
+              to = add2(to, pair(w0, w1));
+              pk[8 * h + e] = CODED ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
             }
+            if constexpr (CODED) sum[h] = fma2(add2(mine[0], mine[1]), pair(unit, unit), sum[h]);
           }
           tmem_st16(col_s + q * 16, pk);   // (over scores that are in registers or done with)
         };
@@ -1152,12 +1425,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           if (h == 0) {
             tmem_ld_wait();
             scores32(col_s + 96, sb);
-            shape(2, sa);
+            mask(2, sa);
             tmem_ld_wait();
-            shape(3, sb);
+            mask(3, sb);
           }
         }
-        const float2 all = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+        const float2 all = unpair(add2(sum[0], sum[1]));
         l += all.x + all.y;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c.meta_empty[k % kMeta]));
@@ -1182,7 +1455,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         const uint32_t lives = __ballot_sync(0xffffffffu, live);
         const float inv = n > 0 ? inverse<CODED>(l) : 0.f;
         const uint64_t invp = pair(inv, inv);
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
           if (n > 0) {
@@ -1228,7 +1501,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           mine[2 * kTile + rr] = n > 0 ? l : 0.f;
         }
         if (i * kTile + (warp & 3) * 32 < rows) {
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < D / 16; ++q) {
             uint32_t o[16];
             if (n > 0) {
@@ -1302,9 +1575,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 
 namespace {
 
-template <int FMT, int D>
+template <int FMT, int D, bool BOXED>
 int launch_one(const ChunkArgs& a, void* stream) {
-  const auto kernel = chunk_kernel<FMT, D>;
+  const auto kernel = chunk_kernel<FMT, D, BOXED>;
   // (set on every call: the attribute belongs to the current device, like the launch)
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkSmem<D>::bytes);
   int dev = 0, sms = 0;
@@ -1326,7 +1599,8 @@ int launch_one(const ChunkArgs& a, void* stream) {
 
 template <int FMT>
 int launch_format(const ChunkArgs& a, void* stream) {
-  return a.head_dim == 128 ? launch_one<FMT, 128>(a, stream) : launch_one<FMT, 64>(a, stream);
+  if (a.head_dim == 128) return a.box_tokens ? launch_one<FMT, 128, true>(a, stream) : launch_one<FMT, 128, false>(a, stream);
+  return a.box_tokens ? launch_one<FMT, 64, true>(a, stream) : launch_one<FMT, 64, false>(a, stream);
 }
 
 }  // namespace

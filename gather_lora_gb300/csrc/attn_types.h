@@ -79,6 +79,8 @@ struct DecodeArgs {
 };
 
 struct ChunkArgs {
+  TensorMapBytes map_k;      // pages as [num_pages, kv_heads, page_size, head_dim] (heads_inside: heads and slots change places),
+  TensorMapBytes map_v;      // boxes of box_tokens slots (used if that is not 0)
   KvView c;
   const uint16_t* q;
   long long q_stride;
@@ -96,6 +98,8 @@ struct ChunkArgs {
   int window, sinks;
   int head_block;            // query heads of a row tile: the group's, in blocks of at most 128
   int tile_tokens;           // tokens of a row tile: 128 / head_block
+  int box_tokens;            // slots of a page that one TMA copy brings: 8, 16, .. 128; 0: pages are read token by token
+  int heads_inside;
 };
 
 struct PrefillArgs {

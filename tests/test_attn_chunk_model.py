@@ -19,6 +19,7 @@ def const(name):
 
 
 TILE, MOST, GROUP, SNAP = const("kTile"), const("kMostCtas"), const("kJoinGroup"), const("kSnap")
+COST, LEAST = const("kItemCost"), const("kLeast")
 EVERY = 2 ** 31 - 1
 
 
@@ -33,7 +34,8 @@ def span(first, end, window, sinks):
 
 
 def items(seqs, step, subs, window, sinks):
-    """(sequence, sub, pair, first unit, tiles) in the kernel's order, and the units in all."""
+    """(sequence, sub, pair, first unit, tiles) in the kernel's order, and the units in all: an item's are its tiles and COST
+    before them."""
     out, u = [], 0
     for b, (n, length) in enumerate(seqs):
         np = -(-n // step)
@@ -42,13 +44,13 @@ def items(seqs, step, subs, window, sinks):
                 t = span(length - n + x * step, length - n + min((x + 1) * step, n) - 1, window, sinks)[3]
                 if t:
                     out.append((b, sub, x, u, t))
-                    u += t
+                    u += COST + t
     return out, u
 
 
 def plan(every, total, grid):
     """Pieces of each CTA: (item, first tile, tiles), and the number of CTAs with work."""
-    ctas = min(grid, (total + 1) // 2)
+    ctas = min(grid, -(-total // LEAST))
     snap = min(SNAP, total // max(ctas, 1) // 4)
     if not ctas:
         return [], 0, snap
@@ -59,23 +61,23 @@ def plan(every, total, grid):
         if r >= total:
             ends.append(total)
             continue
-        while every[at][3] + every[at][4] <= r:
+        while every[at][3] + COST + every[at][4] <= r:
             at += 1
         s0, tiles = every[at][3:]
-        tile = r - s0
-        ends.append(s0 if tile <= snap else s0 + tiles if tiles - tile <= snap else r)
+        tile = r - s0 - COST
+        ends.append(s0 if tile <= snap else s0 + COST + tiles if tiles - tile <= snap else r)
     pieces = []
     at = 0
     for c in range(ctas):
         mine, u = [], ends[c]
         while u < ends[c + 1]:
-            while every[at][3] + every[at][4] <= u:
+            while every[at][3] + COST + every[at][4] <= u:
                 at += 1
             s0, tiles = every[at][3:]
-            ta = u - s0
-            n = min(tiles, ta + ends[c + 1] - u) - ta
+            ta = max(0, u - s0 - COST)
+            n = min(tiles, ends[c + 1] - s0 - COST) - ta
             mine.append((at, ta, n))
-            u += n
+            u = s0 + COST + ta + n
         pieces.append(mine)
     return pieces, ctas, snap
 
@@ -96,8 +98,8 @@ def check(seqs, step, subs, window, sinks, grid):
         if len(got) == 1:
             continue
         # the CTAs of the item as the kernel works them out, its slots and its counters
-        c0 = -(-((s0 + snap + 1) * ctas) // total) - 1
-        c1 = -(-((s0 + tiles - snap) * ctas) // total) - 1
+        c0 = -(-((s0 + COST + snap + 1) * ctas) // total) - 1
+        c1 = -(-((s0 + COST + tiles - snap) * ctas) // total) - 1
         assert [c for c, _, _ in got] == list(range(c0, c1 + 1)), (got, c0, c1)
         for c, ta, _ in got:
             slot = 2 * c + (ta == 0)
