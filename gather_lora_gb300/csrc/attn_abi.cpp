@@ -342,6 +342,10 @@ int lora_attn_chunk(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* out
   a.window = window;
   a.sinks = sinks;
   row_tiles(q_heads / cache->kv_heads, a.head_block, a.tile_tokens);
+  const uint64_t qd[3] = {static_cast<uint64_t>(a.head_dim), static_cast<uint64_t>(q_heads), static_cast<uint64_t>(total_q)};
+  const uint64_t qs[2] = {static_cast<uint64_t>(a.head_dim) * 2, static_cast<uint64_t>(q_row_stride) * 2};
+  const uint32_t qb[3] = {64, static_cast<uint32_t>(a.head_block), static_cast<uint32_t>(a.tile_tokens)};
+  if (int rc = glora::encode_bf16_map(&a.map_q, q, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B, "q")) return rc;
   if (int rc = page_boxes(cache, a)) return rc;
   const int rc = glora::launch_chunk(a, stream);
   return rc ? cuda_fail(rc, "lora_attn_chunk launch") : ok();

@@ -15,7 +15,7 @@
 // finished by its CTA; otherwise its rows' sums go to the workspace and the last CTA of the item to arrive joins them in CTA
 // order (in two levels beyond kJoinGroup), so the bits never depend on who was last.
 //
-// Roles of a CTA's 16 warps: 0-7 softmax, 8 issues the MMAs, 9 plans and loads Q, 10 loads Q, 11-15 bring K and V. Where the pages'
+// Roles of a CTA's 16 warps: 0-7 softmax, 8 issues the MMAs, 9 plans and loads Q (TMA), 11-15 bring K and V. Where the pages'
 // size and strides allow (BOXED: sizes in eights), warp 11 looks the pages up, a lane four tokens, and issues TMA, a box a page,
 // and warps 12-15 take what has landed over: codes are converted in place in their stage, V that some rows see and others do
 // not is looked through. Otherwise the five warps take groups of 16 tokens in turn by cp.async (BF16) or through registers.
@@ -46,7 +46,7 @@ namespace {
 constexpr unsigned kChunkTimeoutBit = 0x2u;     // LORA_DEV_TIMEOUT
 constexpr int kTile = 128;                      // rows of a tile, tokens of a key tile
 constexpr int kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
-constexpr int kMmaWarp = 8, kPlanWarp = 9, kQWarps = 2, kLoadWarp = 11, kLoaders = 5, kTakers = 4;
+constexpr int kMmaWarp = 8, kPlanWarp = 9, kLoadWarp = 11, kLoaders = 5, kTakers = 4;
 constexpr int kChunkThreads = 512, kChunkWarps = kChunkThreads / 32;
 // Registers a thread: 128 at launch; two warpgroups give away what the softmax's rows of scores need: 2 * 104 + 2 * 152 = 4 * 128.
 constexpr int kHelperRegs = 104, kSoftRegs = 152;
@@ -78,9 +78,8 @@ template <int D>
 struct ChunkShape {
   static constexpr int tile_bytes = kTile * D * 2;              // Q row tile, K tile or V tile
   static constexpr int pairs = D == 128 ? 2 : 4;                // ring: stages of K and V
-  static constexpr int bufs = D == 128 ? 2 : 3;                 // score buffers in tensor memory: what O0 and O1 leave
+  // Tensor memory, all of it (its address is 0): score buffers of the row tiles at columns 0 and 128, O0 and O1 at the end.
   static constexpr uint32_t col_o = 512 - 2 * D;
-  static __device__ __forceinline__ uint32_t buf(int i, int j) { return bufs == 2 ? i : (2u * j + i) % 3u; }
   // Byte of 16-byte chunk c of row r: 64-column blocks, 128-byte swizzle.
   static __device__ __forceinline__ uint32_t at(int r, int c) { return (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
 };
@@ -107,7 +106,7 @@ struct ChunkCtl {
   unsigned long long full[8], empty[8];              // K stages even, V stages odd
   unsigned long long landed[8];                      // (BOXED) full but for the look or the conversion
   unsigned long long meta_full[kMeta], meta_empty[kMeta];
-  unsigned long long q_full, q_empty;
+  unsigned long long q_landed, q_full, q_empty;
   unsigned long long s_full[2][2], p_ready[2][2][2], o_done[2][2];   // [row tile][parity of its key tile] ([half])
   unsigned long long piece_full[kPieces], piece_empty[kPieces];
   unsigned long long drain;
@@ -125,8 +124,7 @@ struct ChunkSmem {
   using Sh = ChunkShape<D>;
   static constexpr int q = 0, ring = 2 * Sh::tile_bytes, stage = ring + 2 * Sh::pairs * Sh::tile_bytes;
   static constexpr int meta = stage + kSoftWarps * kStageBytes;
-  static constexpr int qf = meta + kMeta * static_cast<int>(sizeof(ChunkMeta));
-  static constexpr int ctl = qf + kPieces * 2 * kTile * 4;
+  static constexpr int ctl = meta + kMeta * static_cast<int>(sizeof(ChunkMeta));
   static constexpr int bytes = ctl + static_cast<int>(sizeof(ChunkCtl));
   static_assert(sizeof(ChunkMeta) % 16 == 0 && bytes <= 232448, "shared memory");
   static_assert(kMostSeqs * 8 <= 2 * Sh::pairs * Sh::tile_bytes, "the plan's sums lie in the ring");
@@ -246,6 +244,11 @@ __device__ __forceinline__ uint4 chunk_or_zero(const uint4& x) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n"
+               ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+               : "memory");
+}
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int c0, int c1, int c2, int c3, uint32_t bar) {
   asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n"
                ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
@@ -507,7 +510,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   unsigned char* const base = chunk_smem;
   const uint32_t q_s = smem_u32(chunk_smem) + Sm::q, ring = smem_u32(chunk_smem) + Sm::ring;
   ChunkMeta* const metas = reinterpret_cast<ChunkMeta*>(base + Sm::meta);
-  float* const q_factor = reinterpret_cast<float*>(base + Sm::qf);           // [kPieces][256]
   ChunkCtl& c = *reinterpret_cast<ChunkCtl*>(base + Sm::ctl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -521,7 +523,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       mbar_init(smem_u32(&c.meta_full[s]), BOXED ? 1 : kGroups);
       mbar_init(smem_u32(&c.meta_empty[s]), kSoftWarps + (BOXED && CODED ? kTakers : 0));
     }
-    mbar_init(smem_u32(&c.q_full), kQWarps);
+    mbar_init(smem_u32(&c.q_landed), 1);
+    mbar_init(smem_u32(&c.q_full), CODED ? kSoftWarps : 1);
     mbar_init(smem_u32(&c.q_empty), 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&c.s_full[i >> 1][i & 1]), 1);
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(smem_u32(&c.piece_full[i]), 1);
-      mbar_init(smem_u32(&c.piece_empty[i]), kSoftWarps + 1 + (kQWarps - 1) + kLoaders);
+      mbar_init(smem_u32(&c.piece_empty[i]), kSoftWarps + 1 + kLoaders);
     }
     mbar_init(smem_u32(&c.drain), 1);
     c.failed = 0;
@@ -615,15 +618,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     }
     __syncthreads();
   }
-  const uint32_t tmem = c.tmem;
+  if (tid == 0 && c.tmem != 0) *reinterpret_cast<volatile int*>(&c.failed) = 1;     // (never: all columns are this CTA's)
   const long long total = c.total, ctas = working(total, gridDim.x);
   const bool works = blockIdx.x < ctas;
 
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kHelperRegs));
-  if (warp == kPlanWarp || warp == kPlanWarp + 1) {
+  if (warp == kPlanWarp) {
     // ===================== pieces, and the rows of Q ======================
-    // Warp 9 walks the range; both load half of a piece's rows.
     int b = 0, sub = 0, x = 0, tile = 0, tiles = 0;       // the item under the walk, and its next tile
     long long s0 = 0, u = 0, u1 = 0;                      // its first unit; the walk's position and end
     Seq s{};
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       tile = 0;
       tiles = pair_tiles(p, s, step, x);
     };
-    if (warp == kPlanWarp && works) {
+    if (works) {
       // The item that holds a cut, by prefix sums over its sequence's pairs; 0: this CTA's first unit, 1: the next one's.
       for (int e = 1; e >= 0; --e) {
         const long long r = cut(blockIdx.x + e, total, ctas);
@@ -692,100 +694,65 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     uint32_t loads = 0;
     for (int it = 0;; ++it) {
       const int sl = it % kPieces;
-      if (warp == kPlanWarp) {
-        // (a slot is written again only when all have left it, after a failure too: nobody stops before the last piece)
-        if (it >= kPieces && wait(c, c.piece_empty[sl], ((it / kPieces) - 1) & 1))
-          mbar_wait_limit(smem_u32(&c.piece_empty[sl]), ((it / kPieces) - 1) & 1, kDrainLimitCycles);
-        __syncwarp();
-        const bool go = u < u1 && !__any_sync(0xffffffffu, failed(c));
-        if (lane == 0) {
-          ChunkPiece w;
-          w.valid = go;
-          if (go) {
-            const int t0 = x * step, t1 = min(t0 + step, s.n);
-            w.b = b;
-            w.row0 = s.q0 + t0;
-            w.first = s.len - s.n + t0;
-            w.end = s.len - s.n + t1 - 1;
-            w.kvh = sub / blocks;
-            w.h0 = w.kvh * G + (sub - w.kvh * blocks) * GB;
-            w.heads = min(GB, w.kvh * G + G - w.h0);
-            const Span v = span(p, w.first, w.end);
-            w.low = v.low;
-            w.kept = v.kept;
-            w.skip = v.skip;
-            w.tiles = tiles;
-            w.ta = tile;
-            w.n = tiles_here();
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {                 // tiles that hold a token its last row may see
-              const int last = min(w.first + (i + 1) * TT - 1, w.end), any = w.first + i * TT <= w.end && last >= 0;
-              w.ni[i] = any ? max(0, min(w.ta + w.n, last / kTile + 1 - w.skip) - w.ta) : 0;
-            }
-            w.c0 = static_cast<int>(((s0 + kItemCost + snap + 1) * ctas + total - 1) / total) - 1;
-            w.c1 = static_cast<int>(((s0 + kItemCost + tiles - snap) * ctas + total - 1) / total) - 1;
-          }
-          c.piece[sl] = w;
-          *reinterpret_cast<volatile int*>(&c.bad[sl]) = 0;
-          mbar_arrive(smem_u32(&c.piece_full[sl]));
-        }
-        __syncwarp();
-        if (go) {
-          tile += tiles_here();
-          u = s0 + kItemCost + tile;
-          if (u < u1) next_item();
-        }
-      }
-      wait(c, c.piece_full[sl], (it / kPieces) & 1);
+      // (a slot is written again only when all have left it, after a failure too: nobody stops before the last piece)
+      if (it >= kPieces && wait(c, c.piece_empty[sl], ((it / kPieces) - 1) & 1))
+        mbar_wait_limit(smem_u32(&c.piece_empty[sl]), ((it / kPieces) - 1) & 1, kDrainLimitCycles);
       __syncwarp();
-      const ChunkPiece& w = c.piece[sl];
-      const bool valid = __shfl_sync(0xffffffffu, w.valid, 0);
-      if (valid && !__any_sync(0xffffffffu, failed(c))) {
-        if (loads > 0) wait(c, c.q_empty, (loads - 1) & 1);
-        ++loads;
-        __syncwarp();
-        // Rows of Q: 128 of each row tile, by 16-byte chunks; rows of nobody are zero.
-        constexpr int CH = D / 8, RPI = 32 / CH;          // chunks of a row; rows of an instruction
-        const int ch = lane % CH, tokens = w.end - w.first + 1;
-        const uint16_t* const q = p.q + w.h0 * D + ch * 8;
-        for (int r = (warp - kPlanWarp) * kTile + lane / CH; r < (warp - kPlanWarp + 1) * kTile; r += RPI) {
-          const int i = r >> 7, rr = r & 127, t_in = rr / GB, g = rr - t_in * GB, tok = i * TT + t_in;
-          const bool live = t_in < TT && g < w.heads && tok < tokens;
-          const uint16_t* const from = live ? q + (static_cast<long long>(w.row0) + tok) * p.q_stride + g * D : p.q;
-          copy16(q_s + i * Sh::tile_bytes + Sh::at(rr, ch), from, live);
-        }
-        cp_async_commit();
-        copies_left<0>();
-        if constexpr (CODED) {
-          // BF16 -> f16, each row's largest magnitude at 2^14 .. 2^15, by a power of two
-          for (int r = (warp - kPlanWarp) * kTile + lane / CH; r < (warp - kPlanWarp + 1) * kTile; r += RPI) {
-            const uint32_t at = q_s + (r >> 7) * Sh::tile_bytes + Sh::at(r & 127, ch);
-            const uint4 v = lds128(at);
-            const uint32_t m2 = abs_max2(0, v);
-            uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+      const bool go = u < u1 && !__any_sync(0xffffffffu, failed(c));
+      if (lane == 0) {
+        ChunkPiece w;
+        w.valid = go;
+        if (go) {
+          const int t0 = x * step, t1 = min(t0 + step, s.n);
+          w.b = b;
+          w.row0 = s.q0 + t0;
+          w.first = s.len - s.n + t0;
+          w.end = s.len - s.n + t1 - 1;
+          w.kvh = sub / blocks;
+          w.h0 = w.kvh * G + (sub - w.kvh * blocks) * GB;
+          w.heads = min(GB, w.kvh * G + G - w.h0);
+          const Span v = span(p, w.first, w.end);
+          w.low = v.low;
+          w.kept = v.kept;
+          w.skip = v.skip;
+          w.tiles = tiles;
+          w.ta = tile;
+          w.n = tiles_here();
 #pragma unroll
-            for (int o = CH / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int e = static_cast<int>(top >> 7) - 127;
-            const int up = top == 0 || e == 128 ? 0 : max(-126, min(126, 14 - e));
-            const float f = __int_as_float((127 + up) << 23);
-            const uint32_t x4[4] = {v.x, v.y, v.z, v.w};
-            uint32_t h[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = pack_f16x2(__uint_as_float(x4[j] << 16) * f, __uint_as_float(x4[j] & 0xffff0000u) * f);
-            sts128(at, make_uint4(h[0], h[1], h[2], h[3]));
-            if (ch == 0) q_factor[sl * 2 * kTile + r] = __int_as_float((127 - up) << 23);
+          for (int i = 0; i < 2; ++i) {                 // tiles that hold a token its last row may see
+            const int last = min(w.first + (i + 1) * TT - 1, w.end), any = w.first + i * TT <= w.end && last >= 0;
+            w.ni[i] = any ? max(0, min(w.ta + w.n, last / kTile + 1 - w.skip) - w.ta) : 0;
           }
+          w.c0 = static_cast<int>(((s0 + kItemCost + snap + 1) * ctas + total - 1) / total) - 1;
+          w.c1 = static_cast<int>(((s0 + kItemCost + tiles - snap) * ctas + total - 1) / total) - 1;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&c.q_full));
+        c.piece[sl] = w;
+        *reinterpret_cast<volatile int*>(&c.bad[sl]) = 0;
+        mbar_arrive(smem_u32(&c.piece_full[sl]));
       }
-      if (warp != kPlanWarp) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&c.piece_empty[sl]));
+      __syncwarp();
+      if (!go) break;
+      const int t0 = x * step, tokens = min(step, s.n - t0), row0 = s.q0 + t0, kvh = sub / blocks, h0 = kvh * G + (sub - kvh * blocks) * GB;
+      tile += tiles_here();
+      u = s0 + kItemCost + tile;
+      if (u < u1) next_item();
+      // Q: rows of other sequences or heads that a box brings along are nobody's.
+      if (loads > 0) wait(c, c.q_empty, (loads - 1) & 1);
+      ++loads;
+      __syncwarp();
+      if (lane == 0 && !failed(c)) {
+        const uint32_t bar = smem_u32(CODED ? &c.q_landed : &c.q_full);
+        const int both = tokens > TT ? 2 : 1;
+        mbar_arrive_expect_tx(bar, both * (D / 64) * GB * TT * 128);
+        for (int y = 0; y < both * (D / 64); ++y) {
+          const int i = y / (D / 64), a = y % (D / 64);
+          tma_load_3d(q_s + i * Sh::tile_bytes + a * (kTile * 128), &p.map_q, a * 64, h0, row0 + i * TT, bar);
+        }
       }
-      if (!valid) break;
+      __syncwarp();
     }
+    if (lane == 0 && loads > 0 && failed(c)) mbar_wait_limit(smem_u32(CODED ? &c.q_landed : &c.q_full), (loads - 1) & 1, kDrainLimitCycles);
+    __syncwarp();
   } else if (BOXED && warp == kLoadWarp) {
     // ==================== pages looked up, TMA of K and V ====================
     // A lane has 4 consecutive tokens of a tile (of one page: boxes are of 8 slots or more); the first lane of a box issues it. A
@@ -1167,113 +1134,104 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     copies_left<0>();
   } else if (warp == kMmaWarp) {
     // ============================ MMA issue ===============================
-    // The whole warp takes every step, one elected lane issues. Row tile i's scores of key tile j + 1 go out
-    // after its P V of key tile j when there are two score buffers (one per row tile), so a warpgroup waits for
-    // both; with three buffers they go out half a step earlier and are there when it is done with its weights.
+    // The warp takes every step together, lane 0 issues. The steps are compiled for each stage of the ring, so that descriptors and
+    // addresses are constants: with run-time ones an MMA took 36 instructions and the warp was busy all the time. Step j, row
+    // tile after row tile: P V of key tile j, then the scores of key tile j + 1.
     constexpr uint32_t type = CODED ? (1u << 7) | (1u << 10) : 0u;     // f16 instead of BF16
     constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile) & ~type;
     constexpr uint32_t id_o = (idesc_bf16_f32(kTile, D) & ~type) | (1u << 16);   // V: MN-major
-    uint32_t kt = 0, st[2] = {0, 0}, pt[2] = {0, 0};   // key tiles of the pieces before; by row tile: scores, P V
-    int loads = 0, n0 = 0, n1 = 0, n = 0;
+    uint32_t kt = 0, pt[2] = {0, 0}, st[2] = {0, 0};   // key tiles of the pieces before; by row tile: P V, scores so far
+    int loads = 0;
     bool dead = false;
-    auto scores = [&](auto row_tile, int j) {          // S_i = Q_i K_j^T
-      constexpr int i = decltype(row_tile)::value;
-      const uint32_t k = kt + j, ks = 2 * (k % NP);
-      if (Sh::bufs == 3 && (i == 0 || j >= n0)) {
-        dead |= wait(c, c.full[ks], (k / NP) & 1);        // the key tile's first use
-        __syncwarp();
-        tc_fence_after();
-      }
-      const uint64_t qa = smem_desc(q_s + i * Sh::tile_bytes, 1024, Swz::k128);
-      const uint64_t ka = smem_desc(ring + ks * Sh::tile_bytes, 1024, Swz::k128);
-      const uint32_t to = tmem + Sh::buf(i, j) * kTile;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {            // (descriptors hold addresses in 16-byte units)
-        const uint64_t o = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
-        umma_bf16_warp(to, qa + o, ka + o, id_s, kk != 0);
-      }
-      umma_commit_warp(smem_u32(&c.s_full[i][st[i] & 1]));
-      ++st[i];
-    };
-    // After the last use of K tile j.
-    auto keys_done = [&](int j) {
-      umma_commit_warp(smem_u32(&c.empty[2 * ((kt + j) % NP)]));
-      if (j + 1 == n) umma_commit_warp(smem_u32(&c.q_empty));
-    };
-    auto values = [&](auto row_tile, int j, uint32_t vs) {   // O_i (+)= P_i V_j, as its halves of the keys come
-      constexpr int i = decltype(row_tile)::value;
-      const uint64_t va = smem_desc_mn128(ring + vs * Sh::tile_bytes, kTile * 128, 1024);
-      const uint32_t from = tmem + Sh::buf(i, j) * kTile;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (Sh::bufs == 2 || half == 0) {
-          dead |= wait(c, c.p_ready[i][pt[i] & 1][Sh::bufs == 2 ? half : 1], (pt[i] >> 1) & 1);
-          __syncwarp();
-          tc_fence_after();
-        }
-#pragma unroll
-        for (int kk = half * (kTile / 32); kk < (half + 1) * (kTile / 32); ++kk)
-          umma_bf16_ts_warp(tmem + Sh::col_o + i * D, from + kk * 8, va + kk * (2048 >> 4), id_o, kk != 0 || j != 0);
-      }
-      umma_commit_warp(smem_u32(&c.o_done[i][pt[i] & 1]));
-      ++pt[i];
-    };
-    constexpr std::integral_constant<int, 0> r0{};
-    constexpr std::integral_constant<int, 1> r1{};
     for (int it = 0;; ++it) {
       const int sl = it % kPieces;
       wait(c, c.piece_full[sl], (it / kPieces) & 1);
       __syncwarp();
       const bool valid = __shfl_sync(0xffffffffu, c.piece[sl].valid, 0);
-      n0 = __shfl_sync(0xffffffffu, c.piece[sl].ni[0], 0);
-      n1 = __shfl_sync(0xffffffffu, c.piece[sl].ni[1], 0);
-      n = __shfl_sync(0xffffffffu, c.piece[sl].n, 0);
+      const int n0 = __shfl_sync(0xffffffffu, c.piece[sl].ni[0], 0), n1 = __shfl_sync(0xffffffffu, c.piece[sl].ni[1], 0);
+      const int n = __shfl_sync(0xffffffffu, c.piece[sl].n, 0);
       if (lane == 0) mbar_arrive(smem_u32(&c.piece_empty[sl]));
       __syncwarp();
       if (!valid) break;
       dead |= wait(c, c.q_full, loads & 1);
       ++loads;
       if (__any_sync(0xffffffffu, dead)) continue;
-      // Scores of key tile j for both row tiles, in the order of use, with the release of K behind the last one.
-      auto keys = [&](auto row_tile, int j) {
-        constexpr int i = decltype(row_tile)::value;
-        scores(row_tile, j);
-        if (i == 1 || j >= n1) keys_done(j);
-      };
-      if constexpr (Sh::bufs == 2) {
-        dead |= wait(c, c.full[2 * (kt % NP)], (kt / NP) & 1);
-        __syncwarp();
-        tc_fence_after();
-      }
-      if (n0 > 0) keys(r0, 0);
-      if (n1 > 0) keys(r1, 0);
-      if (Sh::bufs == 3 && n0 > 1) keys(r0, 1);
-      for (int j = 0; j < n; ++j) {
-        const uint32_t k = kt + j, vs = 2 * (k % NP) + 1;
-        dead |= wait(c, c.full[vs], (k / NP) & 1);
-        if (Sh::bufs == 2 && j + 1 < n) dead |= wait(c, c.full[2 * ((k + 1) % NP)], ((k + 1) / NP) & 1);
-        __syncwarp();
-        tc_fence_after();
-        if (j < n0) values(r0, j, vs);
-        if (Sh::bufs == 2 ? j + 1 < n0 : j + 1 < n1) {
-          if constexpr (Sh::bufs == 2) keys(r0, j + 1); else keys(r1, j + 1);
-        }
-        if (j < n1) values(r1, j, vs);
-        umma_commit_warp(smem_u32(&c.empty[vs]));
-        if (Sh::bufs == 2 ? j + 1 < n1 : j + 2 < n0) {
-          if constexpr (Sh::bufs == 2) keys(r1, j + 1); else keys(r0, j + 2);
-        }
-        if (j >= n0 && j >= n1) {          // (a tile that no row of the piece needs: its K is let go here)
-          if constexpr (Sh::bufs == 3) dead |= wait(c, c.full[vs - 1], (k / NP) & 1);
-          keys_done(j);
-        }
+      for (int j = -1; j < n; ++j) {
+        auto step_at = [&](auto slot) {
+          constexpr int S = decltype(slot)::value, N = (S + 1) % NP;       // ring slots of key tiles j and j + 1
+          const uint32_t k = kt + j;
+          auto values = [&](auto row_tile) {           // O_i (+)= P_i V_j, as its halves of the keys come
+            constexpr int i = decltype(row_tile)::value;
+            const uint64_t va = smem_desc_mn128(ring + (2 * S + 1) * Sh::tile_bytes, kTile * 128, 1024);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              dead |= wait(c, c.p_ready[i][pt[i] & 1][half], (pt[i] >> 1) & 1);
+              __syncwarp();
+              tc_fence_after();
+              const uint32_t done = smem_u32(&c.o_done[i][pt[i] & 1]);
+              if (elect_one()) {
+#pragma unroll
+                for (int kk = half * (kTile / 32); kk < (half + 1) * (kTile / 32); ++kk)
+                  umma_bf16_ts(Sh::col_o + i * D, i * kTile + kk * 8, va + kk * (2048 >> 4), id_o, kk != 0 || j != 0);
+                if (half) umma_commit(done);
+              }
+              __syncwarp();
+            }
+            ++pt[i];
+          };
+          auto scores = [&](auto row_tile, bool release) {   // S_i = Q_i K_{j+1}^T; release: K's last use
+            constexpr int i = decltype(row_tile)::value;
+            const uint64_t qa = smem_desc(q_s + i * Sh::tile_bytes, 1024, Swz::k128), ka = smem_desc(ring + 2 * N * Sh::tile_bytes, 1024, Swz::k128);
+            const uint32_t done = smem_u32(&c.s_full[i][st[i] & 1]);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {            // (descriptors hold addresses in 16-byte units)
+                constexpr uint64_t atom = (kTile * 128) >> 4;
+                const uint64_t o = (kk >> 2) * atom + (kk & 3) * 2;
+                umma_bf16(i * kTile, qa + o, ka + o, id_s, kk != 0);
+              }
+              umma_commit(done);
+              if (release) {
+                umma_commit(smem_u32(&c.empty[2 * N]));
+                if (j + 2 == n) umma_commit(smem_u32(&c.q_empty));
+              }
+            }
+            __syncwarp();
+            ++st[i];
+          };
+          constexpr std::integral_constant<int, 0> r0{};
+          constexpr std::integral_constant<int, 1> r1{};
+          if (j >= 0) dead |= wait(c, c.full[2 * S + 1], (k / NP) & 1);
+          if (j + 1 < n) dead |= wait(c, c.full[2 * N], ((k + 1) / NP) & 1);
+          __syncwarp();
+          tc_fence_after();
+          if (j >= 0 && j < n0) values(r0);
+          if (j + 1 < n0) scores(r0, j + 1 >= n1);
+          if (j >= 0 && j < n1) values(r1);
+          if (j >= 0 && elect_one()) umma_commit(smem_u32(&c.empty[2 * S + 1]));
+          __syncwarp();
+          if (j + 1 < n1) scores(r1, true);
+          if (j + 1 < n && j + 1 >= n0 && j + 1 >= n1) {     // (a tile that no row of the piece needs)
+            if (elect_one()) {
+              umma_commit(smem_u32(&c.empty[2 * N]));
+              if (j + 2 == n) umma_commit(smem_u32(&c.q_empty));
+            }
+            __syncwarp();
+          }
+        };
+        const uint32_t slot = (kt + j) % NP;
+        if (slot == 0) step_at(std::integral_constant<int, 0>{});
+        else if (slot == 1) step_at(std::integral_constant<int, 1>{});
+        else if (NP > 2 && slot == 2) step_at(std::integral_constant<int, 2 % NP>{});
+        else if (NP > 2) step_at(std::integral_constant<int, 3 % NP>{});
         if (__any_sync(0xffffffffu, dead)) break;
       }
       kt += n;
     }
     if (failed(c)) {                     // let the MMAs in flight end
       __syncwarp();
-      umma_commit_warp(smem_u32(&c.drain));
+      if (elect_one()) umma_commit(smem_u32(&c.drain));
+      __syncwarp();
       mbar_wait_limit(smem_u32(&c.drain), 0, kDrainLimitCycles);
     }
     __syncwarp();
@@ -1282,8 +1240,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
     // ============================= softmax ================================
     const int i = warp >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t col_o = lane_base + Sh::col_o + i * D;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t col_s = lane_base + i * kTile, col_o = lane_base + Sh::col_o + i * D;
     const float sl2 = p.scale * kLog2e, grow = CODED ? kGrow : kGrow / sl2;
     const int t_in = row / GB, g = row - t_in * GB;
     const uint32_t stage = smem_u32(chunk_smem) + Sm::stage + warp * kStageBytes;
@@ -1298,18 +1256,41 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       const int pos = w.first + i * TT + t_in, n = w.ni[i];
       const bool live = t_in < TT && g < w.heads && pos <= w.end;
       float qf = 1.f;                      // 8 bits: Q was divided by it
-      uint32_t buf = Sh::buf(i, 0);
+      if constexpr (CODED) {               // Q from BF16 to f16, the row's largest magnitude at 2^14 .. 2^15, by a power of two
+        wait(c, c.q_landed, it & 1);
+        __syncwarp();
+        if (i == 0 || w.end - w.first + 1 > TT) {
+          const uint32_t at = q_s + i * Sh::tile_bytes;
+          uint32_t m2 = 0;
+#pragma unroll 4
+          for (int ch = 0; ch < D / 8; ++ch) m2 = abs_max2(m2, lds128(at + Sh::at(row, ch)));
+          const uint32_t biggest = max(m2 & 0xffffu, m2 >> 16);
+          const int e = static_cast<int>(biggest >> 7) - 127;
+          const int up = biggest == 0 || e == 128 ? 0 : max(-126, min(126, 14 - e));
+          const float f = exp2_int(up);
+          qf = exp2_int(-up);
+#pragma unroll 2
+          for (int ch = 0; ch < D / 8; ++ch) {
+            const uint4 v = lds128(at + Sh::at(row, ch));
+            const uint32_t x4[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) h[y] = pack_f16x2(__uint_as_float(x4[y] << 16) * f, __uint_as_float(x4[y] & 0xffff0000u) * f);
+            sts128(at + Sh::at(row, ch), make_uint4(h[0], h[1], h[2], h[3]));
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.q_full));
+      }
       float ref = -INFINITY, l = 0.f;      // exponents are relative to ref (BF16: in units of raw scores, less kGrow)
       for (int j = 0; j < n; ++j, ++t) {
-        const uint32_t col_s = lane_base + buf * kTile;
-        if constexpr (Sh::bufs == 3) buf = buf == 0 ? 2 : buf - 1;   // (2 j + i) mod 3
         const uint32_t k = kt + j;
         const ChunkMeta& m = metas[k % kMeta];
         dead |= wait(c, c.meta_full[k % kMeta], (k / kMeta) & 1);
         dead |= wait(c, c.s_full[i][t & 1], (t >> 1) & 1);
         __syncwarp();
         tc_fence_after();
-        if (CODED && j == 0) qf = q_factor[sl * 2 * kTile + i * kTile + row];
         // What the row sees of the tile.
         const int tile = w.ta + j, t0 = (tile < w.kept ? tile : tile + w.skip) * kTile;
         const uint4 there = *reinterpret_cast<const uint4*>(m.live);
@@ -1373,7 +1354,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           const float f = nr == -INFINITY ? 1.f : exp2_fast(CODED ? ref - nr : (ref - nr) * sl2);
           ref = nr;
           l *= f;
-          // (with three score buffers the P V before may still run)
           dead |= wait(c, c.o_done[i][(t - 1) & 1], ((t - 1) >> 1) & 1);
           __syncwarp();
           tc_fence_after();
@@ -1416,12 +1396,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           weights(2 * h, sa);
           if (h == 0) scores32(col_s + 64, sa);
           weights(2 * h + 1, sb);
-          if (Sh::bufs == 2 || h == 1) {   // (with three score buffers nothing of this warpgroup waits for P V: one hand-over)
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&c.p_ready[i][t & 1][h]));
-          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&c.p_ready[i][t & 1][h]));
           if (h == 0) {
             tmem_ld_wait();
             scores32(col_s + 96, sb);
@@ -1569,7 +1547,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   if (tid == 0 && failed(c)) atomicOr(&g_chunk_status, kChunkTimeoutBit);
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(0, 512);
   }
 }
 

@@ -79,6 +79,7 @@ struct DecodeArgs {
 };
 
 struct ChunkArgs {
+  TensorMapBytes map_q;      // q as [total_q, q_heads, head_dim], box {64, head_block, tile_tokens}, 128-byte swizzle
   TensorMapBytes map_k;      // pages as [num_pages, kv_heads, page_size, head_dim] (heads_inside: heads and slots change places),
   TensorMapBytes map_v;      // boxes of box_tokens slots (used if that is not 0)
   KvView c;
