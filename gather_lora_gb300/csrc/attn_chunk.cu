@@ -48,8 +48,6 @@ constexpr int kTile = 128;                      // rows of a tile, tokens of a k
 constexpr int kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
 constexpr int kMmaWarp = 8, kPlanWarp = 9, kLoadWarp = 11, kLoaders = 5, kTakers = 4;
 constexpr int kChunkThreads = 512, kChunkWarps = kChunkThreads / 32;
-// Registers a thread: 128 at launch; two warpgroups give away what the softmax's rows of scores need: 2 * 104 + 2 * 152 = 4 * 128.
-constexpr int kHelperRegs = 104, kSoftRegs = 152;
 constexpr int kPieces = 4;                      // depth of the ring of pieces
 constexpr int kMeta = 4;                        // depth of the ring of tokens' masks and scales
 constexpr int kGroup = 16, kGroups = kTile / kGroup;   // tokens of a loader's group; groups of a tile
@@ -253,23 +251,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int c
   asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n"
                ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
                : "memory");
-}
-
-// 32 columns of scores (valid after tmem_ld_wait), in two blocks: register blocks of 16 leave the allocator room where one of 32
-// made it spill.
-__device__ __forceinline__ void scores32(uint32_t at, uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(at)
-      : "memory");
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      : "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-      : "r"(at + 16)
-      : "memory");
 }
 
 // ---- the plan ---------------------------------------------------------------
@@ -623,7 +604,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   const bool works = blockIdx.x < ctas;
 
   if (warp >= kSoftWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kHelperRegs));
   if (warp == kPlanWarp) {
     // ===================== pieces, and the rows of Q ======================
     int b = 0, sub = 0, x = 0, tile = 0, tiles = 0;       // the item under the walk, and its next tile
@@ -1237,7 +1217,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     __syncwarp();
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
     // ============================= softmax ================================
     const int i = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -1297,18 +1276,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         const int hi = pos - t0, lo = hi - min(p.window - 1, max(pos, 0)), sk = p.sinks - t0;    // sees x <= hi with x >= lo or x < sk
         const bool whole = hi >= kTile - 1 && (lo <= 0 || sk >= kTile) && (there.x & there.y & there.z & there.w) == 0xffffffffu;
         const bool cuts = __any_sync(0xffffffffu, live && !whole);
-        // A quarter of the scores at a time, the next one on its way from tensor memory; what is not seen at -infinity. (Loops over
-        // the halves, not unrolled: see wait() on code size.)
-        uint32_t sa[32], sb[32];
-        auto mask = [&](int q, uint32_t (&s)[32]) {
+        // 16 columns of the scores at a time, the next 16 on their way from tensor memory; what is not seen at -infinity. The loops are
+        // not unrolled further: the roles' loops share the instruction caches, and unrolled once more these took 1.25 times as long.
+        uint32_t sa[16], sb[16];
+        auto mask = [&](int g16, uint32_t (&s)[16]) {
           if (!cuts) return;
-          auto below = [&](int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1; };   // bits under x
-          const uint32_t see = m.live[q] & below(min(hi, kTile) + 1 - q * 32) & (~below(lo - q * 32) | below(sk - q * 32));
+          auto below = [&](int x) { return x <= 0 ? 0u : x >= 16 ? 0xffffu : (1u << x) - 1; };   // bits under x
+          const int at = g16 * 16;
+          const uint32_t see = reinterpret_cast<const uint16_t*>(m.live)[g16] & below(min(hi, kTile) + 1 - at) & (~below(lo - at) | below(sk - at));
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
+          for (int e = 0; e < 16; ++e)
             if (!((see >> e) & 1)) s[e] = 0xff800000u;
         };
-        // Factor of the scores and what is added to them (8 bits: of 16 columns; the factor is never 0, -infinity stays itself).
+        // Factor of the scores and what is added to them (8 bits: the group's; the factor is never 0, -infinity stays itself).
         auto factor = [&](int g16, float& f, float& add, float& unit) {
           if constexpr (CODED) {
             const float4 g4 = m.group[g16];
@@ -1317,35 +1297,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             unit = g4.z;
           }
         };
-        auto most = [&](int q, const uint32_t (&s)[32], float top) {
-          float a[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            a[h] = __uint_as_float(s[16 * h]);
-#pragma unroll
-            for (int e = 1; e < 15; e += 2) a[h] = max3(a[h], __uint_as_float(s[16 * h + e]), __uint_as_float(s[16 * h + e + 1]));
-            a[h] = fmaxf(a[h], __uint_as_float(s[16 * h + 15]));
-            if constexpr (CODED) {
-              float f, add, unit;
-              factor(2 * q + h, f, add, unit);
-              a[h] = __fmaf_rn(a[h], f, add);
-            }
-          }
-          return max3(top, a[0], a[1]);
-        };
-        // The maximum over all four (the first two stay), then their weights.
         float top = -INFINITY;
-        scores32(col_s + 96, sb);
+        auto most = [&](int g16, uint32_t (&s)[16]) {
+          mask(g16, s);
+          float a = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[15])), b = __uint_as_float(s[1]);
+#pragma unroll
+          for (int e = 2; e < 14; e += 4) {
+            a = max3(a, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+            b = max3(b, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+          }
+          a = max3(a, b, __uint_as_float(s[14]));
+          if constexpr (CODED) {
+            float f, add, unit;
+            factor(g16, f, add, unit);
+            a = __fmaf_rn(a, f, add);
+          }
+          top = fmaxf(top, a);
+        };
+        tmem_ld16(col_s, sa);
 #pragma unroll 1
-        for (int h = 1; h >= 0; --h) {
+        for (int g16 = 0; g16 < kGroups; g16 += 2) {
           tmem_ld_wait();
-          scores32(col_s + h * 64, sa);
-          mask(2 * h + 1, sb);
-          top = most(2 * h + 1, sb, top);
+          tmem_ld16(col_s + g16 * 16 + 16, sb);
+          most(g16, sa);
           tmem_ld_wait();
-          if (h) scores32(col_s + 32, sb);
-          mask(2 * h, sa);
-          top = most(2 * h, sa, top);
+          tmem_ld16(col_s + (g16 * 16 + 32) % kTile, sa);    // (at the end: the first 16 again)
+          most(g16 + 1, sb);
         }
         if (j == 0) {
           ref = top;
@@ -1370,42 +1347,39 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         // (nothing seen: every weight is 0)
         const float off = ref == -INFINITY ? 0.f : CODED ? kTop - ref : __fmaf_rn(-ref, sl2, -kGrow);
         uint64_t sum[2] = {0, 0};
-        auto weights = [&](int q, const uint32_t (&s)[32]) {
-          uint32_t pk[16];
+        uint32_t pk[16];                   // 32 columns
+        auto weights = [&](int g16, auto which, uint32_t (&s)[16]) {
+          constexpr int h = decltype(which)::value;
+          mask(g16, s);
+          float f = sl2, add = 0.f, unit = 0.f;
+          factor(g16, f, add, unit);
+          add += off;
+          const uint64_t fp = pair(f, f), addp = pair(add, add);
+          uint64_t mine[2] = {0, 0};       // 8 bits: the group's sum
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float f = sl2, add = 0.f, unit = 0.f;
-            factor(2 * q + h, f, add, unit);
-            add += off;
-            const uint64_t fp = pair(f, f), addp = pair(add, add);
-            uint64_t mine[2] = {0, 0};     // 8 bits: the group's sum
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 x = unpair(fma2(pair(__uint_as_float(s[16 * h + 2 * e]), __uint_as_float(s[16 * h + 2 * e + 1])), fp, addp));
-              const float w0 = exp2_fast(x.x), w1 = exp2_fast(x.y);
-              uint64_t& to = CODED ? mine[e & 1] : sum[e & 1];
-              to = add2(to, pair(w0, w1));
-              pk[8 * h + e] = CODED ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
-            }
-            if constexpr (CODED) sum[h] = fma2(add2(mine[0], mine[1]), pair(unit, unit), sum[h]);
+          for (int e = 0; e < 8; ++e) {
+            const float2 x = unpair(fma2(pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), fp, addp));
+            const float w0 = exp2_fast(x.x), w1 = exp2_fast(x.y);
+            uint64_t& to = CODED ? mine[e & 1] : sum[e & 1];
+            to = add2(to, pair(w0, w1));
+            pk[8 * h + e] = CODED ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
           }
-          tmem_st16(col_s + q * 16, pk);   // (over scores that are in registers or done with)
+          if constexpr (CODED) sum[h] = fma2(add2(mine[0], mine[1]), pair(unit, unit), sum[h]);
         };
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          weights(2 * h, sa);
-          if (h == 0) scores32(col_s + 64, sa);
-          weights(2 * h + 1, sb);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&c.p_ready[i][t & 1][h]));
-          if (h == 0) {
-            tmem_ld_wait();
-            scores32(col_s + 96, sb);
-            mask(2, sa);
-            tmem_ld_wait();
-            mask(3, sb);
+        for (int g16 = 0; g16 < kGroups; g16 += 2) {
+          tmem_ld_wait();
+          tmem_ld16(col_s + g16 * 16 + 16, sb);
+          weights(g16, std::integral_constant<int, 0>{}, sa);
+          tmem_ld_wait();
+          if (g16 + 2 < kGroups) tmem_ld16(col_s + g16 * 16 + 32, sa);
+          weights(g16 + 1, std::integral_constant<int, 1>{}, sb);
+          tmem_st16(col_s + g16 * 8, pk);  // (over scores that are in registers or done with)
+          if (g16 & 2) {                   // half of the tile
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c.p_ready[i][t & 1][g16 >> 2]));
           }
         }
         const float2 all = unpair(add2(sum[0], sum[1]));
