@@ -84,8 +84,11 @@ struct ChunkShape {
 
 struct ChunkMeta {           // of a key tile
   uint32_t live[4];          // tokens that are there and that some row sees
-  float4 group[kGroups];     // 8 bits, of 16 tokens: scale log2(e) times K's power of two, log2 of V's, kSumUnit over V's
-  uint32_t mk[kTile];        // (BOXED) a token's K scale over the group's, as two f16 whose sum it is
+  // 8 bits, of 16 tokens: scale log2(e) times K's power of two, log2 of V's, kSumUnit over V's, and whether the group's scales
+  // are taken token by token instead (ab)
+  float4 group[kGroups];
+  float2 ab[kTile];          // scale log2(e) times the token's K scale, log2 of its V scale
+  uint32_t mk[kTile];        // (BOXED) what K's codes are multiplied with: the token's scale over the group's, as two f16 whose sum it is
   uint32_t mv[kTile];        // V's
 };
 
@@ -209,15 +212,27 @@ __device__ __forceinline__ int group_exponent(float most) {
 }
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + e) << 23); }
 __device__ __forceinline__ float finite_magnitude(float s) { return fabsf(s) < INFINITY ? fabsf(s) : 0.f; }
+// Scales of 16 tokens differ too much for one power of two.
+constexpr float kWide = 4096.f;
+__device__ __forceinline__ bool wide(float most, float least) { return most > least * kWide; }
 // What the softmax needs of a group. (One whose scales are all 0 only counts in the sums: 2^-64 keeps it from raising the reference.)
 template <int FMT>
-__device__ __forceinline__ float4 group_of(float most_k, float most_v, float sl2) {
+__device__ __forceinline__ float4 group_of(float most_k, float most_v, float sl2, bool exact) {
   const int ev = most_v == 0.f ? -64 : group_exponent<FMT>(most_v);
-  return make_float4(most_k == 0.f ? sl2 : exp2_int(group_exponent<FMT>(most_k)) * sl2, static_cast<float>(ev), kSumUnit * exp2_int(-ev), 0.f);
+  return make_float4(most_k == 0.f ? sl2 : exp2_int(group_exponent<FMT>(most_k)) * sl2, static_cast<float>(ev), kSumUnit * exp2_int(-ev), exact);
 }
+// What the codes of a token with scale s are multiplied with.
 template <int FMT>
 __device__ __forceinline__ uint32_t scale_of(float s, float most) {
   return split_f16(most == 0.f && s == s ? 0.f : s * exp2_int(-group_exponent<FMT>(most == 0.f ? 1.f : most)));
+}
+// Token by token: codes of K as they are, of V with the scale's sign (0: they only count in the sum).
+constexpr uint32_t kOne = 0x3c00u;
+__device__ __forceinline__ uint32_t sign_of(float s) { return s == 0.f ? 0u : s < 0.f ? 0xbc00u : kOne; }
+// A V scale of 0 is 2^-64 to the weights (see above); below 2^-110, under what lora_kv_write stores, it is 2^-110.
+__device__ __forceinline__ float2 scales_of(float k, float v, float sl2) {
+  const float mag = v == 0.f ? 5.421010862427522e-20f : fmaxf(fabsf(v), 7.703719777548943e-34f);
+  return make_float2(k * sl2, log2f(v != v ? v : mag));     // (fmaxf drops NaN)
 }
 
 // Chunks of V: whether all is finite, and with what is not set to zero.
@@ -808,22 +823,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         for (int o = 1; o < 8; o <<= 1) live |= __shfl_xor_sync(0xffffffffu, live, o);
         if ((lane & 7) == 0) m.live[lane >> 3] = live;
         if constexpr (CODED) {
-          float mk = 0.f, mv = 0.f;
+          float mk = 0.f, mv = 0.f, lk = INFINITY, lv = INFINITY;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            mk = fmaxf(mk, finite_magnitude(sk[x]));
-            mv = fmaxf(mv, finite_magnitude(sv[x]));
+            const float fk = finite_magnitude(sk[x]), fv = finite_magnitude(sv[x]);
+            mk = fmaxf(mk, fk);
+            mv = fmaxf(mv, fv);
+            lk = fk == 0.f ? lk : fminf(lk, fk);
+            lv = fv == 0.f ? lv : fminf(lv, fv);
           }
 #pragma unroll
           for (int o = 1; o < 4; o <<= 1) {
             mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
             mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+            lk = fminf(lk, __shfl_xor_sync(0xffffffffu, lk, o));
+            lv = fminf(lv, __shfl_xor_sync(0xffffffffu, lv, o));
           }
-          if ((lane & 3) == 0) m.group[lane >> 2] = group_of<FMT>(mk, mv, sl2);
+          const int tg = first_token(j) + (lane & ~3) * 4;
+          const bool exact = wide(mk, lk) || wide(mv, lv) || !(tg + kGroup - 1 <= w.first && (tg > w.end - p.window || tg + kGroup - 1 < p.sinks));
+          if ((lane & 3) == 0) m.group[lane >> 2] = group_of<FMT>(mk, mv, sl2, exact);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            m.mk[lane * 4 + x] = scale_of<FMT>(sk[x], mk);
-            m.mv[lane * 4 + x] = scale_of<FMT>(sv[x], mv);
+            if (exact) m.ab[lane * 4 + x] = scales_of(sk[x], sv[x], sl2);
+            m.mk[lane * 4 + x] = exact ? kOne : scale_of<FMT>(sk[x], mk);
+            m.mv[lane * 4 + x] = exact ? sign_of(sv[x]) : scale_of<FMT>(sv[x], mv);
           }
         }
         __syncwarp();
@@ -1038,7 +1061,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       } else {
         // A group's codes are loaded while the one before it is converted, its pages looked up one ahead of that.
         uint4 cur[NI], ahead[NI];
-        float ks = 0.f, vs = 0.f;        // scales of the group loaded last (K groups: of both; V groups: V's)
+        float ks = 0.f, vs = 0.f;        // scales of the group loaded last (of both: K's and V's groups decide alike)
         bool there = false;
         int slot = 0, page = g0 < groups ? look_up(g0, slot) : -1;
         auto fetch = [&](int g) {        // the group whose page was looked up
@@ -1048,7 +1071,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           ks = vs = 0.f;
           if (there) {
             const long long si = scale_index(p.c, page, w.kvh, slot);
-            if (keys) ks = __ldg(p.c.ks + si);
+            ks = __ldg(p.c.ks + si);
             vs = __ldg(p.c.vs + si);
           }
           const unsigned char* const from = keys ? p.c.k : p.c.v;
@@ -1076,18 +1099,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           const int r0 = (g % kGroups) * kGroup, t0 = token0(g);
           // The group's powers of two (lanes 16 .. 31 as lanes 0 .. 15), a token's scale over them.
           float most_k = finite_magnitude(k_scale), most_v = finite_magnitude(v_scale);
+          float least_k = most_k == 0.f ? INFINITY : most_k, least_v = most_v == 0.f ? INFINITY : most_v;
 #pragma unroll
           for (int o = 1; o < kGroup; o <<= 1) {
             most_k = fmaxf(most_k, __shfl_xor_sync(0xffffffffu, most_k, o));
             most_v = fmaxf(most_v, __shfl_xor_sync(0xffffffffu, most_v, o));
+            least_k = fminf(least_k, __shfl_xor_sync(0xffffffffu, least_k, o));
+            least_v = fminf(least_v, __shfl_xor_sync(0xffffffffu, least_v, o));
           }
-          if (keys && lane == 0) {
+          const bool split = partly(g), exact = split || wide(most_k, least_k) || wide(most_v, least_v);
+          if (keys) {
             ChunkMeta& m = metas[(kt + g / (2 * kGroups)) % kMeta];
-            reinterpret_cast<uint16_t*>(m.live)[g % kGroups] = static_cast<uint16_t>(live);
-            m.group[g % kGroups] = group_of<FMT>(most_k, most_v, sl2);
+            if (lane == 0) {
+              reinterpret_cast<uint16_t*>(m.live)[g % kGroups] = static_cast<uint16_t>(live);
+              m.group[g % kGroups] = group_of<FMT>(most_k, most_v, sl2, exact);
+            }
+            if (exact && lane < kGroup) m.ab[r0 + lane] = scales_of(k_scale, v_scale, sl2);
           }
-          const uint32_t mult = keys ? scale_of<FMT>(k_scale, most_k) : scale_of<FMT>(v_scale, most_v);
-          const bool look = !keys && partly(g);
+          const uint32_t mult = exact ? (keys ? kOne : sign_of(v_scale)) : keys ? scale_of<FMT>(k_scale, most_k) : scale_of<FMT>(v_scale, most_v);
+          const bool look = !keys && split;
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
             const int t = i * TPI + sub_t, r = r0 + t;
@@ -1289,17 +1319,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             if (!((see >> e) & 1)) s[e] = 0xff800000u;
         };
         // Factor of the scores and what is added to them (8 bits: the group's; the factor is never 0, -infinity stays itself).
-        auto factor = [&](int g16, float& f, float& add, float& unit) {
+        // A group whose scales are taken token by token has y in the scores' place behind this: true.
+        auto factor = [&](int g16, float& f, float& add, float& unit, uint32_t (&s)[16]) {
           if constexpr (CODED) {
             const float4 g4 = m.group[g16];
             f = fmaxf(g4.x * qf, 1e-37f);
             add = g4.y;
             unit = g4.z;
+            if (g4.w != 0.f) {
+              f = 1.f;
+              add = 0.f;
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const float4 ab = *reinterpret_cast<const float4*>(m.ab + g16 * 16 + e);
+                s[e] = __float_as_uint(__fmaf_rn(__uint_as_float(s[e]) * qf, ab.x, ab.y));
+                s[e + 1] = __float_as_uint(__fmaf_rn(__uint_as_float(s[e + 1]) * qf, ab.z, ab.w));
+              }
+              mask(g16, s);                // (what is not seen may have any scale)
+              return true;
+            }
           }
+          return false;
         };
         float top = -INFINITY;
         auto most = [&](int g16, uint32_t (&s)[16]) {
           mask(g16, s);
+          float f = 1.f, add = 0.f, unit;
+          factor(g16, f, add, unit, s);
           float a = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[15])), b = __uint_as_float(s[1]);
 #pragma unroll
           for (int e = 2; e < 14; e += 4) {
@@ -1307,11 +1353,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             b = max3(b, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
           }
           a = max3(a, b, __uint_as_float(s[14]));
-          if constexpr (CODED) {
-            float f, add, unit;
-            factor(g16, f, add, unit);
-            a = __fmaf_rn(a, f, add);
-          }
+          if constexpr (CODED) a = __fmaf_rn(a, f, add);
           top = fmaxf(top, a);
         };
         tmem_ld16(col_s, sa);
@@ -1352,7 +1394,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           constexpr int h = decltype(which)::value;
           mask(g16, s);
           float f = sl2, add = 0.f, unit = 0.f;
-          factor(g16, f, add, unit);
+          const bool exact = factor(g16, f, add, unit, s);
           add += off;
           const uint64_t fp = pair(f, f), addp = pair(add, add);
           uint64_t mine[2] = {0, 0};       // 8 bits: the group's sum
@@ -1364,7 +1406,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             to = add2(to, pair(w0, w1));
             pk[8 * h + e] = CODED ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
           }
-          if constexpr (CODED) sum[h] = fma2(add2(mine[0], mine[1]), pair(unit, unit), sum[h]);
+          if constexpr (CODED) {
+            if (exact) {                   // sum of weight / scale, token by token
+              float each = 0.f;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float y = __uint_as_float(s[e]), b = m.ab[g16 * 16 + e].y;
+                if (y != -INFINITY) each += exp2_fast(y + add) * (kSumUnit * exp2_fast(-b));
+              }
+              sum[h] = add2(sum[h], pair(each, 0.f));
+            } else {
+              sum[h] = fma2(add2(mine[0], mine[1]), pair(unit, unit), sum[h]);
+            }
+          }
         };
 #pragma unroll 1
         for (int g16 = 0; g16 < kGroups; g16 += 2) {

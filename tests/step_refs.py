@@ -44,8 +44,10 @@ def seen(n, total, window, sinks, device="cuda"):
     return (t <= p) & ((t > p - window) | (t < sinks))
 
 
-def chunk_want(q, kval, vval, table, cu, lens, page, scale, q_heads, window=EVERY, sinks=0):
-    """(out [total_q, q_heads, D], lse, bound, covered rows) in 64 bits; pages outside the cache are left out."""
+def chunk_want(q, kval, vval, table, cu, lens, page, scale, q_heads, window=EVERY, sinks=0, rounded=0.0):
+    """(out [total_q, q_heads, D], lse, bound, covered rows) in 64 bits; pages outside the cache are left out. rounded:
+    K's and V's elements may be off by so much of themselves (lora_attn_chunk holds codes times scales in 11 bits): a score
+    by dz = rounded * scale * sum |q k|, so every weight over their sum by a factor within e^(+-2 dz); V by its part."""
     kv, D = kval.shape[1], kval.shape[3]
     G = q_heads // kv
     dev = q.device
@@ -66,5 +68,11 @@ def chunk_want(q, kval, vval, table, cu, lens, page, scale, q_heads, window=EVER
         pg, sl = pg[ok], (t % page)[ok]
         for h in range(q_heads):
             o, l, e = R.attend(q[rows].double().view(n, q_heads, D)[:, h], kval[pg, h // G, sl], vval[pg, h // G, sl], scale, vis)
+            if rounded and vis.any():
+                a, k, v = q[rows].double().view(n, q_heads, D)[:, h], kval[pg, h // G, sl], vval[pg, h // G, sl]
+                used = vis.any(0)
+                dz = rounded * torch.where(vis[:, used], scale * (a.abs() @ k[used].abs().T), 0.0).amax(1, keepdim=True)
+                z = torch.where(vis[:, used], scale * (a @ k[used].T), -torch.inf)
+                e = e + (torch.expm1(2 * dz) + rounded) * (torch.softmax(z, 1).nan_to_num(0) @ v[used].abs())
             out[rows, h], lse[rows, h], bound[rows, h] = o, l, e
     return out, lse, bound, covered
