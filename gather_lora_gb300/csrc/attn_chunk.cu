@@ -46,7 +46,7 @@ namespace {
 constexpr unsigned kChunkTimeoutBit = 0x2u;     // LORA_DEV_TIMEOUT
 constexpr int kTile = 128;                      // rows of a tile, tokens of a key tile
 constexpr int kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
-constexpr int kMmaWarp = 8, kPlanWarp = 9, kLoadWarp = 11, kLoaders = 5, kTakers = 4;
+constexpr int kMmaWarp = 8, kPlanWarp = 9, kWatchWarp = 10, kLoadWarp = 11, kLoaders = 5, kTakers = 4;
 constexpr int kChunkThreads = 512, kChunkWarps = kChunkThreads / 32;
 constexpr int kPieces = 4;                      // depth of the ring of pieces
 constexpr int kMeta = 4;                        // depth of the ring of tokens' masks and scales
@@ -62,7 +62,6 @@ constexpr int kSnap = 2;
 constexpr int kItemCost = 2;                    // what an item costs besides its key tiles, in key tiles
 constexpr int kMostSeqs = 8192;                 // LORA_MAX_SEQS
 constexpr int kFewPairs = 8;                    // sequences of more row-tile pairs are summed by a warp
-static_assert(kWaitLimitCycles < (1LL << 32), "waits are limited by a 32-bit clock");
 static_assert(kMostCtas <= kJoinGroup * kJoinGroup, "two levels of joins");
 
 // Workspace: counters [3][kMostCtas] (an item's first join group, by its first CTA; its other groups, by theirs; its
@@ -110,11 +109,11 @@ struct ChunkCtl {
   unsigned long long q_landed, q_full, q_empty;
   unsigned long long s_full[2][2], p_ready[2][2][2], o_done[2][2];   // [row tile][parity of its key tile] ([half])
   unsigned long long piece_full[kPieces], piece_empty[kPieces];
-  unsigned long long drain;
+  unsigned long long drain, ended;
   ChunkPiece piece[kPieces];
   int bad[kPieces];                                  // something in V was set to zero
   uint32_t tmem;
-  int failed, last;
+  int failed, last, progress;
   // the plan
   long long warp_sum[kChunkWarps], total, sum[2], rem[2];
   int seq[2];
@@ -133,18 +132,14 @@ struct ChunkSmem {
 
 __device__ __forceinline__ bool failed(const ChunkCtl& c) { return *reinterpret_cast<const volatile int*>(&c.failed) != 0; }
 
-// Bounded wait; true if it ran out. Once one has, all others of the CTA end at once, the roles leave their loops and nothing
-// more is stored (what runs on until then stays in bounds).
-// (Small, as it is inlined at every wait: the roles' loops share the instruction caches. The status word is set at the end.)
+// Bounded wait; true if the CTA has failed: warp 10 watches over all of them and says so when no key tile has been taken up
+// for kWaitLimitCycles. Then all waits end at once, the roles go through the pieces that are left and nothing more is stored (what
+// runs on until then stays in bounds). (Small, as it is inlined at every wait: the roles' loops share the instruction caches.)
 __device__ __forceinline__ bool wait(ChunkCtl& c, unsigned long long& bar, uint32_t parity) {
   const uint32_t b = smem_u32(&bar);
-  if (mbar_try_wait(b, parity, 100000)) return false;
-  const uint32_t t0 = static_cast<uint32_t>(clock());
 #pragma unroll 1
-  while (!mbar_try_wait(b, parity, 100000)) {
-    if (static_cast<uint32_t>(clock()) - t0 > static_cast<uint32_t>(kWaitLimitCycles)) *reinterpret_cast<volatile int*>(&c.failed) = 1;
+  while (!mbar_try_wait(b, parity, 100000))
     if (failed(c)) return true;
-  }
   return false;
 }
 __device__ __forceinline__ bool passed(unsigned long long& bar, uint32_t parity) {
@@ -507,7 +502,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   const uint32_t q_s = smem_u32(chunk_smem) + Sm::q, ring = smem_u32(chunk_smem) + Sm::ring;
   ChunkMeta* const metas = reinterpret_cast<ChunkMeta*>(base + Sm::meta);
   ChunkCtl& c = *reinterpret_cast<ChunkCtl*>(base + Sm::ctl);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);    // (the same for the warp to the compiler, too)
 
   if (tid == 0) {
     for (int s = 0; s < 2 * NP; ++s) {
@@ -533,7 +529,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       mbar_init(smem_u32(&c.piece_empty[i]), kSoftWarps + 1 + kLoaders);
     }
     mbar_init(smem_u32(&c.drain), 1);
+    mbar_init(smem_u32(&c.ended), kSoftWarps);
     c.failed = 0;
+    c.progress = 0;
     mbar_fence_init();
   }
   if (warp == kMmaWarp) {
@@ -748,6 +746,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     }
     if (lane == 0 && loads > 0 && failed(c)) mbar_wait_limit(smem_u32(CODED ? &c.q_landed : &c.q_full), (loads - 1) & 1, kDrainLimitCycles);
     __syncwarp();
+  } else if (warp == kWatchWarp) {
+    // ============================== watch =================================
+    long long t0 = clock64();
+    int seen = 0;
+    while (!mbar_try_wait(smem_u32(&c.ended), 0, 1000000)) {
+      const int now = *reinterpret_cast<volatile int*>(&c.progress);
+      if (now != seen) {
+        seen = now;
+        t0 = clock64();
+      } else if (clock64() - t0 > kWaitLimitCycles) {
+        *reinterpret_cast<volatile int*>(&c.failed) = 1;
+      }
+      if (failed(c)) break;
+    }
+    __syncwarp();
   } else if (BOXED && warp == kLoadWarp) {
     // ==================== pages looked up, TMA of K and V ====================
     // A lane has 4 consecutive tokens of a tile (of one page: boxes are of 8 slots or more); the first lane of a box issues it. A
@@ -896,16 +909,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             const uint32_t* const mult = x ? metas[k % kMeta].mv : metas[k % kMeta].mk;
             constexpr int CH = D / 16, RPI = 32 / CH, NI = 32 / RPI;
             const int ch = lane % CH, r0 = q * 32 + lane / CH;
-            uint4 v[NI];
-#pragma unroll
-            for (int i = 0; i < NI; ++i) v[i] = lds128(at + Sh::tile_bytes / 2 + (r0 + i * RPI) * D + ch * 16);
-            if constexpr (D == 64) asm volatile("bar.sync 2, %0;\n" ::"n"(kTakers * 32) : "memory");
-            else __syncwarp();
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-              const int r = r0 + i * RPI;
+            const uint32_t from = at + Sh::tile_bytes / 2 + ch * 16;
+            auto convert = [&](int r, const uint4& v) {
               const uint32_t m = mult[r];
-              uint4 a = scaled8<FMT>(v[i].x, v[i].y, m), b = scaled8<FMT>(v[i].z, v[i].w, m);
+              uint4 a = scaled8<FMT>(v.x, v.y, m), b = scaled8<FMT>(v.z, v.w, m);
               if (x && partly && part_seen(t0 - q * 32 + r) && !(chunk_finite<true>(a) && chunk_finite<true>(b))) {
                 bad = true;
                 a = chunk_or_zero<true>(a);
@@ -915,6 +922,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
               const bool swap = CH == 8 && ch >= 4;
               sts128(at + Sh::at(r, 2 * ch + swap), swap ? b : a);
               sts128(at + Sh::at(r, 2 * ch + !swap), swap ? a : b);
+            };
+            if constexpr (D == 64) {
+              uint4 v[NI];
+#pragma unroll
+              for (int i = 0; i < NI; ++i) v[i] = lds128(from + (r0 + i * RPI) * D);
+              asm volatile("bar.sync 2, %0;\n" ::"n"(kTakers * 32) : "memory");
+#pragma unroll
+              for (int i = 0; i < NI; ++i) convert(r0 + i * RPI, v[i]);
+            } else {
+              uint4 next = lds128(from + r0 * D);
+#pragma unroll 1
+              for (int i = 0; i < NI; ++i) {
+                const uint4 v = next;
+                if (i + 1 < NI) next = lds128(from + (r0 + (i + 1) * RPI) * D);
+                __syncwarp();              // (all lanes have read these rows)
+                convert(r0 + i * RPI, v);
+              }
             }
             fence_proxy_async_smem();
           } else if (partly) {
@@ -1229,6 +1253,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             __syncwarp();
           }
         };
+        if (lane == 0) *reinterpret_cast<volatile int*>(&c.progress) = static_cast<int>(kt + j + 2);
         const uint32_t slot = (kt + j) % NP;
         if (slot == 0) step_at(std::integral_constant<int, 0>{});
         else if (slot == 1) step_at(std::integral_constant<int, 1>{});
@@ -1557,6 +1582,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c.piece_empty[sl]));
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&c.ended));
     // Rows that stand before the first token, in whole pairs of row tiles (others are rows of an item): zeros.
     for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
       const Seq s = sequence(p, b);
