@@ -87,8 +87,7 @@ struct ChunkMeta {           // of a key tile
   // are taken token by token instead (ab)
   float4 group[kGroups];
   float2 ab[kTile];          // scale log2(e) times the token's K scale, log2 of its V scale
-  uint32_t mk[kTile];        // (BOXED) what K's codes are multiplied with: the token's scale over the group's, as two f16 whose sum it is
-  uint32_t mv[kTile];        // V's
+  float ks[kTile], vs[kTile];   // (BOXED) the scales as they are
 };
 
 struct ChunkPiece {
@@ -153,6 +152,9 @@ __device__ __forceinline__ bool passed(unsigned long long& bar, uint32_t parity)
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void copies_left() {
@@ -508,12 +510,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   if (tid == 0) {
     for (int s = 0; s < 2 * NP; ++s) {
       mbar_init(smem_u32(&c.full[s]), !BOXED ? kGroups : CODED || (s & 1) ? kTakers : 1);
-      mbar_init(smem_u32(&c.landed[s]), 1);
+      mbar_init(smem_u32(&c.landed[s]), CODED && !(s & 1) ? 33 : 1);     // (K: each lane's scales as well)
       mbar_init(smem_u32(&c.empty[s]), 1);
     }
     for (int s = 0; s < kMeta; ++s) {
-      mbar_init(smem_u32(&c.meta_full[s]), BOXED ? 1 : kGroups);
-      mbar_init(smem_u32(&c.meta_empty[s]), kSoftWarps + (BOXED && CODED ? kTakers : 0));
+      mbar_init(smem_u32(&c.meta_full[s]), BOXED ? 1 + (CODED ? kTakers : 0) : kGroups);
+      mbar_init(smem_u32(&c.meta_empty[s]), kSoftWarps);
     }
     mbar_init(smem_u32(&c.q_landed), 1);
     mbar_init(smem_u32(&c.q_full), CODED ? kSoftWarps : 1);
@@ -766,7 +768,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     // A lane has 4 consecutive tokens of a tile (of one page: boxes are of 8 slots or more); the first lane of a box issues it. A
     // page that is not there is asked for behind the last: its rows are filled with zeros.
     const int BT = p.box_tokens;
-    const float sl2 = p.scale * kLog2e;
     constexpr uint32_t bytes = CODED ? kTile * D : Sh::tile_bytes;
     uint32_t kt = 0, tiles = 0;          // key tiles of the pieces before; issued
     for (int it = 0;; ++it) {
@@ -799,15 +800,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 #pragma unroll
         for (int x = 0; x < 4; ++x)
           if (there && t + x <= w.end && (t + x >= w.low || t + x < p.sinks)) seen |= 1u << x;
-        float sk[4], sv[4];
-        if constexpr (CODED) {
-          const long long si = there ? scale_index(p.c, my_page, w.kvh, my_slot) : 0;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            sk[x] = there ? __ldg(p.c.ks + si + x) : 0.f;
-            sv[x] = there ? __ldg(p.c.vs + si + x) : 0.f;
-          }
-        }
         if (j + 1 < w.n) look_up(j + 1);
         ChunkMeta& m = metas[k % kMeta];
         if (k >= kMeta) wait(c, c.meta_empty[k % kMeta], ((k / kMeta) - 1) & 1);
@@ -830,38 +822,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           }
         };
         if (__any_sync(0xffffffffu, failed(c))) break;
+        if constexpr (CODED) {             // the scales (of tokens that are not there: 0) land with K's codes
+          const long long si = there ? scale_index(p.c, my_page, w.kvh, my_slot) : 0;
+          const uint32_t to = smem_u32(m.ks + lane * 4);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            copy4(to + x * 4, p.c.ks + si + x, there);
+            copy4(to + kTile * 4 + x * 4, p.c.vs + si + x, there);
+          }
+          cp_async_arrive_noinc(smem_u32(&c.landed[ks]));
+        }
         copies(ks, p.map_k);
         uint32_t live = seen << (4 * (lane & 7));
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) live |= __shfl_xor_sync(0xffffffffu, live, o);
         if ((lane & 7) == 0) m.live[lane >> 3] = live;
-        if constexpr (CODED) {
-          float mk = 0.f, mv = 0.f, lk = INFINITY, lv = INFINITY;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float fk = finite_magnitude(sk[x]), fv = finite_magnitude(sv[x]);
-            mk = fmaxf(mk, fk);
-            mv = fmaxf(mv, fv);
-            lk = fk == 0.f ? lk : fminf(lk, fk);
-            lv = fv == 0.f ? lv : fminf(lv, fv);
-          }
-#pragma unroll
-          for (int o = 1; o < 4; o <<= 1) {
-            mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-            lk = fminf(lk, __shfl_xor_sync(0xffffffffu, lk, o));
-            lv = fminf(lv, __shfl_xor_sync(0xffffffffu, lv, o));
-          }
-          const int tg = first_token(j) + (lane & ~3) * 4;
-          const bool exact = wide(mk, lk) || wide(mv, lv) || !(tg + kGroup - 1 <= w.first && (tg > w.end - p.window || tg + kGroup - 1 < p.sinks));
-          if ((lane & 3) == 0) m.group[lane >> 2] = group_of<FMT>(mk, mv, sl2, exact);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if (exact) m.ab[lane * 4 + x] = scales_of(sk[x], sv[x], sl2);
-            m.mk[lane * 4 + x] = exact ? kOne : scale_of<FMT>(sk[x], mk);
-            m.mv[lane * 4 + x] = exact ? sign_of(sv[x]) : scale_of<FMT>(sv[x], mv);
-          }
-        }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c.meta_full[k % kMeta]));
         if (k >= NP) wait(c, c.empty[ks + 1], ((k / NP) - 1) & 1);
@@ -886,6 +861,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     // Warp q of the four has rows 32 q .. of every tile. 8 bits: a tile's codes lie in the upper half of its stage; at head_dim 128 a row's
     // are where the second half of its f16 goes, so that a warp's rows are its own; at 64 all four have read theirs before any writes.
     const int q = warp - kLoadWarp - 1;
+    const float sl2 = p.scale * kLog2e;
     uint32_t kt = 0;
     for (int it = 0;; ++it) {
       const int sl = it % kPieces;
@@ -899,19 +875,41 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         const bool partly = !(t0 + 31 <= w.first && (t0 > w.end - p.window || t0 + 31 < p.sinks));   // some rows see some of it, others not
         auto part_seen = [&](int t) { return !(t <= w.first && (t > w.end - p.window || t < p.sinks)); };
         bool bad = false;
+        uint32_t mult_k = 0, mult_v = 0;
 #pragma unroll 1
         for (int x = CODED ? 0 : 1; x < 2; ++x) {
           const uint32_t st = 2 * (k % NP) + x, at = ring + st * Sh::tile_bytes;
           wait(c, c.landed[st], (k / NP) & 1);
           __syncwarp();
           if constexpr (CODED) {
-            if (x == 0) wait(c, c.meta_full[k % kMeta], (k / kMeta) & 1);
-            const uint32_t* const mult = x ? metas[k % kMeta].mv : metas[k % kMeta].mk;
+            if (x == 0) {                  // lane: the token of a row; its group: 16 lanes
+              ChunkMeta& m = metas[k % kMeta];
+              const int r = q * 32 + lane, t = t0 + lane, tg = t & ~(kGroup - 1);
+              const float sk = m.ks[r], sv = m.vs[r];
+              float most_k = finite_magnitude(sk), most_v = finite_magnitude(sv);
+              float least_k = most_k == 0.f ? INFINITY : most_k, least_v = most_v == 0.f ? INFINITY : most_v;
+#pragma unroll
+              for (int o = 1; o < kGroup; o <<= 1) {
+                most_k = fmaxf(most_k, __shfl_xor_sync(0xffffffffu, most_k, o));
+                most_v = fmaxf(most_v, __shfl_xor_sync(0xffffffffu, most_v, o));
+                least_k = fminf(least_k, __shfl_xor_sync(0xffffffffu, least_k, o));
+                least_v = fminf(least_v, __shfl_xor_sync(0xffffffffu, least_v, o));
+              }
+              const bool exact = wide(most_k, least_k) || wide(most_v, least_v) ||
+                                 !(tg + kGroup - 1 <= w.first && (tg > w.end - p.window || tg + kGroup - 1 < p.sinks));
+              if ((lane & (kGroup - 1)) == 0) m.group[r / kGroup] = group_of<FMT>(most_k, most_v, sl2, exact);
+              if (exact) m.ab[r] = scales_of(sk, sv, sl2);
+              mult_k = exact ? kOne : scale_of<FMT>(sk, most_k);
+              mult_v = exact ? sign_of(sv) : scale_of<FMT>(sv, most_v);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&c.meta_full[k % kMeta]));
+            }
+            const uint32_t mult = x ? mult_v : mult_k;
             constexpr int CH = D / 16, RPI = 32 / CH, NI = 32 / RPI;
             const int ch = lane % CH, r0 = q * 32 + lane / CH;
             const uint32_t from = at + Sh::tile_bytes / 2 + ch * 16;
             auto convert = [&](int r, const uint4& v) {
-              const uint32_t m = mult[r];
+              const uint32_t m = __shfl_sync(0xffffffffu, mult, r - q * 32);
               uint4 a = scaled8<FMT>(v.x, v.y, m), b = scaled8<FMT>(v.z, v.w, m);
               if (x && partly && part_seen(t0 - q * 32 + r) && !(chunk_finite<true>(a) && chunk_finite<true>(b))) {
                 bad = true;
@@ -959,7 +957,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(smem_u32(&c.full[st]));
-            if (CODED && x) mbar_arrive(smem_u32(&c.meta_empty[k % kMeta]));
           }
         }
       }
@@ -1331,46 +1328,51 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         const int hi = pos - t0, lo = hi - min(p.window - 1, max(pos, 0)), sk = p.sinks - t0;    // sees x <= hi with x >= lo or x < sk
         const bool whole = hi >= kTile - 1 && (lo <= 0 || sk >= kTile) && (there.x & there.y & there.z & there.w) == 0xffffffffu;
         const bool cuts = __any_sync(0xffffffffu, live && !whole);
-        // 16 columns of the scores at a time, the next 16 on their way from tensor memory; what is not seen at -infinity. The loops are
-        // not unrolled further: the roles' loops share the instruction caches, and unrolled once more these took 1.25 times as long.
-        uint32_t sa[16], sb[16];
-        auto mask = [&](int g16, uint32_t (&s)[16]) {
-          if (!cuts) return;
+        // Tiles that not all rows see whole, or with scales to be taken token by token, go through tensor memory once more first: what
+        // is not seen to -infinity, y in the place of such scores. The loops behind that know nothing of it.
+        uint32_t exact = 0;                // groups taken token by token
+        if constexpr (CODED) {
+#pragma unroll 1
+          for (int g16 = 0; g16 < kGroups; ++g16) exact |= static_cast<uint32_t>(m.group[g16].w != 0.f) << g16;
+        }
+        if (cuts || exact) {
           auto below = [&](int x) { return x <= 0 ? 0u : x >= 16 ? 0xffffu : (1u << x) - 1; };   // bits under x
-          const int at = g16 * 16;
-          const uint32_t see = reinterpret_cast<const uint16_t*>(m.live)[g16] & below(min(hi, kTile) + 1 - at) & (~below(lo - at) | below(sk - at));
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (!((see >> e) & 1)) s[e] = 0xff800000u;
-        };
-        // Factor of the scores and what is added to them (8 bits: the group's; the factor is never 0, -infinity stays itself).
-        // A group whose scales are taken token by token has y in the scores' place behind this: true.
-        auto factor = [&](int g16, float& f, float& add, float& unit, uint32_t (&s)[16]) {
-          if constexpr (CODED) {
-            const float4 g4 = m.group[g16];
-            f = fmaxf(g4.x * qf, 1e-37f);
-            add = g4.y;
-            unit = g4.z;
-            if (g4.w != 0.f) {
-              f = 1.f;
-              add = 0.f;
+#pragma unroll 1
+          for (int g16 = 0; g16 < kGroups; ++g16) {
+            const int at = g16 * 16;
+            const uint32_t see = reinterpret_cast<const uint16_t*>(m.live)[g16] & below(min(hi, kTile) + 1 - at) & (~below(lo - at) | below(sk - at));
+            uint32_t s[16];
+            tmem_ld16(col_s + at, s);
+            tmem_ld_wait();
+            if (CODED && (exact >> g16 & 1)) {
 #pragma unroll
               for (int e = 0; e < 16; e += 2) {
-                const float4 ab = *reinterpret_cast<const float4*>(m.ab + g16 * 16 + e);
+                const float4 ab = *reinterpret_cast<const float4*>(m.ab + at + e);
                 s[e] = __float_as_uint(__fmaf_rn(__uint_as_float(s[e]) * qf, ab.x, ab.y));
                 s[e + 1] = __float_as_uint(__fmaf_rn(__uint_as_float(s[e + 1]) * qf, ab.z, ab.w));
               }
-              mask(g16, s);                // (what is not seen may have any scale)
-              return true;
             }
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (!((see >> e) & 1)) s[e] = 0xff800000u;
+            tmem_st16(col_s + at, s);
           }
-          return false;
+          tmem_st_wait();
+        }
+        // 16 columns at a time, the next 16 on their way from tensor memory. The loops are not unrolled further: the roles' loops
+        // share the instruction caches, and unrolled once more these took 1.25 times as long.
+        uint32_t sa[16], sb[16];
+        // Factor of the scores, what is added to them, and the unit of the sum (8 bits: the group's; the factor is never 0, -infinity
+        // stays itself; what is y already is summed apart).
+        auto factor = [&](int g16, float& f, float& add, float& unit) {
+          const float4 g4 = m.group[g16];
+          const bool y = g4.w != 0.f;
+          f = y ? 1.f : fmaxf(g4.x * qf, 1e-37f);
+          add = y ? 0.f : g4.y;
+          unit = y ? 0.f : g4.z;
         };
         float top = -INFINITY;
-        auto most = [&](int g16, uint32_t (&s)[16]) {
-          mask(g16, s);
-          float f = 1.f, add = 0.f, unit;
-          factor(g16, f, add, unit, s);
+        auto most = [&](int g16, const uint32_t (&s)[16]) {
           float a = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[15])), b = __uint_as_float(s[1]);
 #pragma unroll
           for (int e = 2; e < 14; e += 4) {
@@ -1378,7 +1380,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             b = max3(b, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
           }
           a = max3(a, b, __uint_as_float(s[14]));
-          if constexpr (CODED) a = __fmaf_rn(a, f, add);
+          if constexpr (CODED) {
+            float f, add, unit;
+            factor(g16, f, add, unit);
+            a = __fmaf_rn(a, f, add);
+          }
           top = fmaxf(top, a);
         };
         tmem_ld16(col_s, sa);
@@ -1414,12 +1420,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         // (nothing seen: every weight is 0)
         const float off = ref == -INFINITY ? 0.f : CODED ? kTop - ref : __fmaf_rn(-ref, sl2, -kGrow);
         uint64_t sum[2] = {0, 0};
+        if (CODED && exact) {              // sums of weight / scale, token by token
+#pragma unroll 1
+          for (int g16 = 0; g16 < kGroups; ++g16) {
+            if (!(exact >> g16 & 1)) continue;
+            uint32_t s[16];
+            tmem_ld16(col_s + g16 * 16, s);
+            tmem_ld_wait();
+            float each = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float y = __uint_as_float(s[e]), b = m.ab[g16 * 16 + e].y;
+              if (y != -INFINITY) each += exp2_fast(y + off) * (kSumUnit * exp2_fast(-b));
+            }
+            l += each;
+          }
+        }
         uint32_t pk[16];                   // 32 columns
-        auto weights = [&](int g16, auto which, uint32_t (&s)[16]) {
+        auto weights = [&](int g16, auto which, const uint32_t (&s)[16]) {
           constexpr int h = decltype(which)::value;
-          mask(g16, s);
           float f = sl2, add = 0.f, unit = 0.f;
-          const bool exact = factor(g16, f, add, unit, s);
+          if constexpr (CODED) factor(g16, f, add, unit);
           add += off;
           const uint64_t fp = pair(f, f), addp = pair(add, add);
           uint64_t mine[2] = {0, 0};       // 8 bits: the group's sum
@@ -1431,19 +1452,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             to = add2(to, pair(w0, w1));
             pk[8 * h + e] = CODED ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
           }
-          if constexpr (CODED) {
-            if (exact) {                   // sum of weight / scale, token by token
-              float each = 0.f;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float y = __uint_as_float(s[e]), b = m.ab[g16 * 16 + e].y;
-                if (y != -INFINITY) each += exp2_fast(y + add) * (kSumUnit * exp2_fast(-b));
-              }
-              sum[h] = add2(sum[h], pair(each, 0.f));
-            } else {
-              sum[h] = fma2(add2(mine[0], mine[1]), pair(unit, unit), sum[h]);
-            }
-          }
+          if constexpr (CODED) sum[h] = fma2(add2(mine[0], mine[1]), pair(unit, unit), sum[h]);
         };
 #pragma unroll 1
         for (int g16 = 0; g16 < kGroups; g16 += 2) {
