@@ -12,8 +12,9 @@
 // tokens' and the window's. All units of the batch, item after item, are cut into equal contiguous ranges, one per CTA (one
 // CTA per SM), so that any mix of long and short chunks and contexts takes equal time everywhere; ends within kSnap units of
 // an item's end move there. A range is walked piece by piece (its part of one item). A piece that is a whole item is
-// finished by its CTA; otherwise its rows' sums go to the workspace and the last CTA of the item to arrive joins them in CTA
-// order (in two levels beyond kJoinGroup), so the bits never depend on who was last.
+// finished by its CTA; otherwise its rows' exponents, sums and O go to the workspace, and a second kernel joins an item's parts in
+// CTA order: the bits never depend on who was last. (Joined by the item's last CTA to arrive they took 19 us at the end of
+// every range, as one CTA's loads and as code that crowded the loops out of the instruction caches.)
 //
 // Roles of a CTA's 16 warps: 0-7 softmax, 8 issues the MMAs, 9 plans and loads Q (TMA), 11-15 bring K and V. Where the pages'
 // size and strides allow (BOXED: sizes in eights), warp 11 looks the pages up, a lane four tokens, and issues TMA, a box a page,
@@ -45,7 +46,7 @@ namespace {
 
 constexpr unsigned kChunkTimeoutBit = 0x2u;     // LORA_DEV_TIMEOUT
 constexpr int kTile = 128;                      // rows of a tile, tokens of a key tile
-constexpr int kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
+constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 8, kPlanWarp = 9, kWatchWarp = 10, kLoadWarp = 11, kLoaders = 5, kTakers = 4;
 constexpr int kChunkThreads = 512, kChunkWarps = kChunkThreads / 32;
 constexpr int kPieces = 4;                      // depth of the ring of pieces
@@ -57,19 +58,17 @@ constexpr float kGrow = 8.f;                    // the reference moves when the 
 constexpr float kTop = 7.f;                     // 8 bits: a weight at the reference is 2^7, at most 2^15
 constexpr float kSumUnit = 6.103515625e-05f;    // 8 bits: 2^-14, so that weight / scale stays in range
 constexpr int kMostCtas = 160;                  // slots in the workspace
-constexpr int kJoinGroup = 16;                  // parts of a join
 constexpr int kSnap = 2;
 constexpr int kItemCost = 2;                    // what an item costs besides its key tiles, in key tiles
 constexpr int kMostSeqs = 8192;                 // LORA_MAX_SEQS
 constexpr int kFewPairs = 8;                    // sequences of more row-tile pairs are summed by a warp
-static_assert(kMostCtas <= kJoinGroup * kJoinGroup, "two levels of joins");
 
-// Workspace: counters [3][kMostCtas] (an item's first join group, by its first CTA; its other groups, by theirs; its
-// groups together), then 2 slots per CTA of exponent[256], sum[256], O[256][D], 4 words of flags.
-constexpr int kCounterBytes = 4096;
+// Workspace: a head per CTA (the item that it begins and does not end, if any), then 2 slots per CTA (of the item that it goes on
+// with, of the one it begins): exponent[256], sum[256], O[256][D], 4 words of flags. All written anew by every call.
+constexpr int kHead = 128, kHeadBytes = 32768;
 template <int D>
 constexpr int kSlotFloats = 2 * 2 * kTile + 2 * kTile * D + 4;
-static_assert(3 * kMostCtas * 4 <= kCounterBytes && kCounterBytes + 2LL * kMostCtas * kSlotFloats<128> * 4 <= (48 << 20), "workspace");
+static_assert(kMostCtas * kHead <= kHeadBytes && kHeadBytes + 2LL * kMostCtas * kSlotFloats<128> * 4 <= (48 << 20), "workspace");
 
 template <int D>
 struct ChunkShape {
@@ -100,6 +99,7 @@ struct ChunkPiece {
   int ni[2];                 // tiles of each row tile
   int c0, c1;                // the item's CTAs
 };
+static_assert(sizeof(ChunkPiece) <= kHead, "heads");
 
 struct ChunkCtl {
   unsigned long long full[8], empty[8];              // K stages even, V stages odd
@@ -112,7 +112,7 @@ struct ChunkCtl {
   ChunkPiece piece[kPieces];
   int bad[kPieces];                                  // something in V was set to zero
   uint32_t tmem;
-  int failed, last, progress;
+  int failed, progress;
   // the plan
   long long warp_sum[kChunkWarps], total, sum[2], rem[2];
   int seq[2];
@@ -160,7 +160,6 @@ template <int N>
 __device__ __forceinline__ void copies_left() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(kSoftThreads) : "memory"); }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -311,8 +310,13 @@ constexpr int kLeast = 4;
 __device__ __forceinline__ long long working(long long total, unsigned grid) {
   return min(static_cast<long long>(grid), (total + kLeast - 1) / kLeast);
 }
+// a / b of two numbers that are not negative, in 32 bits where they fit (a 64-bit division is a call of a hundred instructions).
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 // Unit at which CTA c's range begins, before ends move.
-__device__ __forceinline__ long long cut(long long c, long long total, long long n) { return c * total / n; }
+__device__ __forceinline__ long long cut(long long c, long long total, long long n) { return divide(c * total, n); }
 
 // Rows of an item up to the last that is somebody's.
 __device__ __forceinline__ int rows_of(const ChunkArgs& p, const ChunkPiece& w) {
@@ -395,102 +399,6 @@ __device__ __noinline__ void add_not_finite(const ChunkArgs& p, const ChunkPiece
       }
     }
   }
-}
-
-// Joins an item's parts in the slots of CTAs first, first + by, .. (at most kJoinGroup): into the result rows, or in place
-// into the first's slot. By the softmax warps. (Not inlined: its registers are not the softmax loop's.)
-template <int FMT, int D>
-__device__ __noinline__ void join(const ChunkArgs& p, ChunkCtl& c, const ChunkPiece& w, float* factors, int first, int count, int by, bool last) {
-  constexpr bool CODED = FMT != kKvBf16;
-  constexpr int SF = kSlotFloats<D>, FLAG = SF - 4;
-  const int tid = threadIdx.x, rows = rows_of(p, w), tokens = w.end - w.first + 1, TT = p.tile_tokens, GB = p.head_block;
-  float* const slots = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kCounterBytes);
-  // (the item's first CTA has its part in the second of its slots)
-  auto slot_of = [&](int y) { return slots + static_cast<long long>(2 * (first + y * by) + (first + y * by == w.c0)) * SF; };
-  float e_all = -INFINITY, l_all = 0.f;
-  if (tid < rows) {
-    for (int y = 0; y < count; ++y) {
-      const float e = __ldcg(slot_of(y) + tid);
-      factors[y * 2 * kTile + tid] = e;
-      e_all = fmaxf(e_all, e);
-    }
-    const float from = e_all == -INFINITY ? 0.f : e_all;
-    for (int y = 0; y < count; ++y) l_all += __ldcg(slot_of(y) + 2 * kTile + tid) * exp2_fast(factors[y * 2 * kTile + tid] - from);
-    const float inv = last ? inverse<CODED>(l_all) : 1.f;
-    for (int y = 0; y < count; ++y) factors[y * 2 * kTile + tid] = exp2_fast(factors[y * 2 * kTile + tid] - from) * inv;
-  }
-  bool bad = false;
-  for (int y = 0; y < count; ++y) bad = bad || __float_as_int(__ldcg(slot_of(y) + FLAG)) != 0;
-  soft_sync();
-  // A thread's task: 4 consecutive dimensions of a row. It takes T of them and Y parts of each at a time, their loads in flight
-  // together: many rows have few parts as a rule, few rows many.
-  auto tasks = [&](auto t_at_once, auto y_at_once) {
-    constexpr int T = decltype(t_at_once)::value, Y = decltype(y_at_once)::value;
-    const int all = rows * (D / 4);
-#pragma unroll 1
-    for (int first_task = tid; first_task < all; first_task += T * kSoftThreads) {
-      float4 acc[T];
-#pragma unroll
-      for (int x = 0; x < T; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-      for (int y0 = 0; y0 < count; y0 += Y) {
-        float4 v[T][Y];
-#pragma unroll
-        for (int x = 0; x < T; ++x)
-#pragma unroll
-          for (int y = 0; y < Y; ++y) {
-            const int task = first_task + x * kSoftThreads;
-            v[x][y] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (task < all && y0 + y < count) v[x][y] = __ldcg(reinterpret_cast<const float4*>(slot_of(y0 + y) + 4 * kTile) + task);
-          }
-#pragma unroll
-        for (int x = 0; x < T; ++x)
-#pragma unroll
-          for (int y = 0; y < Y; ++y) {
-            const int task = first_task + x * kSoftThreads;
-            if (task < all && y0 + y < count) {
-              const float f = factors[(y0 + y) * 2 * kTile + task / (D / 4)];
-              acc[x].x += v[x][y].x * f;
-              acc[x].y += v[x][y].y * f;
-              acc[x].z += v[x][y].z * f;
-              acc[x].w += v[x][y].w * f;
-            }
-          }
-      }
-#pragma unroll 1
-      for (int x = 0; x < T; ++x) {
-        const int task = first_task + x * kSoftThreads, r = task / (D / 4), d = task % (D / 4) * 4;
-        if (task >= all) break;
-        float4 a = acc[0];
-#pragma unroll
-        for (int z = 1; z < T; ++z)
-          if (x == z) a = acc[z];
-        if (last) {
-          const int ri = r / kTile, rt = r % kTile / GB, rg = r % kTile - rt * GB, tok = ri * TT + rt;
-          if (rt < TT && rg < w.heads && tok < tokens && !failed(c))
-            *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(w.row0) + tok) * p.out_stride + (w.h0 + rg) * D + d) =
-                make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-        } else {
-          *(reinterpret_cast<float4*>(slot_of(0) + 4 * kTile) + task) = a;
-        }
-      }
-    }
-  };
-  if (rows * (D / 4) > 2 * kSoftThreads) tasks(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-  else tasks(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
-  if (last) {
-    const int rt = tid % kTile / GB, rg = tid % kTile - rt * GB, tok = tid / kTile * TT + rt;
-    if (p.lse && tid < rows && rt < TT && rg < w.heads && tok < tokens && !failed(c))
-      p.lse[(static_cast<long long>(w.row0) + tok) * p.q_heads + w.h0 + rg] = log_sum<CODED>(e_all, l_all);
-  } else {
-    if (tid < rows) {
-      slot_of(0)[tid] = e_all;
-      slot_of(0)[2 * kTile + tid] = l_all;
-    }
-    if (tid == 0) slot_of(0)[FLAG] = __int_as_float(bad);
-  }
-  soft_sync();                       // (the factors lie where the warps stage their results)
-  if (last && bad && !failed(c)) add_not_finite<FMT, D>(p, w, tid >> 5, tid & 31);
 }
 
 template <int FMT, int D, bool BOXED>
@@ -624,7 +532,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     int b = 0, sub = 0, x = 0, tile = 0, tiles = 0;       // the item under the walk, and its next tile
     long long s0 = 0, u = 0, u1 = 0;                      // its first unit; the walk's position and end
     Seq s{};
-    const int snap = static_cast<int>(min(static_cast<long long>(kSnap), total / max(ctas, 1LL) / 4));
+    const int snap = static_cast<int>(min(static_cast<long long>(kSnap), divide(total, max(ctas, 1LL)) / 4));
     auto first_pair = [&]() { return max(0, (s.n - s.len) / step); };       // the first with a tile (s.len > 0)
     auto next_item = [&]() {                              // (there is one)
       s0 += kItemCost + tiles;
@@ -652,7 +560,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         b = c.seq[e];
         s = sequence(p, b);
         const long long su = c.sum[e];
-        sub = static_cast<int>(c.rem[e] / su);
+        sub = static_cast<int>(divide(c.rem[e], su));
         const long long rest = c.rem[e] - sub * su;
         const int np = (s.n - 1) / step + 1;
         long long before = 0;
@@ -718,8 +626,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             const int last = min(w.first + (i + 1) * TT - 1, w.end), any = w.first + i * TT <= w.end && last >= 0;
             w.ni[i] = any ? max(0, min(w.ta + w.n, last / kTile + 1 - w.skip) - w.ta) : 0;
           }
-          w.c0 = static_cast<int>(((s0 + kItemCost + snap + 1) * ctas + total - 1) / total) - 1;
-          w.c1 = static_cast<int>(((s0 + kItemCost + tiles - snap) * ctas + total - 1) / total) - 1;
+          w.c0 = static_cast<int>(divide((s0 + kItemCost + snap + 1) * ctas + total - 1, total)) - 1;
+          w.c1 = static_cast<int>(divide((s0 + kItemCost + tiles - snap) * ctas + total - 1, total)) - 1;
         }
         c.piece[sl] = w;
         *reinterpret_cast<volatile int*>(&c.bad[sl]) = 0;
@@ -1276,7 +1184,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const float sl2 = p.scale * kLog2e, grow = CODED ? kGrow : kGrow / sl2;
     const int t_in = row / GB, g = row - t_in * GB;
     const uint32_t stage = smem_u32(chunk_smem) + Sm::stage + warp * kStageBytes;
-    bool dead = false;
+    bool dead = false, begun = false;    // (begun: an item that the next CTA goes on with)
     uint32_t t = 0, kt = 0;              // key tiles of this row tile so far; of the pieces before
     for (int it = 0;; ++it) {
       const int sl = it % kPieces;
@@ -1439,7 +1347,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         uint32_t pk[16];                   // 32 columns
         auto weights = [&](int g16, auto which, const uint32_t (&s)[16]) {
           constexpr int h = decltype(which)::value;
-          float f = sl2, add = 0.f, unit = 0.f;
+          float f = sl2, add = 0.f;
+          [[maybe_unused]] float unit = 0.f;
           if constexpr (CODED) factor(g16, f, add, unit);
           add += off;
           const uint64_t fp = pair(f, f), addp = pair(add, add);
@@ -1529,9 +1438,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           add_not_finite<FMT, D>(p, w, warp, lane);
         }
       } else {
-        // A part: exponent, sum and O of its rows into this CTA's slot; the last CTA of the item joins them.
-        int* const counters = static_cast<int*>(p.workspace);
-        float* const slots = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kCounterBytes);
+        // A part: exponent, sum and O of its rows into this CTA's slot, and what item it is if it begins here.
+        float* const slots = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kHeadBytes);
         constexpr int SF = kSlotFloats<D>, FLAG = SF - 4;
         const int me = blockIdx.x, rows = rows_of(p, w);
         float* const mine = slots + static_cast<long long>(2 * me + (w.ta == 0)) * SF;
@@ -1540,6 +1448,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           mine[rr] = n > 0 ? exponent : -INFINITY;
           mine[2 * kTile + rr] = n > 0 ? l : 0.f;
         }
+        if (tid == 0) {
+          mine[FLAG] = __int_as_float(*reinterpret_cast<volatile int*>(&c.bad[sl]));
+          if (w.ta == 0) begun = true;
+        }
+        if (w.ta == 0 && tid < static_cast<int>(sizeof(ChunkPiece) / 4))
+          reinterpret_cast<int*>(static_cast<unsigned char*>(p.workspace) + static_cast<long long>(me) * kHead)[tid] = reinterpret_cast<const int*>(&w)[tid];
         if (i * kTile + (warp & 3) * 32 < rows) {
 #pragma unroll 1
           for (int q = 0; q < D / 16; ++q) {
@@ -1565,34 +1479,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           }
         }
         tc_fence_before();
-        if (tid == 0) mine[FLAG] = __int_as_float(*reinterpret_cast<volatile int*>(&c.bad[sl]));
-
-        // Arrive at a counter; true in the CTA that is the last of `count`, which sets it back to 0.
-        auto last_of = [&](int* counter, int count) {
-          soft_sync();
-          if (tid == 0) {   // releases the CTA's writes before the barrier, acquires those of the CTAs before it
-            int seen;
-            asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;\n" : "=r"(seen) : "l"(counter) : "memory");
-            c.last = seen == count - 1;
-            if (c.last) *counter = 0;
-          }
-          soft_sync();
-          return *const_cast<const volatile int*>(&c.last) != 0;
-        };
-        float* const factors = reinterpret_cast<float*>(base + Sm::stage);    // over all warps' staging
-        static_assert(kJoinGroup * 2 * kTile * 4 <= kSoftWarps * kStageBytes, "factors of a join");
-        const int groups = (w.c1 - w.c0) / kJoinGroup + 1, gi = (me - w.c0) / kJoinGroup;
-        const int head = w.c0 + gi * kJoinGroup, count = min(kJoinGroup, w.c1 - head + 1);
-        if (last_of(counters + (gi ? kMostCtas : 0) + head, count)) {
-          join<FMT, D>(p, c, w, factors, head, count, 1, groups == 1);
-          if (groups > 1 && last_of(counters + 2 * kMostCtas + w.c0, groups)) join<FMT, D>(p, c, w, factors, w.c0, groups, kJoinGroup, true);
-        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c.piece_empty[sl]));
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&c.ended));
+    if (tid == 0 && (!begun || failed(c))) *reinterpret_cast<int*>(static_cast<unsigned char*>(p.workspace) + static_cast<long long>(blockIdx.x) * kHead) = 0;   // (the head's `valid`)
     // Rows that stand before the first token, in whole pairs of row tiles (others are rows of an item): zeros.
     for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
       const Seq s = sequence(p, b);
@@ -1612,6 +1505,91 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(0, 512);
+  }
+}
+
+// Joins the parts of the item that CTA blockIdx.x began, if others went on with it: rows 32 blockIdx.y .. of it.
+template <int FMT, int D>
+__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkArgs p) {
+  constexpr bool CODED = FMT != kKvBf16;
+  constexpr int SF = kSlotFloats<D>, FLAG = SF - 4, T = 32 * (D / 4) / 256, Y = 8 / T > 2 ? 8 / T : 2;
+  __shared__ float s_top[32], s_inv[32];
+  __shared__ int s_bad;
+  const int tid = threadIdx.x, r0 = blockIdx.y * 32;
+  if (tid == 0) s_bad = 0;
+  pdl_wait_then_release();
+  const ChunkPiece& w = *reinterpret_cast<const ChunkPiece*>(static_cast<const unsigned char*>(p.workspace) + static_cast<long long>(blockIdx.x) * kHead);
+  if (!__ldcg(&w.valid)) return;
+  const int rows = rows_of(p, w), tokens = w.end - w.first + 1, TT = p.tile_tokens, GB = p.head_block, count = w.c1 - w.c0 + 1;
+  if (r0 >= rows) return;
+  const float* const slots = reinterpret_cast<const float*>(static_cast<const unsigned char*>(p.workspace) + kHeadBytes) + static_cast<long long>(2 * w.c0) * SF;
+  // (the item's first CTA has its part in the second of its slots)
+  auto slot_of = [&](int y) { return slots + (y == 0 ? 1LL : 2LL * y) * SF; };
+  __syncthreads();
+  if (tid < 32) {
+    const int r = r0 + tid;
+    float e_all = -INFINITY, l_all = 0.f;
+    if (r < rows) {
+#pragma unroll 8
+      for (int y = 0; y < count; ++y) e_all = fmaxf(e_all, __ldcg(slot_of(y) + r));
+      const float from = e_all == -INFINITY ? 0.f : e_all;
+#pragma unroll 8
+      for (int y = 0; y < count; ++y) l_all += __ldcg(slot_of(y) + 2 * kTile + r) * exp2_fast(__ldcg(slot_of(y) + r) - from);
+      s_top[tid] = from;
+      s_inv[tid] = inverse<CODED>(l_all);
+      const int rt = r % kTile / GB, rg = r % kTile - rt * GB, tok = r / kTile * TT + rt;
+      if (p.lse && rt < TT && rg < w.heads && tok < tokens)
+        p.lse[(static_cast<long long>(w.row0) + tok) * p.q_heads + w.h0 + rg] = log_sum<CODED>(e_all, l_all);
+    }
+  } else {
+    for (int y = tid - 32; y < count; y += 224)
+      if (__float_as_int(__ldcg(slot_of(y) + FLAG)) != 0) s_bad = 1;
+  }
+  __syncthreads();
+  // A team of D / 4 lanes a row, 16 bytes a lane and part: T rows and Y parts of each thread in flight together.
+  constexpr int LANES = D / 4, TEAMS = 256 / LANES;
+  const int team = tid / LANES, d = tid % LANES * 4;
+  float4 acc[T];
+#pragma unroll
+  for (int x = 0; x < T; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int y0 = 0; y0 < count; y0 += Y) {
+    float4 v[T][Y];
+    float e[T][Y];
+#pragma unroll
+    for (int y = 0; y < Y; ++y)
+#pragma unroll
+      for (int x = 0; x < T; ++x) {
+        const int r = r0 + team + x * TEAMS;
+        e[x][y] = -INFINITY;
+        v[x][y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (y0 + y < count && r < rows) {
+          e[x][y] = __ldcg(slot_of(y0 + y) + r);
+          v[x][y] = __ldcg(reinterpret_cast<const float4*>(slot_of(y0 + y) + 4 * kTile + r * D + d));
+        }
+      }
+#pragma unroll
+    for (int y = 0; y < Y; ++y)
+#pragma unroll
+      for (int x = 0; x < T; ++x) {
+        if (y0 + y >= count) continue;
+        const float f = exp2_fast(e[x][y] - s_top[(team + x * TEAMS) & 31]);
+        acc[x].x += v[x][y].x * f;
+        acc[x].y += v[x][y].y * f;
+        acc[x].z += v[x][y].z * f;
+        acc[x].w += v[x][y].w * f;
+      }
+  }
+#pragma unroll
+  for (int x = 0; x < T; ++x) {
+    const int at = team + x * TEAMS, r = r0 + at, rt = r % kTile / GB, rg = r % kTile - rt * GB, tok = r / kTile * TT + rt;
+    if (r >= rows || rt >= TT || rg >= w.heads || tok >= tokens) continue;
+    const float inv = s_inv[at];
+    *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(w.row0) + tok) * p.out_stride + (w.h0 + rg) * D + d) =
+        make_uint2(pack_bf16x2(acc[x].x * inv, acc[x].y * inv), pack_bf16x2(acc[x].z * inv, acc[x].w * inv));
+  }
+  if (s_bad) {
+    __syncthreads();
+    if (tid < 32) add_not_finite<FMT, D>(p, w, blockIdx.y, tid);
   }
 }
 
@@ -1636,7 +1614,12 @@ int launch_one(const ChunkArgs& a, void* stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, a));
+  e = cudaLaunchKernelEx(&cfg, kernel, a);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  cfg.gridDim.y = 2 * kTile / 32;
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, chunk_join_kernel<FMT, D>, a));
 }
 
 template <int FMT>

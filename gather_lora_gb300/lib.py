@@ -25,7 +25,7 @@ TMAP_MIN_RANK = 32         # LORA_TMAP_MIN_RANK: a_tmaps are used from this max_
 DELTA_DENSE_MIN_ROWS = 256  # LORA_DELTA_DENSE_MIN_ROWS: lora_delta's tensor-core path from this m up
 
 
-# enum lora_kv_format, and the scratch lora_attn_decode and lora_attn_chunk want (zero-filled once)
+# enum lora_kv_format, and the scratch lora_attn_decode (zero-filled once) and lora_attn_chunk want
 KV_BF16, KV_E4M3, KV_INT8 = 0, 1, 2
 ATTN_WORKSPACE = 16 << 20   # LORA_ATTN_WORKSPACE
 CHUNK_WORKSPACE = 48 << 20  # LORA_CHUNK_WORKSPACE
@@ -337,7 +337,7 @@ def lora_attn_decode_window(q, q_row_stride, out, out_row_stride, batch, q_heads
 def lora_attn_chunk(q, q_row_stride, out, out_row_stride, cu_q, batch, total_q, q_heads, scale, cache, block_table,
                     table_stride, max_pages, seq_lens, window, sinks, workspace, workspace_bytes, lse=None, stream=None):
     """Attention of chunks of new tokens over the cache (see lora_attn_chunk in include/gather_lora.h).
-    workspace: at least CHUNK_WORKSPACE bytes, zero-filled once; window: NO_WINDOW for none."""
+    workspace: at least CHUNK_WORKSPACE bytes; window: NO_WINDOW for none."""
     return _check(load().lora_attn_chunk(_addr(q), q_row_stride, _addr(out), out_row_stride, _addr(cu_q), batch, total_q, q_heads,
                                          scale, _cache(cache), _addr(block_table), table_stride, max_pages, _addr(seq_lens),
                                          window, sinks, _addr(lse), _addr(workspace), workspace_bytes, _stream(stream)))

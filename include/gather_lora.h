@@ -592,7 +592,9 @@ int lora_attn_decode_window(const lora_bf16_t* q, int64_t q_row_stride, lora_bf1
  *               overlap are not defined); rows of no sequence stay unchanged
  *   block_table, table_stride, max_pages, seq_lens, scale   as in lora_attn_decode
  *   lse         optional [total_q, q_heads] f32: ln sum_t exp(z_t)
- *   workspace   as in lora_attn_decode, LORA_CHUNK_WORKSPACE bytes, its own
+ *   workspace   device scratch of at least LORA_CHUNK_WORKSPACE bytes, 16-byte
+ *               aligned, whatever it holds; calls that may run at the same time need
+ *               one each
  * How the work is split follows the whole batch: the same call gives the same bits.
  */
 #define LORA_CHUNK_WORKSPACE (48 << 20)

@@ -1,7 +1,7 @@
 """A CPU model of how lora_attn_chunk shares a batch out (csrc/attn_chunk.cu): key tiles that rows see, cuts of the units,
-pieces, the CTAs of an item and the joins' slots and counters. For any lengths every key tile that some row sees is in one
-piece, the parts of an item are those of the CTAs that its join counts, and no two joins share a counter or a slot. The
-bounds of the kernel's arrays hold."""
+pieces, the CTAs of an item and the joins' slots. For any lengths every key tile that some row sees is in one piece, the
+parts of an item are those of the CTAs that its join counts, no two joins share a slot or a head, and the workspace holds
+them."""
 from __future__ import annotations
 
 import os
@@ -18,7 +18,7 @@ def const(name):
     return int(re.search(rf"constexpr int {name} = (\d+)[;,]", SRC).group(1))
 
 
-TILE, MOST, GROUP, SNAP = const("kTile"), const("kMostCtas"), const("kJoinGroup"), const("kSnap")
+TILE, MOST, SNAP = const("kTile"), const("kMostCtas"), const("kSnap")
 COST, LEAST = const("kItemCost"), const("kLeast")
 EVERY = 2 ** 31 - 1
 
@@ -91,13 +91,13 @@ def check(seqs, step, subs, window, sinks, grid):
         for at, ta, n in mine:
             assert n > 0
             parts.setdefault(at, []).append((c, ta, n))
-    counters, slots = set(), set()
+    heads, slots = set(), set()
     for at, (b, sub, x, s0, tiles) in enumerate(every):
         got = parts[at]
         assert [ta for _, ta, _ in got] == [sum(n for _, _, n in got[:k]) for k in range(len(got))] and sum(n for _, _, n in got) == tiles
         if len(got) == 1:
             continue
-        # the CTAs of the item as the kernel works them out, its slots and its counters
+        # the CTAs of the item as the kernel works them out, its slots, and the head that its first CTA writes
         c0 = -(-((s0 + COST + snap + 1) * ctas) // total) - 1
         c1 = -(-((s0 + COST + tiles - snap) * ctas) // total) - 1
         assert [c for c, _, _ in got] == list(range(c0, c1 + 1)), (got, c0, c1)
@@ -105,12 +105,8 @@ def check(seqs, step, subs, window, sinks, grid):
             slot = 2 * c + (ta == 0)
             assert (ta == 0) == (c == c0) and slot not in slots and slot < 2 * MOST
             slots.add(slot)
-        groups = (c1 - c0) // GROUP + 1
-        assert groups <= GROUP
-        names = [(1 if g else 0, c0 + g * GROUP) for g in range(groups)] + ([(2, c0)] if groups > 1 else [])
-        for name in names:
-            assert name not in counters and name[1] < MOST
-            counters.add(name)
+        assert c0 not in heads and c0 < MOST
+        heads.add(c0)
 
 
 @pytest.mark.parametrize("seed", range(150))
@@ -151,7 +147,8 @@ def test_tiles_are_those_that_some_row_sees(seed):
 
 
 def test_the_workspace_holds_the_slots():
+    head, heads = int(re.search(r"kHead = (\d+)", SRC).group(1)), int(re.search(r"kHeadBytes = (\d+);", SRC).group(1))
     for d in (64, 128):
         slot = 2 * 2 * TILE + 2 * TILE * d + 4
-        assert const("kCounterBytes") + 2 * MOST * slot * 4 <= 48 << 20 and 3 * MOST * 4 <= const("kCounterBytes")
-        assert slot % 4 == 0 and const("kCounterBytes") % 16 == 0
+        assert heads + 2 * MOST * slot * 4 <= 48 << 20 and MOST * head <= heads
+        assert slot % 4 == 0 and heads % 16 == 0
