@@ -21,8 +21,8 @@
 // and warps 12-15 take what has landed over: codes are converted in place in their stage, V that some rows see and others do
 // not is looked through. Otherwise the five warps take groups of 16 tokens in turn by cp.async (BF16) or through registers.
 //
-// 8-bit formats run in f16: the codes of both formats are exact in it, times their scale over a power of two that a group of 16
-// tokens shares (a product rounded once, to 11 bits), so that the softmax meets scales once in 16 columns: with one a token,
+// 8-bit formats run in f16: the codes of both formats are exact in it, times their scale over a power of two that the tokens of a tile
+// share (BOXED; else 16 tokens; a product rounded once, to 11 bits), so that the softmax meets scales once a tile: with one a token,
 // read from shared memory by every row, it took 2.8 times as long, as the MMAs leave little of that memory's bandwidth. K's
 // power of two multiplies the scores; V's the weight: to keep weights of any scale in f16's range the running reference is that of
 // y_t = z_t + log2 of V's, the weight w = 2^(y - ref) multiplies V and the softmax's own sum is that of w over V's. Q is brought
@@ -82,10 +82,11 @@ struct ChunkShape {
 
 struct ChunkMeta {           // of a key tile
   uint32_t live[4];          // tokens that are there and that some row sees
-  // 8 bits, of 16 tokens: scale log2(e) times K's power of two, log2 of V's, kSumUnit over V's, and whether the group's scales
-  // are taken token by token instead (ab)
+  // 8 bits, of 16 tokens (BOXED: the first, of all): scale log2(e) times K's power of two, log2 of V's, kSumUnit over V's, and
+  // whether their scales are taken token by token instead (ab)
   float4 group[kGroups];
   float2 ab[kTile];          // scale log2(e) times the token's K scale, log2 of its V scale
+  float iv[kTile];           // kSumUnit over its V scale
   float ks[kTile], vs[kTile];   // (BOXED) the scales as they are
 };
 
@@ -101,7 +102,7 @@ struct ChunkPiece {
 };
 static_assert(sizeof(ChunkPiece) <= kHead, "heads");
 
-struct ChunkCtl {
+struct alignas(16) ChunkCtl {
   unsigned long long full[8], empty[8];              // K stages even, V stages odd
   unsigned long long landed[8];                      // (BOXED) full but for the look or the conversion
   unsigned long long meta_full[kMeta], meta_empty[kMeta];
@@ -111,6 +112,7 @@ struct ChunkCtl {
   unsigned long long drain, ended;
   ChunkPiece piece[kPieces];
   int bad[kPieces];                                  // something in V was set to zero
+  float4 extremes[2][kTakers];                       // largest and least scales of a tile, by the converting warps
   uint32_t tmem;
   int failed, progress;
   // the plan
@@ -160,6 +162,8 @@ template <int N>
 __device__ __forceinline__ void copies_left() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
+
+__device__ __forceinline__ void takers_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(kTakers * 32) : "memory"); }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -226,10 +230,12 @@ __device__ __forceinline__ uint32_t scale_of(float s, float most) {
 constexpr uint32_t kOne = 0x3c00u;
 __device__ __forceinline__ uint32_t sign_of(float s) { return s == 0.f ? 0u : s < 0.f ? 0xbc00u : kOne; }
 // A V scale of 0 is 2^-64 to the weights (see above); below 2^-110, under what lora_kv_write stores, it is 2^-110.
-__device__ __forceinline__ float2 scales_of(float k, float v, float sl2) {
-  const float mag = v == 0.f ? 5.421010862427522e-20f : fmaxf(fabsf(v), 7.703719777548943e-34f);
-  return make_float2(k * sl2, log2f(v != v ? v : mag));     // (fmaxf drops NaN)
+__device__ __forceinline__ float magnitude_of(float v) {
+  return v == 0.f ? 5.421010862427522e-20f : v != v ? v : fmaxf(fabsf(v), 7.703719777548943e-34f);     // (fmaxf drops NaN)
 }
+__device__ __forceinline__ float2 scales_of(float k, float v, float sl2) { return make_float2(k * sl2, log2f(magnitude_of(v))); }
+// (NaN: the weight is NaN where it is seen, and 0 times this must stay 0 where it is not)
+__device__ __forceinline__ float over_scale(float v) { return v != v ? 0.f : kSumUnit / magnitude_of(v); }
 
 // Chunks of V: whether all is finite, and with what is not set to zero.
 template <bool CODED>
@@ -550,6 +556,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       tiles = pair_tiles(p, s, step, x);
     };
     if (works) {
+      const Seq both[2] = {sequence(p, c.seq[0]), sequence(p, blockIdx.x + 1 < ctas ? c.seq[1] : c.seq[0])};
       // The item that holds a cut, by prefix sums over its sequence's pairs; 0: this CTA's first unit, 1: the next one's.
       for (int e = 1; e >= 0; --e) {
         const long long r = cut(blockIdx.x + e, total, ctas);
@@ -558,7 +565,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           continue;
         }
         b = c.seq[e];
-        s = sequence(p, b);
+        s = both[e];
         const long long su = c.sum[e];
         sub = static_cast<int>(divide(c.rem[e], su));
         const long long rest = c.rem[e] - sub * su;
@@ -718,15 +725,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           const uint32_t bar = smem_u32(!CODED && !(stage & 1) ? &c.full[stage] : &c.landed[stage]);
           if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
           __syncwarp();
-          if ((lane * 4) % BT == 0) {
-            const int c1 = p.heads_inside ? w.kvh : my_slot, c2 = p.heads_inside ? my_slot : w.kvh;
+          // (box by box by one lane: issued by the boxes' own lanes they took twice as long)
+#pragma unroll 1
+          for (int box = 0; box < kTile; box += BT) {
+            const int at = __shfl_sync(0xffffffffu, my_slot, box / 4), of = __shfl_sync(0xffffffffu, my_page, box / 4);
+            const int c1 = p.heads_inside ? w.kvh : at, c2 = p.heads_inside ? at : w.kvh;
             const uint32_t to = ring + stage * Sh::tile_bytes;
-            if constexpr (CODED) {
-              tma_load_4d(to + Sh::tile_bytes / 2 + lane * 4 * D, &map, 0, c1, c2, my_page, bar);
-            } else {
+            if (elect_one()) {
+              if constexpr (CODED) {
+                tma_load_4d(to + Sh::tile_bytes / 2 + box * D, &map, 0, c1, c2, of, bar);
+              } else {
 #pragma unroll
-              for (int a = 0; a < D / 64; ++a) tma_load_4d(to + a * (kTile * 128) + lane * 4 * 128, &map, a * 64, c1, c2, my_page, bar);
+                for (int a = 0; a < D / 64; ++a) tma_load_4d(to + a * (kTile * 128) + box * 128, &map, a * 64, c1, c2, of, bar);
+              }
             }
+            __syncwarp();
           }
         };
         if (__any_sync(0xffffffffu, failed(c))) break;
@@ -790,23 +803,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           wait(c, c.landed[st], (k / NP) & 1);
           __syncwarp();
           if constexpr (CODED) {
-            if (x == 0) {                  // lane: the token of a row; its group: 16 lanes
+            if (x == 0) {                  // lane: the token of a row
               ChunkMeta& m = metas[k % kMeta];
-              const int r = q * 32 + lane, t = t0 + lane, tg = t & ~(kGroup - 1);
+              const int r = q * 32 + lane, tt = t0 - q * 32;
               const float sk = m.ks[r], sv = m.vs[r];
               float most_k = finite_magnitude(sk), most_v = finite_magnitude(sv);
               float least_k = most_k == 0.f ? INFINITY : most_k, least_v = most_v == 0.f ? INFINITY : most_v;
 #pragma unroll
-              for (int o = 1; o < kGroup; o <<= 1) {
+              for (int o = 1; o < 32; o <<= 1) {
                 most_k = fmaxf(most_k, __shfl_xor_sync(0xffffffffu, most_k, o));
                 most_v = fmaxf(most_v, __shfl_xor_sync(0xffffffffu, most_v, o));
                 least_k = fminf(least_k, __shfl_xor_sync(0xffffffffu, least_k, o));
                 least_v = fminf(least_v, __shfl_xor_sync(0xffffffffu, least_v, o));
               }
+              float4* const of_warps = c.extremes[k & 1];        // (two in turn: nobody is two tiles ahead)
+              if (lane == 0) of_warps[q] = make_float4(most_k, most_v, least_k, least_v);
+              takers_sync();
+#pragma unroll
+              for (int y = 0; y < kTakers; ++y) {
+                const float4 z = of_warps[y];
+                most_k = fmaxf(most_k, z.x);
+                most_v = fmaxf(most_v, z.y);
+                least_k = fminf(least_k, z.z);
+                least_v = fminf(least_v, z.w);
+              }
               const bool exact = wide(most_k, least_k) || wide(most_v, least_v) ||
-                                 !(tg + kGroup - 1 <= w.first && (tg > w.end - p.window || tg + kGroup - 1 < p.sinks));
-              if ((lane & (kGroup - 1)) == 0) m.group[r / kGroup] = group_of<FMT>(most_k, most_v, sl2, exact);
-              if (exact) m.ab[r] = scales_of(sk, sv, sl2);
+                                 !(tt + kTile - 1 <= w.first && (tt > w.end - p.window || tt + kTile - 1 < p.sinks));
+              if (q == 0 && lane == 0) m.group[0] = group_of<FMT>(most_k, most_v, sl2, exact);
+              if (exact) {
+                m.ab[r] = scales_of(sk, sv, sl2);
+                m.iv[r] = over_scale(sv);
+              }
               mult_k = exact ? kOne : scale_of<FMT>(sk, most_k);
               mult_v = exact ? sign_of(sv) : scale_of<FMT>(sv, most_v);
               __syncwarp();
@@ -833,7 +860,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
               uint4 v[NI];
 #pragma unroll
               for (int i = 0; i < NI; ++i) v[i] = lds128(from + (r0 + i * RPI) * D);
-              asm volatile("bar.sync 2, %0;\n" ::"n"(kTakers * 32) : "memory");
+              takers_sync();
 #pragma unroll
               for (int i = 0; i < NI; ++i) convert(r0 + i * RPI, v[i]);
             } else {
@@ -1043,7 +1070,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
               reinterpret_cast<uint16_t*>(m.live)[g % kGroups] = static_cast<uint16_t>(live);
               m.group[g % kGroups] = group_of<FMT>(most_k, most_v, sl2, exact);
             }
-            if (exact && lane < kGroup) m.ab[r0 + lane] = scales_of(k_scale, v_scale, sl2);
+            if (exact && lane < kGroup) {
+              m.ab[r0 + lane] = scales_of(k_scale, v_scale, sl2);
+              m.iv[r0 + lane] = over_scale(v_scale);
+            }
           }
           const uint32_t mult = exact ? (keys ? kOne : sign_of(v_scale)) : keys ? scale_of<FMT>(k_scale, most_k) : scale_of<FMT>(v_scale, most_v);
           const bool look = !keys && split;
@@ -1239,7 +1269,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         // Tiles that not all rows see whole, or with scales to be taken token by token, go through tensor memory once more first: what
         // is not seen to -infinity, y in the place of such scores. The loops behind that know nothing of it.
         uint32_t exact = 0;                // groups taken token by token
-        if constexpr (CODED) {
+        // Factor of the scores, what is added to them, and the unit of the sum (8 bits: the tile's or the group's; the factor is never
+        // 0, -infinity stays itself; what is y already is summed apart).
+        float f_tile = sl2, add_tile = 0.f, unit_tile = 1.f;
+        auto factor = [&](int g16, float& f, float& add, float& unit) {
+          const float4 g4 = m.group[g16];
+          const bool y = g4.w != 0.f;
+          f = y ? 1.f : fmaxf(g4.x * qf, 1e-37f);
+          add = y ? 0.f : g4.y;
+          unit = y ? 0.f : g4.z;
+        };
+        if constexpr (CODED && BOXED) {
+          factor(0, f_tile, add_tile, unit_tile);
+          exact = unit_tile == 0.f ? (1u << kGroups) - 1 : 0;
+        } else if constexpr (CODED) {
 #pragma unroll 1
           for (int g16 = 0; g16 < kGroups; ++g16) exact |= static_cast<uint32_t>(m.group[g16].w != 0.f) << g16;
         }
@@ -1249,6 +1292,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           for (int g16 = 0; g16 < kGroups; ++g16) {
             const int at = g16 * 16;
             const uint32_t see = reinterpret_cast<const uint16_t*>(m.live)[g16] & below(min(hi, kTile) + 1 - at) & (~below(lo - at) | below(sk - at));
+            if (!(exact >> g16 & 1) && __all_sync(0xffffffffu, see == 0xffffu || !live)) continue;
             uint32_t s[16];
             tmem_ld16(col_s + at, s);
             tmem_ld_wait();
@@ -1270,15 +1314,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         // 16 columns at a time, the next 16 on their way from tensor memory. The loops are not unrolled further: the roles' loops
         // share the instruction caches, and unrolled once more these took 1.25 times as long.
         uint32_t sa[16], sb[16];
-        // Factor of the scores, what is added to them, and the unit of the sum (8 bits: the group's; the factor is never 0, -infinity
-        // stays itself; what is y already is summed apart).
-        auto factor = [&](int g16, float& f, float& add, float& unit) {
-          const float4 g4 = m.group[g16];
-          const bool y = g4.w != 0.f;
-          f = y ? 1.f : fmaxf(g4.x * qf, 1e-37f);
-          add = y ? 0.f : g4.y;
-          unit = y ? 0.f : g4.z;
-        };
         float top = -INFINITY;
         auto most = [&](int g16, const uint32_t (&s)[16]) {
           float a = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[15])), b = __uint_as_float(s[1]);
@@ -1288,7 +1323,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             b = max3(b, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
           }
           a = max3(a, b, __uint_as_float(s[14]));
-          if constexpr (CODED) {
+          if constexpr (CODED && !BOXED) {
             float f, add, unit;
             factor(g16, f, add, unit);
             a = __fmaf_rn(a, f, add);
@@ -1305,6 +1340,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           tmem_ld16(col_s + (g16 * 16 + 32) % kTile, sa);    // (at the end: the first 16 again)
           most(g16 + 1, sb);
         }
+        if constexpr (CODED && BOXED) top = __fmaf_rn(top, f_tile, add_tile);
         if (j == 0) {
           ref = top;
         } else if (__any_sync(0xffffffffu, live && top > ref + grow)) {   // (rows of nobody hold anything: no say)
@@ -1335,33 +1371,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             uint32_t s[16];
             tmem_ld16(col_s + g16 * 16, s);
             tmem_ld_wait();
-            float each = 0.f;
+            float each[2] = {0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float y = __uint_as_float(s[e]), b = m.ab[g16 * 16 + e].y;
-              if (y != -INFINITY) each += exp2_fast(y + off) * (kSumUnit * exp2_fast(-b));
+            for (int e = 0; e < 16; e += 2) {
+              const float2 iv = *reinterpret_cast<const float2*>(m.iv + g16 * 16 + e);
+              each[0] = __fmaf_rn(exp2_fast(__uint_as_float(s[e]) + off), iv.x, each[0]);
+              each[1] = __fmaf_rn(exp2_fast(__uint_as_float(s[e + 1]) + off), iv.y, each[1]);
             }
-            l += each;
+            l += each[0] + each[1];
           }
         }
         uint32_t pk[16];                   // 32 columns
         auto weights = [&](int g16, auto which, const uint32_t (&s)[16]) {
           constexpr int h = decltype(which)::value;
-          float f = sl2, add = 0.f;
+          float f = f_tile, add = add_tile;
           [[maybe_unused]] float unit = 0.f;
-          if constexpr (CODED) factor(g16, f, add, unit);
+          if constexpr (CODED && !BOXED) factor(g16, f, add, unit);
           add += off;
           const uint64_t fp = pair(f, f), addp = pair(add, add);
-          uint64_t mine[2] = {0, 0};       // 8 bits: the group's sum
+          uint64_t mine[2] = {0, 0};       // the group's sum
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float2 x = unpair(fma2(pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), fp, addp));
             const float w0 = exp2_fast(x.x), w1 = exp2_fast(x.y);
-            uint64_t& to = CODED ? mine[e & 1] : sum[e & 1];
+            uint64_t& to = CODED && !BOXED ? mine[e & 1] : sum[e & 1];
             to = add2(to, pair(w0, w1));
             pk[8 * h + e] = CODED ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
           }
-          if constexpr (CODED) sum[h] = fma2(add2(mine[0], mine[1]), pair(unit, unit), sum[h]);
+          if constexpr (CODED && !BOXED) sum[h] = fma2(add2(mine[0], mine[1]), pair(unit, unit), sum[h]);
         };
 #pragma unroll 1
         for (int g16 = 0; g16 < kGroups; g16 += 2) {
@@ -1380,7 +1417,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           }
         }
         const float2 all = unpair(add2(sum[0], sum[1]));
-        l += all.x + all.y;
+        l += CODED && BOXED ? (all.x + all.y) * unit_tile : all.x + all.y;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c.meta_empty[k % kMeta]));
         if ((j & 15) == 15 && __any_sync(0xffffffffu, dead)) break;
