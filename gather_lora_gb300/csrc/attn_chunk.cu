@@ -843,18 +843,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             constexpr int CH = D / 16, RPI = 32 / CH, NI = 32 / RPI;
             const int ch = lane % CH, r0 = q * 32 + lane / CH;
             const uint32_t from = at + Sh::tile_bytes / 2 + ch * 16;
-            auto convert = [&](int r, const uint4& v) {
-              const uint32_t m = __shfl_sync(0xffffffffu, mult, r - q * 32);
+            // The lane's two chunks of f16 in its first row (lanes of the upper half of a row store them in the other order: no bank
+            // twice); in its i-th one RPI rows further, where rows four apart swap halves of the swizzle.
+            const bool swap = CH == 8 && ch >= 4;
+            const uint32_t to1 = at + Sh::at(r0, 2 * ch + swap), to2 = at + Sh::at(r0, 2 * ch + !swap);
+            auto convert = [&](int i, const uint4& v) {
+              const uint32_t m = __shfl_sync(0xffffffffu, mult, lane / CH + i * RPI), flip = RPI == 4 ? (i & 1) * 64 : 0;
               uint4 a = scaled8<FMT>(v.x, v.y, m), b = scaled8<FMT>(v.z, v.w, m);
-              if (x && partly && part_seen(t0 - q * 32 + r) && !(chunk_finite<true>(a) && chunk_finite<true>(b))) {
+              if (x && partly && part_seen(t0 - q * 32 + r0 + i * RPI) && !(chunk_finite<true>(a) && chunk_finite<true>(b))) {
                 bad = true;
                 a = chunk_or_zero<true>(a);
                 b = chunk_or_zero<true>(b);
               }
-              // (lanes of the upper half of a row store their chunks in the other order: no bank twice)
-              const bool swap = CH == 8 && ch >= 4;
-              sts128(at + Sh::at(r, 2 * ch + swap), swap ? b : a);
-              sts128(at + Sh::at(r, 2 * ch + !swap), swap ? a : b);
+              sts128((to1 ^ flip) + i * RPI * 128, swap ? b : a);
+              sts128((to2 ^ flip) + i * RPI * 128, swap ? a : b);
             };
             if constexpr (D == 64) {
               uint4 v[NI];
@@ -862,15 +864,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
               for (int i = 0; i < NI; ++i) v[i] = lds128(from + (r0 + i * RPI) * D);
               takers_sync();
 #pragma unroll
-              for (int i = 0; i < NI; ++i) convert(r0 + i * RPI, v[i]);
+              for (int i = 0; i < NI; ++i) convert(i, v[i]);
             } else {
               uint4 next = lds128(from + r0 * D);
-#pragma unroll 1
+#pragma unroll 2
               for (int i = 0; i < NI; ++i) {
                 const uint4 v = next;
                 if (i + 1 < NI) next = lds128(from + (r0 + (i + 1) * RPI) * D);
                 __syncwarp();              // (all lanes have read these rows)
-                convert(r0 + i * RPI, v);
+                convert(i, v);
               }
             }
             fence_proxy_async_smem();
