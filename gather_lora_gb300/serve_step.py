@@ -10,9 +10,14 @@
 `prefill` takes prompts, or further chunks of prompts whose first part is cached (read back with
 lora_kv_read), `decode` one new token per sequence. Pages come from a plain free list.
 
+With positions (`rotary`), head norms (`norms`) or a sliding window (`window`, `sinks`) the new rows are normed and
+rotated on their way into the cache (lora_kv_append) and attend over the cache itself: chunks by
+lora_attn_chunk, single tokens by lora_attn_decode or lora_attn_decode_window. New prompts without a window are
+rotated in their rows (lora_qk_rope) and take lora_attn_prefill.
+
     python -m gather_lora_gb300.serve_step        # a small run on the current GPU, checked against itself
 
-There is no position encoding, normalisation or MLP here: the layer shows how the calls fit together.
+There is no MLP here: the layer shows how the calls fit together.
 """
 from __future__ import annotations
 
@@ -23,7 +28,13 @@ from . import lib as L
 
 class AttentionLayer:
     def __init__(self, hidden=512, q_heads=8, kv_heads=2, head_dim=64, max_loras=4, rank=16, pages=64, page_size=16,
-                 cache="e4m3", device="cuda", seed=0):
+                 cache="e4m3", device="cuda", seed=0, rotary=None, norms=False, window=None, sinks=0):
+        """rotary: an L.Rope for head_dim (one position axis: the place in the sequence); norms: RMS norms of the query and
+        key heads; window, sinks: a row sees the last `window` tokens up to itself and the first `sinks`."""
+        if rotary is not None and (rotary.struct.head_dim != head_dim or rotary.struct.axes != 1):
+            raise ValueError(f"rotary is for head_dim {rotary.struct.head_dim} and {rotary.struct.axes} axes: {head_dim} and 1 are wanted")
+        if (window is not None and window < 1) or sinks < 0:
+            raise ValueError(f"window {window}, sinks {sinks}: at least 1 and 0")
         g = torch.Generator(device=device).manual_seed(seed)
         self.hidden, self.hq, self.hkv, self.d, self.rank, self.max_loras = hidden, q_heads, kv_heads, head_dim, rank, max_loras
         self.page_size, self.device = page_size, torch.device(device)
@@ -51,6 +62,14 @@ class AttentionLayer:
         self.tables = {}                     # sequence -> its pages
         self.lengths = {}                    # sequence -> cached tokens
         self.workspace = torch.zeros(L.ATTN_WORKSPACE, dtype=torch.uint8, device=device)
+        # positions, norms, window
+        self.window, self.sinks = L.NO_WINDOW if window is None else window, sinks
+        self.plain = rotary is None and not norms
+        self.norms = [(1 + 0.1 * torch.randn(head_dim, generator=g, device=device)).bfloat16() if norms else None for _ in range(2)]
+        if not self.plain:
+            self.rotary = L.Rope(head_dim, rotary_dim=0) if rotary is None else rotary
+        if not self.plain or window is not None:
+            self.chunk_workspace = torch.empty(L.CHUNK_WORKSPACE, dtype=torch.uint8, device=device)
 
     def _fold(self, name, x, out, column, seq_slot):
         """The adapters of projection `name` folded into out[:, column : column + n_out], in place."""
@@ -98,12 +117,52 @@ class AttentionLayer:
         L.lora_kv_write(qkv.data_ptr() + 2 * q, qkv.stride(0), qkv.data_ptr() + 2 * (q + k), qkv.stride(0), slots,
                         qkv.shape[0], self.cache)
 
+    def _turn(self, qkv, positions):
+        """Queries and keys normed and rotated in their rows."""
+        q = self.widths[0]
+        L.lora_qk_rope(qkv, qkv.stride(0), qkv, qkv.stride(0), qkv.data_ptr() + 2 * q, qkv.stride(0), qkv.data_ptr() + 2 * q, qkv.stride(0),
+                       qkv.shape[0], self.hq, self.hkv, self.rotary, positions, qkv.shape[0], q_norm=self.norms[0], k_norm=self.norms[1])
+
+    def _append(self, qkv, slots, positions):
+        """The same, keys and values going into their pages; or, without positions and norms, those alone."""
+        if self.plain:
+            return self._write(qkv, slots)
+        q, k, _ = self.widths
+        L.lora_kv_append(qkv, qkv.stride(0), qkv, qkv.stride(0), self.hq, qkv.data_ptr() + 2 * q, qkv.stride(0), qkv.data_ptr() + 2 * (q + k),
+                         qkv.stride(0), slots, qkv.shape[0], self.cache, self.rotary, positions, qkv.shape[0], q_norm=self.norms[0], k_norm=self.norms[1])
+
+    def _table(self, seqs):
+        """Block table of the sequences: its width, the pages (-1: none)."""
+        width = max((len(self.tables[s]) for s in seqs), default=0)
+        return width, torch.tensor([self.tables[s] + [-1] * (width - len(self.tables[s])) for s in seqs], dtype=torch.int32, device=self.device)
+
+    def _positions(self, before, counts):
+        return torch.tensor([b + i for b, n in zip(before, counts) for i in range(n)], dtype=torch.int32, device=self.device)
+
+    def _over_cache(self, x, seqs, before, counts, seq_slot, slots):
+        """Prompts or chunks that attend over the cache."""
+        qkv = self._qkv(x, seq_slot)
+        self._append(qkv, slots, self._positions(before, counts))
+        for s, b, n in zip(seqs, before, counts):
+            self.lengths[s] = b + n
+        a = torch.empty(x.shape[0], self.widths[0], dtype=torch.bfloat16, device=self.device)
+        cu = torch.tensor([sum(counts[:i]) for i in range(len(counts) + 1)], dtype=torch.int32, device=self.device)
+        lens = torch.tensor([self.lengths[s] for s in seqs], dtype=torch.int32, device=self.device)
+        width, table = self._table(seqs)
+        L.lora_attn_chunk(qkv, qkv.stride(0), a, a.stride(0), cu, len(seqs), x.shape[0], self.hq, self.d ** -0.5, self.cache, table, width, width,
+                          lens, self.window, self.sinks, self.chunk_workspace, self.chunk_workspace.numel())
+        return self._out(a, seq_slot)
+
     def prefill(self, x, seqs, counts, seq_slot):
         """Rows x [sum(counts), hidden] of the sequences `seqs`, each after what of it is cached already."""
         self._check(x, seqs, counts, seq_slot)
         before = [self.lengths.get(s, 0) for s in seqs]
         slots = torch.cat([self._slots(s, b, n) for s, b, n in zip(seqs, before, counts)]).to(self.device)
+        if self.window != L.NO_WINDOW or (not self.plain and any(before)):
+            return self._over_cache(x, seqs, before, counts, seq_slot, slots)
         qkv = self._qkv(x, seq_slot)
+        if not self.plain:
+            self._turn(qkv, self._positions(before, counts))
         self._write(qkv, slots)
         for s, b, n in zip(seqs, before, counts):
             self.lengths[s] = b + n
@@ -129,17 +188,19 @@ class AttentionLayer:
         self._check(x, seqs, [1] * len(seqs), seq_slot)
         slots = torch.cat([self._slots(s, self.lengths.get(s, 0), 1) for s in seqs]).to(self.device)
         qkv = self._qkv(x, seq_slot)
-        self._write(qkv, slots)
+        self._append(qkv, slots, self._positions([self.lengths.get(s, 0) for s in seqs], [1] * len(seqs)))
         for s in seqs:
             self.lengths[s] = self.lengths.get(s, 0) + 1
-        width = max(len(self.tables[s]) for s in seqs)
-        table = torch.tensor([self.tables[s] + [-1] * (width - len(self.tables[s])) for s in seqs], dtype=torch.int32,
-                             device=self.device)
+        width, table = self._table(seqs)
         lens = torch.tensor([self.lengths[s] for s in seqs], dtype=torch.int32, device=self.device)
         q = self.widths[0]
         a = torch.empty(x.shape[0], q, dtype=torch.bfloat16, device=self.device)
-        L.lora_attn_decode(qkv, qkv.stride(0), a, q, len(seqs), self.hq, self.d ** -0.5, self.cache, table, width, width, lens,
-                           self.workspace, self.workspace.numel())
+        if self.window == L.NO_WINDOW:
+            L.lora_attn_decode(qkv, qkv.stride(0), a, q, len(seqs), self.hq, self.d ** -0.5, self.cache, table, width, width, lens,
+                               self.workspace, self.workspace.numel())
+        else:
+            L.lora_attn_decode_window(qkv, qkv.stride(0), a, q, len(seqs), self.hq, self.d ** -0.5, self.cache, table, width, width, lens,
+                                      self.window, self.sinks, self.workspace, self.workspace.numel())
         return self._out(a, seq_slot)
 
     def release(self, seq):
@@ -149,11 +210,14 @@ class AttentionLayer:
 
 def main() -> None:
     """Three requests with different adapters: prompts, a second chunk for one, then decode steps; the
-    same rows through one prefill call on a fresh layer must agree (the cache's rounding apart)."""
+    same rows through one prefill call on a fresh layer must agree (the cache's rounding apart). Then with positions and
+    head norms, and with a sliding window beside them."""
     counts, extra, steps, hidden = [37, 5, 70], 20, 3, 512
     g = torch.Generator(device="cuda").manual_seed(1)
-    for cache, most in (("bf16", 0.02), ("int8", 0.03), ("e4m3", 0.1)):
-        layer, whole = (AttentionLayer(hidden, cache=c) for c in (cache, "bf16"))
+    turned = dict(rotary=L.Rope(64), norms=True)
+    for cache, most, more in (("bf16", 0.02, {}), ("int8", 0.03, {}), ("e4m3", 0.1, {}), ("bf16", 0.02, turned), ("int8", 0.03, turned),
+                              ("e4m3", 0.1, turned), ("bf16", 0.02, dict(turned, window=24, sinks=2)), ("e4m3", 0.1, dict(turned, window=24, sinks=2))):
+        layer, whole = (AttentionLayer(hidden, cache=c, **more) for c in (cache, "bf16"))
         adapter = [0, -1, 2]
         rows = [torch.randn(n + (extra if s == 1 else 0) + steps, hidden, generator=g, device="cuda").bfloat16()
                 for s, n in enumerate(counts)]
@@ -172,7 +236,7 @@ def main() -> None:
         want = whole.prefill(torch.cat(rows), [0, 1, 2], [r.shape[0] for r in rows], torch.cat(slot))
         have = torch.cat([torch.cat(p) for p in got])
         off = ((have.double() - want.double()).norm() / want.double().norm()).item()
-        print(f"cache {cache}: {have.shape[0]} rows over prompts, a chunk and decode steps, {off:.4f} off one prefill")
+        print(f"cache {cache}{', positions and norms' if more else ''}{', window' if 'window' in more else ''}: {have.shape[0]} rows over prompts, a chunk and decode steps, {off:.4f} off one prefill")
         assert off < most, (cache, off)
 
 
