@@ -16,7 +16,15 @@
 // Layout. A team of D / 8 lanes holds a head row, 8 values a lane: four pairs, so that no lane needs another's values for
 // the rotation (halves apart: elements 4 i .. and rotary_dim / 2 + 4 i ..; neighbours: 8 i .. 8 i + 7), and the rows' sums and
 // maxima take 3 or 4 shuffles. A team takes kHeads heads of one token, in the order q, k, v: their loads are in flight
-// together and the lane's four sines and cosines serve all of them. Calls too small to fill the GPU with that take one.
+// together and the lane's four sines and cosines serve all of them; the teams of a warp take the same heads of consecutive tokens,
+// so that a warp does not go through what is done for queries, keys and values one after another. Calls too small to fill the
+// GPU with that take one head a team.
+//
+// Measured on a GB300 (copy rate 6.8 TB/s): 16411 rows of 28 + 4 heads of 128 in 45 us (6.0 TB/s); appended with 8 key-value heads,
+// 20011 rows of 32 heads of 128 in BF16 82 us (6.0 TB/s; heads side by side in a warp instead of tokens 89), in E4M3 97 (4.7), 40009
+// rows of 32 heads of 64 in INT8 93 (4.9). HBM bounds the 16-bit forms, the 8-bit ones instruction issue (INT8: 74% of it, 21
+// instructions a value). A fourth block an SM is worth its registers in INT8 (99 -> 93), not in E4M3 (spills, 97 -> 99) or BF16
+// (82 -> 85). A few rows are latency: the host's time for the call and two trips to memory.
 #include "attn_common.cuh"
 
 namespace glora {
@@ -34,12 +42,19 @@ __device__ __forceinline__ void unpack4(const uint2& v, float (&f)[4]) {
 }
 __device__ __forceinline__ uint2 pack4(const float (&f)[4]) { return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])); }
 
+// Tokens of a unit, and units that a block has in hand at a time: with several heads a team, the teams of a warp take the same heads
+// of consecutive tokens.
+template <int D, int U>
+struct RopeUnits {
+  static constexpr int tokens = U > 1 ? 32 / (D / 8) : 1, takers = kRopeThreads / (U > 1 ? 32 : D / 8);
+};
+
 }  // namespace
 
 // FMT: the cache's format, or kRopeRows. INTER: pairs are neighbours. U: heads of a team at a time.
 template <int FMT, int D, bool INTER, int U>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs p) {
-  constexpr int TPR = D / 8, TEAMS = kRopeThreads / TPR;
+__global__ void __launch_bounds__(kRopeThreads, FMT == kKvInt8 && U > 1 ? 4 : 0) rope_kernel(const __grid_constant__ RopeArgs p) {
+  constexpr int TPR = D / 8, TOKS = RopeUnits<D, U>::tokens, TAKERS = RopeUnits<D, U>::takers;
   __shared__ __align__(16) unsigned long long s_turns[64];
   __shared__ __align__(4) unsigned char s_axis[64];
   const int tid = threadIdx.x, i = tid % TPR;
@@ -54,17 +69,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int lo = INTER || !turns ? 8 * i : 4 * i, hi = INTER || !turns ? 8 * i + 4 : half + 4 * i;   // the lane's elements: four from each
   const int heads = p.q_heads + p.kv_heads * (FMT == kRopeRows ? 1 : 2), groups = (heads + U - 1) / U;
 
-  // Units: (token, U of its heads). Consecutive teams take consecutive units.
-  const long long unit = static_cast<long long>(blockIdx.x) * TEAMS + tid / TPR, stride = static_cast<long long>(gridDim.x) * TEAMS;
+  // Units: (TOKS tokens, U of their heads).
+  const int who = TOKS > 1 ? __shfl_sync(0xffffffffu, tid >> 5, 0) : tid / TPR;
+  const long long unit = static_cast<long long>(blockIdx.x) * TAKERS + who, stride = static_cast<long long>(gridDim.x) * TAKERS;
   const int step_tok = static_cast<int>(stride / groups), step_grp = static_cast<int>(stride - static_cast<long long>(step_tok) * groups);
   long long tok = unit / groups;
   int grp = static_cast<int>(unit - tok * groups);
+  tok = tok * TOKS + (TOKS > 1 ? (tid & 31) / TPR : 0);
 
   pdl_wait_then_release();
 
   // Teams of a warp stay together: the shuffles below need all of its lanes.
-  const long long first_of_warp = static_cast<long long>(blockIdx.x) * TEAMS + (tid & ~31) / TPR;
-  const long long units = static_cast<long long>(p.n) * groups;
+  const long long first_of_warp = TOKS > 1 ? unit : static_cast<long long>(blockIdx.x) * TAKERS + (tid & ~31) / TPR;
+  const long long units = static_cast<long long>((p.n + TOKS - 1) / TOKS) * groups;
   for (long long w = first_of_warp; w < units; w += stride) {
     const bool live = tok < p.n;
     uint2 x[U][2];
@@ -194,11 +211,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         }
       }
     }
-    tok += step_tok;
+    tok += static_cast<long long>(step_tok) * TOKS;
     grp += step_grp;
     if (grp >= groups) {
       grp -= groups;
-      ++tok;
+      tok += TOKS;
     }
   }
 }
@@ -207,9 +224,9 @@ namespace {
 
 template <int FMT, int D, bool INTER, int U>
 int launch_units(const RopeArgs& a, void* stream) {
-  constexpr int TEAMS = kRopeThreads / (D / 8);
-  const long long heads = a.q_heads + a.kv_heads * (FMT == kRopeRows ? 1LL : 2LL), units = (heads + U - 1) / U * a.n;
-  const long long blocks = (units + TEAMS - 1) / TEAMS;
+  constexpr int TOKS = RopeUnits<D, U>::tokens, TAKERS = RopeUnits<D, U>::takers;
+  const long long heads = a.q_heads + a.kv_heads * (FMT == kRopeRows ? 1LL : 2LL), units = (heads + U - 1) / U * ((a.n + TOKS - 1) / TOKS);
+  const long long blocks = (units + TAKERS - 1) / TAKERS;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks < 152 * 8 * 4 ? blocks : 152 * 8 * 4), 1, 1);
   cfg.blockDim = dim3(kRopeThreads, 1, 1);
