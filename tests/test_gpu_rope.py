@@ -211,6 +211,13 @@ def test_append(fmt, d, rot, inter, axes, layout, n, hq, hkv, page):
     assert ((code * scale - y).abs() <= half + 2.0 ** -22 * top + 2 * e).all()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("d,inter,n", [(64, False, 4003), (64, True, 4001), (128, False, 2003)])
+def test_append_in_large_calls(fmt, d, inter, n):
+    """Heads in fours and tokens side by side in a warp, neither count a multiple."""
+    test_append(fmt, d, d, inter, 1, "hnd", n, 33, 4, 16)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_append_rows_that_are_not_finite_or_all_but_zero(fmt):
     """A key head with NaN or an infinity: scale NaN, codes 0; one below 2^-100: zeros; its neighbours as ever."""
