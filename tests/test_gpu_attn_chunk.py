@@ -309,3 +309,32 @@ def test_one_row_is_the_decode_call():
     q = q.contiguous()
     for got in (run(cache, table, q, cu, lens, 8, 0.1), A.run_decode(q, cache, table, A.int32(lens), 8, 0.1)):
         R.check(got.view(want.shape), want, bound)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_as_many_sequences_as_a_call_takes(fmt):
+    """8192 sequences, many threads' worth of the plan's: every one as its like among seven."""
+    nl = [(1, 1), (2, 40), (0, 130), (1, 0), (3, 77), (1, 260), (2, 1)]
+    cache, kval, vval, table, q, cu, lens = case(50, nl, 1, 2, 64, 16, fmt)
+    out, _, bound, _ = S.chunk_want(q, kval, vval, table, cu, lens, 16, 0.1, 2, rounded=ROUNDED if fmt != "bf16" else 0.0)
+    if fmt != "bf16":
+        bound = bound + f16_floor(vval, lens)
+    like = [b * 5 % 7 for b in range(8192)]
+    rows = torch.tensor([r for b in like for r in range(cu[b], cu[b + 1])], device="cuda")
+    got = run(cache, table[torch.tensor(like, device="cuda")].contiguous(), q[rows], starts([nl[b][0] for b in like]), [lens[b] for b in like], 2, 0.1)
+    R.check(got.view(len(rows), 2, 64), out[rows], bound[rows], "8192")
+
+
+def test_two_calls_at_once():
+    """On two streams, each with a workspace of its own: the bits that they give one after another."""
+    data = [case(60 + i, [(300 + i, 3000), (5, 700)], 2, 4, 128, 16, "bf16") for i in range(2)]
+    apart = [run(c, t, q, cu, lens, 8, 0.1) for c, _, _, t, q, cu, lens in data]
+    streams, spaces, outs = [torch.cuda.Stream() for _ in range(2)], [workspace() for _ in range(2)], [torch.full_like(a, float("nan")) for a in apart]
+    ints = [(A.int32(d[5]), A.int32(d[6])) for d in data]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (c, _, _, t, q, _, _), (cu, lens), s, ws, o in zip(data, ints, streams, spaces, outs):
+            run(c, t, q, cu, lens, 8, 0.1, ws=ws, out=o, stream=s)
+    torch.cuda.synchronize()
+    for a, o in zip(apart, outs):
+        assert torch.equal(a, o)
