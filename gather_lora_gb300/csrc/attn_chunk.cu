@@ -1495,10 +1495,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           mine[rr] = n > 0 ? exponent : -INFINITY;
           mine[2 * kTile + rr] = n > 0 ? l : 0.f;
         }
-        if (tid == 0) {
-          mine[FLAG] = __int_as_float(*reinterpret_cast<volatile int*>(&c.bad[sl]));
-          if (w.ta == 0) begun = true;
-        }
+        // Each row tile says for itself whether something in V was set to zero: it has waited for its last P V, before which that is
+        // known of every tile that its rows see. (The other row tile's tiles may go on behind its own.)
+        if (tid % (kSoftWarps / 2 * 32) == 0) mine[FLAG + i] = __int_as_float(*reinterpret_cast<volatile int*>(&c.bad[sl]));
+        if (tid == 0 && w.ta == 0) begun = true;
         if (w.ta == 0 && tid < static_cast<int>(sizeof(ChunkPiece) / 4))
           reinterpret_cast<int*>(static_cast<unsigned char*>(p.workspace) + static_cast<long long>(me) * kHead)[tid] = reinterpret_cast<const int*>(&w)[tid];
         if (i * kTile + (warp & 3) * 32 < rows) {
@@ -1589,8 +1589,10 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
         p.lse[(static_cast<long long>(w.row0) + tok) * p.q_heads + w.h0 + rg] = log_sum<CODED>(e_all, l_all);
     }
   } else {
-    for (int y = tid - 32; y < count; y += 224)
-      if (__float_as_int(__ldcg(slot_of(y) + FLAG)) != 0) s_bad = 1;
+    for (int y = tid - 32; y < count; y += 224) {
+      const int2 flags = __ldcg(reinterpret_cast<const int2*>(slot_of(y) + FLAG));
+      if ((flags.x | flags.y) != 0) s_bad = 1;
+    }
   }
   __syncthreads();
   // A team of D / 4 lanes a row, 16 bytes a lane and part: T rows and Y parts of each thread in flight together.
