@@ -359,8 +359,8 @@ __device__ __noinline__ void add_not_finite(const ChunkArgs& p, const ChunkPiece
   const int i = warp >> 2, r0 = (warp & 3) * 32, GB = p.head_block, TT = p.tile_tokens;
   const int32_t* const table = p.table + w.b * p.table_stride;
   for (int t_in = r0 / GB; t_in <= (r0 + 31) / GB && t_in < TT; ++t_in) {
+    if (i * TT + t_in > w.end - w.first) break;
     const int pos = w.first + i * TT + t_in;
-    if (pos > w.end) break;
     if (pos < 0) continue;
     float s[E];
 #pragma unroll
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           w.n = tiles_here();
 #pragma unroll
           for (int i = 0; i < 2; ++i) {                 // tiles that hold a token its last row may see
-            const int last = min(w.first + (i + 1) * TT - 1, w.end), any = w.first + i * TT <= w.end && last >= 0;
+            const int last = w.first + min((i + 1) * TT, t1 - t0) - 1, any = i * TT < t1 - t0 && last >= 0;
             w.ni[i] = any ? max(0, min(w.ta + w.n, last / kTile + 1 - w.skip) - w.ta) : 0;
           }
           w.c0 = static_cast<int>(divide((s0 + kItemCost + snap + 1) * ctas + total - 1, total)) - 1;
@@ -1232,8 +1232,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       __syncwarp();
       const ChunkPiece& w = c.piece[sl];
       if (!w.valid) break;               // (the only way out: all eight warps meet at the joins' barriers)
-      const int pos = w.first + i * TT + t_in, n = w.ni[i];
-      const bool live = t_in < TT && g < w.heads && pos <= w.end;
+      const int at_row = i * TT + t_in, n = w.ni[i];
+      const bool live = t_in < TT && g < w.heads && at_row <= w.end - w.first;
+      const int pos = w.first + min(at_row, w.end - w.first);      // (the rows behind stand there too: positions go up to 2^31 - 65)
       float qf = 1.f;                      // 8 bits: Q was divided by it
       if constexpr (CODED) {               // Q from BF16 to f16, the row's largest magnitude at 2^14 .. 2^15, by a power of two
         wait(c, c.q_landed, it & 1);
