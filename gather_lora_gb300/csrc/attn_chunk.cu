@@ -74,6 +74,7 @@ constexpr int kFewPairs = 8;                    // sequences of more row-tile pa
 // Workspace: a head per CTA (the item that it begins and does not end, if any), then 2 slots per CTA (of the item that it goes on
 // with, of the one it begins): exponent[256], sum[256], O[256][D], 4 words of flags. All written anew by every call.
 constexpr int kHead = 128, kHeadBytes = 32768;
+constexpr int kGone = 2;                        // in a slot's flags: its CTA has failed
 template <int D>
 constexpr int kSlotFloats = 2 * 2 * kTile + 2 * kTile * D + 4;
 static_assert(kMostCtas * kHead <= kHeadBytes && kHeadBytes + 2LL * kMostCtas * kSlotFloats<128> * 4 <= (48 << 20), "workspace");
@@ -142,14 +143,22 @@ struct ChunkSmem {
 __device__ __forceinline__ bool failed(const ChunkCtl& c) { return *reinterpret_cast<const volatile int*>(&c.failed) != 0; }
 
 // Bounded wait; true if the CTA has failed: warp 10 watches over all of them and says so when no key tile has been taken up
-// for kWaitLimitCycles. Then all waits end at once, the roles go through the pieces that are left and nothing more is stored (what
-// runs on until then stays in bounds). (Small, as it is inlined at every wait: the roles' loops share the instruction caches.)
+// for kWaitLimitCycles. Then all waits end at once. A piece is read only by who saw, behind the wait for it, that the CTA had not
+// failed (piece_here), as only then it is known to be there; the others leave, and so do loops over its tiles. The planning warp publishes
+// and overwrites nothing any more. What runs on until then stays in bounds; results are not stored, nor joined from what this CTA
+// put into the workspace. (Small, as it is inlined at every wait: the roles' loops share the instruction caches.)
 __device__ __forceinline__ bool wait(ChunkCtl& c, unsigned long long& bar, uint32_t parity) {
   const uint32_t b = smem_u32(&bar);
 #pragma unroll 1
   while (!mbar_try_wait(b, parity, 100000))
     if (failed(c)) return true;
   return false;
+}
+// The whole warp: the next piece is there and is one (not the end).
+__device__ __forceinline__ bool piece_here(ChunkCtl& c, int it) {
+  wait(c, c.piece_full[it % kPieces], (it / kPieces) & 1);
+  __syncwarp();
+  return !__any_sync(0xffffffffu, failed(c)) && c.piece[it % kPieces].valid;
 }
 __device__ __forceinline__ bool passed(unsigned long long& bar, uint32_t parity) {
   uint32_t done;
@@ -172,6 +181,16 @@ __device__ __forceinline__ void copies_left() {
 }
 
 __device__ __forceinline__ void takers_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(kTakers * 32) : "memory"); }
+// The same, and whether one of the warps has seen that the CTA failed: they stay together, as the others would wait at the next
+// barrier for one that has left.
+__device__ __forceinline__ bool takers_failed(const ChunkCtl& c) {
+  uint32_t any;
+  asm volatile("{\n .reg .pred f, a;\n setp.ne.u32 f, %1, 0;\n bar.red.or.pred a, 1, %2, f;\n selp.u32 %0, 1, 0, a;\n}\n"
+               : "=r"(any)
+               : "r"(static_cast<uint32_t>(failed(c))), "n"(kTakers * 32)
+               : "memory");
+  return any != 0;
+}
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -454,6 +473,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     }
     mbar_init(smem_u32(&c.drain), 1);
     mbar_init(smem_u32(&c.ended), kSoftWarps);
+    for (int i = 0; i < kPieces; ++i) c.piece[i].valid = 0;
     c.failed = 0;
     c.progress = 0;
     mbar_fence_init();
@@ -612,13 +632,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     uint32_t loads = 0;
     for (int it = 0;; ++it) {
       const int sl = it % kPieces;
-      // (a slot is written again only when all have left it, after a failure too: nobody stops before the last piece)
-      if (it >= kPieces && wait(c, c.piece_empty[sl], ((it / kPieces) - 1) & 1))
-        mbar_wait_limit(smem_u32(&c.piece_empty[sl]), ((it / kPieces) - 1) & 1, kDrainLimitCycles);
+      // (a slot is written again only when all have left it; after a failure not at all, as some may still be reading)
+      if (it >= kPieces) wait(c, c.piece_empty[sl], ((it / kPieces) - 1) & 1);
       __syncwarp();
-      const bool go = u < u1 && !__any_sync(0xffffffffu, failed(c));
+      if (__any_sync(0xffffffffu, failed(c))) break;
+      const bool go = u < u1;
       if (lane == 0) {
-        ChunkPiece w;
+        ChunkPiece w{};
         w.valid = go;
         if (go) {
           const int t0 = x * step, t1 = min(t0 + step, s.n);
@@ -695,10 +715,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     uint32_t kt = 0, tiles = 0;          // key tiles of the pieces before; issued
     for (int it = 0;; ++it) {
       const int sl = it % kPieces;
-      wait(c, c.piece_full[sl], (it / kPieces) & 1);
-      __syncwarp();
+      if (!piece_here(c, it)) break;
       const ChunkPiece& w = c.piece[sl];
-      if (!w.valid) break;
       const int32_t* const table = p.table + w.b * p.table_stride;
       auto first_token = [&](int j) {
         const int t = w.ta + j;
@@ -794,21 +812,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     uint32_t kt = 0;
     for (int it = 0;; ++it) {
       const int sl = it % kPieces;
-      wait(c, c.piece_full[sl], (it / kPieces) & 1);
-      __syncwarp();
+      const bool here = piece_here(c, it);
+      if (CODED && takers_failed(c)) break;       // (else all four have the same piece, or the end)
+      if (!here) break;
       const ChunkPiece& w = c.piece[sl];
-      if (!w.valid) break;
       for (int j = 0; j < w.n; ++j) {
         const uint32_t k = kt + j;
         const int tile = w.ta + j, t0 = (tile < w.kept ? tile : tile + w.skip) * kTile + q * 32;
         const bool partly = !(t0 + 31 <= w.first && (t0 > w.end - p.window || t0 + 31 < p.sinks));   // some rows see some of it, others not
         auto part_seen = [&](int t) { return !(t <= w.first && (t > w.end - p.window || t < p.sinks)); };
-        bool bad = false;
+        bool bad = false, gone = false;
         uint32_t mult_k = 0, mult_v = 0;
 #pragma unroll 1
         for (int x = CODED ? 0 : 1; x < 2; ++x) {
           const uint32_t st = 2 * (k % NP) + x, at = ring + st * Sh::tile_bytes;
-          wait(c, c.landed[st], (k / NP) & 1);
+          [[maybe_unused]] const bool late = wait(c, c.landed[st], (k / NP) & 1);
+          if constexpr (!CODED) {
+            gone = __any_sync(0xffffffffu, late);
+            if (gone) break;
+          }
           __syncwarp();
           if constexpr (CODED) {
             if (x == 0) {                  // lane: the token of a row
@@ -826,7 +848,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
               }
               float4* const of_warps = c.extremes[k & 1];        // (two in turn: nobody is two tiles ahead)
               if (lane == 0) of_warps[q] = make_float4(most_k, most_v, least_k, least_v);
-              takers_sync();
+              gone = takers_failed(c);
+              if (gone) break;
 #pragma unroll
               for (int y = 0; y < kTakers; ++y) {
                 const float4 z = of_warps[y];
@@ -904,6 +927,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             mbar_arrive(smem_u32(&c.full[st]));
           }
         }
+        if (gone) break;
       }
       kt += w.n;
       __syncwarp();
@@ -920,10 +944,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const int ch = lane % CH, sub_t = lane / CH;
     for (int it = 0;; ++it) {
       const int sl = it % kPieces;
-      wait(c, c.piece_full[sl], (it / kPieces) & 1);
-      __syncwarp();
+      if (!piece_here(c, it)) break;
       const ChunkPiece& w = c.piece[sl];
-      if (!w.valid) break;
       const int32_t* const table = p.table + w.b * p.table_stride;
       const int groups = w.n * 2 * kGroups, ta = w.ta, kept = w.kept, skip = w.skip, end = w.end, low = w.low;
       const long long head_off = w.kvh * p.c.head_bytes;
@@ -1124,9 +1146,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     bool dead = false;
     for (int it = 0;; ++it) {
       const int sl = it % kPieces;
-      wait(c, c.piece_full[sl], (it / kPieces) & 1);
-      __syncwarp();
-      const bool valid = __shfl_sync(0xffffffffu, c.piece[sl].valid, 0);
+      const bool valid = piece_here(c, it);
       const int n0 = __shfl_sync(0xffffffffu, c.piece[sl].ni[0], 0), n1 = __shfl_sync(0xffffffffu, c.piece[sl].ni[1], 0);
       const int n = __shfl_sync(0xffffffffu, c.piece[sl].n, 0);
       if (lane == 0) mbar_arrive(smem_u32(&c.piece_empty[sl]));
@@ -1228,10 +1248,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     uint32_t t = 0, kt = 0;              // key tiles of this row tile so far; of the pieces before
     for (int it = 0;; ++it) {
       const int sl = it % kPieces;
-      wait(c, c.piece_full[sl], (it / kPieces) & 1);
-      __syncwarp();
+      if (!piece_here(c, it)) break;
       const ChunkPiece& w = c.piece[sl];
-      if (!w.valid) break;               // (the only way out: all eight warps meet at the joins' barriers)
       const int at_row = i * TT + t_in, n = w.ni[i];
       const bool live = t_in < TT && g < w.heads && at_row <= w.end - w.first;
       const int pos = w.first + min(at_row, w.end - w.first);      // (the rows behind stand there too: positions go up to 2^31 - 65)
@@ -1435,8 +1453,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       }
       for (int j = n; j < w.n; ++j) {      // tiles that this row tile has no use for
         const uint32_t k = kt + j;
-        wait(c, c.meta_full[k % kMeta], (k / kMeta) & 1);
-        __syncwarp();
+        const bool late = wait(c, c.meta_full[k % kMeta], (k / kMeta) & 1);
+        if (__any_sync(0xffffffffu, late)) break;
         if (lane == 0) mbar_arrive(smem_u32(&c.meta_empty[k % kMeta]));
       }
       kt += w.n;
@@ -1549,7 +1567,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && failed(c)) atomicOr(&g_chunk_status, kChunkTimeoutBit);
+  if (tid == 0 && failed(c)) {           // items that this CTA has a part of are not joined
+    atomicOr(&g_chunk_status, kChunkTimeoutBit);
+    float* const slots = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kHeadBytes);
+    for (int y = 2 * blockIdx.x; y < 2 * static_cast<int>(blockIdx.x) + 2; ++y)
+      slots[static_cast<long long>(y) * kSlotFloats<D> + kSlotFloats<D> - 4] = __int_as_float(kGone);
+  }
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(0, 512);
@@ -1562,9 +1585,9 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
   constexpr bool CODED = FMT != kKvBf16;
   constexpr int SF = kSlotFloats<D>, FLAG = SF - 4, T = 32 * (D / 4) / 256, Y = 8 / T > 2 ? 8 / T : 2;
   __shared__ float s_top[32], s_inv[32];
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_gone;
   const int tid = threadIdx.x, r0 = blockIdx.y * 32;
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) s_bad = s_gone = 0;
   pdl_wait_then_release();
   const ChunkPiece& w = *reinterpret_cast<const ChunkPiece*>(static_cast<const unsigned char*>(p.workspace) + static_cast<long long>(blockIdx.x) * kHead);
   if (!__ldcg(&w.valid)) return;
@@ -1574,9 +1597,9 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
   // (the item's first CTA has its part in the second of its slots)
   auto slot_of = [&](int y) { return slots + (y == 0 ? 1LL : 2LL * y) * SF; };
   __syncthreads();
+  float e_all = -INFINITY, l_all = 0.f;
   if (tid < 32) {
     const int r = r0 + tid;
-    float e_all = -INFINITY, l_all = 0.f;
     if (r < rows) {
 #pragma unroll 8
       for (int y = 0; y < count; ++y) e_all = fmaxf(e_all, __ldcg(slot_of(y) + r));
@@ -1585,17 +1608,21 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
       for (int y = 0; y < count; ++y) l_all += __ldcg(slot_of(y) + 2 * kTile + r) * exp2_fast(__ldcg(slot_of(y) + r) - from);
       s_top[tid] = from;
       s_inv[tid] = inverse<CODED>(l_all);
-      const int rt = r % kTile / GB, rg = r % kTile - rt * GB, tok = r / kTile * TT + rt;
-      if (p.lse && rt < TT && rg < w.heads && tok < tokens)
-        p.lse[(static_cast<long long>(w.row0) + tok) * p.q_heads + w.h0 + rg] = log_sum<CODED>(e_all, l_all);
     }
   } else {
     for (int y = tid - 32; y < count; y += 224) {
       const int2 flags = __ldcg(reinterpret_cast<const int2*>(slot_of(y) + FLAG));
-      if ((flags.x | flags.y) != 0) s_bad = 1;
+      if (((flags.x | flags.y) & 1) != 0) s_bad = 1;
+      if (((flags.x | flags.y) & kGone) != 0) s_gone = 1;
     }
   }
   __syncthreads();
+  if (s_gone) return;
+  if (p.lse && tid < 32 && r0 + tid < rows) {
+    const int r = r0 + tid, rt = r % kTile / GB, rg = r % kTile - rt * GB, tok = r / kTile * TT + rt;
+    if (rt < TT && rg < w.heads && tok < tokens)
+      p.lse[(static_cast<long long>(w.row0) + tok) * p.q_heads + w.h0 + rg] = log_sum<CODED>(e_all, l_all);
+  }
   // A team of D / 4 lanes a row, 16 bytes a lane and part: T rows and Y parts of each thread in flight together.
   constexpr int LANES = D / 4, TEAMS = 256 / LANES;
   const int team = tid / LANES, d = tid % LANES * 4;
