@@ -554,6 +554,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         at += all;
       }
     }
+    fence_proxy_async_smem();            // the sums' bytes are TMA's next (each thread orders its own accesses before the barrier)
     __syncthreads();
   }
   if (tid == 0 && c.tmem != 0) *reinterpret_cast<volatile int*>(&c.failed) = 1;     // (never: all columns are this CTA's)
