@@ -231,17 +231,17 @@ __device__ __forceinline__ uint4 scaled8(uint32_t c0, uint32_t c1, uint32_t m) {
   }
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
-// Exponent of the power of two of a group whose largest finite scale is `most`: codes times scales are below 2^15 of it.
+// Exponent of the power of two of a group whose largest scale is `most`: codes times scales are below 2^15 of it.
 template <int FMT>
 __device__ __forceinline__ int group_exponent(float most) {
   constexpr int bits = FMT == kKvE4m3 ? 9 : 7;             // codes are below 2^bits
   return max(-120, (__float_as_int(most) >> 23) - 127 + 1 + bits - 15);
 }
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + e) << 23); }
-__device__ __forceinline__ float finite_magnitude(float s) { return fabsf(s) < INFINITY ? fabsf(s) : 0.f; }
-// Scales of 16 tokens differ too much for one power of two.
+__device__ __forceinline__ float magnitude(float s) { return fabsf(s) < INFINITY ? fabsf(s) : INFINITY; }
+// Scales of a tile (of 16 tokens) differ too much for one power of two, or one is not finite.
 constexpr float kWide = 4096.f;
-__device__ __forceinline__ bool wide(float most, float least) { return most > least * kWide; }
+__device__ __forceinline__ bool wide(float most, float least) { return most > least * kWide || most == INFINITY; }
 // What the softmax needs of a group. (One whose scales are all 0 only counts in the sums: 2^-64 keeps it from raising the reference.)
 template <int FMT>
 __device__ __forceinline__ float4 group_of(float most_k, float most_v, float sl2, bool exact) {
@@ -251,18 +251,18 @@ __device__ __forceinline__ float4 group_of(float most_k, float most_v, float sl2
 // What the codes of a token with scale s are multiplied with.
 template <int FMT>
 __device__ __forceinline__ uint32_t scale_of(float s, float most) {
-  return split_f16(most == 0.f && s == s ? 0.f : s * exp2_int(-group_exponent<FMT>(most == 0.f ? 1.f : most)));
+  return split_f16(most == 0.f ? 0.f : s * exp2_int(-group_exponent<FMT>(most)));
 }
-// Token by token: codes of K as they are, of V with the scale's sign (0: they only count in the sum).
+// Token by token: codes of K as they are, of V with the scale's sign (0: they only count in the sum; not finite: NaN, times 0 too).
 constexpr uint32_t kOne = 0x3c00u;
-__device__ __forceinline__ uint32_t sign_of(float s) { return s == 0.f ? 0u : s < 0.f ? 0xbc00u : kOne; }
-// A V scale of 0 is 2^-64 to the weights (see above); below 2^-110, under what lora_kv_write stores, it is 2^-110.
+__device__ __forceinline__ uint32_t sign_of(float s) { return s == 0.f ? 0u : !(fabsf(s) < INFINITY) ? 0x7e00u : s < 0.f ? 0xbc00u : kOne; }
+// A V scale of 0 is 2^-64 to the weights (see above), and so is one that is not finite: the scores and their sum do not go by V. Below 2^-110,
+// under what lora_kv_write stores, it is 2^-110.
 __device__ __forceinline__ float magnitude_of(float v) {
-  return v == 0.f ? 5.421010862427522e-20f : v != v ? v : fmaxf(fabsf(v), 7.703719777548943e-34f);     // (fmaxf drops NaN)
+  return v == 0.f || !(fabsf(v) < INFINITY) ? 5.421010862427522e-20f : fmaxf(fabsf(v), 7.703719777548943e-34f);
 }
 __device__ __forceinline__ float2 scales_of(float k, float v, float sl2) { return make_float2(k * sl2, log2f(magnitude_of(v))); }
-// (NaN: the weight is NaN where it is seen, and 0 times this must stay 0 where it is not)
-__device__ __forceinline__ float over_scale(float v) { return v != v ? 0.f : kSumUnit / magnitude_of(v); }
+__device__ __forceinline__ float over_scale(float v) { return kSumUnit / magnitude_of(v); }
 
 // Chunks of V: whether all is finite, and with what is not set to zero.
 template <bool CODED>
@@ -838,7 +838,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
               ChunkMeta& m = metas[k % kMeta];
               const int r = q * 32 + lane, tt = t0 - q * 32;
               const float sk = m.ks[r], sv = m.vs[r];
-              float most_k = finite_magnitude(sk), most_v = finite_magnitude(sv);
+              float most_k = magnitude(sk), most_v = magnitude(sv);
               float least_k = most_k == 0.f ? INFINITY : most_k, least_v = most_v == 0.f ? INFINITY : most_v;
 #pragma unroll
               for (int o = 1; o < 32; o <<= 1) {
@@ -1087,7 +1087,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           const uint32_t at = ring + stage_of(g) * Sh::tile_bytes;
           const int r0 = (g % kGroups) * kGroup, t0 = token0(g);
           // The group's powers of two (lanes 16 .. 31 as lanes 0 .. 15), a token's scale over them.
-          float most_k = finite_magnitude(k_scale), most_v = finite_magnitude(v_scale);
+          float most_k = magnitude(k_scale), most_v = magnitude(v_scale);
           float least_k = most_k == 0.f ? INFINITY : most_k, least_v = most_v == 0.f ? INFINITY : most_v;
 #pragma unroll
           for (int o = 1; o < kGroup; o <<= 1) {

@@ -90,3 +90,47 @@ def test_last_tiles_of_windows_and_packed_chunks(fmt, d, kv, G, page, window, si
             for x, t in enumerate((m - 1 - head % 5, m - n // 3, max(0, m - n - window + n // 2) if window < m else m - 3)):
                 put(cache, vval, page, table, b, head, t, (5 * head + 17 * x + b) % d, (INF, -INF, NAN)[(b + x) % 3])
     same_everywhere(data, kv * G, 0.1, window, sinks)
+
+
+def spoil_scales(cache, page, table, b, t, head, bad):
+    pg, sl = C.place(table, page, b, t)
+    cache.tensors[3][pg, head, sl] = bad
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("d,G,page", [(64, 1, 16), (128, 4, 16), (128, 2, 20)])
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("spread", [1.0, 1e4])                         # (1e4: scales of a tile too far apart for one factor)
+def test_the_sum_of_the_weights_does_not_go_by_v(fmt, d, G, page, bad, spread):
+    """A V scale that is not finite, in tokens that all rows see and in tokens that some see: lse is what it is without V,
+    the rows that see the token are NaN in that head and the others are as they were."""
+    kv, nl = 2, [(200, 500), (3, 130), (300, 3000)]
+    cache, kval, vval, table, q, cu, lens = C.case(d + G, nl, kv, G, d, page, fmt)
+    cache.tensors[3][:, :, ::3] *= spread
+    vval[:, :, ::3] *= spread
+    h, clean = kv * G, C.run(cache, table, q, cu, lens, kv * G, 0.1).view(-1, kv, G, d)
+    _, wl, _, _ = S.chunk_want(q, kval, vval, table, cu, lens, page, 0.1, h, rounded=C.ROUNDED)
+    hit = torch.zeros(q.shape[0], kv, dtype=torch.bool, device="cuda")
+    for b, (n, m) in enumerate(nl):
+        for head, at in ((0, [m - 1, m - n // 2 - 1]), (1, [10] if b else [m - 150])):
+            spoil_scales(cache, page, table, b, at, head, bad)
+            hit[cu[b]:cu[b + 1], head] = S.seen(n, m, S.EVERY, 0)[:, at].any(1)
+    lse = torch.full((q.shape[0], h), 5.0, device="cuda")
+    out = C.run(cache, table, q, cu, lens, h, 0.1, lse=lse).view(-1, kv, G, d)
+    assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], clean[~hit])
+    mag = 0.1 * d * q.double().abs().amax() * kval.abs().amax()
+    C.R.check_lse(lse, wl, mag * (1 + C.ROUNDED * 2 ** 24 / 140), "lse")
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("page", [16, 20])
+def test_a_scale_that_is_not_finite_among_zeros(fmt, page):
+    """All other scales of V are 0: the rows that see the one token are not finite, the others are 0."""
+    n, m, d = 50, 400, 64
+    cache, kval, vval, table, q, cu, lens = C.case(3, [(n, m)], 2, 2, d, page, fmt)
+    cache.tensors[3][:] = 0
+    for head, t in ((0, 60), (1, m - 20)):
+        spoil_scales(cache, page, table, 0, [t], head, INF)
+    out = C.run(cache, table, q, cu, lens, 4, 0.1).view(n, 2, 2, d)
+    assert not torch.isfinite(out[:, 0]).any()
+    assert not torch.isfinite(out[n - 20:, 1]).any() and (out[:n - 20, 1] == 0).all()
