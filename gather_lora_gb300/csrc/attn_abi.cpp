@@ -157,6 +157,28 @@ int check_window(int32_t window, int32_t sinks) {
   return sinks >= 0 ? LORA_OK : fail(LORA_ERR_SIZE, "sinks %d < 0", sinks);
 }
 
+// freq / (2 pi) less its whole part in units of 2^-64, to the nearest, |freq| < 2^64: the product of freq's 53 bits with the first 192
+// of 1 / (2 pi) as integers (Machin's formula gives them). What is cut off moves it by less than 2^-64 units more.
+uint64_t turns_of(double freq) {
+  static const uint64_t inv_2pi[3] = {0x28be60db9391054aull, 0x7f09d5f47d4d3770ull, 0x36d8a5664f10e410ull};
+  int e = 0;
+  const uint64_t m = static_cast<uint64_t>(std::ldexp(std::frexp(std::fabs(freq), &e), 53));   // |freq| = m 2^(e - 53)
+  uint64_t p[4] = {};                                   // m / (2 pi) in units of 2^-192, low word first
+  for (int i = 0; i < 3; ++i) {
+    const unsigned __int128 t = static_cast<unsigned __int128>(m) * inv_2pi[2 - i] + p[i];
+    p[i] = static_cast<uint64_t>(t);
+    p[i + 1] = static_cast<uint64_t>(t >> 64);
+  }
+  const int shift = 128 - (e - 53);                     // >= 117: units of 2^-64 begin at this bit of p
+  auto word = [&](int w) { return w < 4 ? p[w] : uint64_t{0}; };
+  auto bits = [&](int at) {                             // 64 bits of p from bit `at`
+    const int w = at / 64, off = at % 64;
+    return off ? word(w) >> off | word(w + 1) << (64 - off) : word(w);
+  };
+  const uint64_t t = bits(shift) + (bits(shift - 1) & 1);
+  return freq < 0 ? 0 - t : t;
+}
+
 // What lora_qk_rope and lora_kv_append share: the rotation, positions and norms, and a pair of q rows.
 int rope_args(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* q_out, int64_t q_out_row_stride, int32_t n, int32_t q_heads,
               const lora_rope* rope, const int32_t* positions, int64_t position_stride, const lora_bf16_t* q_norm,
@@ -361,12 +383,9 @@ int lora_rope_init(lora_rope* rope, int32_t head_dim, int32_t rotary_dim, const 
   if (rotary_dim && !freqs) return fail(LORA_ERR_NULL, "freqs is NULL");
   lora_rope r{};
   for (int j = 0; j < rotary_dim / 2; ++j) {
-    if (!std::isfinite(freqs[j])) return fail(LORA_ERR_SIZE, "freqs[%d] is not finite", j);
+    if (!(std::fabs(freqs[j]) < 0x1p64)) return fail(LORA_ERR_SIZE, "freqs[%d] %g is not below 2^64 in magnitude", j, freqs[j]);
     if (axis && axis[j] >= axes) return fail(LORA_ERR_SIZE, "axis %d of pair %d is not below axes %d", axis[j], j, axes);
-    // (taken of the magnitude: there the difference is exact; 63 bits of it, which double's 53 do not pass)
-    const double t = std::fabs(freqs[j]) * 0.15915494309189535;    // 1 / (2 pi)
-    const uint64_t part = static_cast<uint64_t>(std::ldexp(t - std::floor(t), 63)) << 1;
-    r.turns[j] = freqs[j] < 0 ? 0 - part : part;
+    r.turns[j] = turns_of(freqs[j]);
     r.axis[j] = axis ? axis[j] : 0;
   }
   r.head_dim = head_dim;

@@ -9,8 +9,8 @@
 // few rows. All of a value's work is done in fp32 registers and rounded once.
 //
 // Angles. A position turns pair j by position * turns_j, in units of 2^-64 of a full turn: the 64-bit product drops
-// whole turns by wrapping around, exactly, and its upper 32 bits are the angle in (-pi, pi] to 2^-32 of a turn,
-// whatever the position. The special-function unit's sine and cosine are then within 2^-21 absolutely, a
+// whole turns by wrapping around, exactly, and its upper 32 bits are the angle in [-pi, pi), off by at most the 2^-32 of a turn cut off and
+// the position times the table's rounding, 2^31 * 2^-65 turns. The special-function unit's sine and cosine are then within 2^-21 absolutely, a
 // 2^12th of what rounding the result to BF16 costs.
 //
 // Layout. A team of D / 8 lanes holds a head row, 8 values a lane: four pairs, so that no lane needs another's values for

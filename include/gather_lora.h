@@ -491,9 +491,9 @@ int lora_attn_prefill(const lora_bf16_t* q, int64_t q_row_stride, const lora_bf1
  * j < rotary_dim / 2, is turned by the angle position[axis j] * freqs[j]:
  *   (y0, y1) = (x0 cos - x1 sin, x1 cos + x0 sin),
  * its elements j and j + rotary_dim / 2, or (interleaved) 2 j and 2 j + 1.
- * Elements from rotary_dim on are not turned. Angles are reduced exactly: the
- * turns a position makes are held as a fraction of 2^64, so positions may be
- * any int32, however far.
+ * Elements from rotary_dim on are not turned. The turns a position makes are
+ * held as a fraction of 2^64, rounded to the nearest once, and whole turns drop out
+ * exactly: for any int32 position the angle is off by less than 2^-31 of a turn.
  */
 #define LORA_MAX_ROPE_AXES 4
 typedef struct lora_rope {
@@ -504,8 +504,8 @@ typedef struct lora_rope {
 
 /*
  * lora_rope_init — host helper: fills *rope. head_dim 64 or 128, rotary_dim a
- * multiple of 8 in [0, head_dim], freqs [rotary_dim / 2] finite angles (radians)
- * per position, axis [rotary_dim / 2] with values below axes (NULL: all 0),
+ * multiple of 8 in [0, head_dim], freqs [rotary_dim / 2] angles (radians, below
+ * 2^64 in magnitude) per position, axis [rotary_dim / 2] with values below axes (NULL: all 0),
  * axes in [1, LORA_MAX_ROPE_AXES].
  */
 int lora_rope_init(lora_rope* rope, int32_t head_dim, int32_t rotary_dim, const double* freqs,
