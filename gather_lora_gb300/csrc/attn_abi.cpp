@@ -193,7 +193,7 @@ int rope_args(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* q_out, in
     return fail(LORA_ERR_SIZE, "axes %d outside [1, %d]", rope->axes, LORA_MAX_ROPE_AXES);
   for (int j = 0; j < rope->rotary_dim / 2; ++j)
     if (rope->axis[j] >= rope->axes) return fail(LORA_ERR_SIZE, "axis %d of pair %d is not below axes %d", rope->axis[j], j, rope->axes);
-  if (position_stride < n) return fail(LORA_ERR_STRIDE, "position_stride %lld < n %d", (long long)position_stride, n);
+  if (rope->rotary_dim && position_stride < n) return fail(LORA_ERR_STRIDE, "position_stride %lld < n %d", (long long)position_stride, n);
   if ((q_norm || k_norm) && !(std::isfinite(eps) && eps >= 0.f)) return fail(LORA_ERR_SIZE, "eps %g is not finite and >= 0", (double)eps);
   if (q_heads) {
     const int64_t width = static_cast<int64_t>(q_heads) * rope->head_dim;

@@ -524,7 +524,7 @@ int lora_rope_init(lora_rope* rope, int32_t head_dim, int32_t rotary_dim, const 
  * The results go to q_out and k_out, which may be q and k themselves (with the
  * same strides) but must not overlap them otherwise.
  *   positions  [axes, position_stride] int32, n used per axis (row i: positions[a *
- *              position_stride + i]); ignored for rotary_dim 0
+ *              position_stride + i]); they and their stride are ignored for rotary_dim 0
  *   eps        finite, >= 0 (used with a norm)
  * All rows 16-byte aligned, their strides multiples of 8; n in [0, LORA_MAX_KV_ROWS].
  */
