@@ -59,6 +59,7 @@ constexpr int kJoinMost = kMaxCtas / kJoinGroup; // parts of one join: the group
 static_assert(kMaxCtas % kJoinGroup == 0 && kJoinMost >= kJoinGroup, "a join holds a whole group, and all groups of a segment");
 constexpr int kWhole = 2 * kDecWarps;            // segments of at most this many tiles are not divided
 constexpr int kRows = 16;                        // query heads of a segment
+constexpr long long kOneLive = 1LL << 48;
 
 // Workspace: counters [3][kMaxCtas] (a segment's first join group, by its first CTA; its other groups, by
 // theirs: that CTA may also start the next segment; its groups together), then 2 slots per CTA of m[16],
@@ -244,7 +245,9 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
   long long mine = 0, before, total = 0;
   for (int b = b0; b < b1; ++b) {
     int len;
-    mine += tiles_of<TOK, WIN>(p, b, len);
+    const int t = tiles_of<TOK, WIN>(p, b, len);
+    mine += t;
+    if constexpr (WIN) mine += t ? kOneLive : 0;     // (sequences with tiles are counted above the tiles, of which there are fewer than 2^41)
   }
   before = mine;
 #pragma unroll
@@ -260,16 +263,24 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
     if (w < warp) before += s_sum[w];
     total += s_sum[w];
   }
+  [[maybe_unused]] const long long segments = WIN ? total / kOneLive * subs : 0;   // that have tiles
+  if constexpr (WIN) before %= kOneLive, mine %= kOneLive, total %= kOneLive;
   before *= subs;
   mine *= subs;
   total *= subs;
   long long n = min(static_cast<long long>(gridDim.x), (total + kDecWarps - 1) / kDecWarps);   // CTAs with work
   if constexpr (WIN) {
-    // Short windows in small batches: no more CTAs than one join takes parts of a segment, so that there is no second join, until the
-    // longer pieces cost more than it saves. Measured on a GB300, one sequence, 4 key-value heads of 128 in BF16, all CTAs -> this many:
-    // 1028 tokens 17.1 -> 10.1 us, 2048 13.1 -> 11.2, 4096 13.4 -> 13.2, 8192 14.1 -> 17.0; 6 tiles a warp are 5760 such tokens.
-    const long long segments = static_cast<long long>(p.batch) * subs;
-    if (total <= 6 * kDecWarps * (kJoinGroup - 1) * segments) n = min(n, (kJoinGroup - 1) * segments);
+    // Short windows in small batches: no more CTAs than one join takes parts of a segment (of the mean length: in an uneven batch a longer
+    // one may still take a second), so that there is no second join, until the longer pieces cost more than it saves.
+    // Measured on a GB300 with cold caches, one sequence of 1 / 4 / 8 key-value heads, all CTAs -> this many, us:
+    //   BF16, 128:  1028 tokens 11.9 -> 9.8 / 17.2 -> 10.4 / 17.9 -> 11.1, 5000 13.5 -> 13.1 / 15.2 -> 14.1 / 16.8 -> 15.0, 8192 14.7 -> 15.7 / 16.4 -> 16.9 / 18.8 -> 18.0
+    //   E4M3, 128:  2048 12.2 -> 10.2 / 18.4 -> 11.2 / 19.3 -> 12.2, 8192 13.7 -> 14.4 / 20.0 -> 15.9 / 16.9 -> 17.2, 12000 14.5 -> 16.6 / 16.6 -> 18.6 / 18.9 -> 19.9
+    //   E4M3, 64:   4096 10.4 -> 9.5 / 15.4 -> 10.1 / 16.1 -> 10.7, 8192 10.8 -> 11.2 / 16.2 -> 12.2 / 16.9 -> 13.0, 20000 11.8 -> 15.4 / 13.8 -> 17.0 / 16.3 -> 18.4
+    // (INT8 as E4M3, BF16 with heads of 64 as E4M3 of 128). They meet at 5000 to 8500 tokens in the first, 6000 to 11000 in the others:
+    // the rule ends at 96 tokens a warp (5760) and 160 (9600). Idle sequences have no say (one of 1028 tokens and an idle one, 4 heads, BF16:
+    // 17.3 -> 10.5); seven sequences of 100 tokens beside it have (17.6).
+    constexpr int kMostTokens = (TOK == 16 ? 96 : 160) * kDecWarps * (kJoinGroup - 1);
+    if (total <= kMostTokens / TOK * segments) n = min(n, (kJoinGroup - 1) * segments);
   }
   const int c = blockIdx.x;
   if (c >= n) {
