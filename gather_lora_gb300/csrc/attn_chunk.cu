@@ -1242,7 +1242,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const int i = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t col_s = lane_base + i * kTile, col_o = lane_base + Sh::col_o + i * D;
-    const float sl2 = p.scale * kLog2e, grow = CODED ? kGrow : kGrow / sl2;
+    // (finite, so that any maximum passes a reference of -infinity by it, with the smallest scales too)
+    const float sl2 = p.scale * kLog2e, grow = CODED ? kGrow : fminf(kGrow / sl2, 3.402823466e38f);
     const int t_in = row / GB, g = row - t_in * GB;
     const uint32_t stage = smem_u32(chunk_smem) + Sm::stage + warp * kStageBytes;
     bool dead = false, begun = false;    // (begun: an item that the next CTA goes on with)
