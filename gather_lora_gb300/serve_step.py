@@ -33,8 +33,8 @@ class AttentionLayer:
         key heads; window, sinks: a row sees the last `window` tokens up to itself and the first `sinks`."""
         if rotary is not None and (rotary.struct.head_dim != head_dim or rotary.struct.axes != 1):
             raise ValueError(f"rotary is for head_dim {rotary.struct.head_dim} and {rotary.struct.axes} axes: {head_dim} and 1 are wanted")
-        if (window is not None and window < 1) or sinks < 0:
-            raise ValueError(f"window {window}, sinks {sinks}: at least 1 and 0")
+        if (window is not None and not 1 <= window <= L.NO_WINDOW) or not 0 <= sinks <= L.NO_WINDOW:
+            raise ValueError(f"window {window}, sinks {sinks}: at least 1 and 0, at most {L.NO_WINDOW}")
         g = torch.Generator(device=device).manual_seed(seed)
         self.hidden, self.hq, self.hkv, self.d, self.rank, self.max_loras = hidden, q_heads, kv_heads, head_dim, rank, max_loras
         self.page_size, self.device = page_size, torch.device(device)
