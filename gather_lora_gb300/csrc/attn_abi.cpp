@@ -343,8 +343,6 @@ int lora_attn_chunk(const lora_bf16_t* q, int64_t q_row_stride, lora_bf16_t* out
     return fail(LORA_ERR_NULL, "a required pointer is NULL (q, out, cu_q, block_table, seq_lens, workspace)");
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace))
     return fail(LORA_ERR_ALIGN, "q, out and workspace must be 16-byte aligned");
-  a.q = q;
-  a.q_stride = q_row_stride;
   a.out = out;
   a.out_stride = out_row_stride;
   a.cu_q = cu_q;

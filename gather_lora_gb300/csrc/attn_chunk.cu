@@ -169,17 +169,6 @@ __device__ __forceinline__ bool passed(unsigned long long& bar, uint32_t parity)
   return done != 0;
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void copies_left() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
-}
-
 __device__ __forceinline__ void takers_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(kTakers * 32) : "memory"); }
 // The same, and whether one of the warps has seen that the CTA failed: they stay together, as the others would wait at the next
 // barrier for one that has left.
@@ -192,25 +181,6 @@ __device__ __forceinline__ bool takers_failed(const ChunkCtl& c) {
   return any != 0;
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// Four codes as f16 pairs.
-template <int FMT>
-__device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
-  if constexpr (FMT == kKvE4m3) {
-    e4m3x4_to_f16(c, lo, hi);
-  } else {   // 0x6400 | (code + 128) is the f16 number 1152 + code
-    c ^= 0x80808080u;
-    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-    uint32_t l = __byte_perm(c, 0x64646464u, 0x4140), h = __byte_perm(c, 0x64646464u, 0x4342);
-    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&l), off), y = __hsub2(*reinterpret_cast<__half2*>(&h), off);
-    lo = *reinterpret_cast<const uint32_t*>(&x);
-    hi = *reinterpret_cast<const uint32_t*>(&y);
-  }
-}
 // A scale over its group's power of two as f16 hi + lo (hi in the low half): 22 bits of it.
 __device__ __forceinline__ uint32_t split_f16(float m) {
   const __half hi = __float2half_rn(m), lo = __float2half_rn(m - __half2float(hi));
@@ -286,11 +256,6 @@ __device__ __forceinline__ uint4 chunk_or_zero(const uint4& x) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int c0, int c1, int c2, uint32_t bar) {
-  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n"
-               ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-               : "memory");
-}
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int c0, int c1, int c2, int c3, uint32_t bar) {
   asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n"
                ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
@@ -775,8 +740,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           const uint32_t to = smem_u32(m.ks + lane * 4);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            copy4(to + x * 4, p.c.ks + si + x, there);
-            copy4(to + kTile * 4 + x * 4, p.c.vs + si + x, there);
+            cp_async4_n(to + x * 4, p.c.ks + si + x, there ? 4 : 0);
+            cp_async4_n(to + kTile * 4 + x * 4, p.c.vs + si + x, there ? 4 : 0);
           }
           cp_async_arrive_noinc(smem_u32(&c.landed[ks]));
         }
@@ -1023,7 +988,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           const uint32_t live = __ballot_sync(0xffffffffu, there) & 0xffffu;
           if (g + kLoaders < groups) page = look_up(g + kLoaders, slot);     // (while this group is on its way)
           if (!ready(g, false)) {        // (what is in flight may be what it waits for)
-            copies_left<0>();
+            cp_async_wait_n<0>();
             while (next < g) hand_over();
             ready(g, true);
             if (__any_sync(0xffffffffu, failed(c))) break;
@@ -1037,15 +1002,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
           for (int i = 0; i < NI; ++i) {
             const int t = i * TPI + sub_t;
             const long long o = __shfl_sync(0xffffffffu, off, t);
-            copy16(at + Sh::at(r0 + t, ch), from + (o < 0 ? 0 : o) + ch * 16, o >= 0);
+            cp_async16_n(at + Sh::at(r0 + t, ch), from + (o < 0 ? 0 : o) + ch * 16, o < 0 ? 0 : 16);
           }
           cp_async_commit();
           if (next + kLag * kLoaders <= g) {
-            copies_left<kLag>();
+            cp_async_wait_n<kLag>();
             hand_over();
           }
         }
-        copies_left<0>();
+        cp_async_wait_n<0>();
         while (next < groups && !__any_sync(0xffffffffu, failed(c))) hand_over();
       } else {
         // A group's codes are loaded while the one before it is converted, its pages looked up one ahead of that.
@@ -1133,7 +1098,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c.piece_empty[sl]));
     }
-    copies_left<0>();
+    cp_async_wait_n<0>();
   } else if (warp == kMmaWarp) {
     // ============================ MMA issue ===============================
     // The warp takes every step together, lane 0 issues. The steps are compiled for each stage of the ring, so that descriptors and

@@ -125,12 +125,6 @@ __device__ __forceinline__ bool pre_wait(PrefillCtl& c, unsigned long long& bar,
   return false;
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int c0, int c1, int c2, uint32_t bar) {
-  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n"
-               ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-               : "memory");
-}
-
 // The grid's next block that has not started, taken over by this CTA: the answer (16 bytes at shared
 // address `to`) arrives on mbarrier `bar`.
 __device__ __forceinline__ void ask_next_block(uint32_t to, uint32_t bar) {

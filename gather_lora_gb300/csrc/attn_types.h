@@ -83,8 +83,6 @@ struct ChunkArgs {
   TensorMapBytes map_k;      // pages as [num_pages, kv_heads, page_size, head_dim] (heads_inside: heads and slots change places),
   TensorMapBytes map_v;      // boxes of box_tokens slots (used if that is not 0)
   KvView c;
-  const uint16_t* q;
-  long long q_stride;
   uint16_t* out;
   long long out_stride;
   const int32_t* cu_q;
