@@ -94,8 +94,8 @@ struct ChunkMeta {           // of a key tile
   // 8 bits, of 16 tokens (BOXED: the first, of all): scale log2(e) times K's power of two, log2 of V's, kSumUnit over V's, and
   // whether their scales are taken token by token instead (ab)
   float4 group[kGroups];
-  float2 ab[kTile];          // scale log2(e) times the token's K scale, log2 of its V scale
-  float iv[kTile];           // kSumUnit over its V scale
+  float2 ab[kTile];          // scale log2(e) times the token's K scale, log2 of its V scale over 2^kRaise
+  float iv[kTile];           // kSumUnit over that
   float ks[kTile], vs[kTile];   // (BOXED) the scales as they are
 };
 
@@ -203,9 +203,10 @@ __device__ __forceinline__ uint4 scaled8(uint32_t c0, uint32_t c1, uint32_t m) {
 }
 // Exponent of the power of two of a group whose largest scale is `most`: codes times scales are below 2^15 of it.
 template <int FMT>
+constexpr int kCodeBits = FMT == kKvE4m3 ? 9 : 7;          // codes are below 2 to that
+template <int FMT>
 __device__ __forceinline__ int group_exponent(float most) {
-  constexpr int bits = FMT == kKvE4m3 ? 9 : 7;             // codes are below 2^bits
-  return max(-120, (__float_as_int(most) >> 23) - 127 + 1 + bits - 15);
+  return max(-120, (__float_as_int(most) >> 23) - 127 + 1 + kCodeBits<FMT> - 15);
 }
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + e) << 23); }
 __device__ __forceinline__ float magnitude(float s) { return fabsf(s) < INFINITY ? fabsf(s) : INFINITY; }
@@ -223,16 +224,25 @@ template <int FMT>
 __device__ __forceinline__ uint32_t scale_of(float s, float most) {
   return split_f16(most == 0.f ? 0.f : s * exp2_int(-group_exponent<FMT>(most)));
 }
-// Token by token: codes of K as they are, of V with the scale's sign (0: they only count in the sum; not finite: NaN, times 0 too).
-constexpr uint32_t kOne = 0x3c00u;
-__device__ __forceinline__ uint32_t sign_of(float s) { return s == 0.f ? 0u : !(fabsf(s) < INFINITY) ? 0x7e00u : s < 0.f ? 0xbc00u : kOne; }
+// Token by token: codes of K as they are, of V times 2^kRaise with the scale's sign (0: they only count in the sum; not finite: NaN, times 0
+// too). With kRaise they lie below 2^15 as those of a group do, and a weight says as much of a token's part in the result: without it the
+// weights beside a largest one that is taken token by token were 2^kRaise nearer to f16's least.
+template <int FMT>
+constexpr int kRaise = 15 - kCodeBits<FMT>;
+constexpr uint32_t kOne = 0x3c00u;                         // (f16; adding to its exponent multiplies by powers of two)
+template <int FMT>
+__device__ __forceinline__ uint32_t sign_of(float s) {
+  return s == 0.f ? 0u : !(fabsf(s) < INFINITY) ? 0x7e00u : kOne + (kRaise<FMT> << 10) + (s < 0.f ? 0x8000u : 0u);
+}
 // A V scale of 0 is 2^-64 to the weights (see above), and so is one that is not finite: the scores and their sum do not go by V. Below 2^-110,
 // under what lora_kv_write stores, it is 2^-110.
 __device__ __forceinline__ float magnitude_of(float v) {
   return v == 0.f || !(fabsf(v) < INFINITY) ? 5.421010862427522e-20f : fmaxf(fabsf(v), 7.703719777548943e-34f);
 }
-__device__ __forceinline__ float2 scales_of(float k, float v, float sl2) { return make_float2(k * sl2, log2f(magnitude_of(v))); }
-__device__ __forceinline__ float over_scale(float v) { return kSumUnit / magnitude_of(v); }
+template <int FMT>
+__device__ __forceinline__ float2 scales_of(float k, float v, float sl2) { return make_float2(k * sl2, log2f(magnitude_of(v)) - kRaise<FMT>); }
+template <int FMT>
+__device__ __forceinline__ float over_scale(float v) { return kSumUnit * (1 << kRaise<FMT>) / magnitude_of(v); }
 
 // Chunks of V: whether all is finite, and with what is not set to zero.
 template <bool CODED>
@@ -828,11 +838,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                                  !(tt + kTile - 1 <= w.first && (tt > w.end - p.window || tt + kTile - 1 < p.sinks));
               if (q == 0 && lane == 0) m.group[0] = group_of<FMT>(most_k, most_v, sl2, exact);
               if (exact) {
-                m.ab[r] = scales_of(sk, sv, sl2);
-                m.iv[r] = over_scale(sv);
+                m.ab[r] = scales_of<FMT>(sk, sv, sl2);
+                m.iv[r] = over_scale<FMT>(sv);
               }
               mult_k = exact ? kOne : scale_of<FMT>(sk, most_k);
-              mult_v = exact ? sign_of(sv) : scale_of<FMT>(sv, most_v);
+              mult_v = exact ? sign_of<FMT>(sv) : scale_of<FMT>(sv, most_v);
               __syncwarp();
               if (lane == 0) mbar_arrive(smem_u32(&c.meta_full[k % kMeta]));
             }
@@ -1069,11 +1079,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
               m.group[g % kGroups] = group_of<FMT>(most_k, most_v, sl2, exact);
             }
             if (exact && lane < kGroup) {
-              m.ab[r0 + lane] = scales_of(k_scale, v_scale, sl2);
-              m.iv[r0 + lane] = over_scale(v_scale);
+              m.ab[r0 + lane] = scales_of<FMT>(k_scale, v_scale, sl2);
+              m.iv[r0 + lane] = over_scale<FMT>(v_scale);
             }
           }
-          const uint32_t mult = exact ? (keys ? kOne : sign_of(v_scale)) : keys ? scale_of<FMT>(k_scale, most_k) : scale_of<FMT>(v_scale, most_v);
+          const uint32_t mult = exact ? (keys ? kOne : sign_of<FMT>(v_scale)) : keys ? scale_of<FMT>(k_scale, most_k) : scale_of<FMT>(v_scale, most_v);
           const bool look = !keys && split;
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
