@@ -13,8 +13,9 @@
 // CTA per SM), so that any mix of long and short chunks and contexts takes equal time everywhere; ends within kSnap units of
 // an item's end move there. A range is walked piece by piece (its part of one item). A piece that is a whole item is
 // finished by its CTA; otherwise its rows' exponents, sums and O go to the workspace, and a second kernel joins an item's parts in
-// CTA order: the bits never depend on who was last. (Joined by the item's last CTA to arrive they took 19 us at the end of
-// every range, as one CTA's loads and as code that crowded the loops out of the instruction caches.)
+// CTA order: the bits never depend on who was last. (Joined by the item's last CTA to arrive, 16 rows after 1000 tokens took 36 us instead
+// of 26, four packed chunks 252 instead of 238: one CTA's loads at the end of a range, and code that crowds the loops out of the
+// instruction caches.)
 //
 // Roles of a CTA's 16 warps: 0-7 softmax, 8 issues the MMAs, 9 plans and loads Q (TMA), 11-15 bring K and V. Where the pages'
 // size and strides allow (BOXED: sizes in eights), warp 11 looks the pages up, a lane four tokens, and issues TMA, a box a page,
@@ -22,25 +23,28 @@
 // not is looked through. Otherwise the five warps take groups of 16 tokens in turn by cp.async (BF16) or through registers.
 //
 // 8-bit formats run in f16: the codes of both formats are exact in it, times their scale over a power of two that the tokens of a tile
-// share (BOXED; else 16 tokens; a product rounded once, to 11 bits), so that the softmax meets scales once a tile: with one a token,
-// read from shared memory by every row, it took 2.8 times as long, as the MMAs leave little of that memory's bandwidth. K's
+// share (BOXED; else 16 tokens; a product rounded once, to 11 bits), so that the softmax meets scales once a tile. One a token is
+// read from shared memory by every row, whose bandwidth the MMAs need: that is how tiles are taken whose scales are more than 2^12 apart or
+// not finite, or that some rows of the item see and others do not. K's
 // power of two multiplies the scores; V's the weight: to keep weights of any scale in f16's range the running reference is that of
 // y_t = z_t + log2 of V's, the weight w = 2^(y - ref) multiplies V and the softmax's own sum is that of w over V's. Q is brought
 // into f16's range by a power of two a row.
 //
-// Rounding to fewer bits: the weights (BF16 over a BF16 cache, else f16: the tensor cores' operand types), the result.
+// Rounding to fewer bits: the weights (BF16 over a BF16 cache, else f16: the tensor cores' operand types; f16 ones lose bits below 2^-21 of a
+// row's largest and are 0 below 2^-32, times V's codes below 2^15), K and V of 8 bits (once, to 11 bits), the result.
 //
 // Zero weight times what is not finite is NaN in an MMA. The loaders look through what some rows of the item see and others
 // do not (its last tokens, and the first ones of its windows), set what is not finite in V to zero, and the softmax
 // warps (or the join) add it to the stored rows that see it.
 //
 // Measured on a GB300 (cuBLAS bf16 1.9 PFLOP/s, copy 6.8 TB/s). Operations bound long chunks: four chunks of up to 1500 rows after 4000
-// tokens, 32 heads of 128 over 8 in BF16, 241 us (floor 126; tensor pipe 47%: a key tile is about 1900 clocks of a softmax warpgroup and
-// 2700 of the MMA warp's issue and waits for both row tiles, against 2048 of MMA); 2048 rows after 30000 over E4M3 1.09 ms (floor
-// 0.55; 41%: the converting warps bring a K tile every 1600 clocks or so). Bytes bound few rows: 32 sequences of up to 6 rows after 8192
-// in BF16 124 us (floor 77; one warp looks up the pages of 16 tokens and issues their copies). A window of 2048 over INT8 with heads
-// of 64: 109 us (floor 10; 28% of the tiles are seen in part and scaled token by token, in a pass of their own, and an item
-// costs as much as 2 tiles beside its 18 or so). 16 rows after 1000 tokens 22 us: the plan, the look-up, two launches of cold code.
+// tokens, 32 heads of 128 over 8 in BF16, 236 us (floor 126; tensor pipe 47%: the chain of a key tile through softmax and MMA warp); 2048
+// rows after 30000 over E4M3 1.10 ms (floor 0.55; 41%: that chain beside the conversion of the codes; over BF16 0.88). Bytes bound few rows: 32
+// sequences of up to 6 rows after 8192 in BF16 124 us (floor 77; one warp looks up the pages of 16 tokens and issues their copies; of 64
+// tokens 114), over E4M3 157. A window of 2048 over INT8 with heads of 64: 110 us (floor 10; 28% of the tiles are seen in part and
+// scaled token by token, in a pass of their own, and an item costs as much as 2 tiles beside its 18 or so). 16 rows after 1000 tokens 22 us: the plan,
+// the look-up, two launches of cold code. Without TMA (pages of 20 tokens) the first takes 328 us, the second 1.79 ms, few rows 161 over
+// BF16 and 248 over E4M3.
 #include <type_traits>
 
 #include "attn_common.cuh"

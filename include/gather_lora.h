@@ -447,6 +447,8 @@ int lora_kv_read(lora_bf16_t* k_out, int64_t k_row_stride, lora_bf16_t* v_out, i
  *                ready for the next on the same stream. Calls that may run at the
  *                same time need one each.
  *   scale        positive and finite (1 / sqrt(head_dim) as a rule)
+ * Weights multiply V in BF16 over a BF16 cache and with TF32's 11 bits over an 8-bit one, whose codes are
+ * exact there and whose scales are f32; everything else is f32, the result rounded once.
  * How a sequence is split over the GPU follows the lengths of the whole batch:
  * results are the same bits for the same batch, and may differ in the last bits
  * between batches.
@@ -585,8 +587,15 @@ int lora_attn_decode_window(const lora_bf16_t* q, int64_t q_row_stride, lora_bf1
  * a row that sees no token (p < 0) gives zeros and lse = -infinity. Tokens that a
  * row does not see have no influence on it, whatever they hold; a token whose
  * page is outside [0, num_pages) is left out. L is clamped as in lora_attn_decode.
+ * Numerics: f32 sums and statistics, the result rounded once. Weights multiply V in
+ * BF16 over a BF16 cache. Over an 8-bit one K and V are code times scale rounded to 11 bits
+ * (their scales in f32 where those of neighbours are more than 2^12 apart) and weights
+ * are f16: 11 bits down to 2^-21 of a row's largest, fewer below, 0 under 2^-32 of it. A single token is thus
+ * as exact as through lora_attn_decode_window over BF16 and less over 8 bits, where 11 bits of K
+ * move a score by up to 2^-12 of scale * sum |q k|. A value of an 8-bit cache that
+ * is not finite counts as NaN.
  *   q, out      [total_q, row stride] BF16, q_heads * head_dim values used, 16-byte
- *               aligned, strides multiples of 8
+ *               aligned, strides multiples of 8; out must not overlap q
  *   cu_q        [batch + 1] int32, non-decreasing, in [0, total_q] (a sequence whose
  *               own two fall or leave that range is left out; rows of sequences that
  *               overlap are not defined); rows of no sequence stay unchanged
